@@ -237,6 +237,93 @@ fa_status fa_decode_paged(const void* q, const void* k_cache, const void* v_cach
                           int num_pages, int max_pages, float scale, int dtype, void* stream);
 
 /*
+ * Rotary positions.  The pages attend to queries and keys as given; a model that marks positions
+ * by rotation turns them first.  In row l of sequence b, at position m, every pair (x1, x2) of
+ * the first rotary_dim elements of a head becomes
+ *     y1 = mscale * (x1 cos(m theta_i) - x2 sin(m theta_i)),
+ *     y2 = mscale * (x2 cos(m theta_i) + x1 sin(m theta_i)),      i = 0 .. rotary_dim/2 - 1,
+ * the pairs being elements (i, i + rotary_dim/2), or (2i, 2i+1) with interleaved = 1; elements
+ * past rotary_dim are copied.  Computed in fp32 and rounded once.  inverse = 1 turns by the
+ * negative angle: the gradient of the inputs from the gradient of the outputs.
+ *   q, q_out: [B, Hq, L, D], k, k_out: [B, Hk, L, D] views (strides[0..3] = q, k, q_out, k_out;
+ *             Hk = 0 or Hq = 0: that operand is absent and its pointers are ignored);
+ *             D in {64, 128}; an output may be its own input (same pointer and strides), or
+ *             interleave with another operand as a part of one packed tensor; no other overlap;
+ *   positions: [B, L] int32, device, rows position_stride elements apart (0: one row for all
+ *             sequences; negative positions turn backwards), or null: position l;
+ *   freqs:    [rotary_dim / 2] int64, device: theta_i as a fraction of a turn, theta_i / (2 pi)
+ *             * 2^64, as fa_rotary_freqs makes it (angles are reduced exactly at any position);
+ *   rotary_dim: even, 2 .. D.  B * L < 2^31.
+ */
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out,
+                    const fa_strides* strides, const int32_t* positions, int64_t position_stride,
+                    const int64_t* freqs, int rotary_dim, float mscale, int interleaved,
+                    int inverse, int B, int Hq, int Hk, int L, int D, int dtype, void* stream);
+
+/*
+ * Frequencies for fa_rotary, on the host: fills freqs[0 .. rotary_dim/2) and *mscale.
+ *   FA_ROTARY_PLAIN   theta_i = base^(-2i / rotary_dim)
+ *   FA_ROTARY_LINEAR  theta_i / factor (positions interpolated)
+ *   FA_ROTARY_NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in the place of base: the
+ *                     highest frequency stays, the lowest is divided by factor
+ *   FA_ROTARY_YARN    by parts (Peng et al., "YaRN", 2023): a frequency that turns 32 times or more
+ *                     within original_len positions stays, one that turns once or less is divided
+ *                     by factor, a linear ramp between; mscale = 0.1 ln(factor) + 1
+ * mscale is 1 otherwise.  base >= 1, factor >= 1; original_len > 0 (YaRN only).
+ */
+typedef enum {
+    FA_ROTARY_PLAIN = 0,
+    FA_ROTARY_LINEAR = 1,
+    FA_ROTARY_NTK = 2,
+    FA_ROTARY_YARN = 3
+} fa_rotary_scaling;
+fa_status fa_rotary_freqs(int rotary_dim, double base, int scaling, double factor,
+                          double original_len, int64_t* freqs, float* mscale);
+
+/*
+ * What a paged cache holds.  FA_CACHE_16BIT: rows of the call's dtype, as fa_decode_paged reads
+ * them.  FA_CACHE_E4M3: a row x of D values as D e4m3 bytes, e4m3(x_i * 2^-e), and one byte e + 127
+ * in k_exp / v_exp, e being the smallest integer in [-127, 127] with max|x| <= 448 * 2^e (values
+ * rounded to nearest even; the scaling is exact).  A row with an infinity or a NaN gets the byte
+ * 255 and reads back as NaN.
+ */
+typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_E4M3 = 1 } fa_cache_dtype;
+
+/*
+ * Writes new keys and values into a paged cache.  Sequence b adds new_lens[b] rows (rows
+ * 0 .. new_lens[b]-1 of k[b], v[b]), which become its last tokens seq_lens[b] - new_lens[b] ..
+ * seq_lens[b] - 1; rows of k and v behind them are not read, other slots keep what they hold.
+ *   k, v:        [B, H, L, D] views of dtype (strides[0..1]);
+ *   k_cache, v_cache: [num_pages, H, FA_PAGE_TOKENS, D], k_exp, v_exp: [num_pages, H,
+ *                FA_PAGE_TOKENS] bytes (ignored for a 16-bit cache), 16-byte aligned, contiguous;
+ *   block_tables [B, max_pages], seq_lens [B], new_lens [B]: int32, device.  new_lens null: every
+ *                sequence adds L rows, one of length 0 (an unused place of the batch) none;
+ *   rotary_dim > 0 rotates each key by its token index (fa_rotary's freqs, mscale, interleaved)
+ *                in fp32 before it is rounded or quantised; 0 writes the keys as they are.
+ * A token must have one owner: pages that two sequences of the batch share may be read by both,
+ * but not written in one call.  A bad length or page index (device data) is reported by
+ * fa_get_device_status() as FA_ERR_INVALID_ARG; the sequence's rows with it are not written.
+ */
+fa_status fa_cache_append(const void* k, const void* v, const fa_strides* strides, void* k_cache,
+                          void* v_cache, void* k_exp, void* v_exp, const int32_t* block_tables,
+                          const int32_t* seq_lens, const int32_t* new_lens, const int64_t* freqs,
+                          int rotary_dim, float mscale, int interleaved, int B, int H, int L, int D,
+                          int num_pages, int max_pages, int dtype, int cache_dtype, void* stream);
+
+/*
+ * Reads a paged cache back: rows 0 .. L-1 of every sequence as dense k, v [B, H, L, D] views of
+ * dtype (strides[0..1]); rows at or past seq_lens[b] are written as zeros.  An e4m3 row is
+ * its values times 2^e, rounded to dtype (exact in bf16, but for a value that quantising rounded up
+ * to 2^128).  For a prompt that continues behind
+ * cached tokens: the dense rows are the keys and values of fa_fwd_ex with Lk > Lq.  Bad device data
+ * is reported as for fa_cache_append; those rows are written as zeros.
+ */
+fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_exp,
+                        const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,
+                        void* k, void* v, const fa_strides* strides, int B, int H, int L, int D,
+                        int num_pages, int max_pages, int dtype, int cache_dtype, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's status word.  Returns
  * FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call,
  * FA_ERR_INVALID_ARG if a decode kernel found a page index or sequence length out of range, or

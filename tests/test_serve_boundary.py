@@ -1,0 +1,182 @@
+"""Argument checks of the rotary, cache and grouped decode calls on the host (no GPU work).
+
+Every call here is refused, or has nothing to do, before the library touches the CUDA runtime.
+"""
+import math
+
+import pytest
+
+import tiled_attention_08_gb300 as fa
+
+A = 0x100000  # fake, 16-byte aligned device addresses: never dereferenced by these calls
+MB = 1 << 20
+BAD, UNS, OK = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_OK
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    from tiled_attention_08_gb300 import build
+    build.build()
+    return fa.load_library()
+
+
+def _rotary(B=2, Hq=2, Hk=1, L=16, D=64, rd=64, mscale=1.0, inter=0, inverse=0, dtype=0, pstride=16,
+            strides=None, **ptrs):
+    p = dict(q=A, k=A + MB, qo=A + 2 * MB, ko=A + 3 * MB, pos=A + 4 * MB, freqs=A + 5 * MB)
+    p.update(ptrs)
+    sq, sk = (Hq * L * D, L * D, D), (Hk * L * D, L * D, D)
+    return fa.fa_rotary(p["q"], p["k"], p["qo"], p["ko"], strides or [sq, sk, sq, sk], p["pos"],
+                        pstride, p["freqs"], rd, mscale, inter, inverse, B, Hq, Hk, L, D, dtype, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=2), BAD),
+    (dict(B=-1), BAD),
+    (dict(Hk=-1), BAD),
+    (dict(L=-1), BAD),
+    (dict(D=0), BAD),
+    (dict(D=96), UNS),
+    (dict(rd=0), BAD),
+    (dict(rd=63), BAD),
+    (dict(rd=66), BAD),
+    (dict(rd=-2), BAD),
+    (dict(mscale=math.nan), BAD),
+    (dict(mscale=math.inf), BAD),
+    (dict(inter=2), BAD),
+    (dict(inverse=-1), BAD),
+    (dict(q=0), BAD),
+    (dict(ko=0), BAD),
+    (dict(freqs=0), BAD),
+    (dict(freqs=A + 5 * MB + 4), BAD),           # freqs not 8-byte aligned
+    (dict(pos=A + 4 * MB + 2), BAD),
+    (dict(pstride=-1), BAD),
+    (dict(q=A + 8), BAD),                        # misaligned
+    (dict(qo=A + 1024), BAD),                    # inside q, but not q itself
+    (dict(ko=A), BAD),                           # k's output on q
+    (dict(ko=A + 2 * MB + 2048), BAD),           # the outputs overlap
+    (dict(qo=A + 4 * MB), BAD),                  # on the positions
+    (dict(strides=[(2048, 1024, 60)] * 4), BAD),
+    (dict(strides=[(2048, 0, 64)] * 4), BAD),    # zero head stride with two heads
+    (dict(B=1 << 20, L=1 << 12), UNS),
+    (dict(Hq=65535, Hk=1, B=1, L=1), UNS),
+    (dict(B=0), OK),
+    (dict(L=0, q=0, k=0, qo=0, ko=0, freqs=0), OK),
+    (dict(Hq=0, Hk=0), OK),
+], ids=lambda x: str(x)[:48])
+def test_rotary_argument_checks(kw, status):
+    assert _rotary(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), OK),
+    (dict(scaling=3, factor=16.0, orig=4096.0), OK),
+    (dict(rd=0), BAD),
+    (dict(rd=7), BAD),
+    (dict(base=0.5), BAD),
+    (dict(base=math.inf), BAD),
+    (dict(base=math.nan), BAD),
+    (dict(scaling=4), BAD),
+    (dict(scaling=-1), BAD),
+    (dict(scaling=1, factor=0.5), BAD),
+    (dict(scaling=1, factor=math.nan), BAD),
+    (dict(scaling=3, factor=2.0), BAD),          # needs the trained length
+    (dict(scaling=3, factor=2.0, orig=math.inf), BAD),
+    (dict(scaling=2, factor=2.0, rd=2), BAD),    # exponent rd / (rd - 2)
+    (dict(scaling=2, factor=1e300, rd=4), BAD),  # the grown base overflows
+], ids=lambda x: str(x)[:48])
+def test_rotary_freqs_checks(kw, status):
+    kw = dict(dict(rd=64, base=10000.0, scaling=0, factor=1.0, orig=0.0), **kw)
+    assert fa.fa_rotary_freqs(kw["rd"], kw["base"], kw["scaling"], kw["factor"], kw["orig"])[0] == status
+
+
+@pytest.mark.parametrize("scaling", ["none", "linear", "ntk", "yarn"])
+def test_rotary_freqs_values(scaling):
+    """Turns per position of every form, in 64-bit fixed point."""
+    rd, base, f, orig = 64, 10000.0, 8.0, 2048.0
+    st, freqs, mscale = fa.fa_rotary_freqs(rd, base, fa.FA_ROTARY_SCALING[scaling], f, orig)
+    assert st == OK and len(freqs) == rd // 2
+    for i, w in enumerate(freqs):
+        b = base * f ** (rd / (rd - 2)) if scaling == "ntk" else base
+        th = b ** (-2 * i / rd)
+        if scaling == "linear":
+            th /= f
+        if scaling == "yarn":
+            keep = min(1.0, max(0.0, (orig * th / (2 * math.pi) - 1) / 31))
+            th = th * keep + th / f * (1 - keep)
+        # pow and the quotient are each within a step or two of 2^-53; the fixed point rounds to
+        # a whole number of 2^-64 turns, off by half of one: 2 pi 2^-65 radians
+        assert abs(w / 2.0 ** 64 * 2 * math.pi - th) <= th * 2.0 ** -49 + 2 * math.pi * 2.0 ** -65, i
+    assert abs(mscale - (0.1 * math.log(f) + 1 if scaling == "yarn" else 1.0)) <= 2.0 ** -23
+    with pytest.raises(ValueError):
+        fa.rotary_freqs(64, scaling="cubic", device="cpu")
+    with pytest.raises(fa.FaError):
+        fa.rotary_freqs(65, device="cpu")
+    table, _ = fa.rotary_freqs(rd, base, scaling, f, orig, device="cpu")
+    assert table.tolist() == freqs
+
+
+def _append(B=2, H=2, L=4, D=64, rd=0, pages=8, maxp=4, dtype=0, cdtype=1, **ptrs):
+    p = dict(k=A, v=A + MB, kc=A + 2 * MB, vc=A + 3 * MB, ke=A + 4 * MB, ve=A + 5 * MB, bt=A + 6 * MB,
+             sl=A + 7 * MB, nl=A + 8 * MB, freqs=A + 9 * MB, st=None)
+    p.update(ptrs)
+    c = (H * L * D, L * D, D)
+    return fa.fa_cache_append(p["k"], p["v"], p["st"] or [c, c], p["kc"], p["vc"], p["ke"], p["ve"],
+                              p["bt"], p["sl"], p["nl"], p["freqs"], rd, 1.0, 0, B, H, L, D, pages, maxp,
+                              dtype, cdtype, None)
+
+
+def _read(B=2, H=2, L=4, D=64, pages=8, maxp=4, dtype=0, cdtype=1, **ptrs):
+    p = dict(k=A, v=A + MB, kc=A + 2 * MB, vc=A + 3 * MB, ke=A + 4 * MB, ve=A + 5 * MB, bt=A + 6 * MB,
+             sl=A + 7 * MB, st=None)
+    p.update(ptrs)
+    c = (H * L * D, L * D, D)
+    return fa.fa_cache_read(p["kc"], p["vc"], p["ke"], p["ve"], p["bt"], p["sl"], p["k"], p["v"],
+                            p["st"] or [c, c], B, H, L, D, pages, maxp, dtype, cdtype, None)
+
+
+COMMON = [
+    (dict(dtype=7), BAD),
+    (dict(cdtype=2), BAD),
+    (dict(B=-1), BAD),
+    (dict(L=-1), BAD),
+    (dict(pages=-1), BAD),
+    (dict(D=0), BAD),
+    (dict(D=80), UNS),
+    (dict(B=65536), UNS),
+    (dict(H=65536), UNS),
+    (dict(maxp=1 << 28), UNS),                   # 16 * max_pages past 31 bits
+    (dict(k=0), BAD),
+    (dict(v=A + MB + 2), BAD),
+    (dict(kc=0), BAD),
+    (dict(ke=0), BAD),
+    (dict(bt=0), BAD),
+    (dict(sl=0), BAD),
+    (dict(sl=A + 7 * MB + 1), BAD),
+    (dict(st=[(512, 256, 65)] * 2), BAD),
+    (dict(st=[(512, -256, 64)] * 2), BAD),
+    (dict(kc=A + 512), BAD),                     # the cache on the rows
+    (dict(v=A + 4 * MB), BAD),                   # the rows on the exponents
+    (dict(L=0, k=0, v=0), OK),
+    (dict(B=0), OK),
+    (dict(H=0), OK),
+]
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(rd=3), BAD),
+    (dict(rd=66), BAD),
+    (dict(rd=64, freqs=0), BAD),
+    (dict(nl=A + 8 * MB + 2), BAD),
+    (dict(vc=A + 2 * MB + 4096), BAD),           # the two caches overlap
+    (dict(ve=A + 3 * MB), BAD),                  # exponents on the value cache
+    (dict(bt=A + 2 * MB), BAD),                  # the table inside the cache
+], ids=lambda x: str(x)[:48])
+def test_append_argument_checks(kw, status):
+    assert _append(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", COMMON + [
+    (dict(v=A + 256), BAD),                      # the outputs overlap
+], ids=lambda x: str(x)[:48])
+def test_read_argument_checks(kw, status):
+    assert _read(**kw) == status

@@ -29,13 +29,17 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "fa_selftest_wait_timeout", "fa_trace_next_call", "fa_launch_count", "fa_status_string",
            "fa_bwd_noalloc", "forward", "backward", "attention", "attention_blhd",
            "attention_qkvpacked", "FaStrides", "fa_decode_paged", "fa_decode_workspace_bytes",
-           "decode_paged", "FA_PAGE_TOKENS",
+           "decode_paged", "FA_PAGE_TOKENS", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
+           "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
+           "FA_CACHE_16BIT", "FA_CACHE_E4M3",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_BF16", "FA_FP16"]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 FA_BF16, FA_FP16 = 0, 1
 FA_PAGE_TOKENS = 16
+FA_CACHE_16BIT, FA_CACHE_E4M3 = 0, 1
+FA_ROTARY_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libfa.so")
@@ -46,7 +50,8 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_bwd_workspace_bytes_ex", "fa_set_forward_pair", "fa_get_device_status",
             "fa_set_wait_timeout_ns", "fa_selftest_wait_timeout", "fa_trace_next_call",
             "fa_launch_count", "fa_status_string", "fa_bwd_noalloc", "fa_decode_paged",
-            "fa_decode_workspace_bytes")
+            "fa_decode_workspace_bytes", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
+            "fa_cache_read")
 
 
 class FaStrides(ctypes.Structure):
@@ -94,6 +99,18 @@ def load_library():
         lib.fa_decode_workspace_bytes.restype = sz
         lib.fa_decode_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, f, i, vp]
         lib.fa_decode_paged.restype = i
+        i64 = ctypes.c_int64
+        lib.fa_rotary_freqs.argtypes = [i, d64, i, d64, d64, ctypes.POINTER(i64),
+                                        ctypes.POINTER(f)]
+        lib.fa_rotary_freqs.restype = i
+        lib.fa_rotary.argtypes = [vp, vp, vp, vp, sp, vp, i64, vp, i, f, i, i, i, i, i, i, i, i, vp]
+        lib.fa_rotary.restype = i
+        lib.fa_cache_append.argtypes = [vp, vp, sp, vp, vp, vp, vp, vp, vp, vp, vp, i, f, i, i, i,
+                                        i, i, i, i, i, i, vp]
+        lib.fa_cache_append.restype = i
+        lib.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sp, i, i, i, i, i, i, i, i,
+                                      vp]
+        lib.fa_cache_read.restype = i
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i,
                                        vp]
         lib.fa_bwd_noalloc.restype = i
@@ -158,6 +175,41 @@ def fa_decode_paged(q, k_cache, v_cache, block_tables, seq_lens, o, lse, workspa
     return load_library().fa_decode_paged(q, k_cache, v_cache, block_tables, seq_lens, o, lse,
                                           workspace, workspace_bytes, B, H, D, num_pages,
                                           max_pages, scale, dtype, stream)
+
+
+def fa_rotary(q, k, q_out, k_out, strides, positions, position_stride, freqs, rotary_dim, mscale,
+              interleaved, inverse, B, Hq, Hk, L, D, dtype, stream) -> int:
+    """``strides``: four (batch, head, row) tuples for q, k, q_out, k_out."""
+    return load_library().fa_rotary(q, k, q_out, k_out, _strides_array(strides), positions,
+                                    position_stride, freqs, rotary_dim, mscale, int(interleaved),
+                                    int(inverse), B, Hq, Hk, L, D, dtype, stream)
+
+
+def fa_rotary_freqs(rotary_dim, base, scaling, factor, original_len):
+    """(status, list of rotary_dim/2 int64 frequencies, mscale)."""
+    out = (ctypes.c_int64 * max(1, int(rotary_dim) // 2))()
+    m = ctypes.c_float(0.0)
+    st = load_library().fa_rotary_freqs(int(rotary_dim), float(base), int(scaling), float(factor),
+                                        float(original_len), out, ctypes.byref(m))
+    return st, list(out), float(m.value)
+
+
+def fa_cache_append(k, v, strides, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens,
+                    new_lens, freqs, rotary_dim, mscale, interleaved, B, H, L, D, num_pages,
+                    max_pages, dtype, cache_dtype, stream) -> int:
+    """``strides``: two (batch, head, row) tuples for k, v."""
+    return load_library().fa_cache_append(k, v, _strides_array(strides), k_cache, v_cache, k_exp,
+                                          v_exp, block_tables, seq_lens, new_lens, freqs,
+                                          rotary_dim, mscale, int(interleaved), B, H, L, D,
+                                          num_pages, max_pages, dtype, cache_dtype, stream)
+
+
+def fa_cache_read(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, k, v, strides, B, H, L,
+                  D, num_pages, max_pages, dtype, cache_dtype, stream) -> int:
+    """``strides``: two (batch, head, row) tuples for k, v."""
+    return load_library().fa_cache_read(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, k,
+                                        v, _strides_array(strides), B, H, L, D, num_pages,
+                                        max_pages, dtype, cache_dtype, stream)
 
 
 def fa_bwd_workspace_bytes(B, H, L, D) -> int:
@@ -410,3 +462,274 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
     if status != FA_OK:
         raise FaError("fa_decode_paged", status)
     return o, l
+
+
+# ---------------------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------------------
+def _on_device(name, t, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _current(device):
+    """Context in which `device` is the current CUDA device (the library launches there)."""
+    import contextlib
+
+    import torch
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _kernel_view(t):
+    """`t` itself where the kernels can read its strides, else a contiguous copy (an expanded
+    gradient, for one, has strides of 0)."""
+    if t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
+            t.stride(i) % 8 == 0 and (t.stride(i) > 0 or (t.size(i) == 1 and i < 2))
+            for i in range(3)):
+        return t
+    return t.contiguous()
+
+
+def rotary_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_len: float = 0.0, device="cuda"):
+    """The frequency table of ``rotary`` and ``cache_append`` and the factor ``mscale``:
+    (int64 tensor [rotary_dim / 2] on ``device``, float).  ``scaling``: "none", "linear", "ntk" or
+    "yarn" (which needs ``original_len``), by ``factor``; see fa_rotary_freqs in fa.h.  Made once
+    and kept, like a weight."""
+    import torch
+    if scaling not in FA_ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(FA_ROTARY_SCALING)}, not {scaling!r}")
+    st, freqs, mscale = fa_rotary_freqs(rotary_dim, base, FA_ROTARY_SCALING[scaling], factor,
+                                        original_len)
+    if st != FA_OK:
+        raise FaError("fa_rotary_freqs", st)
+    return torch.tensor(freqs, dtype=torch.int64, device=device), mscale
+
+
+def _check_freqs(freqs, device):
+    import torch
+    if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise TypeError("freqs must be a contiguous one-dimensional int64 tensor (rotary_freqs)")
+    _on_device("freqs", freqs, device)
+    return 2 * freqs.numel()
+
+
+def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
+    """The library call for one or two [B, H, L, D] views; returns the outputs."""
+    import torch
+    x = xs[0]
+    device = x.device
+    dt = _dtype_code(x)
+    B, _, L, D = x.shape
+    xs = [t if outs is not None else _kernel_view(t) for t in xs]
+    st_in = [_view_strides(t, "x", (B, t.shape[1], L, D)) for t in xs]
+    for t in xs:
+        if t.dtype != x.dtype:
+            raise TypeError("the operands must share a dtype")
+        _on_device("x", t, device)
+    rotary_dim = _check_freqs(freqs, device)
+    pos_ptr, pos_stride = None, 0
+    if positions is not None:
+        if positions.dtype != torch.int32:
+            raise TypeError("positions must be int32")
+        _on_device("positions", positions, device)
+        if positions.dim() == 1:
+            positions = positions[None].expand(B, -1)
+        if tuple(positions.shape) != (B, L) or (L > 1 and positions.stride(1) != 1):
+            raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
+        pos_ptr = positions.data_ptr()
+        pos_stride = positions.stride(0) if B > 1 else 0
+    if outs is None:
+        outs = [torch.empty_like(t) for t in xs]
+    st_out = [_view_strides(o, "out", t.shape) for o, t in zip(outs, xs)]
+    for o in outs:
+        if o.dtype != x.dtype:
+            raise TypeError("out must have the dtype of x")
+        _on_device("out", o, device)
+    two = len(xs) == 2
+    with _current(device):
+        status = fa_rotary(xs[0].data_ptr(), xs[1].data_ptr() if two else None,
+                           outs[0].data_ptr(), outs[1].data_ptr() if two else None,
+                           [st_in[0], st_in[-1], st_out[0], st_out[-1]], pos_ptr, pos_stride,
+                           freqs.data_ptr(), rotary_dim, float(mscale), interleaved, inverse, B,
+                           xs[0].shape[1], xs[1].shape[1] if two else 0, L, D, dt,
+                           _stream_handle(device))
+    if status != FA_OK:
+        raise FaError("fa_rotary", status)
+    return outs
+
+
+def rotary_apply(x, positions, freqs, mscale: float = 1.0, interleaved: bool = False,
+                 inverse: bool = False, out=None):
+    """Rotary positions on one [B, H, L, D] view (bf16 or fp16, contiguous last dimension), outside
+    autograd.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale``
+    from ``rotary_freqs``.  ``out`` may be ``x`` (in place); ``inverse`` turns backwards.  The other
+    arguments as in fa_rotary (fa.h)."""
+    return _rotate([x], positions, freqs, mscale, interleaved, inverse,
+                   None if out is None else [out])[0]
+
+
+_rotary_function = None
+
+
+def _rotary_autograd():
+    global _rotary_function
+    if _rotary_function is None:
+        import torch
+
+        class _Rotary(torch.autograd.Function):
+            """Linear in its tensors, so the backward is the same function turned the other way
+            (and can itself be differentiated)."""
+
+            @staticmethod
+            def forward(ctx, positions, freqs, mscale, interleaved, inverse, *xs):
+                ctx.save_for_backward(positions, freqs)
+                ctx.args = (mscale, interleaved, inverse)
+                return tuple(_rotate(list(xs), positions, freqs, mscale, interleaved, inverse))
+
+            @staticmethod
+            def backward(ctx, *grads):
+                positions, freqs = ctx.saved_tensors
+                mscale, interleaved, inverse = ctx.args
+                out = [None] * len(grads)
+                want = [i for i, g in enumerate(grads)
+                        if g is not None and ctx.needs_input_grad[5 + i]]
+                if want:
+                    turned = _Rotary.apply(positions, freqs, mscale, interleaved, not inverse,
+                                           *[grads[i] for i in want])
+                    for i, g in zip(want, turned):
+                        out[i] = g
+                return (None,) * 5 + tuple(out)
+
+        _rotary_function = _Rotary
+    return _rotary_function
+
+
+def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = False):
+    """Rotary positions on queries [B, Hq, L, D] and keys [B, Hk, L, D] in one launch,
+    differentiable; returns the rotated (q, k).  Any strides with a contiguous last dimension:
+    [B, L, H, D] tensors transposed, or the parts of a packed [B, L, 3, H, D] tensor, are read in
+    place.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale`` from
+    ``rotary_freqs``.  The rotated tensors go to ``attention`` (or, one row per sequence, to
+    ``decode_paged``)."""
+    import torch
+    if k.shape[0] != q.shape[0] or tuple(k.shape[2:]) != tuple(q.shape[2:]):
+        raise ValueError("q and k must agree in B, L and D")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad):
+        return _rotary_autograd().apply(positions, freqs, mscale, interleaved, False, q, k)
+    return tuple(_rotate([q, k], positions, freqs, mscale, interleaved, False))
+
+
+# ---------------------------------------------------------------------------------------
+# The paged cache: writing rows and reading them back
+# ---------------------------------------------------------------------------------------
+def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, device):
+    """(cache_dtype, num_pages, H, D, k_exp pointer, v_exp pointer) of a checked pair of caches."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape[2] != FA_PAGE_TOKENS or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [num_pages, H, FA_PAGE_TOKENS, D]")
+    num_pages, H, _, D = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        _on_device(name, t, device)
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must share a dtype")
+    if k_exp is None and v_exp is None:
+        if k_cache.dtype != dtype:
+            raise TypeError(f"the cache holds {k_cache.dtype}, the call's tensors {dtype}; an "
+                            "e4m3 cache needs k_exp and v_exp")
+        return FA_CACHE_16BIT, num_pages, H, D, None, None
+    if k_cache.dtype != torch.float8_e4m3fn:
+        raise TypeError("a cache with exponents must be float8_e4m3fn")
+    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+        if t is None or t.dtype != torch.uint8 or tuple(t.shape) != (num_pages, H, FA_PAGE_TOKENS) \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 [num_pages, H, FA_PAGE_TOKENS] "
+                             "tensor")
+        _on_device(name, t, device)
+    return FA_CACHE_E4M3, num_pages, H, D, k_exp.data_ptr(), v_exp.data_ptr()
+
+
+def _tables(block_tables, seq_lens, B, device):
+    """max_pages of a checked block table and its lengths."""
+    import torch
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("block_tables must be [B, max_pages] and seq_lens [B]")
+    if not block_tables.is_contiguous() or not seq_lens.is_contiguous():
+        raise ValueError("block_tables and seq_lens must be contiguous")
+    _on_device("block_tables", block_tables, device)
+    _on_device("seq_lens", seq_lens, device)
+    return block_tables.shape[1]
+
+
+def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, k_exp=None,
+                 v_exp=None, freqs=None, mscale: float = 1.0, interleaved: bool = False):
+    """Writes rows of k, v [B, H, L, D] (views, bf16 or fp16) into a paged cache: the first
+    ``new_lens[b]`` (None: all L) rows of sequence b become its last tokens, ``seq_lens[b]`` being
+    its length with them.  The caches are [num_pages, H, FA_PAGE_TOKENS, D] of k's dtype, or
+    float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` (uint8 [num_pages, H, FA_PAGE_TOKENS]),
+    into which rows are quantised.  With ``freqs`` (``rotary_freqs``) each key is first rotated by
+    its token index.  See fa_cache_append in fa.h."""
+    import torch
+    device = k.device
+    dt = _dtype_code(k)
+    st = [_view_strides(k, "k"), _view_strides(v, "v", k.shape)]
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must share a dtype")
+    _on_device("v", v, device)
+    B, H, L, D = k.shape
+    kind, num_pages, Hc, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, k.dtype, device)
+    if Hc != H or Dc != D:
+        raise ValueError(f"the cache has {Hc} heads of {Dc}, k has {H} of {D}")
+    max_pages = _tables(block_tables, seq_lens, B, device)
+    if new_lens is not None:
+        if new_lens.dtype != torch.int32 or tuple(new_lens.shape) != (B,) or not new_lens.is_contiguous():
+            raise ValueError("new_lens must be a contiguous int32 [B] tensor")
+        _on_device("new_lens", new_lens, device)
+    rotary_dim = _check_freqs(freqs, device) if freqs is not None else 0
+    with _current(device):
+        status = fa_cache_append(k.data_ptr(), v.data_ptr(), st, k_cache.data_ptr(),
+                                 v_cache.data_ptr(), kep, vep, block_tables.data_ptr(),
+                                 seq_lens.data_ptr(),
+                                 None if new_lens is None else new_lens.data_ptr(),
+                                 None if freqs is None else freqs.data_ptr(), rotary_dim,
+                                 float(mscale), interleaved, B, H, L, D, num_pages, max_pages, dt,
+                                 kind, _stream_handle(device))
+    if status != FA_OK:
+        raise FaError("fa_cache_append", status)
+
+
+def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None, v_exp=None,
+               dtype=None, out=None):
+    """Tokens 0 .. length-1 of every sequence of a paged cache as dense (k, v), each
+    [B, H, length, D] of ``dtype`` (bf16 or fp16; the cache's own when it is 16-bit); rows past a
+    sequence's end are zeros.  ``out``: an optional pair of views to write.  See fa_cache_read."""
+    import torch
+    device = k_cache.device
+    if dtype is None:
+        dtype = out[0].dtype if out is not None else k_cache.dtype
+    kind, num_pages, H, D, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, device)
+    B = seq_lens.shape[0]
+    max_pages = _tables(block_tables, seq_lens, B, device)
+    if out is None:
+        out = tuple(torch.empty((B, H, length, D), device=device, dtype=dtype) for _ in range(2))
+    k, v = out
+    dt = _dtype_code(k)
+    if k.dtype != dtype or v.dtype != dtype:
+        raise TypeError("out must have the call's dtype")
+    st = [_view_strides(k, "out[0]", (B, H, length, D)), _view_strides(v, "out[1]", k.shape)]
+    _on_device("out[0]", k, device)
+    _on_device("out[1]", v, device)
+    with _current(device):
+        status = fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
+                               block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(),
+                               v.data_ptr(), st, B, H, length, D, num_pages, max_pages, dt, kind,
+                               _stream_handle(device))
+    if status != FA_OK:
+        raise FaError("fa_cache_read", status)
+    return k, v

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_sched.h"
@@ -40,6 +41,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return g_encode;
 }
 
+}  // namespace
+
 // Device address of the status word of the current device (looked up once per device).
 int* status_ptr() {
     int dev = 0;
@@ -62,6 +65,21 @@ bool bind_context() {
     int dev = 0;
     return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
+
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
+
+bool make_tiled_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank,
+                    const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                    CUtensorMapSwizzle swizzle) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint32_t elem[5] = {1, 1, 1, 1, 1};
+    return enc(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
 
 // [B, H, L, D] 16-bit tensor with element strides `st` (D contiguous) viewed as 4-D
 // {D, L, H, B}; box = 64 elements x 128 rows x 1 x 1, with the 128-byte swizzle the tcgen05
@@ -88,25 +106,6 @@ thread_local int t_trace_pairs = 0;
 thread_local cudaEvent_t t_trace_events[2 * kMaxTracePairs];
 std::atomic<uint64_t> g_launches{0};
 
-// Enqueues one kernel through `launch`, bracketed by the armed trace events (if any).
-template <typename F>
-cudaError_t traced_launch(int index, cudaStream_t s, F&& launch) {
-    const bool traced = index < t_trace_pairs;
-    if (traced && cudaEventRecord(t_trace_events[2 * index], s) != cudaSuccess)
-        return cudaErrorInvalidValue;
-    cudaError_t e = launch();
-    if (e != cudaSuccess) return e;
-    g_launches.fetch_add(1);
-    if (traced && cudaEventRecord(t_trace_events[2 * index + 1], s) != cudaSuccess)
-        return cudaErrorInvalidValue;
-    return cudaSuccess;
-}
-
-// Consumes the trace arming at the end of a public call, whatever its outcome.
-struct TraceDisarm {
-    ~TraceDisarm() { t_trace_pairs = 0; }
-};
-
 // Heads per schedule group: the streamed per-head operands (two [L, D] 16-bit tensors) of a
 // group should take at most kGroupBytes of L2, so that tiles of the same head that run at the
 // same time reuse them from L2 instead of HBM.
@@ -118,17 +117,6 @@ int schedule_group(int BH, int L, int D) {
     if (g > (size_t)BH) g = (size_t)BH;
     return (int)g;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void* p, size_t bytes) {
-    uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, a + bytes};
-}
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 struct Shape {
     int BH = 0, H = 0, Lq = 0, Lk = 0, D = 0, n_qtiles = 0, n_ktiles = 0, Lqpad = 0;
@@ -160,26 +148,6 @@ fa_status check_shape(int B, int H, int Lq, int Lk, int D, float scale, int caus
     sh->lse_bytes = (size_t)bh * (size_t)Lq * 4u;
     sh->empty = (bh == 0 || Lq == 0);  // no output row
     return FA_OK;
-}
-
-// A caller's strides, checked for the TMA rules (positive multiples of 8 elements = 16 bytes,
-// below 2^39 elements); a stride of 0 is accepted for a dimension of size 1 and replaced by 8.
-bool take_strides(const fa_strides& in, int B, int H, Strides* out) {
-    long long v[3] = {in.batch, in.head, in.row};
-    const int size[3] = {B, H, 2};  // the row dimension always counts
-    for (int i = 0; i < 3; ++i) {
-        if (v[i] == 0 && size[i] == 1) v[i] = 8;
-        if (v[i] <= 0 || (v[i] & 7) != 0 || v[i] >= (1LL << 39)) return false;
-    }
-    *out = {v[0], v[1], v[2]};
-    return true;
-}
-
-// Bytes from the first to one past the last element of a strided [B, H, L, D] 16-bit operand.
-Range extent(const void* p, const Strides& s, int B, int H, int L, int D) {
-    const long long last = (long long)(B - 1) * s.b + (long long)(H - 1) * s.h +
-                           (long long)(L - 1) * s.l + D;
-    return range(p, (size_t)last * 2u);
 }
 
 // Two outputs of the same shape and strides whose extents overlap are still disjoint element by
@@ -227,6 +195,38 @@ size_t bwd_workspace_need(const Shape& sh, int D, bool dq_reduce) {
 }
 
 }  // namespace
+
+cudaError_t trace_before(int index, cudaStream_t s) {
+    if (index < t_trace_pairs && cudaEventRecord(t_trace_events[2 * index], s) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+cudaError_t trace_after(int index, cudaStream_t s) {
+    g_launches.fetch_add(1);
+    if (index < t_trace_pairs && cudaEventRecord(t_trace_events[2 * index + 1], s) != cudaSuccess)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+// A caller's strides, checked for the TMA rules (positive multiples of 8 elements = 16 bytes,
+// below 2^39 elements); a stride of 0 is accepted for a dimension of size 1 and replaced by 8.
+bool take_strides(const fa_strides& in, int B, int H, Strides* out) {
+    long long v[3] = {in.batch, in.head, in.row};
+    const int size[3] = {B, H, 2};  // the row dimension always counts
+    for (int i = 0; i < 3; ++i) {
+        if (v[i] == 0 && size[i] == 1) v[i] = 8;
+        if (v[i] <= 0 || (v[i] & 7) != 0 || v[i] >= (1LL << 39)) return false;
+    }
+    *out = {v[0], v[1], v[2]};
+    return true;
+}
+
+// Bytes from the first to one past the last element of a strided [B, H, L, D] 16-bit operand.
+Range extent(const void* p, const Strides& s, int B, int H, int L, int D) {
+    const long long last = (long long)(B - 1) * s.b + (long long)(H - 1) * s.h +
+                           (long long)(L - 1) * s.l + D;
+    return range(p, (size_t)last * 2u);
+}
 
 void trace_disarm() { t_trace_pairs = 0; }
 

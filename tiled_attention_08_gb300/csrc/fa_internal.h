@@ -131,6 +131,57 @@ struct BwdParams {
     uint64_t timeout_ns;
 };
 
+// Rotary positions (fa_rotary): one operand of the launch, a [B, H, L, D] view.
+struct RotaryOperand {
+    const void* x;
+    void* y;  // may be x itself (same strides)
+    Strides sx, sy;
+    int H;
+};
+
+// The rotation shared by fa_rotary and fa_cache_append.
+struct RotaryParams {
+    const long long* freqs;  // [rotary_dim / 2] turns per position, fixed point (2^64 = one turn)
+    int rotary_dim;          // even; 0: no rotation
+    float mscale;            // factor on cos and sin
+    int interleaved;         // pairs (2i, 2i+1) instead of (i, i + rotary_dim/2)
+};
+
+struct RotaryLaunch {
+    RotaryOperand op[2];     // queries, keys (op[1].H = 0 when there is no second operand)
+    RotaryParams rot;
+    const int* positions;    // [B, L] with batch stride pos_stride, or null: the row index
+    long long pos_stride;
+    int B, L, D;
+    int inverse;             // rotate by the negative angle (the gradient)
+    int copy_rest;           // elements past rotary_dim are copied (some output is not in place)
+};
+
+// Writing rows into a paged cache (fa_cache_append) and reading them back (fa_cache_read).
+struct CacheAppendParams {
+    const void *k, *v;        // [B, H, L, D] 16-bit views
+    Strides sk, sv;
+    void *k_cache, *v_cache;  // [num_pages, H, 16, D] 16-bit, or e4m3 bytes
+    uint8_t *k_exp, *v_exp;   // [num_pages, H, 16] biased exponents (e4m3 caches), else null
+    const int* block_tables;  // [B, max_pages]
+    const int* seq_lens;      // [B] lengths with the new rows
+    const int* new_lens;      // [B] rows that each sequence adds, or null: L (0 when empty)
+    RotaryParams rot;         // applied to the keys
+    int B, H, L, D, num_pages, max_pages;
+    int* status;
+};
+
+struct CacheReadParams {
+    const void *k_cache, *v_cache;
+    const uint8_t *k_exp, *v_exp;
+    const int* block_tables;
+    const int* seq_lens;
+    void *k, *v;  // [B, H, L, D] 16-bit views
+    Strides sk, sv;
+    int B, H, L, D, num_pages, max_pages;
+    int* status;
+};
+
 // Host-side helpers of the C-ABI layer shared with the other entry-point units.
 // Consumes the fa_trace_next_call arming of the calling thread (every public call ends so).
 void trace_disarm();
@@ -173,6 +224,9 @@ cudaError_t launch_bwd_dq(const BwdParams& p, int D, bool bf16, bool causal, boo
                           cudaStream_t s);
 cudaError_t launch_wait_selftest(int* status, uint64_t timeout_ns, cudaStream_t s);
 cudaError_t launch_decode(const DecodeParams& p, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_rotary(const RotaryLaunch& p, bool bf16, cudaStream_t s);
+cudaError_t launch_cache_append(const CacheAppendParams& p, bool bf16, bool q8, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheReadParams& p, bool bf16, bool q8, cudaStream_t s);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);
 

@@ -1,0 +1,291 @@
+// fa_serve.cu -- C entry points of the operators around attention: rotary positions and the paged
+// cache's writing and reading.  Argument checks and launches; the kernels are in fa_rotary.cu and
+// fa_cache.cu.
+#include <cmath>
+#include <cstring>
+
+#include "fa_host.h"
+
+using namespace fa;
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Rows of two operands with the same strides whose extents overlap but whose elements do not:
+// parts of one packed tensor (a row's heads lie together, one part's before the other's).
+bool packed_parts(const void* a, int Ha, const void* b, int Hb, const Strides& s, int L, int D) {
+    const intptr_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
+    const long long delta = (pa < pb ? pb - pa : pa - pb) / 2;
+    const long long first = (long long)(pa < pb ? Ha : Hb) * D;
+    const long long second = (long long)(pa < pb ? Hb : Ha) * D;
+    return s.h == D && delta >= first && delta + second <= s.l && s.b >= (long long)L * s.l;
+}
+bool same(const Strides& a, const Strides& b) { return a.b == b.b && a.h == b.h && a.l == b.l; }
+
+// The rotation of fa_rotary and fa_cache_append; freqs may be null only with rotary_dim = 0.
+fa_status check_rotation(const int64_t* freqs, int rotary_dim, float mscale, int interleaved, int D,
+                         RotaryParams* out) {
+    if (rotary_dim < 0 || rotary_dim > D || (rotary_dim & 1)) return FA_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || !std::isfinite(mscale)) return FA_ERR_INVALID_ARG;
+    if (rotary_dim > 0 && (!freqs || !aligned8(freqs))) return FA_ERR_INVALID_ARG;
+    out->freqs = reinterpret_cast<const long long*>(freqs);
+    out->rotary_dim = rotary_dim;
+    out->mscale = mscale;
+    out->interleaved = interleaved;
+    return FA_OK;
+}
+
+// Bytes of a paged cache's values and, for e4m3, of its exponents.
+size_t cache_bytes(int num_pages, int H, int D, int cache_dtype) {
+    return (size_t)num_pages * H * kPageTokens * D * (cache_dtype == FA_CACHE_E4M3 ? 1u : 2u);
+}
+size_t exp_bytes(int num_pages, int H) { return (size_t)num_pages * H * kPageTokens; }
+
+// Sizes and flags shared by the calls on a paged cache.
+fa_status check_cache(int B, int H, int L, int D, int num_pages, int max_pages, int dtype,
+                      int cache_dtype) {
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    if (cache_dtype != FA_CACHE_16BIT && cache_dtype != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+    if (B < 0 || H < 0 || L < 0 || D <= 0 || num_pages < 0 || max_pages < 0)
+        return FA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    if (B > 65535 || H > 65535 || max_pages > 0x7fffffff / kPageTokens) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// Pointers of a paged cache.
+bool cache_pointers_ok(const void* kc, const void* vc, const void* ke, const void* ve,
+                       const void* tables, const void* lens, int num_pages, int max_pages,
+                       int cache_dtype) {
+    if (num_pages > 0 && (!kc || !vc)) return false;
+    if (num_pages > 0 && cache_dtype == FA_CACHE_E4M3 && (!ke || !ve)) return false;
+    if (!lens || (max_pages > 0 && !tables)) return false;
+    return aligned16(kc) && aligned16(vc) && aligned16(ke) && aligned16(ve) && aligned4(tables) &&
+           aligned4(lens);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status fa_rotary_freqs(int rotary_dim, double base, int scaling, double factor,
+                          double original_len, int64_t* freqs, float* mscale) {
+    if (rotary_dim < 2 || (rotary_dim & 1) || !freqs || !mscale) return FA_ERR_INVALID_ARG;
+    if (!(base >= 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor))
+        return FA_ERR_INVALID_ARG;
+    if (scaling < FA_ROTARY_PLAIN || scaling > FA_ROTARY_YARN) return FA_ERR_INVALID_ARG;
+    if (scaling == FA_ROTARY_YARN && (!(original_len > 0.0) || !std::isfinite(original_len)))
+        return FA_ERR_INVALID_ARG;
+    if (scaling == FA_ROTARY_NTK) {
+        if (rotary_dim == 2) return FA_ERR_INVALID_ARG;
+        base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+        if (!std::isfinite(base)) return FA_ERR_INVALID_ARG;
+    }
+    const double two_pi = 6.283185307179586476925286766559;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double theta = std::pow(base, -2.0 * i / rotary_dim);
+        if (scaling == FA_ROTARY_LINEAR) theta /= factor;
+        if (scaling == FA_ROTARY_YARN) {
+            const double turns = original_len * theta / two_pi;  // within the trained length
+            double keep = (turns - 1.0) / 31.0;
+            keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+            theta = theta * keep + theta / factor * (1.0 - keep);
+        }
+        freqs[i] = (int64_t)std::llrint(std::ldexp(theta / two_pi, 64));  // theta <= 1
+    }
+    *mscale = scaling == FA_ROTARY_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return FA_OK;
+}
+
+fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out,
+                    const fa_strides* strides, const int32_t* positions, int64_t position_stride,
+                    const int64_t* freqs, int rotary_dim, float mscale, int interleaved,
+                    int inverse, int B, int Hq, int Hk, int L, int D, int dtype, void* stream) {
+    TraceDisarm disarm;
+    if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_INVALID_ARG;
+    if (B < 0 || Hq < 0 || Hk < 0 || L < 0 || D <= 0) return FA_ERR_INVALID_ARG;
+    if (inverse != 0 && inverse != 1) return FA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    RotaryLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    const bool empty = B == 0 || L == 0 || (Hq == 0 && Hk == 0);
+    if (rotary_dim == 0) return FA_ERR_INVALID_ARG;
+    if (!empty && !freqs) return FA_ERR_INVALID_ARG;
+    static const int64_t kNone[1] = {0};
+    fa_status st = check_rotation(empty ? kNone : freqs, rotary_dim, mscale, interleaved, D, &p.rot);
+    if (st != FA_OK) return st;
+    if (empty) return FA_OK;
+    if ((long long)Hq + Hk > 65535) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * L > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    if (!strides || position_stride < 0 || !aligned4(positions)) return FA_ERR_INVALID_ARG;
+    const void* in[2] = {q, k};
+    void* out[2] = {q_out, k_out};
+    const int H[2] = {Hq, Hk};
+    Range rin[2] = {{0, 0}, {0, 0}}, rout[2] = {{0, 0}, {0, 0}};
+    for (int i = 0; i < 2; ++i) {
+        RotaryOperand& o = p.op[i];
+        o.H = H[i];
+        if (H[i] == 0) continue;
+        if (!in[i] || !out[i] || !aligned16(in[i]) || !aligned16(out[i])) return FA_ERR_INVALID_ARG;
+        if (!take_strides(strides[i], B, H[i], &o.sx) ||
+            !take_strides(strides[2 + i], B, H[i], &o.sy))
+            return FA_ERR_INVALID_ARG;
+        o.x = in[i];
+        o.y = out[i];
+        rin[i] = extent(in[i], o.sx, B, H[i], L, D);
+        rout[i] = extent(out[i], o.sy, B, H[i], L, D);
+        if (o.x != o.y) p.copy_rest = 1;
+    }
+    const Range rpos = positions
+                           ? range(positions, ((size_t)(B - 1) * position_stride + L) * 4u)
+                           : Range{0, 0};
+    const Range rfreq = range(freqs, (size_t)rotary_dim / 2 * 8u);
+    for (int i = 0; i < 2; ++i) {
+        if (H[i] == 0) continue;
+        if (overlap(rout[i], rpos) || overlap(rout[i], rfreq)) return FA_ERR_INVALID_ARG;
+        for (int j = 0; j < 2; ++j) {
+            if (H[j] == 0) continue;
+            const RotaryOperand &a = p.op[i], &b = p.op[j];
+            // An output may be its own input (in place); parts of one packed tensor may interleave.
+            if (overlap(rout[i], rin[j]) && !(i == j && a.y == b.x && same(a.sy, b.sx)) &&
+                !(same(a.sy, b.sx) && packed_parts(a.y, a.H, b.x, b.H, a.sy, L, D)))
+                return FA_ERR_INVALID_ARG;
+            if (i < j && overlap(rout[i], rout[j]) &&
+                !(same(a.sy, b.sy) && packed_parts(a.y, a.H, b.y, b.H, a.sy, L, D)))
+                return FA_ERR_INVALID_ARG;
+        }
+    }
+    if (Hq == 0) {  // the kernel's first operand is never empty
+        p.op[0] = p.op[1];
+        p.op[1].H = 0;
+    }
+    p.positions = positions;
+    p.pos_stride = position_stride;
+    p.B = B;
+    p.L = L;
+    p.D = D;
+    p.inverse = inverse;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!bind_context()) return FA_ERR_CUDA;
+    return traced_launch(0, s, [&] { return launch_rotary(p, dtype == FA_BF16, s); }) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_append(const void* k, const void* v, const fa_strides* strides, void* k_cache,
+                          void* v_cache, void* k_exp, void* v_exp, const int32_t* block_tables,
+                          const int32_t* seq_lens, const int32_t* new_lens, const int64_t* freqs,
+                          int rotary_dim, float mscale, int interleaved, int B, int H, int L, int D,
+                          int num_pages, int max_pages, int dtype, int cache_dtype, void* stream) {
+    TraceDisarm disarm;
+    fa_status st = check_cache(B, H, L, D, num_pages, max_pages, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    const bool empty = B == 0 || H == 0 || L == 0;
+    CacheAppendParams p;
+    std::memset(&p, 0, sizeof(p));
+    static const int64_t kNone[1] = {0};
+    st = check_rotation(empty ? kNone : freqs, rotary_dim, mscale, interleaved, D, &p.rot);
+    if (st != FA_OK) return st;
+    if (empty) return FA_OK;
+    if (!k || !v || !strides || !aligned16(k) || !aligned16(v) || !aligned4(new_lens))
+        return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages,
+                           max_pages, cache_dtype))
+        return FA_ERR_INVALID_ARG;
+    if (!take_strides(strides[0], B, H, &p.sk) || !take_strides(strides[1], B, H, &p.sv))
+        return FA_ERR_INVALID_ARG;
+    const bool q8 = cache_dtype == FA_CACHE_E4M3;
+    const size_t cb = cache_bytes(num_pages, H, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, H) : 0;
+    const Range outs[] = {range(k_cache, cb), range(v_cache, cb), range(k_exp, eb), range(v_exp, eb)};
+    const Range ins[] = {extent(k, p.sk, B, H, L, D),
+                         extent(v, p.sv, B, H, L, D),
+                         range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u),
+                         range(new_lens, new_lens ? (size_t)B * 4u : 0),
+                         range(freqs, (size_t)rotary_dim / 2 * 8u)};
+    for (int a = 0; a < 4; ++a) {
+        for (const Range& b : ins)
+            if (overlap(outs[a], b)) return FA_ERR_INVALID_ARG;
+        for (int b = a + 1; b < 4; ++b)
+            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
+    }
+    p.k = k;
+    p.v = v;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_exp = q8 ? static_cast<uint8_t*>(k_exp) : nullptr;
+    p.v_exp = q8 ? static_cast<uint8_t*>(v_exp) : nullptr;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.B = B;
+    p.H = H;
+    p.L = L;
+    p.D = D;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    if (!bind_context()) return FA_ERR_CUDA;
+    p.status = status_ptr();
+    if (!p.status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return traced_launch(0, s, [&] { return launch_cache_append(p, dtype == FA_BF16, q8, s); }) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_exp,
+                        const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,
+                        void* k, void* v, const fa_strides* strides, int B, int H, int L, int D,
+                        int num_pages, int max_pages, int dtype, int cache_dtype, void* stream) {
+    TraceDisarm disarm;
+    fa_status st = check_cache(B, H, L, D, num_pages, max_pages, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || H == 0 || L == 0) return FA_OK;
+    if (!k || !v || !strides || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages,
+                           max_pages, cache_dtype))
+        return FA_ERR_INVALID_ARG;
+    CacheReadParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!take_strides(strides[0], B, H, &p.sk) || !take_strides(strides[1], B, H, &p.sv))
+        return FA_ERR_INVALID_ARG;
+    const bool q8 = cache_dtype == FA_CACHE_E4M3;
+    const size_t cb = cache_bytes(num_pages, H, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, H) : 0;
+    const Range outs[] = {extent(k, p.sk, B, H, L, D), extent(v, p.sv, B, H, L, D)};
+    const Range ins[] = {range(k_cache, cb), range(v_cache, cb), range(k_exp, eb), range(v_exp, eb),
+                         range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u)};
+    for (const Range& o : outs)
+        for (const Range& i : ins)
+            if (overlap(o, i)) return FA_ERR_INVALID_ARG;
+    if (overlap(outs[0], outs[1]) &&
+        !(same(p.sk, p.sv) && packed_parts(k, H, v, H, p.sk, L, D)))
+        return FA_ERR_INVALID_ARG;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_exp = q8 ? static_cast<const uint8_t*>(k_exp) : nullptr;
+    p.v_exp = q8 ? static_cast<const uint8_t*>(v_exp) : nullptr;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.k = k;
+    p.v = v;
+    p.B = B;
+    p.H = H;
+    p.L = L;
+    p.D = D;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    if (!bind_context()) return FA_ERR_CUDA;
+    p.status = status_ptr();
+    if (!p.status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return traced_launch(0, s, [&] { return launch_cache_read(p, dtype == FA_BF16, q8, s); }) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+}  // extern "C"
