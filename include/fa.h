@@ -323,6 +323,25 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
                         void* k, void* v, const fa_strides* strides, int B, int H, int L, int D,
                         int num_pages, int max_pages, int dtype, int cache_dtype, void* stream);
 
+/* Bytes of device workspace fa_decode_paged_ex needs: the partial results of the splits of the page
+ * range (fp32), 0 when there is one split.  0 for invalid sizes. */
+size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages);
+
+/*
+ * fa_decode_paged with grouped heads and either kind of cache: q, o [B, Hq, D] and lse [B, Hq],
+ * caches [num_pages, Hk, FA_PAGE_TOKENS, D] of dtype (FA_CACHE_16BIT) or e4m3 bytes with k_exp, v_exp
+ * [num_pages, Hk, FA_PAGE_TOKENS] (FA_CACHE_E4M3; ignored otherwise).  Hq is a multiple of Hk and
+ * query head h reads cache head h / (Hq / Hk).  Everything else is as for fa_decode_paged: empty
+ * sequences get O = 0, LSE = -inf, slots past a sequence's end may hold anything, a bad length or
+ * page index is reported by fa_get_device_status().  Two kernels when the page range is split, else
+ * one.
+ */
+fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_cache,
+                             const void* k_exp, const void* v_exp, const int32_t* block_tables,
+                             const int32_t* seq_lens, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
+                             int max_pages, float scale, int dtype, int cache_dtype, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's status word.  Returns
  * FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call,

@@ -180,3 +180,53 @@ def test_append_argument_checks(kw, status):
 ], ids=lambda x: str(x)[:48])
 def test_read_argument_checks(kw, status):
     assert _read(**kw) == status
+
+
+def _decode(B=2, Hq=4, Hk=2, D=64, pages=8, maxp=4, scale=0.125, dtype=0, cdtype=1, ws_bytes=1 << 20, **ptrs):
+    p = dict(q=A, kc=A + MB, vc=A + 2 * MB, ke=A + 3 * MB, ve=A + 4 * MB, bt=A + 5 * MB, sl=A + 6 * MB,
+             o=A + 7 * MB, lse=A + 8 * MB, ws=A + 9 * MB)
+    p.update(ptrs)
+    return fa.fa_decode_paged_ex(p["q"], p["kc"], p["vc"], p["ke"], p["ve"], p["bt"], p["sl"], p["o"],
+                                 p["lse"], p["ws"], ws_bytes, B, Hq, Hk, D, pages, maxp, scale, dtype,
+                                 cdtype, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=9), BAD),
+    (dict(cdtype=-1), BAD),
+    (dict(D=96), UNS),
+    (dict(D=-64), BAD),
+    (dict(Hq=-1), BAD),
+    (dict(Hq=5), BAD),                           # not a multiple of Hk
+    (dict(Hk=0), BAD),
+    (dict(scale=math.nan), BAD),
+    (dict(B=65536), UNS),
+    (dict(Hq=65536 * 20, Hk=65536), UNS),
+    (dict(Hq=1 << 20, Hk=4, B=1 << 12), UNS),
+    (dict(q=0), BAD),
+    (dict(lse=0), BAD),
+    (dict(ve=0), BAD),
+    (dict(kc=A + MB + 8), BAD),
+    (dict(ke=A + 3 * MB + 8), BAD),
+    (dict(bt=0), BAD),
+    (dict(o=A + MB), BAD),                       # o inside the key cache
+    (dict(lse=A + 7 * MB + 64), BAD),            # lse overlaps o
+    (dict(o=A + 3 * MB), BAD),                   # o on the exponents
+    (dict(B=1, Hq=1, Hk=1, maxp=64, ws_bytes=16), BAD),
+    (dict(B=1, Hq=1, Hk=1, maxp=64, ws=0), BAD),
+    (dict(B=1, Hq=1, Hk=1, maxp=64, ws=A + 7 * MB), BAD),
+    (dict(B=0), OK),
+    (dict(Hq=0), OK),
+], ids=lambda x: str(x)[:48])
+def test_grouped_decode_argument_checks(kw, status):
+    assert _decode(**kw) == status
+
+
+def test_grouped_decode_workspace():
+    assert fa.fa_decode_workspace_bytes_ex(256, 32, 8, 128, 256) == 0   # enough CTAs without splits
+    assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 128, 16) == 0       # one split of 16 pages
+    need = fa.fa_decode_workspace_bytes_ex(1, 8, 1, 128, 1024)
+    assert need > 0 and need % (8 * (128 + 1) * 4) == 0
+    assert fa.fa_decode_workspace_bytes_ex(1, 8, 3, 128, 1024) == 0     # invalid
+    assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 96, 1024) == 0
+    assert fa.fa_decode_workspace_bytes_ex(-1, 8, 1, 64, 1024) == 0

@@ -31,7 +31,7 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "attention_qkvpacked", "FaStrides", "fa_decode_paged", "fa_decode_workspace_bytes",
            "decode_paged", "FA_PAGE_TOKENS", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
            "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
-           "FA_CACHE_16BIT", "FA_CACHE_E4M3",
+           "FA_CACHE_16BIT", "FA_CACHE_E4M3", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_BF16", "FA_FP16"]
 
@@ -51,7 +51,7 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_set_wait_timeout_ns", "fa_selftest_wait_timeout", "fa_trace_next_call",
             "fa_launch_count", "fa_status_string", "fa_bwd_noalloc", "fa_decode_paged",
             "fa_decode_workspace_bytes", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
-            "fa_cache_read")
+            "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex")
 
 
 class FaStrides(ctypes.Structure):
@@ -111,6 +111,11 @@ def load_library():
         lib.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sp, i, i, i, i, i, i, i, i,
                                       vp]
         lib.fa_cache_read.restype = i
+        lib.fa_decode_workspace_bytes_ex.argtypes = [i, i, i, i, i]
+        lib.fa_decode_workspace_bytes_ex.restype = sz
+        lib.fa_decode_paged_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i,
+                                           i, i, f, i, i, vp]
+        lib.fa_decode_paged_ex.restype = i
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i,
                                        vp]
         lib.fa_bwd_noalloc.restype = i
@@ -210,6 +215,19 @@ def fa_cache_read(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, k, v, 
     return load_library().fa_cache_read(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, k,
                                         v, _strides_array(strides), B, H, L, D, num_pages,
                                         max_pages, dtype, cache_dtype, stream)
+
+
+def fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages) -> int:
+    return int(load_library().fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages))
+
+
+def fa_decode_paged_ex(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o, lse, workspace,
+                       workspace_bytes, B, Hq, Hk, D, num_pages, max_pages, scale, dtype,
+                       cache_dtype, stream) -> int:
+    return load_library().fa_decode_paged_ex(q, k_cache, v_cache, k_exp, v_exp, block_tables,
+                                             seq_lens, o, lse, workspace, workspace_bytes, B, Hq,
+                                             Hk, D, num_pages, max_pages, scale, dtype, cache_dtype,
+                                             stream)
 
 
 def fa_bwd_workspace_bytes(B, H, L, D) -> int:
@@ -430,11 +448,18 @@ def attention_qkvpacked(qkv, causal: bool = False, scale: float | None = None):
 
 
 def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | None = None,
-                 out=None, lse=None, workspace=None):
+                 out=None, lse=None, workspace=None, k_exp=None, v_exp=None):
     """One decode step over a paged cache: q [B, H, D]; k_cache, v_cache
     [num_pages, H, FA_PAGE_TOKENS, D] (bf16 or fp16, contiguous); block_tables [B, max_pages] and
-    seq_lens [B] int32 CUDA tensors.  Returns O [B, H, D] and LSE [B, H] (fp32)."""
+    seq_lens [B] int32 CUDA tensors.  Returns O [B, H, D] and LSE [B, H] (fp32).
+
+    The caches may have fewer heads than q (a divisor: each is shared by a group of query heads),
+    and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote."""
     import torch
+    if k_exp is not None or v_exp is not None or (k_cache.dim() == 4 and q.dim() == 3 and
+                                                  k_cache.shape[1] != q.shape[1]):
+        return _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse,
+                                workspace, k_exp, v_exp)
     for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
                     ("block_tables", block_tables), ("seq_lens", seq_lens)):
         if not t.is_cuda or not t.is_contiguous():
@@ -733,3 +758,57 @@ def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None
     if status != FA_OK:
         raise FaError("fa_cache_read", status)
     return k, v
+
+
+def _decode_outputs(q, out, lse):
+    """Checked (B, Hq, D, dtype code, o, lse) of a decode step."""
+    import torch
+    if not q.is_cuda or q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B, H, D] CUDA tensor")
+    B, Hq, D = q.shape
+    dt = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    if lse is None:
+        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [B, H] tensor")
+    _on_device("out", out, q.device)
+    _on_device("lse", lse, q.device)
+    return B, Hq, D, dt, out, lse
+
+
+def _workspace(workspace, need, device):
+    """(pointer, bytes) of the caller's workspace, or of a new one where any is needed; the tensor
+    itself keeps it alive until the call has been enqueued."""
+    import torch
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, device=device, dtype=torch.uint8)
+    _on_device("workspace", workspace, device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace, k_exp,
+                     v_exp):
+    B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
+    device = q.device
+    kind, num_pages, Hk, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, q.dtype, device)
+    if Dc != D:
+        raise ValueError(f"the cache has heads of {Dc}, q of {D}")
+    max_pages = _tables(block_tables, seq_lens, B, device)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _current(device):
+        need = fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages)
+        wp, wb, keep = _workspace(workspace, need, device)
+        status = fa_decode_paged_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
+                                    block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                                    l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
+                                    float(scale), dt, kind, _stream_handle(device))
+    if status != FA_OK:
+        raise FaError("fa_decode_paged_ex", status)
+    return o, l

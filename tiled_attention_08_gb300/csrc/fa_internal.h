@@ -182,6 +182,39 @@ struct CacheReadParams {
     int* status;
 };
 
+// Partial results of attention over parts of the keys, merged by fa_merge_parts_kernel: part i of
+// query row r is o[(r * parts + i) * D ..] (normalised, fp32) and lse2[r * parts + i] (log2
+// domain; -inf: the part holds no key and its o is not written).
+struct PartsRef {
+    const float* o;
+    const float* lse2;
+    int parts;
+};
+
+// One decode step with grouped heads over a paged cache (fa_decode_paged_ex).
+struct GqaParams {
+    CUtensorMap tm_k, tm_v;    // {D, 16, num_pages * Hk}: one box is a page's rows of one head
+    const void* q;             // [B, Hq, D] 16-bit
+    const uint8_t *k_exp, *v_exp;  // [num_pages, Hk, 16] (e4m3 caches)
+    const int* block_tables;   // [B, max_pages]
+    const int* seq_lens;       // [B]
+    void* o;                   // [B, Hq, D] 16-bit  (splits == 1 and no other parts)
+    float* lse;                // [B, Hq] natural log
+    float* part_o;             // [B*Hq, splits, D] fp32, or null: o and lse are written
+    float* part_lse;           // [B*Hq, splits] log2 domain
+    int B, Hq, Hk, group, q_blocks, num_pages, max_pages, splits, pages_per_split, stages;
+    float scale_log2;
+    int* status;
+    uint64_t timeout_ns;
+};
+
+struct MergeParams {
+    PartsRef parts;
+    void* o;     // [rows, D] 16-bit
+    float* lse;  // [rows] natural log
+    int rows;
+};
+
 // Host-side helpers of the C-ABI layer shared with the other entry-point units.
 // Consumes the fa_trace_next_call arming of the calling thread (every public call ends so).
 void trace_disarm();
@@ -207,6 +240,24 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// The same, allowed to start before the previous kernel of the stream has finished: `kern` calls
+// griddepcontrol.wait before it touches anything that kernel writes.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t s, Args&&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 // Launchers (one per kernel unit).  Return the launch error, if any.
 cudaError_t launch_fwd(const FwdParams& p, int D, bool bf16, bool causal, bool drop,
                        cudaStream_t s);
@@ -227,6 +278,12 @@ cudaError_t launch_decode(const DecodeParams& p, int D, bool bf16, cudaStream_t 
 cudaError_t launch_rotary(const RotaryLaunch& p, bool bf16, cudaStream_t s);
 cudaError_t launch_cache_append(const CacheAppendParams& p, bool bf16, bool q8, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheReadParams& p, bool bf16, bool q8, cudaStream_t s);
+// q8: an e4m3 cache; else one of q's type (bf16 or fp16).
+cudaError_t launch_decode_gqa(const GqaParams& p, int D, bool bf16, bool q8, cudaStream_t s);
+cudaError_t launch_merge_parts(const MergeParams& p, int D, bool bf16, cudaStream_t s);
+// Query blocks of 8 or 16 rows per cache head, and the splits of the page range.
+int gqa_q_blocks(int group);
+int gqa_splits(int B, int Hk, int group, int max_pages);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);
 

@@ -1,6 +1,6 @@
-// fa_serve.cu -- C entry points of the operators around attention: rotary positions and the paged
-// cache's writing and reading.  Argument checks and launches; the kernels are in fa_rotary.cu and
-// fa_cache.cu.
+// fa_serve.cu -- C entry points of the operators around attention: rotary positions, the paged
+// cache's writing and reading, and the decode step with grouped heads.  Argument checks and
+// launches; the kernels are in fa_rotary.cu, fa_cache.cu and fa_decode_gqa.cu.
 #include <cmath>
 #include <cstring>
 
@@ -65,6 +65,38 @@ bool cache_pointers_ok(const void* kc, const void* vc, const void* ke, const voi
     return aligned16(kc) && aligned16(vc) && aligned16(ke) && aligned16(ve) && aligned4(tables) &&
            aligned4(lens);
 }
+
+// Tensor map of a paged cache: one box is the 16 rows of a page's head (128 bytes of each at most).
+bool make_cache_map(CUtensorMap* m, const void* cache, int num_pages, int H, int D, int dtype,
+                    bool q8) {
+    const cuuint64_t row = (cuuint64_t)D * (q8 ? 1 : 2);
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)kPageTokens, (cuuint64_t)num_pages * H};
+    const cuuint64_t strides[2] = {row, row * kPageTokens};
+    const cuuint32_t inner = row < 128 ? 64 : 128;  // bytes
+    const cuuint32_t box[3] = {q8 ? inner : inner / 2, (cuuint32_t)kPageTokens, 1};
+    return make_tiled_map(m,
+                          q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                             : (dtype == FA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16),
+                          cache, 3, dims, strides, box,
+                          inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Sizes of a decode step with grouped heads.
+fa_status check_decode(int B, int Hq, int Hk, int D, int num_pages, int max_pages, float scale,
+                       int dtype, int cache_dtype) {
+    if (Hq < 0 || Hk < 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(B, Hk, 0, D, num_pages, max_pages, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0) return FA_OK;
+    if (Hk == 0 || Hq % Hk != 0) return FA_ERR_INVALID_ARG;
+    if ((long long)Hk * gqa_q_blocks(Hq / Hk) > 65535 || (long long)B * Hq > 0x7fffffffLL ||
+        (long long)num_pages * Hk > 0x7fffffffLL)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+size_t parts_bytes(size_t rows, int parts, int D) { return rows * parts * (size_t)(D + 1) * 4u; }
 
 }  // namespace
 
@@ -284,6 +316,84 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return traced_launch(0, s, [&] { return launch_cache_read(p, dtype == FA_BF16, q8, s); }) ==
                    cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages) {
+    if (B <= 0 || Hq <= 0 ||
+        check_decode(B, Hq, Hk, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK)
+        return 0;
+    const int splits = gqa_splits(B, Hk, Hq / Hk, max_pages);
+    return splits > 1 ? parts_bytes((size_t)B * Hq, splits, D) : 0;
+}
+
+fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_cache,
+                             const void* k_exp, const void* v_exp, const int32_t* block_tables,
+                             const int32_t* seq_lens, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
+                             int max_pages, float scale, int dtype, int cache_dtype, void* stream) {
+    TraceDisarm disarm;
+    fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0) return FA_OK;
+    const bool q8 = cache_dtype == FA_CACHE_E4M3;
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse))
+        return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages,
+                           max_pages, cache_dtype))
+        return FA_ERR_INVALID_ARG;
+    GqaParams p;
+    std::memset(&p, 0, sizeof(p));
+    const size_t rows = (size_t)B * Hq;
+    p.splits = gqa_splits(B, Hk, Hq / Hk, max_pages);
+    const size_t ws_need = p.splits > 1 ? parts_bytes(rows, p.splits, D) : 0;
+    if (ws_need > 0 && (!workspace || workspace_bytes < ws_need || !aligned16(workspace)))
+        return FA_ERR_INVALID_ARG;
+    const size_t cb = cache_bytes(num_pages, Hk, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, Hk) : 0;
+    const Range ins[] = {range(q, rows * D * 2u), range(k_cache, cb), range(v_cache, cb),
+                         range(k_exp, eb), range(v_exp, eb),
+                         range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u)};
+    const Range outs[] = {range(o, rows * D * 2u), range(lse, rows * 4u), range(workspace, ws_need)};
+    for (int a = 0; a < 3; ++a) {
+        for (const Range& in : ins)
+            if (overlap(outs[a], in)) return FA_ERR_INVALID_ARG;
+        for (int b = a + 1; b < 3; ++b)
+            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
+    }
+    if (!bind_context()) return FA_ERR_CUDA;
+    if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, q8) ||
+                          !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, q8)))
+        return FA_ERR_CUDA;
+    p.q = q;
+    p.k_exp = static_cast<const uint8_t*>(k_exp);
+    p.v_exp = static_cast<const uint8_t*>(v_exp);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.part_o = ws_need ? static_cast<float*>(workspace) : nullptr;
+    p.part_lse = ws_need ? static_cast<float*>(workspace) + rows * p.splits * D : nullptr;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.group = Hq / Hk;
+    p.q_blocks = gqa_q_blocks(p.group);
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.pages_per_split = max_pages > 0 ? (max_pages + p.splits - 1) / p.splits : 1;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = status_ptr();
+    p.timeout_ns = wait_timeout_ns();
+    if (!p.status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == FA_BF16;
+    if (traced_launch(0, s, [&] { return launch_decode_gqa(p, D, bf16, q8, s); }) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (p.splits == 1) return FA_OK;
+    const MergeParams mp = {{p.part_o, p.part_lse, p.splits}, o, lse, (int)rows};
+    return traced_launch(1, s, [&] { return launch_merge_parts(mp, D, bf16, s); }) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
