@@ -342,6 +342,33 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
                              size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
                              int max_pages, float scale, int dtype, int cache_dtype, void* stream);
 
+/* Bytes of device workspace fa_decode_shared_prefix needs (fp32 parts of every query row).  0 for
+ * invalid sizes, and when there is neither a prefix nor a page. */
+size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
+                                        int max_pages);
+
+/*
+ * One decode step of a batch whose sequences all begin with the same prefix_len tokens (a system
+ * prompt, a document), which lie once in the cache: token t of the prefix in page
+ * prefix_table[t / 16] at slot t % 16, and sequence b's own seq_lens[b] tokens behind it in the pages
+ * of block_tables[b], from that table's first slot on (a prefix that ends inside a page leaves the
+ * rest of that page unused).  O[b,h] and LSE[b,h] are those of fa_decode_paged_ex over the prefix's
+ * tokens followed by the sequence's own.  The prefix is read once per cache head for all B * Hq / Hk
+ * query rows of it (tensor-core kernel), the own tokens as by fa_decode_paged_ex, and a third
+ * kernel joins the parts.
+ *   caches of dtype (16-bit), Hq a multiple of Hk with Hq / Hk <= 128; prefix_len >= 0 (a host
+ *   integer; 0: no prefix), prefix_table int32, device, ceil(prefix_len / 16) entries; max_pages 0:
+ *   no sequence has tokens of its own.  A row with no token at all gets O = 0, LSE = -inf.
+ * Bad page indexes and lengths are reported as for fa_decode_paged_ex.  Enqueues up to three
+ * kernels; the second and third may start before the one in front has finished.
+ */
+fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* prefix_table, int prefix_len,
+                                  const int32_t* block_tables, const int32_t* seq_lens, void* o,
+                                  float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                                  int Hk, int D, int num_pages, int max_pages, float scale,
+                                  int dtype, void* stream);
+
 /*
  * Synchronises `stream`, then reads and clears the current device's status word.  Returns
  * FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call,

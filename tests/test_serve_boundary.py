@@ -230,3 +230,60 @@ def test_grouped_decode_workspace():
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 3, 128, 1024) == 0     # invalid
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 96, 1024) == 0
     assert fa.fa_decode_workspace_bytes_ex(-1, 8, 1, 64, 1024) == 0
+
+
+def _prefix(B=2, Hq=4, Hk=2, D=64, prefix=100, pages=8, maxp=4, scale=0.125, dtype=0, ws_bytes=1 << 20, **ptrs):
+    p = dict(q=A, kc=A + MB, vc=A + 2 * MB, pt=A + 3 * MB, bt=A + 5 * MB, sl=A + 6 * MB, o=A + 7 * MB,
+             lse=A + 8 * MB, ws=A + 9 * MB)
+    p.update(ptrs)
+    return fa.fa_decode_shared_prefix(p["q"], p["kc"], p["vc"], p["pt"], prefix, p["bt"], p["sl"], p["o"],
+                                      p["lse"], p["ws"], ws_bytes, B, Hq, Hk, D, pages, maxp, scale, dtype,
+                                      None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(prefix=-1), BAD),
+    (dict(dtype=2), BAD),
+    (dict(D=72), UNS),
+    (dict(Hq=3), BAD),
+    (dict(Hq=129, Hk=1), UNS),                   # more rows of one sequence than a query tile
+    (dict(scale=math.inf), BAD),
+    (dict(q=A + 4), BAD),
+    (dict(o=0), BAD),
+    (dict(kc=0), BAD),
+    (dict(pt=0), BAD),
+    (dict(pt=A + 3 * MB + 2), BAD),
+    (dict(pages=0), BAD),                        # a prefix, but no page
+    (dict(ws=0), BAD),
+    (dict(ws_bytes=64), BAD),
+    (dict(ws=A + 9 * MB + 8), BAD),
+    (dict(ws=A + 3 * MB - 64), BAD),             # the workspace on the prefix's table
+    (dict(o=A + 2 * MB + 1024), BAD),            # o inside the value cache
+    (dict(B=0), OK),
+], ids=lambda x: str(x)[:48])
+def test_shared_prefix_argument_checks(kw, status):
+    assert _prefix(**kw) == status
+
+
+def test_shared_prefix_workspace():
+    ws = fa.fa_shared_prefix_workspace_bytes
+    assert ws(2, 4, 2, 64, 0, 0) == 0
+    assert ws(2, 4, 2, 64, 100, 0) == 2 * 4 * 65 * 4          # one key tile: one part a row
+    assert ws(2, 4, 2, 64, 100, 4) == 2 * 2 * 4 * 65 * 4      # and one of the own tokens
+    assert ws(2, 4, 2, 64, -1, 4) == 0
+    assert ws(2, 130, 1, 64, 100, 4) == 0
+    # every part a CTA can write has a place: all stretches of all sizes
+    for Hk, pairs_b, tiles in ((1, 1, 200), (2, 40, 77), (8, 300, 31), (32, 256, 128), (3, 513, 5)):
+        rows_b = min(128, pairs_b)
+        n_pairs = ((pairs_b + rows_b - 1) // rows_b + 1) // 2
+        units = Hk * n_pairs * tiles
+        grid = min(152, units)
+        first = [units * c // grid for c in range(grid + 1)]
+        most = 0
+        for item in range(Hk * n_pairs):
+            lo, hi = item * tiles, (item + 1) * tiles
+            ctas = [c for c in range(grid) if first[c] < hi and first[c + 1] > lo]
+            assert ctas[0] == ((lo + 1) * grid - 1) // units
+            most = max(most, len(ctas))
+        parts = ws(pairs_b, Hk, Hk, 64, tiles * 128, 0) // (pairs_b * Hk * 65 * 4)
+        assert most <= parts <= tiles, (Hk, pairs_b, tiles, most, parts)

@@ -32,6 +32,7 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "decode_paged", "FA_PAGE_TOKENS", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
            "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
            "FA_CACHE_16BIT", "FA_CACHE_E4M3", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
+           "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "decode_shared_prefix",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_BF16", "FA_FP16"]
 
@@ -51,7 +52,8 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_set_wait_timeout_ns", "fa_selftest_wait_timeout", "fa_trace_next_call",
             "fa_launch_count", "fa_status_string", "fa_bwd_noalloc", "fa_decode_paged",
             "fa_decode_workspace_bytes", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
-            "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex")
+            "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
+            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes")
 
 
 class FaStrides(ctypes.Structure):
@@ -116,6 +118,11 @@ def load_library():
         lib.fa_decode_paged_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i,
                                            i, i, f, i, i, vp]
         lib.fa_decode_paged_ex.restype = i
+        lib.fa_shared_prefix_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        lib.fa_shared_prefix_workspace_bytes.restype = sz
+        lib.fa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, sz, i, i, i,
+                                                i, i, i, f, i, vp]
+        lib.fa_decode_shared_prefix.restype = i
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i,
                                        vp]
         lib.fa_bwd_noalloc.restype = i
@@ -228,6 +235,19 @@ def fa_decode_paged_ex(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens
                                              seq_lens, o, lse, workspace, workspace_bytes, B, Hq,
                                              Hk, D, num_pages, max_pages, scale, dtype, cache_dtype,
                                              stream)
+
+
+def fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages) -> int:
+    return int(load_library().fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages))
+
+
+def fa_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len, block_tables, seq_lens,
+                            o, lse, workspace, workspace_bytes, B, Hq, Hk, D, num_pages, max_pages,
+                            scale, dtype, stream) -> int:
+    return load_library().fa_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len,
+                                                  block_tables, seq_lens, o, lse, workspace,
+                                                  workspace_bytes, B, Hq, Hk, D, num_pages,
+                                                  max_pages, scale, dtype, stream)
 
 
 def fa_bwd_workspace_bytes(B, H, L, D) -> int:
@@ -811,4 +831,41 @@ def _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, ls
                                     float(scale), dt, kind, _stream_handle(device))
     if status != FA_OK:
         raise FaError("fa_decode_paged_ex", status)
+    return o, l
+
+
+def decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, block_tables, seq_lens,
+                         scale: float | None = None, out=None, lse=None, workspace=None):
+    """One decode step of a batch whose sequences share their first ``prefix_len`` tokens: q
+    [B, Hq, D] attends to the prefix (pages ``prefix_table``, int32 [ceil(prefix_len / 16)] at
+    least) and behind it to each sequence's own ``seq_lens[b]`` tokens (pages
+    ``block_tables[b]``), over 16-bit caches [num_pages, Hk, FA_PAGE_TOKENS, D].  The prefix is read
+    once for the whole batch.  Returns O [B, Hq, D] and LSE [B, Hq] (fp32).  See
+    fa_decode_shared_prefix in fa.h."""
+    import torch
+    B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
+    device = q.device
+    _, num_pages, Hk, Dc, _, _ = _paged_cache(k_cache, v_cache, None, None, q.dtype, device)
+    if Dc != D:
+        raise ValueError(f"the cache has heads of {Dc}, q of {D}")
+    max_pages = _tables(block_tables, seq_lens, B, device)
+    if prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous():
+        raise TypeError("prefix_table must be a contiguous one-dimensional int32 tensor")
+    _on_device("prefix_table", prefix_table, device)
+    prefix_len = int(prefix_len)
+    if prefix_len < 0 or prefix_len > FA_PAGE_TOKENS * prefix_table.shape[0]:
+        raise ValueError(f"prefix_table has room for {FA_PAGE_TOKENS * prefix_table.shape[0]} tokens, "
+                         f"not {prefix_len}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _current(device):
+        need = fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages)
+        wp, wb, keep = _workspace(workspace, need, device)
+        status = fa_decode_shared_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                         prefix_table.data_ptr(), prefix_len,
+                                         block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
+                                         l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
+                                         float(scale), dt, _stream_handle(device))
+    if status != FA_OK:
+        raise FaError("fa_decode_shared_prefix", status)
     return o, l

@@ -88,11 +88,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-__device__ __forceinline__ void pdl_launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Maximum over the lanes that hold the same column (lanes with the same t).
 __device__ __forceinline__ float column_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -144,13 +139,14 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (pg0 >= pg1) {  // no key in this split
         if (threadIdx.x < n_q) {
             if (p.part_o)
-                p.part_lse[(row0 + threadIdx.x) * p.splits + split] = -INFINITY;
+                p.part_lse[(row0 + threadIdx.x) * p.parts + p.part0 + split] = -INFINITY;
             else
                 p.lse[row0 + threadIdx.x] = -INFINITY;
         }
         if (!p.part_o)
             for (int i = threadIdx.x; i < n_q * D / 2; i += kWarps * 32)
                 reinterpret_cast<uint32_t*>(p.o)[row0 * D / 2 + i] = 0u;
+        pdl_wait();
         return;
     }
 
@@ -514,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         const float lse2 = M + log2f(L);
         const size_t row = row0 + qi;
         if (p.part_o) {
-            const size_t part = row * p.splits + split;
+            const size_t part = row * p.parts + p.part0 + split;
             *reinterpret_cast<float2*>(p.part_o + part * D + e) = make_float2(x, y);
             if (e == 0) p.part_lse[part] = lse2;
         } else {
@@ -522,6 +518,9 @@ __global__ void __launch_bounds__(kWarps * 32)
             if (e == 0) p.lse[row] = lse2 * kLn2;
         }
     }
+    // Launched early behind a kernel that writes other parts of the same rows, this kernel ends
+    // only after that one, so that the merge waits for both by waiting for this one.
+    pdl_wait();
 }
 
 // Merges the parts of each query row: O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i), with
@@ -568,8 +567,9 @@ cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
     const int smem = C::smem_bytes(q.stages);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3((unsigned)p.splits, (unsigned)(p.Hk * p.q_blocks), (unsigned)p.B),
-                         dim3(kWarps * 32), (size_t)smem, s, q);
+    const dim3 grid((unsigned)p.splits, (unsigned)(p.Hk * p.q_blocks), (unsigned)p.B);
+    return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)smem, s, q)
+                   : launch_kernel(kern, grid, dim3(kWarps * 32), (size_t)smem, s, q);
 }
 
 template <int D, bool Q8, bool BF16>

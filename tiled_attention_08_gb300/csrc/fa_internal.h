@@ -200,10 +200,35 @@ struct GqaParams {
     const int* seq_lens;       // [B]
     void* o;                   // [B, Hq, D] 16-bit  (splits == 1 and no other parts)
     float* lse;                // [B, Hq] natural log
-    float* part_o;             // [B*Hq, splits, D] fp32, or null: o and lse are written
-    float* part_lse;           // [B*Hq, splits] log2 domain
+    float* part_o;             // [B*Hq, parts, D] fp32, or null: o and lse are written
+    float* part_lse;           // [B*Hq, parts] log2 domain
+    int parts, part0;          // split i is part part0 + i of a row
+    int early;                 // launched before the kernel in front of it has finished
     int B, Hq, Hk, group, q_blocks, num_pages, max_pages, splits, pages_per_split, stages;
     float scale_log2;
+    int* status;
+    uint64_t timeout_ns;
+};
+
+// Attention of all query rows of a batch to one shared prefix (fa_prefix.cu).  A work unit is one
+// 128-key tile of one pair of 128-row query tiles of one cache head; CTA c takes the units
+// c * units / grid .. of the order (head, pair, key tile), so a pair's key tiles are one part per
+// CTA that has any of them.
+struct PrefixParams {
+    CUtensorMap tm_q;          // {D, Hq, B}, box {64, group, rows_b}
+    CUtensorMap tm_k, tm_v;    // {D, 16, num_pages * Hk}, box {64, 16, 1}
+    CUtensorMap tm_k_tail, tm_v_tail;  // the same with the last page's rows only
+    const int* table;          // [ceil(prefix_len / 16)]
+    float* part_o;             // [B*Hq, parts, D] fp32
+    float* part_lse;           // [B*Hq, parts] log2 domain
+    int parts, max_segments;   // parts 0 .. max_segments-1 of a row are the prefix's
+    int prefix_len, num_pages;
+    int B, Hq, Hk, group;
+    int rows_b;                // sequences per query tile (group * rows_b <= 128 rows)
+    int n_tiles, n_pairs, key_tiles;
+    int grid;
+    float scale_log2;          // |scale| * log2(e)
+    uint32_t s_negate;
     int* status;
     uint64_t timeout_ns;
 };
@@ -280,6 +305,9 @@ cudaError_t launch_cache_append(const CacheAppendParams& p, bool bf16, bool q8, 
 cudaError_t launch_cache_read(const CacheReadParams& p, bool bf16, bool q8, cudaStream_t s);
 // q8: an e4m3 cache; else one of q's type (bf16 or fp16).
 cudaError_t launch_decode_gqa(const GqaParams& p, int D, bool bf16, bool q8, cudaStream_t s);
+cudaError_t launch_prefix(const PrefixParams& p, int D, bool bf16, cudaStream_t s);
+// The work split of a shared prefix: fills rows_b, n_tiles, n_pairs, key_tiles, grid, max_segments.
+void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p);
 cudaError_t launch_merge_parts(const MergeParams& p, int D, bool bf16, cudaStream_t s);
 // Query blocks of 8 or 16 rows per cache head, and the splits of the page range.
 int gqa_q_blocks(int group);

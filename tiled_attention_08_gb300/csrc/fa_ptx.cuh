@@ -53,6 +53,14 @@ __device__ __forceinline__ void record_timeout(int* status, volatile int* abort_
     atomicCAS(status, 0, 4);
 }
 
+// Programmatic dependent launch: a kernel launched early behind this one may start once every CTA
+// has called launch_dependents (or ended); wait returns when the kernel before has finished and
+// its writes are visible (at once for a kernel that was not launched early).
+__device__ __forceinline__ void pdl_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------------------

@@ -1,6 +1,8 @@
 // fa_serve.cu -- C entry points of the operators around attention: rotary positions, the paged
-// cache's writing and reading, and the decode step with grouped heads.  Argument checks and
-// launches; the kernels are in fa_rotary.cu, fa_cache.cu and fa_decode_gqa.cu.
+// cache's writing and reading, the decode step with grouped heads and that with a shared prefix.
+// Argument checks and launches; the kernels are in fa_rotary.cu, fa_cache.cu, fa_decode_gqa.cu and
+// fa_prefix.cu.
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -375,6 +377,7 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
     p.lse = lse;
     p.part_o = ws_need ? static_cast<float*>(workspace) : nullptr;
     p.part_lse = ws_need ? static_cast<float*>(workspace) + rows * p.splits * D : nullptr;
+    p.parts = p.splits;
     p.B = B;
     p.Hq = Hq;
     p.Hk = Hk;
@@ -394,6 +397,147 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
     if (p.splits == 1) return FA_OK;
     const MergeParams mp = {{p.part_o, p.part_lse, p.splits}, o, lse, (int)rows};
     return traced_launch(1, s, [&] { return launch_merge_parts(mp, D, bf16, s); }) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
+                                        int max_pages) {
+    if (B <= 0 || Hq <= 0 || prefix_len < 0 ||
+        check_decode(B, Hq, Hk, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK ||
+        Hq / Hk > kTileRows)
+        return 0;
+    PrefixParams pp;
+    prefix_plan(B, Hk, Hq / Hk, prefix_len, &pp);
+    const int splits = max_pages > 0 ? gqa_splits(B, Hk, Hq / Hk, max_pages) : 0;
+    return parts_bytes((size_t)B * Hq, pp.max_segments + splits, D);
+}
+
+fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* prefix_table, int prefix_len,
+                                  const int32_t* block_tables, const int32_t* seq_lens, void* o,
+                                  float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                                  int Hk, int D, int num_pages, int max_pages, float scale,
+                                  int dtype, void* stream) {
+    TraceDisarm disarm;
+    if (prefix_len < 0) return FA_ERR_INVALID_ARG;
+    fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, FA_CACHE_16BIT);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0) return FA_OK;
+    const int group = Hq / Hk;
+    if (group > kTileRows) return FA_ERR_UNSUPPORTED;
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse))
+        return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, nullptr, nullptr, block_tables, seq_lens, num_pages,
+                           max_pages, FA_CACHE_16BIT))
+        return FA_ERR_INVALID_ARG;
+    // A prefix needs pages to lie in.
+    if (prefix_len > 0 && (!prefix_table || !aligned4(prefix_table) || num_pages == 0))
+        return FA_ERR_INVALID_ARG;
+    PrefixParams pp;
+    std::memset(&pp, 0, sizeof(pp));
+    prefix_plan(B, Hk, group, prefix_len, &pp);
+    GqaParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.splits = max_pages > 0 ? gqa_splits(B, Hk, group, max_pages) : 0;
+    const int parts = pp.max_segments + p.splits;
+    const size_t rows = (size_t)B * Hq;
+    const size_t ws_need = parts_bytes(rows, parts, D);
+    if (ws_need > 0 && (!workspace || workspace_bytes < ws_need || !aligned16(workspace)))
+        return FA_ERR_INVALID_ARG;
+    const size_t cb = cache_bytes(num_pages, Hk, D, FA_CACHE_16BIT);
+    const int n_prefix_pages = prefix_len / kPageTokens + (prefix_len % kPageTokens != 0);
+    const Range ins[] = {range(q, rows * D * 2u), range(k_cache, cb), range(v_cache, cb),
+                         range(prefix_table, (size_t)n_prefix_pages * 4u),
+                         range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u)};
+    const Range outs[] = {range(o, rows * D * 2u), range(lse, rows * 4u), range(workspace, ws_need)};
+    for (int a = 0; a < 3; ++a) {
+        for (const Range& in : ins)
+            if (overlap(outs[a], in)) return FA_ERR_INVALID_ARG;
+        for (int b = a + 1; b < 3; ++b)
+            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
+    }
+    if (!bind_context()) return FA_ERR_CUDA;
+    if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, false) ||
+                          !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, false)))
+        return FA_ERR_CUDA;
+    float* part_o = static_cast<float*>(workspace);
+    float* part_lse = part_o + rows * parts * D;
+    int* status = status_ptr();
+    if (!status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = dtype == FA_BF16;
+    int n = 0;
+    if (prefix_len > 0) {
+        const CUtensorMapDataType type =
+            bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)B};
+        const cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * Hq * 2};
+        const cuuint32_t qb[3] = {64, (cuuint32_t)group, (cuuint32_t)pp.rows_b};
+        if (!make_tiled_map(&pp.tm_q, type, q, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B))
+            return FA_ERR_CUDA;
+        pp.tm_k = p.tm_k;
+        pp.tm_v = p.tm_v;
+        // The last page's rows alone: what lies behind them reads as zeros.
+        const int tail = prefix_len % kPageTokens;
+        pp.tm_k_tail = p.tm_k;
+        pp.tm_v_tail = p.tm_v;
+        if (tail > 0) {
+            const cuuint64_t d[3] = {(cuuint64_t)D, (cuuint64_t)tail, (cuuint64_t)num_pages * Hk};
+            const cuuint64_t st2[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * kPageTokens};
+            const cuuint32_t box[3] = {64, (cuuint32_t)kPageTokens, 1};
+            if (!make_tiled_map(&pp.tm_k_tail, type, k_cache, 3, d, st2, box,
+                                CU_TENSOR_MAP_SWIZZLE_128B) ||
+                !make_tiled_map(&pp.tm_v_tail, type, v_cache, 3, d, st2, box,
+                                CU_TENSOR_MAP_SWIZZLE_128B))
+                return FA_ERR_CUDA;
+        }
+        pp.table = prefix_table;
+        pp.part_o = part_o;
+        pp.part_lse = part_lse;
+        pp.parts = parts;
+        pp.prefix_len = prefix_len;
+        pp.num_pages = num_pages;
+        pp.B = B;
+        pp.Hq = Hq;
+        pp.Hk = Hk;
+        pp.group = group;
+        // The softmax takes the maximum of the stored scores: a negative scale is moved into the
+        // contraction as an exact sign flip, and the multiplier keeps a masked -inf at -inf.
+        pp.scale_log2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+        pp.s_negate = scale < 0.0f ? 1u : 0u;
+        pp.status = status;
+        pp.timeout_ns = wait_timeout_ns();
+        if (traced_launch(n++, s, [&] { return launch_prefix(pp, D, bf16, s); }) != cudaSuccess)
+            return FA_ERR_CUDA;
+    }
+    if (p.splits > 0) {
+        p.q = q;
+        p.block_tables = block_tables;
+        p.seq_lens = seq_lens;
+        p.part_o = part_o;
+        p.part_lse = part_lse;
+        p.parts = parts;
+        p.part0 = pp.max_segments;
+        p.early = prefix_len > 0;
+        p.B = B;
+        p.Hq = Hq;
+        p.Hk = Hk;
+        p.group = group;
+        p.q_blocks = gqa_q_blocks(group);
+        p.num_pages = num_pages;
+        p.max_pages = max_pages;
+        p.pages_per_split = (max_pages + p.splits - 1) / p.splits;
+        p.scale_log2 = scale * 1.4426950408889634f;
+        p.status = status;
+        p.timeout_ns = wait_timeout_ns();
+        if (traced_launch(n++, s, [&] { return launch_decode_gqa(p, D, bf16, false, s); }) !=
+            cudaSuccess)
+            return FA_ERR_CUDA;
+    }
+    const MergeParams mp = {{part_o, part_lse, parts}, o, lse, (int)rows};
+    return traced_launch(n, s, [&] { return launch_merge_parts(mp, D, bf16, s); }) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
