@@ -323,8 +323,10 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
                         void* k, void* v, const fa_strides* strides, int B, int H, int L, int D,
                         int num_pages, int max_pages, int dtype, int cache_dtype, void* stream);
 
-/* Bytes of device workspace fa_decode_paged_ex needs: the partial results of the splits of the page
- * range (fp32), 0 when there is one split.  0 for invalid sizes. */
+/* Bytes of device workspace fa_decode_paged_ex needs (the parts of rows whose pages are
+ * split, fp32: at D = 128 at most 2.5 MB, from 4864 (sequence, cache head) pairs on 7.5 MB, for every
+ * query head of a group up to 16).  Calls that may
+ * overlap on the GPU need a workspace each.  0 for invalid sizes. */
 size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages);
 
 /*
@@ -333,8 +335,9 @@ size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages)
  * [num_pages, Hk, FA_PAGE_TOKENS] (FA_CACHE_E4M3; ignored otherwise).  Hq is a multiple of Hk and
  * query head h reads cache head h / (Hq / Hk).  Everything else is as for fa_decode_paged: empty
  * sequences get O = 0, LSE = -inf, slots past a sequence's end may hold anything, a bad length or
- * page index is reported by fa_get_device_status().  Two kernels when the page range is split, else
- * one.
+ * page index is reported by fa_get_device_status().  Enqueues two kernels for every 1024 sequences
+ * (the second may start before the first has finished).  B * max_pages, B * Hq and num_pages * Hk
+ * are below 2^31.
  */
 fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_cache,
                              const void* k_exp, const void* v_exp, const int32_t* block_tables,
@@ -342,8 +345,8 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
                              size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
                              int max_pages, float scale, int dtype, int cache_dtype, void* stream);
 
-/* Bytes of device workspace fa_decode_shared_prefix needs (fp32 parts of every query row).  0 for
- * invalid sizes, and when there is neither a prefix nor a page. */
+/* Bytes of device workspace fa_decode_shared_prefix needs: fa_decode_paged_ex's and fp32 parts of
+ * every query row.  0 for invalid sizes. */
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
                                         int max_pages);
 
@@ -359,8 +362,9 @@ size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix
  *   caches of dtype (16-bit), Hq a multiple of Hk with Hq / Hk <= 128; prefix_len >= 0 (a host
  *   integer; 0: no prefix), prefix_table int32, device, ceil(prefix_len / 16) entries; max_pages 0:
  *   no sequence has tokens of its own.  A row with no token at all gets O = 0, LSE = -inf.
- * Bad page indexes and lengths are reported as for fa_decode_paged_ex.  Enqueues up to three
- * kernels; the second and third may start before the one in front has finished.
+ * Bad page indexes and lengths are reported as for fa_decode_paged_ex.  Enqueues three kernels (two
+ * without a prefix, two more for every further 1024 sequences); each may start before the one in
+ * front has finished.
  */
 fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
                                   const int32_t* prefix_table, int prefix_len,

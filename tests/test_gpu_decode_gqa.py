@@ -99,21 +99,20 @@ def test_shapes(q8, D, dtype, Hq, Hk):
     check(o, lse, q, ks, vs, scale, dtype, q8)
 
 
-@pytest.mark.parametrize("lens,Hq,Hk,q8", [([5000], 8, 1, True), ([2000, 0], 4, 4, True),
+@pytest.mark.parametrize("lens,Hq,Hk,q8", [([5000], 8, 1, True), ([70000], 4, 1, True),
+                                           ([20000, 3], 12, 1, False), ([2000, 0], 4, 4, True),
                                            ([17, 4096, 1], 16, 1, False), ([1], 2, 2, True),
                                            ([0], 2, 1, True)])
 def test_split_and_merge(lens, Hq, Hk, q8):
     D, dtype = 128, torch.bfloat16
     rng = np.random.default_rng(len(lens))
     kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, lens, Hk, D, dtype, q8)
-    if max(lens) > 1000:
-        assert fa.fa_decode_workspace_bytes_ex(len(lens), Hq, Hk, D, bt.shape[1]) > 0
     q = randn(len(lens), Hq, D, dtype=dtype)
     o, lse = fa.decode_paged(q, kc, vc, bt, sl, k_exp=ke, v_exp=ve)
     assert status() == fa.FA_OK
     check(o, lse, q, ks, vs, 1.0 / math.sqrt(D), dtype, q8)
     wide = torch.zeros((len(lens), 4 * bt.shape[1] + 40), dtype=torch.int32, device="cuda")
-    wide[:, :bt.shape[1]] = bt  # a table much wider than the sequences: most splits are empty
+    wide[:, :bt.shape[1]] = bt  # a table much wider than the sequences: more warps than pages
     o2, lse2 = fa.decode_paged(q, kc, vc, wide, sl, k_exp=ke, v_exp=ve)
     assert status() == fa.FA_OK
     check(o2, lse2, q, ks, vs, 1.0 / math.sqrt(D), dtype, q8)
@@ -249,6 +248,19 @@ def test_repeated_captured_and_on_another_stream():
     for _, _, o, lse, _ in runs:
         check(o, lse, q, [ks[0][:, :1500], ks[1][:, :33]], [vs[0][:, :1500], vs[1][:, :33]],
               1.0 / math.sqrt(D), dtype, True)
+
+
+def test_many_sequences():
+    """More sequences than one launch takes (1024), most of them short, some empty."""
+    D, dtype, Hk = 64, torch.float16, 1
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(0, 40, 1500)]
+    lens[1023], lens[1024], lens[1499] = 200, 0, 77
+    kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, lens, Hk, D, dtype, True)
+    q = randn(1500, 2, D, dtype=dtype)
+    o, lse = fa.decode_paged(q, kc, vc, bt, sl, k_exp=ke, v_exp=ve)
+    assert status() == fa.FA_OK
+    check(o, lse, q, ks, vs, 1.0 / math.sqrt(D), dtype, True)
 
 
 def test_equal_heads_agree_with_the_plain_step():

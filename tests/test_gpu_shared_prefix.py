@@ -60,6 +60,8 @@ CASES = [
     (400, [11, 70], 128, 1, 64, torch.bfloat16),       # one sequence a tile
     (700, [20, 5, 0], 17 * 3, 3, 128, torch.bfloat16),
     (0, [33, 0], 4, 2, 64, torch.bfloat16),            # no prefix
+    (40, [1, 0, 19] * 400, 1, 1, 64, torch.float16),   # more sequences than one launch takes
+    (150, [3000, 0, 40], 16, 1, 128, torch.float16),   # own tokens split over many warps
 ]
 
 

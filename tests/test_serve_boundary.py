@@ -223,13 +223,84 @@ def test_grouped_decode_argument_checks(kw, status):
 
 
 def test_grouped_decode_workspace():
-    assert fa.fa_decode_workspace_bytes_ex(256, 32, 8, 128, 256) == 0   # enough CTAs without splits
-    assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 128, 16) == 0       # one split of 16 pages
-    need = fa.fa_decode_workspace_bytes_ex(1, 8, 1, 128, 1024)
-    assert need > 0 and need % (8 * (128 + 1) * 4) == 0
+    """8 bytes a unit, then two slots of the group's rows (16 at most) for every warp of a step."""
+    def need(B, Hq, Hk, D, max_pages):
+        g = Hq // Hk
+        q_rows = 8 if g <= 8 else 16
+        chunk = min(B, 1024)
+        units = chunk * Hk * -(-g // q_rows)
+        ctas = min(4 * 152, max(1, -(-units * max_pages // 16)))
+        up = lambda n: (n + 15) // 16 * 16  # noqa: E731
+        slots = 2 * 4 * ctas * min(g, q_rows) * (3 if units >= 2 * 4 * 152 * 4 else 1)
+        return up(8 * units) + up(slots * D * 4) + up(slots * 4)
+
+    for args in ((256, 32, 8, 128, 256), (1, 8, 1, 128, 16), (1, 8, 1, 128, 1024), (5, 40, 2, 64, 9),
+                 (2, 4, 2, 64, 0), (3000, 2, 2, 64, 1), (256, 32, 32, 128, 256)):
+        assert fa.fa_decode_workspace_bytes_ex(*args) == need(*args), args
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 3, 128, 1024) == 0     # invalid
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 96, 1024) == 0
     assert fa.fa_decode_workspace_bytes_ex(-1, 8, 1, 64, 1024) == 0
+
+
+@pytest.mark.parametrize("lens,per_seq,warps,rounds", [
+    ([333], 8, 44, 1), ([0, 0, 5], 1, 4, 1), ([0], 3, 4, 1), ([1] * 40, 2, 20, 1),
+    ([7, 0, 4096, 16, 1], 3, 2432, 1), ([16384, 100], 1, 516, 1), (list(range(300)), 4, 2432, 1),
+    (list(range(300)), 40, 24, 3), ([1, 0, 5000, 17, 64], 8, 12, 3), ([3] * 500, 4, 8, 3),
+    ([17] * 40, 2, 8, 3)])
+def test_grouped_decode_split_model(lens, per_seq, warps, rounds):
+    """The decode kernel's split as its comment states it: every page in one stretch, at most one
+    part of a warp that began before it and one that ends behind it, and the first warp and the
+    number that a unit's first warp notes for the merge those that left its parts."""
+    pages = [-(-n // 16) for n in lens]
+    cum = [0]
+    for n in pages:
+        cum.append(cum[-1] + n)
+    total = cum[-1] * per_seq
+    workers = max(1, min(total // 4, 128 * len(lens) * per_seq, warps))
+    if total < 16 * workers:
+        rounds = 1
+    at = [0, total // 64 * 52, total // 64 * 60, total] if rounds == 3 else [0, total]
+
+    def start(r, i):
+        return at[r] + (at[r + 1] - at[r]) * i // workers
+
+    def worker_of(x):
+        r = 0
+        while r + 1 < rounds and x >= at[r + 1]:
+            r += 1
+        return r * workers + ((x - at[r] + 1) * workers - 1) // (at[r + 1] - at[r])
+
+    left, noted = {}, {}
+    seen = 0
+    for w in range(workers * rounds if total else 0):
+        x0, end = start(w // workers, w % workers), start(w // workers, w % workers + 1)
+        x, slots = x0, set()
+        while x < end:
+            b = max(i for i in range(len(lens)) if cum[i] * per_seq <= x and pages[i])
+            unit, pg = divmod(x - cum[b] * per_seq, pages[b])
+            stop = min(end, x + pages[b] - pg)
+            slot = None
+            if pg > 0 or stop - x < pages[b]:
+                slot = 2 * w + (0 if pg > 0 else 1)
+                assert slot not in slots
+                slots.add(slot)
+            if pg == 0:
+                last = x + pages[b] - 1
+                noted[b, unit] = (w, 1 if last < end else worker_of(last) - w + 1)
+            left.setdefault((b, unit), []).append((w, slot))
+            seen += stop - x
+            x = stop
+    assert seen == total
+    for b in range(len(lens)):
+        for unit in range(per_seq):
+            if not pages[b]:
+                assert (b, unit) not in left
+                continue
+            w0, n = noted[b, unit]
+            if n == 1:
+                assert left[b, unit] == [(w0, None)]
+            else:
+                assert left[b, unit] == [(w, 2 * w + (1 if w == w0 else 0)) for w in range(w0, w0 + n)]
 
 
 def _prefix(B=2, Hq=4, Hk=2, D=64, prefix=100, pages=8, maxp=4, scale=0.125, dtype=0, ws_bytes=1 << 20, **ptrs):
@@ -267,9 +338,11 @@ def test_shared_prefix_argument_checks(kw, status):
 
 def test_shared_prefix_workspace():
     ws = fa.fa_shared_prefix_workspace_bytes
-    assert ws(2, 4, 2, 64, 0, 0) == 0
-    assert ws(2, 4, 2, 64, 100, 0) == 2 * 4 * 65 * 4          # one key tile: one part a row
-    assert ws(2, 4, 2, 64, 100, 4) == 2 * 2 * 4 * 65 * 4      # and one of the own tokens
+    base = fa.fa_decode_workspace_bytes_ex(2, 4, 2, 64, 4)
+    assert ws(2, 4, 2, 64, 0, 4) == base
+    # with a prefix: the rows' own part, and one part for one key tile, two for two
+    assert ws(2, 4, 2, 64, 100, 4) == base + 2 * (2 * 4 * 65 * 4)
+    assert ws(2, 4, 2, 64, 200, 4) == base + 3 * (2 * 4 * 65 * 4)
     assert ws(2, 4, 2, 64, -1, 4) == 0
     assert ws(2, 130, 1, 64, 100, 4) == 0
     # every part a CTA can write has a place: all stretches of all sizes
@@ -277,7 +350,7 @@ def test_shared_prefix_workspace():
         rows_b = min(128, pairs_b)
         n_pairs = ((pairs_b + rows_b - 1) // rows_b + 1) // 2
         units = Hk * n_pairs * tiles
-        grid = min(152, units)
+        grid = min(152, (units + 3) // 4)
         first = [units * c // grid for c in range(grid + 1)]
         most = 0
         for item in range(Hk * n_pairs):
@@ -285,5 +358,6 @@ def test_shared_prefix_workspace():
             ctas = [c for c in range(grid) if first[c] < hi and first[c + 1] > lo]
             assert ctas[0] == ((lo + 1) * grid - 1) // units
             most = max(most, len(ctas))
-        parts = ws(pairs_b, Hk, Hk, 64, tiles * 128, 0) // (pairs_b * Hk * 65 * 4)
+        rows = pairs_b * Hk * 65 * 4
+        parts = (ws(pairs_b, Hk, Hk, 64, tiles * 128, 0) - ws(pairs_b, Hk, Hk, 64, 0, 0)) // rows - 1
         assert most <= parts <= tiles, (Hk, pairs_b, tiles, most, parts)

@@ -18,6 +18,7 @@ TFLOPS to FlashAttention", sections 4.2-4.3).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -74,6 +75,8 @@ def library_path() -> str:
 def load_library():
     """Loads the in-tree libfa.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -105,12 +108,12 @@ def load_library():
         lib.fa_rotary_freqs.argtypes = [i, d64, i, d64, d64, ctypes.POINTER(i64),
                                         ctypes.POINTER(f)]
         lib.fa_rotary_freqs.restype = i
-        lib.fa_rotary.argtypes = [vp, vp, vp, vp, sp, vp, i64, vp, i, f, i, i, i, i, i, i, i, i, vp]
+        lib.fa_rotary.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, i, f, i, i, i, i, i, i, i, i, vp]
         lib.fa_rotary.restype = i
-        lib.fa_cache_append.argtypes = [vp, vp, sp, vp, vp, vp, vp, vp, vp, vp, vp, i, f, i, i, i,
+        lib.fa_cache_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, f, i, i, i,
                                         i, i, i, i, i, i, vp]
         lib.fa_cache_append.restype = i
-        lib.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sp, i, i, i, i, i, i, i, i,
+        lib.fa_cache_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i,
                                       vp]
         lib.fa_cache_read.restype = i
         lib.fa_decode_workspace_bytes_ex.argtypes = [i, i, i, i, i]
@@ -510,33 +513,62 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
 
 
 # ---------------------------------------------------------------------------------------
+# Operators around attention.  The smallest of these calls run for a few microseconds on the GPU, so
+# the checks below read each property of a tensor once and the calls go straight to the library.
+# ---------------------------------------------------------------------------------------
+_raw_stream = None
+
+
+def _launch(name, index, *args):
+    """The library's entry point ``name`` on the current stream of CUDA device ``index`` (made
+    current for the call where it is not); raises on a status other than FA_OK."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    fn = getattr(_lib or load_library(), name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != FA_OK:
+        raise FaError(name, status)
+
+
+def _cuda_index(name, t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _same_device(name, t, index):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _row_strides(name, t, shape):
+    """(batch, head, row) element strides of a view of the given [B, H, L, D] shape."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"{name}: the last (D) dimension must be contiguous")
+    return st[:3]
+
+
+def _int32_vector(name, t, n, index):
+    import torch
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
+    _same_device(name, t, index)
+
+
+# ---------------------------------------------------------------------------------------
 # Rotary positions
 # ---------------------------------------------------------------------------------------
-def _on_device(name, t, device):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _current(device):
-    """Context in which `device` is the current CUDA device (the library launches there)."""
-    import contextlib
-
-    import torch
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _kernel_view(t):
-    """`t` itself where the kernels can read its strides, else a contiguous copy (an expanded
-    gradient, for one, has strides of 0)."""
-    if t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
-            t.stride(i) % 8 == 0 and (t.stride(i) > 0 or (t.size(i) == 1 and i < 2))
-            for i in range(3)):
-        return t
-    return t.contiguous()
-
-
 def rotary_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
                  factor: float = 1.0, original_len: float = 0.0, device="cuda"):
     """The frequency table of ``rotary`` and ``cache_append`` and the factor ``mscale``:
@@ -553,56 +585,65 @@ def rotary_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
     return torch.tensor(freqs, dtype=torch.int64, device=device), mscale
 
 
-def _check_freqs(freqs, device):
+def _rotary_dim(freqs, index):
     import torch
-    if freqs.dtype != torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
+    if freqs.dtype is not torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
         raise TypeError("freqs must be a contiguous one-dimensional int64 tensor (rotary_freqs)")
-    _on_device("freqs", freqs, device)
-    return 2 * freqs.numel()
+    _same_device("freqs", freqs, index)
+    return 2 * freqs.shape[0]
+
+
+def _kernel_view(t):
+    """`t` itself where the kernels can read its strides, else a contiguous copy (an expanded
+    gradient, for one, has strides of 0)."""
+    B, H, _, _ = t.shape
+    b, h, l, d = t.stride()
+    if d == 1 and not (b | h | l) & 7 and l > 0 and (h > 0 or H == 1) and (b > 0 or B == 1) and \
+            not t.data_ptr() & 15:
+        return t
+    return t.contiguous()
 
 
 def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
     """The library call for one or two [B, H, L, D] views; returns the outputs."""
     import torch
     x = xs[0]
-    device = x.device
+    index = _cuda_index("x", x)
+    if x.dim() != 4:
+        raise ValueError("rotary operands are [B, H, L, D] views")
     dt = _dtype_code(x)
-    B, _, L, D = x.shape
-    xs = [t if outs is not None else _kernel_view(t) for t in xs]
-    st_in = [_view_strides(t, "x", (B, t.shape[1], L, D)) for t in xs]
-    for t in xs:
-        if t.dtype != x.dtype:
-            raise TypeError("the operands must share a dtype")
-        _on_device("x", t, device)
-    rotary_dim = _check_freqs(freqs, device)
-    pos_ptr, pos_stride = None, 0
-    if positions is not None:
-        if positions.dtype != torch.int32:
-            raise TypeError("positions must be int32")
-        _on_device("positions", positions, device)
-        if positions.dim() == 1:
-            positions = positions[None].expand(B, -1)
-        if tuple(positions.shape) != (B, L) or (L > 1 and positions.stride(1) != 1):
-            raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
-        pos_ptr = positions.data_ptr()
-        pos_stride = positions.stride(0) if B > 1 else 0
+    B, H, L, D = x.shape
     if outs is None:
+        xs = [_kernel_view(t) for t in xs]
         outs = [torch.empty_like(t) for t in xs]
-    st_out = [_view_strides(o, "out", t.shape) for o, t in zip(outs, xs)]
-    for o in outs:
-        if o.dtype != x.dtype:
-            raise TypeError("out must have the dtype of x")
-        _on_device("out", o, device)
-    two = len(xs) == 2
-    with _current(device):
-        status = fa_rotary(xs[0].data_ptr(), xs[1].data_ptr() if two else None,
-                           outs[0].data_ptr(), outs[1].data_ptr() if two else None,
-                           [st_in[0], st_in[-1], st_out[0], st_out[-1]], pos_ptr, pos_stride,
-                           freqs.data_ptr(), rotary_dim, float(mscale), interleaved, inverse, B,
-                           xs[0].shape[1], xs[1].shape[1] if two else 0, L, D, dt,
-                           _stream_handle(device))
-    if status != FA_OK:
-        raise FaError("fa_rotary", status)
+    k, k_out, Hk = None, None, 0
+    st = [_row_strides("x", xs[0], x.shape)] * 2 + [_row_strides("out", outs[0], x.shape)] * 2
+    if len(xs) == 2:
+        k, k_out, Hk = xs[1], outs[1], xs[1].shape[1]
+        st[1] = _row_strides("k", k, (B, Hk, L, D))
+        st[3] = _row_strides("k's out", k_out, (B, Hk, L, D))
+    for t in (*xs, *outs):
+        if t.dtype is not x.dtype:
+            raise TypeError("the operands must share a dtype")
+        _same_device("an operand", t, index)
+    rotary_dim = _rotary_dim(freqs, index)
+    pos, pos_stride = None, 0
+    if positions is not None:
+        if positions.dtype is not torch.int32:
+            raise TypeError("positions must be int32")
+        _same_device("positions", positions, index)
+        ps, pst = positions.shape, positions.stride()
+        if ps == (L,):
+            ps, pst = (B, L), (0, *pst)
+        if ps != (B, L) or (L > 1 and pst[1] != 1):
+            raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
+        pos = positions.data_ptr()
+        pos_stride = pst[0] if B > 1 else 0
+    _launch("fa_rotary", index, xs[0].data_ptr(), None if k is None else k.data_ptr(),
+            outs[0].data_ptr(), None if k is None else k_out.data_ptr(),
+            (ctypes.c_int64 * 12)(*st[0], *st[1], *st[2], *st[3]), pos, pos_stride,
+            freqs.data_ptr(), rotary_dim, float(mscale), interleaved, inverse, B, H, Hk, L, D,
+            dt)
     return outs
 
 
@@ -660,9 +701,9 @@ def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = Fals
     ``rotary_freqs``.  The rotated tensors go to ``attention`` (or, one row per sequence, to
     ``decode_paged``)."""
     import torch
-    if k.shape[0] != q.shape[0] or tuple(k.shape[2:]) != tuple(q.shape[2:]):
-        raise ValueError("q and k must agree in B, L and D")
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad):
+    if k.dim() != 4:
+        raise ValueError("rotary operands are [B, H, L, D] views")
+    if (q.requires_grad or k.requires_grad) and torch.is_grad_enabled():
         return _rotary_autograd().apply(positions, freqs, mscale, interleaved, False, q, k)
     return tuple(_rotate([q, k], positions, freqs, mscale, interleaved, False))
 
@@ -670,46 +711,49 @@ def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = Fals
 # ---------------------------------------------------------------------------------------
 # The paged cache: writing rows and reading them back
 # ---------------------------------------------------------------------------------------
-def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, device):
+def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index):
     """(cache_dtype, num_pages, H, D, k_exp pointer, v_exp pointer) of a checked pair of caches."""
     import torch
-    if k_cache.dim() != 4 or k_cache.shape[2] != FA_PAGE_TOKENS or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != FA_PAGE_TOKENS or v_cache.shape != shape:
         raise ValueError("caches must be [num_pages, H, FA_PAGE_TOKENS, D]")
-    num_pages, H, _, D = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        _on_device(name, t, device)
-    if v_cache.dtype != k_cache.dtype:
+    num_pages, H, _, D = shape
+    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("the caches must be contiguous")
+    _same_device("k_cache", k_cache, index)
+    _same_device("v_cache", v_cache, index)
+    kind = k_cache.dtype
+    if v_cache.dtype is not kind:
         raise TypeError("k_cache and v_cache must share a dtype")
     if k_exp is None and v_exp is None:
-        if k_cache.dtype != dtype:
-            raise TypeError(f"the cache holds {k_cache.dtype}, the call's tensors {dtype}; an "
-                            "e4m3 cache needs k_exp and v_exp")
+        if kind is not dtype:
+            raise TypeError(f"the cache holds {kind}, the call's tensors {dtype}; an e4m3 cache "
+                            "needs k_exp and v_exp")
         return FA_CACHE_16BIT, num_pages, H, D, None, None
-    if k_cache.dtype != torch.float8_e4m3fn:
+    if kind is not torch.float8_e4m3fn:
         raise TypeError("a cache with exponents must be float8_e4m3fn")
     for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-        if t is None or t.dtype != torch.uint8 or tuple(t.shape) != (num_pages, H, FA_PAGE_TOKENS) \
-                or not t.is_contiguous():
+        if t is None or t.dtype is not torch.uint8 or t.shape != shape[:3] or \
+                not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous uint8 [num_pages, H, FA_PAGE_TOKENS] "
                              "tensor")
-        _on_device(name, t, device)
+        _same_device(name, t, index)
     return FA_CACHE_E4M3, num_pages, H, D, k_exp.data_ptr(), v_exp.data_ptr()
 
 
-def _tables(block_tables, seq_lens, B, device):
+def _tables(block_tables, seq_lens, B, index):
     """max_pages of a checked block table and its lengths."""
     import torch
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+    if block_tables.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(seq_lens.shape) != (B,):
+    shape = block_tables.shape
+    if len(shape) != 2 or shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_tables must be [B, max_pages] and seq_lens [B]")
     if not block_tables.is_contiguous() or not seq_lens.is_contiguous():
         raise ValueError("block_tables and seq_lens must be contiguous")
-    _on_device("block_tables", block_tables, device)
-    _on_device("seq_lens", seq_lens, device)
-    return block_tables.shape[1]
+    _same_device("block_tables", block_tables, index)
+    _same_device("seq_lens", seq_lens, index)
+    return shape[1]
 
 
 def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, k_exp=None,
@@ -720,33 +764,31 @@ def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, 
     float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` (uint8 [num_pages, H, FA_PAGE_TOKENS]),
     into which rows are quantised.  With ``freqs`` (``rotary_freqs``) each key is first rotated by
     its token index.  See fa_cache_append in fa.h."""
-    import torch
-    device = k.device
+    index = _cuda_index("k", k)
     dt = _dtype_code(k)
-    st = [_view_strides(k, "k"), _view_strides(v, "v", k.shape)]
-    if v.dtype != k.dtype:
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("k and v must be [B, H, L, D] views")
+    B, H, L, D = shape
+    ks, vs = _row_strides("k", k, shape), _row_strides("v", v, shape)
+    if v.dtype is not k.dtype:
         raise TypeError("k and v must share a dtype")
-    _on_device("v", v, device)
-    B, H, L, D = k.shape
-    kind, num_pages, Hc, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, k.dtype, device)
+    _same_device("v", v, index)
+    kind, num_pages, Hc, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, k.dtype, index)
     if Hc != H or Dc != D:
         raise ValueError(f"the cache has {Hc} heads of {Dc}, k has {H} of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, device)
+    max_pages = _tables(block_tables, seq_lens, B, index)
+    new, fp, rotary_dim = None, None, 0
     if new_lens is not None:
-        if new_lens.dtype != torch.int32 or tuple(new_lens.shape) != (B,) or not new_lens.is_contiguous():
-            raise ValueError("new_lens must be a contiguous int32 [B] tensor")
-        _on_device("new_lens", new_lens, device)
-    rotary_dim = _check_freqs(freqs, device) if freqs is not None else 0
-    with _current(device):
-        status = fa_cache_append(k.data_ptr(), v.data_ptr(), st, k_cache.data_ptr(),
-                                 v_cache.data_ptr(), kep, vep, block_tables.data_ptr(),
-                                 seq_lens.data_ptr(),
-                                 None if new_lens is None else new_lens.data_ptr(),
-                                 None if freqs is None else freqs.data_ptr(), rotary_dim,
-                                 float(mscale), interleaved, B, H, L, D, num_pages, max_pages, dt,
-                                 kind, _stream_handle(device))
-    if status != FA_OK:
-        raise FaError("fa_cache_append", status)
+        _int32_vector("new_lens", new_lens, B, index)
+        new = new_lens.data_ptr()
+    if freqs is not None:
+        rotary_dim = _rotary_dim(freqs, index)
+        fp = freqs.data_ptr()
+    _launch("fa_cache_append", index, k.data_ptr(), v.data_ptr(), (ctypes.c_int64 * 6)(*ks, *vs),
+            k_cache.data_ptr(), v_cache.data_ptr(), kep, vep, block_tables.data_ptr(),
+            seq_lens.data_ptr(), new, fp, rotary_dim, float(mscale), interleaved, B, H, L, D, num_pages,
+            max_pages, dt, kind)
 
 
 def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None, v_exp=None,
@@ -755,82 +797,89 @@ def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None
     [B, H, length, D] of ``dtype`` (bf16 or fp16; the cache's own when it is 16-bit); rows past a
     sequence's end are zeros.  ``out``: an optional pair of views to write.  See fa_cache_read."""
     import torch
-    device = k_cache.device
+    index = _cuda_index("k_cache", k_cache)
     if dtype is None:
         dtype = out[0].dtype if out is not None else k_cache.dtype
-    kind, num_pages, H, D, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, device)
+    kind, num_pages, H, D, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index)
     B = seq_lens.shape[0]
-    max_pages = _tables(block_tables, seq_lens, B, device)
+    max_pages = _tables(block_tables, seq_lens, B, index)
+    shape = (B, H, length, D)
     if out is None:
-        out = tuple(torch.empty((B, H, length, D), device=device, dtype=dtype) for _ in range(2))
+        out = (torch.empty(shape, device=k_cache.device, dtype=dtype),
+               torch.empty(shape, device=k_cache.device, dtype=dtype))
     k, v = out
     dt = _dtype_code(k)
-    if k.dtype != dtype or v.dtype != dtype:
+    if k.dtype is not dtype or v.dtype is not dtype:
         raise TypeError("out must have the call's dtype")
-    st = [_view_strides(k, "out[0]", (B, H, length, D)), _view_strides(v, "out[1]", k.shape)]
-    _on_device("out[0]", k, device)
-    _on_device("out[1]", v, device)
-    with _current(device):
-        status = fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
-                               block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(),
-                               v.data_ptr(), st, B, H, length, D, num_pages, max_pages, dt, kind,
-                               _stream_handle(device))
-    if status != FA_OK:
-        raise FaError("fa_cache_read", status)
+    ks, vs = _row_strides("out[0]", k, shape), _row_strides("out[1]", v, shape)
+    _same_device("out[0]", k, index)
+    _same_device("out[1]", v, index)
+    _launch("fa_cache_read", index, k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
+            block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(),
+            (ctypes.c_int64 * 6)(*ks, *vs), B, H, length, D, num_pages, max_pages, dt, kind)
     return k, v
 
 
+# ---------------------------------------------------------------------------------------
+# Decode with grouped heads, and with a shared prefix
+# ---------------------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def _decode_need(B, Hq, Hk, D, max_pages):
+    return fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages)
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_need(B, Hq, Hk, D, prefix_len, max_pages):
+    return fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages)
+
+
 def _decode_outputs(q, out, lse):
-    """Checked (B, Hq, D, dtype code, o, lse) of a decode step."""
+    """Checked (device index, B, Hq, D, dtype code, o, lse) of a decode step."""
     import torch
-    if not q.is_cuda or q.dim() != 3 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous [B, H, D] CUDA tensor")
-    B, Hq, D = q.shape
+    index = _cuda_index("q", q)
+    shape = q.shape
+    if len(shape) != 3 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B, H, D] tensor")
     dt = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor like q")
+    else:
+        if out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor like q")
+        _same_device("out", out, index)
     if lse is None:
-        lse = torch.empty((B, Hq), device=q.device, dtype=torch.float32)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 [B, H] tensor")
-    _on_device("out", out, q.device)
-    _on_device("lse", lse, q.device)
-    return B, Hq, D, dt, out, lse
+        lse = torch.empty(shape[:2], device=q.device, dtype=torch.float32)
+    else:
+        if lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 [B, H] tensor")
+        _same_device("lse", lse, index)
+    return index, *shape, dt, out, lse
 
 
-def _workspace(workspace, need, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one where any is needed; the tensor
-    itself keeps it alive until the call has been enqueued."""
+def _workspace(workspace, need, q, index):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one where any is needed; the
+    tensor keeps it alive until the call has been enqueued."""
     import torch
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty(need, device=device, dtype=torch.uint8)
-    _on_device("workspace", workspace, device)
+        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+    else:
+        _same_device("workspace", workspace, index)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace, k_exp,
                      v_exp):
-    B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
-    device = q.device
-    kind, num_pages, Hk, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, q.dtype, device)
+    index, B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
+    kind, num_pages, Hk, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, q.dtype, index)
     if Dc != D:
         raise ValueError(f"the cache has heads of {Dc}, q of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, device)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _current(device):
-        need = fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages)
-        wp, wb, keep = _workspace(workspace, need, device)
-        status = fa_decode_paged_ex(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
-                                    block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-                                    l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
-                                    float(scale), dt, kind, _stream_handle(device))
-    if status != FA_OK:
-        raise FaError("fa_decode_paged_ex", status)
+    max_pages = _tables(block_tables, seq_lens, B, index)
+    wp, wb, keep = _workspace(workspace, _decode_need(B, Hq, Hk, D, max_pages), q, index)
+    _launch("fa_decode_paged_ex", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kep,
+            vep, block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), l.data_ptr(), wp, wb, B,
+            Hq, Hk, D, num_pages, max_pages, 1.0 / math.sqrt(D) if scale is None else float(scale), dt, kind)
     return o, l
 
 
@@ -843,29 +892,22 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, blo
     once for the whole batch.  Returns O [B, Hq, D] and LSE [B, Hq] (fp32).  See
     fa_decode_shared_prefix in fa.h."""
     import torch
-    B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
-    device = q.device
-    _, num_pages, Hk, Dc, _, _ = _paged_cache(k_cache, v_cache, None, None, q.dtype, device)
+    index, B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
+    _, num_pages, Hk, Dc, _, _ = _paged_cache(k_cache, v_cache, None, None, q.dtype, index)
     if Dc != D:
         raise ValueError(f"the cache has heads of {Dc}, q of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, device)
-    if prefix_table.dtype != torch.int32 or prefix_table.dim() != 1 or not prefix_table.is_contiguous():
+    max_pages = _tables(block_tables, seq_lens, B, index)
+    if prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or \
+            not prefix_table.is_contiguous():
         raise TypeError("prefix_table must be a contiguous one-dimensional int32 tensor")
-    _on_device("prefix_table", prefix_table, device)
+    _same_device("prefix_table", prefix_table, index)
     prefix_len = int(prefix_len)
     if prefix_len < 0 or prefix_len > FA_PAGE_TOKENS * prefix_table.shape[0]:
         raise ValueError(f"prefix_table has room for {FA_PAGE_TOKENS * prefix_table.shape[0]} tokens, "
                          f"not {prefix_len}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    with _current(device):
-        need = fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages)
-        wp, wb, keep = _workspace(workspace, need, device)
-        status = fa_decode_shared_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                                         prefix_table.data_ptr(), prefix_len,
-                                         block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-                                         l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
-                                         float(scale), dt, _stream_handle(device))
-    if status != FA_OK:
-        raise FaError("fa_decode_shared_prefix", status)
+    wp, wb, keep = _workspace(workspace, _prefix_need(B, Hq, Hk, D, prefix_len, max_pages), q, index)
+    _launch("fa_decode_shared_prefix", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            prefix_table.data_ptr(), prefix_len, block_tables.data_ptr(), seq_lens.data_ptr(),
+            o.data_ptr(), l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
+            1.0 / math.sqrt(D) if scale is None else float(scale), dt)
     return o, l

@@ -14,9 +14,15 @@
 // The keys are its 16 rows: S^T = K Q^T (16 keys = one page, 8 queries) and O^T += V^T P^T.  At
 // the rate HBM delivers the tensor pipe is under a fifth busy.
 //
-// A CTA is one (sequence, cache head, block of 8 or 16 queries, split of the pages); its four warps
-// take pages in turn, each with its own ring of page slots filled by TMA (one lane issues, an
-// mbarrier per slot), so that no warp waits for another before the end.  Operand layouts, with
+// Work split.  A unit is one (sequence, cache head, block of 8 or 16 queries); its pages, unit
+// after unit, form one line of P pages, of which every warp takes an equal stretch: whatever the
+// sequences' lengths, all warps finish together, and no grid of splits has to be chosen.  P is known
+// on the device only, so each CTA first sums the sequences' pages (a scan over seq_lens in
+// shared memory).  A warp is a worker of its own: it has a ring of page slots filled by TMA
+// (one lane issues, an mbarrier per slot) that runs on from unit to unit; 32 lanes look 32 pages'
+// addresses up at once.  A unit that lies whole in one warp's stretch is written as O and LSE; of
+// a cut one each warp leaves a part (at most two a warp: one that began before it, one that
+// ends behind it), and fa_merge_kernel joins them.  Operand layouts, with
 // lane = 4 g + t as the mma defines them:
 //  * K, A operand (rows g, g+8 = keys): the contraction runs over D in any order that Q follows,
 //    so a lane reads whole 16-byte units of its two rows, units 2t and 2t+1 of each 128-byte row;
@@ -33,6 +39,10 @@
 // a_j = 2^(y_j + ev_j - mo) with the value row's exponent ev_j, so that a weight times its row's
 // scale neither overflows nor is lost in fp16, whatever the rows' magnitudes.  P is rounded to the
 // cache's 16-bit type (fp16 for e4m3: 2^-12), as in the prefill kernels; sums stay fp32.
+#include <atomic>
+#include <cstdlib>
+#include <type_traits>
+
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -43,6 +53,57 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;  // log2 headroom of the references
 constexpr int kWarps = 4;
+constexpr int kGqaSms = 152;     // the grid is sized for this many SMs on any device, so that the
+                                 // workspace does not depend on it
+constexpr int kGqaMinPages = 4;  // pages of a warp's stretch at least (where there are so many)
+
+// The split of the line of `total` pages.  One round: `workers` warps take equal stretches.  Not
+// all SMs get the same share of the memory's bandwidth, so equal stretches end up to 15% apart;
+// with three rounds the line's first 52/64 are dealt out like that, the next 8/64 and the last 4/64
+// again in stretches so much shorter, to CTAs that start as earlier ones end (735 -> 641 us for 256
+// sequences of 1..4096 tokens, 32 heads of 128, e4m3).  Short stretches cut long units into many
+// parts (142 -> 158 us for 48 sequences of up to 16384 tokens with groups of 8), so three rounds
+// need at least two units per warp.
+struct GqaSplit {
+    long long at[4];  // round r has the pages [at[r], at[r + 1])
+    int workers, rounds;
+    __device__ __forceinline__ long long start(int r, int i) const {
+        return at[r] + (at[r + 1] - at[r]) * i / workers;
+    }
+    __device__ __forceinline__ int worker_of(long long x) const {  // the one that has page x
+        int r = 0;
+        while (r + 1 < rounds && x >= at[r + 1]) ++r;
+        return r * workers + (int)(((x - at[r] + 1) * workers - 1) / (at[r + 1] - at[r]));
+    }
+};
+// No warp has under kGqaMinPages pages, and a unit is cut into no more than 128 parts on average.
+__device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int rounds, int units) {
+    const long long a = total / kGqaMinPages, b = 128LL * units;
+    const long long m = a < b ? a : b;
+    GqaSplit s;
+    s.workers = m < 1 ? 1 : m < warps ? (int)m : warps;
+    s.rounds = total >= 16LL * s.workers ? rounds : 1;
+    s.at[0] = 0;
+    s.at[1] = s.rounds > 1 ? total / 64 * 52 : total;
+    s.at[2] = s.rounds > 1 ? total / 64 * 60 : total;
+    s.at[3] = total;
+    return s;
+}
+
+// cudaFuncSetAttribute once per kernel and device (the calls below repeat every few microseconds).
+template <int D, bool Q8, bool BF16, int NT>
+struct kGqaKernelId {};
+template <typename Id, typename K>
+cudaError_t allow_shared(K kern, int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
+    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (r == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
+    return r;
+}
 
 // Q8: an e4m3 cache.
 template <int D, bool Q8>
@@ -53,16 +114,28 @@ struct GqaCfg {
     static constexpr int kPageBytes = kBoxes * kBoxBytes;
     static constexpr int kSteps = D / 16;   // contraction steps of S^T
     static constexpr int kTiles = D / 16;   // 16-element row tiles of O^T
-    // Page slots per warp: about 48-64 KB per CTA.
-    static constexpr int kStages = Q8 ? (D == 128 ? 4 : 6) : (D == 128 ? 3 : 4);
-    static int smem_bytes(int stages) {
-        return kWarps * stages * (2 * kPageBytes + (Q8 ? 32 : 0)) + 1024;
-    }
+    // Page slots per warp.  Small rings and more CTAs per SM win: the serving batch of 256
+    // sequences of 1..4096 tokens, 32 heads of 128, e4m3, takes 646 us with 3 slots, 653 with 2,
+    // 726 with 4 (fewer CTAs fit), 926 with 6.
+    static constexpr int kStages = Q8 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
+    static constexpr int kRingBytes = kWarps * kStages * (2 * kPageBytes + (Q8 ? 32 : 0));
 };
+// CTAs per SM that fit (registers and shared memory); the grid is that many times 152 SMs.
+constexpr int gqa_occupancy(int D, bool q8, int nt) { return nt == 2 || (D == 128 && !q8) ? 3 : 4; }
 
+// A page's rows of one head; the line goes out of L2 first (each is read once).
 __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                              int page_head) {
-    tma_load_3d(dst, map, bar, x, 0, page_head);
+                                              int page_head, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(page_head), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t policy_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 
 template <bool BF16>
@@ -108,159 +181,225 @@ __device__ __forceinline__ float raise(float& ref, float top) {
     return f;
 }
 
+// Pages of one warp, 32 at a time: lane i knows the i-th.
+struct Batch {
+    int page_head;  // page * Hk + head in the cache
+    int b, unit;    // sequence, and (cache head, query block) in it
+    int flags;      // tokens that count (1..16) | first page of its unit << 8 | last << 9
+};
+constexpr int kFirst = 1 << 8, kLast = 1 << 9;
+
 // BF16: the type of q and o (and of a 16-bit cache).  NT: blocks of 8 queries.
 template <int D, bool Q8, bool BF16, int NT>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     fa_decode_gqa_kernel(const __grid_constant__ GqaParams p) {
     using C = GqaCfg<D, Q8>;
     constexpr bool kMmaBf16 = BF16 && !Q8;  // e4m3 values are exact in fp16
+    constexpr int stages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    __shared__ uint64_t bar_full[kWarps][16];
-    __shared__ float red_m[kWarps][NT * 8], red_mo[kWarps][NT * 8], red_l[kWarps][NT * 8];
+    __shared__ uint64_t bar_full[kWarps][stages];
+    __shared__ int warp_sum[kWarps];
+    int* cum = reinterpret_cast<int*>(smem + C::kRingBytes);  // [B + 1] pages before sequence b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x, b = blockIdx.z;
-    const int hk = (int)blockIdx.y / p.q_blocks, qb = (int)blockIdx.y - hk * p.q_blocks;
-    const int q0 = qb * (NT * 8);                    // first query of this block in the group
-    const int n_q = min(NT * 8, p.group - q0);       // queries of this block
-    const size_t row0 = (size_t)b * p.Hq + (size_t)hk * p.group + q0;
-    const int stages = p.stages;
 
     pdl_launch_dependents();
-    int n = p.seq_lens[b];
-    if (n < 0 || n > (long long)p.max_pages * kPageTokens || (n > 0 && p.num_pages == 0)) {
-        if (threadIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
-        n = 0;
-    }
-    const int n_pages = (n + kPageTokens - 1) / kPageTokens;
-    const int pg0 = split * p.pages_per_split;
-    const int pg1 = min(n_pages, pg0 + p.pages_per_split);
-    if (pg0 >= pg1) {  // no key in this split
-        if (threadIdx.x < n_q) {
-            if (p.part_o)
-                p.part_lse[(row0 + threadIdx.x) * p.parts + p.part0 + split] = -INFINITY;
-            else
-                p.lse[row0 + threadIdx.x] = -INFINITY;
-        }
-        if (!p.part_o)
-            for (int i = threadIdx.x; i < n_q * D / 2; i += kWarps * 32)
-                reinterpret_cast<uint32_t*>(p.o)[row0 * D / 2 + i] = 0u;
-        pdl_wait();
-        return;
-    }
-
+    // The queries into L2 (they are read when a warp begins a unit, behind the stream of pages).
+    for (size_t at = ((size_t)blockIdx.x * (kWarps * 32) + threadIdx.x) * 128;
+         at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.q) + at));
     if (lane < stages) mbar_init(&bar_full[warp][lane], 1);
     mbar_fence_init();
-    __syncwarp();
+    // ---- pages before each sequence: every thread sums a run of sequences ----
+    const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32);
+    const int s0 = min((int)threadIdx.x * run, p.B), s1 = min(s0 + run, p.B);
+    auto pages_of = [&](int b) {
+        const int n = p.seq_lens[b];
+        if (n < 0 || n > (long long)p.max_pages * kPageTokens || (n > 0 && p.num_pages == 0)) {
+            if (blockIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
+            return 0;  // counts as empty
+        }
+        return (n + kPageTokens - 1) / kPageTokens;
+    };
+    int sum = 0;
+    for (int b = s0; b < s1; ++b) sum += pages_of(b);
+    int scan = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int before = scan - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    for (int b = s0; b < s1; ++b) {
+        cum[b] = before;
+        before += pages_of(b);
+    }
+    if (threadIdx.x == kWarps * 32 - 1) cum[p.B] = before;
+    __syncthreads();
+    const int per_seq = p.Hk * p.q_blocks;  // units of a sequence
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (cum[b] == cum[b + 1])
+            for (int i = threadIdx.x; i < per_seq; i += kWarps * 32)
+                p.unit_parts[(size_t)b * per_seq + i] = make_int2(0, 0);  // no key, no part
+    const long long total = (long long)cum[p.B] * per_seq;
+    const GqaSplit split = gqa_split(total, p.warps, p.rounds, p.B * per_seq);
+    const int ctas = p.warps / kWarps;  // of a round
+    const int r = (int)blockIdx.x / ctas;
+    const int wi = warp * ctas + (int)blockIdx.x - r * ctas;  // neighbours on different SMs
+    const bool works = r < split.rounds && wi < split.workers;
+    const int w = r * split.workers + wi;
+    const long long x0 = works ? split.start(r, wi) : 0;
+    const int mine = works ? (int)(split.start(r, wi + 1) - x0) : 0;
 
-    // This warp's pages: pg0 + warp, + 4, ...; the ring runs `stages` pages ahead.
-    const int mine = (pg1 - pg0 - warp + kWarps - 1) / kWarps;  // pages of this warp (may be 0)
     uint8_t* ring = smem + (size_t)warp * stages * (2 * C::kPageBytes);
     uint8_t* exps = smem + (size_t)kWarps * stages * (2 * C::kPageBytes) + warp * stages * 32;
-    const int* table = p.block_tables + (size_t)b * p.max_pages + pg0 + warp;
-    auto entry = [&](int i) { return i < mine ? table[(size_t)i * kWarps] : 0; };
-    int cur = entry(lane), nxt = entry(32 + lane);  // table entries of the next 32 + 32 pages
+    auto lookup = [&](int first) {  // pages first .. first + 31 of this warp
+        Batch r = {0, 0, 0, 0};
+        if (first + lane < mine) {
+            const long long x = x0 + first + lane;
+            const int at = (int)(x / per_seq);
+            int lo = 0, hi = p.B;  // the sequence with cum[b] <= at < cum[b + 1]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cum[mid] <= at) lo = mid;
+                else hi = mid;
+            }
+            const int n_pages = cum[lo + 1] - cum[lo];
+            const long long rest = x - (long long)cum[lo] * per_seq;
+            r.b = lo;
+            r.unit = (int)(rest / n_pages);
+            const int pg = (int)(rest - (long long)r.unit * n_pages);
+            int page = p.block_tables[(size_t)lo * p.max_pages + pg];
+            if (page < 0 || page >= p.num_pages) {
+                // Reported; page 0 is read instead: nothing outside the cache is touched.
+                atomicCAS(p.status, 0, (int)kDevBadArg);
+                page = 0;
+            }
+            r.page_head = page * p.Hk + r.unit / p.q_blocks;
+            r.flags = min(p.seq_lens[lo] - pg * kPageTokens, kPageTokens) | (pg == 0 ? kFirst : 0) |
+                      (pg == n_pages - 1 ? kLast : 0);
+        }
+        return r;
+    };
+    const uint64_t policy = policy_evict_first();
+    Batch prod = lookup(0), cons = prod, next = lookup(32);
     auto issue = [&](int i) {  // page i of this warp into slot i % stages; the whole warp calls it
         if (i > 0 && (i & 31) == 0) {
-            cur = nxt;
-            nxt = entry(i + 32 + lane);
+            prod = next;
+            next = lookup(i + 32);
         }
-        int phys = __shfl_sync(0xffffffffu, cur, i & 31);
+        const int ph = __shfl_sync(0xffffffffu, prod.page_head, i & 31);
         if (lane == 0) {
-            const bool bad = phys < 0 || phys >= p.num_pages;
-            if (bad) {  // report it and read page 0 instead: nothing outside the cache is touched
-                atomicCAS(p.status, 0, (int)kDevBadArg);
-                phys = 0;
-            }
             const int st = i % stages;
             uint64_t* bar = &bar_full[warp][st];
             uint8_t* dst = ring + st * (2 * C::kPageBytes);
-            const int ph = phys * p.Hk + hk;
             mbar_arrive_expect_tx(bar, 2 * C::kPageBytes + (Q8 ? 32 : 0));
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
-                tma_load_page(dst + x * C::kBoxBytes, &p.tm_k, bar, x * 64, ph);
+                tma_load_page(dst + x * C::kBoxBytes, &p.tm_k, bar, x * 64, ph, policy);
             if constexpr (Q8) {
                 bulk_load(exps + st * 32, p.k_exp + (size_t)ph * kPageTokens, 16, bar);
                 bulk_load(exps + st * 32 + 16, p.v_exp + (size_t)ph * kPageTokens, 16, bar);
             }
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x)
-                tma_load_page(dst + C::kPageBytes + x * C::kBoxBytes, &p.tm_v, bar, x * 64, ph);
+                tma_load_page(dst + C::kPageBytes + x * C::kBoxBytes, &p.tm_v, bar, x * 64, ph, policy);
         }
     };
-    const int ahead = min(stages, mine);
-    for (int i = 0; i < ahead; ++i) issue(i);
+    for (int i = 0; i < min(stages, mine); ++i) issue(i);
 
     // Q fragments (B operand).  Step s of lane t covers elements elem(s) .. + 3: the order in
     // which the K rows are read below.
     uint32_t qf[C::kSteps][NT][2];
     float q_factor[NT][2];  // factor of S^T's columns 2t, 2t+1: scale * log2(e), and for e4m3 the
                             // power of two that brought the query row into fp16's range
+    auto load_q = [&](size_t row0, int n_q) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int qi = nt * 8 + g;
-        const uint8_t* src = static_cast<const uint8_t*>(p.q) + (row0 + qi) * D * 2;
-        uint32_t w[C::kSteps][2];
+        for (int nt = 0; nt < NT; ++nt) {
+            const int qi = nt * 8 + g;
+            const uint8_t* src = static_cast<const uint8_t*>(p.q) + (row0 + qi) * D * 2;
+            uint32_t w[C::kSteps][2];
 #pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) {
-            const int e = Q8 ? (D / 4) * t + 4 * s : 64 * (s >> 2) + 16 * t + 4 * (s & 3);
-            uint2 u = make_uint2(0u, 0u);
-            if (qi < n_q) u = *reinterpret_cast<const uint2*>(src + e * 2);
-            w[s][0] = u.x;
-            w[s][1] = u.y;
+            for (int s = 0; s < C::kSteps; ++s) {
+                const int e = Q8 ? (D / 4) * t + 4 * s : 64 * (s >> 2) + 16 * t + 4 * (s & 3);
+                uint2 u = make_uint2(0u, 0u);
+                if (qi < n_q) u = *reinterpret_cast<const uint2*>(src + e * 2);
+                w[s][0] = u.x;
+                w[s][1] = u.y;
+            }
+            float f = 1.0f;  // the row's power of two
+            if constexpr (Q8 && BF16) {
+                uint32_t mx = 0;
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mx = max(mx, max((w[s][j] << 16) & 0x7fff0000u, w[s][j] & 0x7fff0000u));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                // Largest magnitude to [2^14, 2^15); 2^100 at most (rows below 2^-86 lose nothing
+                // that a score could show).
+                const int ex = (int)(mx >> 23) - 127;
+                if (mx != 0 && mx < 0x7f800000u) f = __uint_as_float((uint32_t)(127 + min(14 - ex, 100)) << 23);
+#pragma unroll
+                for (int s = 0; s < C::kSteps; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float2 v = unpack2<true>(w[s][j]);
+                        w[s][j] = pack2<false>(v.x * f, v.y * f);
+                    }
+            }
+#pragma unroll
+            for (int s = 0; s < C::kSteps; ++s) {
+                qf[s][nt][0] = w[s][0];
+                qf[s][nt][1] = w[s][1];
+            }
+            const float back = p.scale_log2 / f;
+            q_factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);      // lane of g = 2t
+            q_factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);  // lane of g = 2t + 1
         }
-        float f = 1.0f;  // the row's power of two
-        if constexpr (Q8 && BF16) {
-            uint32_t mx = 0;
-#pragma unroll
-            for (int s = 0; s < C::kSteps; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    mx = max(mx, max((w[s][j] << 16) & 0x7fff0000u, w[s][j] & 0x7fff0000u));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // Largest magnitude to [2^14, 2^15); 2^100 at most (rows below 2^-86 lose nothing
-            // that a score could show).
-            const int ex = (int)(mx >> 23) - 127;
-            if (mx != 0 && mx < 0x7f800000u) f = __uint_as_float((uint32_t)(127 + min(14 - ex, 100)) << 23);
-#pragma unroll
-            for (int s = 0; s < C::kSteps; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 v = unpack2<true>(w[s][j]);
-                    w[s][j] = pack2<false>(v.x * f, v.y * f);
-                }
-        }
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) {
-            qf[s][nt][0] = w[s][0];
-            qf[s][nt][1] = w[s][1];
-        }
-        const float back = p.scale_log2 / f;
-        q_factor[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);      // lane of g = 2t
-        q_factor[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);  // lane of g = 2t + 1
-    }
+    };
 
     float acc[C::kTiles][NT][4];
     float m[NT][2], mo[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            m[nt][j] = mo[nt][j] = -INFINITY;
-            l[nt][j] = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < C::kTiles; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
-    }
-
+    size_t row0 = 0;       // first query row of the unit
+    int n_q = 0;           // queries of its block
+    bool cut = false;      // the unit began in an earlier warp's stretch
     bool ok = true;
     int done = 0;
     for (; done < mine; ++done) {
+        if (done > 0 && (done & 31) == 0) cons = prod;  // (the ring is less than a batch ahead)
+        const int flags = __shfl_sync(0xffffffffu, cons.flags, done & 31);
+        if (done == 0 || (flags & kFirst)) {  // a new unit
+            const int b = __shfl_sync(0xffffffffu, cons.b, done & 31);
+            const int unit = __shfl_sync(0xffffffffu, cons.unit, done & 31);
+            const int hk = unit / p.q_blocks, q0 = (unit - hk * p.q_blocks) * (NT * 8);
+            n_q = min(NT * 8, p.group - q0);
+            row0 = (size_t)b * p.Hq + (size_t)hk * p.group + q0;
+            cut = !(flags & kFirst);
+            load_q(row0, n_q);
+            if (!cut && lane == 0) {  // for the merge: the warps that have the unit's pages
+                const long long last = x0 + done + (cum[b + 1] - cum[b]) - 1;
+                const int n = done + (cum[b + 1] - cum[b]) <= mine ? 1 : split.worker_of(last) - w + 1;
+                p.unit_parts[(size_t)b * per_seq + unit] = make_int2(w, n);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    m[nt][j] = mo[nt][j] = -INFINITY;
+                    l[nt][j] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < C::kTiles; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
+            }
+        }
         const int st = done % stages;
         ok = wait_warp(&bar_full[warp][st], (uint32_t)(done / stages) & 1u, nullptr, p.timeout_ns);
         if (!ok) break;
@@ -316,7 +455,7 @@ __global__ void __launch_bounds__(kWarps * 32)
             }
         }
         // ---- online softmax over the page ----
-        const int left = n - (pg0 + warp + done * kWarps) * kPageTokens;  // tokens from this page on
+        const int left = flags & 31;  // tokens of this page
         const bool partial = left < kPageTokens;
         float fk[2] = {1.0f, 1.0f}, ev[2] = {0.0f, 0.0f};  // rows g, g + 8
         if constexpr (Q8) {
@@ -448,6 +587,69 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
         __syncwarp();  // every lane has read the slot
         if (done + stages < mine) issue(done + stages);
+        const bool ends = (flags & kLast) != 0;
+        if (!ends && done + 1 < mine) continue;
+        // ---- the unit, or this warp's part of it, is done ----
+        // Lane (g, t) holds, for queries 2t and 2t+1, whole runs of elements: e4m3 D/8 from
+        // D/8 g on, 16-bit 8 from 64 x + 8 g on for each box x.
+        const bool whole = !cut && ends && !p.parts_only;
+        float* part_o = nullptr;
+        float* part_lse = nullptr;
+        if (!whole) {
+            const size_t slot = (cut || !ends) ? 2 * (size_t)w + (cut ? 0 : 1) : 0;
+            if (!cut && ends) {  // a whole unit of a row that has other parts
+                part_o = p.full_o + row0 * D;
+                part_lse = p.full_lse + row0;
+            } else {
+                part_o = p.slot_o + slot * p.slot_rows * D;
+                part_lse = p.slot_lse + slot * p.slot_rows;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float L = column_sum(l[nt][j]);
+                const int qi = nt * 8 + 2 * t + j;
+                if (qi >= n_q) continue;
+                // (L = 0: every score is -inf, as if the row saw no key.)  The two references'
+                // distance is taken in two steps: 2^(mo - m) alone may be below fp32's range.
+                const float f = L == 0.0f ? 0.0f : 1.0f / L;
+                const float hop = (!Q8 || mo[nt][j] == -INFINITY || m[nt][j] == -INFINITY)
+                                      ? 1.0f
+                                      : ex2_approx(0.5f * (mo[nt][j] - m[nt][j]));
+                const float lse2 = m[nt][j] + log2f(L);
+                if (g == 0) {
+                    if (whole) p.lse[row0 + qi] = lse2 * kLn2;
+                    else part_lse[qi] = lse2;
+                }
+                constexpr int kRun = Q8 ? C::kTiles : 4;  // tiles of one run
+#pragma unroll
+                for (int x = 0; x < C::kTiles / kRun; ++x) {
+                    const int e = Q8 ? (D / 8) * g : 64 * x + 8 * g;
+                    float v[2 * kRun];
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i) {
+                        v[2 * i] = acc[x * kRun + i][nt][j] * f * hop * hop;
+                        v[2 * i + 1] = acc[x * kRun + i][nt][j + 2] * f * hop * hop;
+                    }
+                    if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (row0 + qi) * D + e);
+#pragma unroll
+                        for (int i = 0; i < kRun / 4; ++i)
+                            dst[i] = make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]),
+                                                pack2<BF16>(v[8 * i + 2], v[8 * i + 3]),
+                                                pack2<BF16>(v[8 * i + 4], v[8 * i + 5]),
+                                                pack2<BF16>(v[8 * i + 6], v[8 * i + 7]));
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(part_o + (size_t)qi * D + e);
+#pragma unroll
+                        for (int i = 0; i < kRun / 2; ++i)
+                            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+            }
+        }
     }
     if (!ok) {
         if (lane == 0) atomicCAS(p.status, 0, (int)kDevTimeout);
@@ -455,106 +657,115 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int i = done; i < min(mine, done + stages); ++i)
             wait_bounded(&bar_full[warp][i % stages], (uint32_t)(i / stages) & 1u, nullptr, p.timeout_ns);
     }
-
-    // ---- merge the four warps ----
-    // Lane (g, t) holds, for queries 2t and 2t+1, the elements e0 + 2i, e0 + 2i + 1 of tile i.
-    __syncthreads();  // every warp is done with its ring
-    float* red_o = reinterpret_cast<float*>(smem);  // [warp][query][D]
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float sum = column_sum(l[nt][j]);
-            const int qi = nt * 8 + 2 * t + j;
-            if (g == 0) {
-                red_m[warp][qi] = m[nt][j];
-                red_mo[warp][qi] = Q8 ? mo[nt][j] : m[nt][j];
-                red_l[warp][qi] = sum;
-            }
-            if (qi < n_q) {
-                float* dst = red_o + ((size_t)warp * (NT * 8) + qi) * D;
-#pragma unroll
-                for (int i = 0; i < C::kTiles; ++i) {
-                    const int e = Q8 ? (D / 8) * g + 2 * i : 64 * (i >> 2) + 8 * g + 2 * (i & 3);
-                    *reinterpret_cast<float2*>(dst + e) = make_float2(acc[i][nt][j], acc[i][nt][j + 2]);
-                }
-            }
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_q * (D / 2); i += kWarps * 32) {
-        const int qi = i / (D / 2), e = (i - qi * (D / 2)) * 2;
-        float M = -INFINITY, MO = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            M = fmaxf(M, red_m[w][qi]);
-            MO = fmaxf(MO, red_mo[w][qi]);
-        }
-        float L = 0.0f, x = 0.0f, y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            // A warp without pages (or whose scores are all -inf) has references of -inf.
-            const float fl = red_m[w][qi] == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2_approx(red_m[w][qi] - M);
-            const float fo = red_mo[w][qi] == -INFINITY ? (MO == -INFINITY ? 1.0f : 0.0f) : ex2_approx(red_mo[w][qi] - MO);
-            const float2 v = *reinterpret_cast<const float2*>(red_o + ((size_t)w * (NT * 8) + qi) * D + e);
-            L = fmaf(red_l[w][qi], fl, L);
-            x = fmaf(v.x, fo, x);
-            y = fmaf(v.y, fo, y);
-        }
-        // The two references' distance in two steps: 2^(MO - M) alone may be below fp32's range.
-        // (L = 0: every score is -inf, as if the row saw no key.)
-        const float f = L == 0.0f ? 0.0f : 1.0f / L;
-        const float hop = (!Q8 || MO == -INFINITY || M == -INFINITY) ? 1.0f : ex2_approx(0.5f * (MO - M));
-        x = x * f * hop * hop;
-        y = y * f * hop * hop;
-        const float lse2 = M + log2f(L);
-        const size_t row = row0 + qi;
-        if (p.part_o) {
-            const size_t part = row * p.parts + p.part0 + split;
-            *reinterpret_cast<float2*>(p.part_o + part * D + e) = make_float2(x, y);
-            if (e == 0) p.part_lse[part] = lse2;
-        } else {
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + row * D + e) = pack2<BF16>(x, y);
-            if (e == 0) p.lse[row] = lse2 * kLn2;
-        }
-    }
-    // Launched early behind a kernel that writes other parts of the same rows, this kernel ends
-    // only after that one, so that the merge waits for both by waiting for this one.
-    pdl_wait();
+    // Launched early behind a kernel that writes other parts of the same rows, this grid ends only
+    // after that one (one CTA waits; the others make room), so that the merge waits for both by
+    // waiting for this one.
+    if (blockIdx.x == 0) pdl_wait();
 }
 
-// Merges the parts of each query row: O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i), with
-// w_i = 2^(LSE2_i - max).  One warp per row; parts without a key (LSE = -inf) are not read.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_merge_parts_kernel(const MergeParams p) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int row = (int)blockIdx.x * 4 + (threadIdx.x >> 5);
+// Joins the parts of each query row: O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i), with
+// w_i = 2^(LSE2_i - max).  Parts 0 .. n_prefix-1 are a shared prefix's, then those that the warps of
+// fa_decode_gqa_kernel left of the row's unit (or the whole unit, in full_o).  WPR warps per row
+// take every WPR-th group of four parts and meet in shared memory.  A row that the decode kernel has
+// written itself is left alone; one without any key gets O = 0, LSE = -inf.
+template <int D, bool BF16, int WPR>
+__global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
+    constexpr int kPer = D / 32, kAhead = 8;  // parts whose loads are in flight together
+    using Vec = typename std::conditional<kPer == 4, float4, float2>::type;
+    __shared__ float red[WPR > 1 ? WPR : 1][D + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = WPR > 1 ? (int)blockIdx.x : (int)blockIdx.x * 8 + warp;
+    const int sub = WPR > 1 ? warp : 0;
     pdl_wait();
     if (row >= p.rows) return;
-    const float* lse2 = p.parts.lse2 + (size_t)row * p.parts.parts;
-    const float* o = p.parts.o + (size_t)row * p.parts.parts * D + lane * kPer;
-    float top = -INFINITY;
-    for (int i = lane; i < p.parts.parts; i += 32) top = fmaxf(top, lse2[i]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.0f, x[kPer];
+    const int b = row / p.Hq, h = row - b * p.Hq;
+    const int hk = h / p.group, gi = h - hk * p.group;
+    const int qb = gi / p.q_rows, qi = gi - qb * p.q_rows;
+    const int2 own = p.unit_parts[((size_t)b * p.Hk + hk) * p.q_blocks + qb];
+    const int w_first = own.x, n_own = own.y;
+    const int n_parts = p.n_prefix + n_own;
+    if (p.n_prefix == 0 && n_own == 1) return;  // written whole
+    const float* pre_o = p.prefix_o + (size_t)row * p.n_prefix * D;
+    const float* pre_lse = p.prefix_lse + (size_t)row * p.n_prefix;
+    auto locate = [&](int i, const float*& o, const float*& lse2) {
+        if (i < p.n_prefix) {
+            o = pre_o + (size_t)i * D;
+            lse2 = pre_lse + i;
+        } else if (n_own == 1) {
+            o = p.full_o + (size_t)row * D;
+            lse2 = p.full_lse + row;
+        } else {
+            const int k = i - p.n_prefix;
+            const size_t at = (2 * (size_t)(w_first + k) + (k == 0 ? 1 : 0)) * p.slot_rows + qi;
+            o = p.slot_o + at * D;
+            lse2 = p.slot_lse + at;
+        }
+    };
+    float top = -INFINITY, sum = 0.0f, x[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < p.parts.parts; ++i) {
-        const float y = lse2[i];
-        if (y == -INFINITY) continue;
-        const float w = ex2_approx(y - top);
-        sum += w;
+    for (int i0 = sub * kAhead; i0 < n_parts; i0 += WPR * kAhead) {
+        Vec v[kAhead];
+        float y[kAhead];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = fmaf(w, o[(size_t)i * D + e], x[e]);
+        for (int j = 0; j < kAhead; ++j) {
+            y[j] = -INFINITY;
+            if (i0 + j < n_parts) {
+                const float *o, *l2;
+                locate(i0 + j, o, l2);
+                y[j] = *l2;
+                v[j] = *reinterpret_cast<const Vec*>(o + lane * kPer);
+            }
+        }
+        float next = top;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) next = fmaxf(next, y[j]);
+        const float base = next == -INFINITY ? 0.0f : next;
+        const float f = ex2_approx(top - base);  // (0 at first: top = -inf)
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] *= f;
+        top = next;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (y[j] == -INFINITY) continue;  // no key: its values were not written
+            const float wj = ex2_approx(y[j] - base);
+            sum += wj;
+            const float* vf = reinterpret_cast<const float*>(&v[j]);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[e] = fmaf(wj, vf[e], x[e]);
+        }
     }
-    const bool any = top != -INFINITY || sum != 0.0f;  // (a NaN part has no maximum, but a sum)
+    if constexpr (WPR > 1) {
+        if (lane == 0) {
+            red[warp][D] = top;
+            red[warp][D + 1] = sum;
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) red[warp][lane * kPer + e] = x[e];
+        __syncthreads();
+        if (warp != 0) return;
+        float all = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < WPR; ++k) all = fmaxf(all, red[k][D]);
+        sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WPR; ++k) {
+            // (a warp without parts has a sum of 0; one with a NaN part keeps its NaN)
+            const float f = red[k][D] == -INFINITY ? 1.0f : ex2_approx(red[k][D] - all);
+            sum = fmaf(red[k][D + 1], f, sum);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[e] = fmaf(red[k][lane * kPer + e], f, x[e]);
+        }
+        top = all;
+    }
+    const bool any = sum != 0.0f;  // (true of a NaN)
     const float f = any ? 1.0f / sum : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * kPer);
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<BF16>(x[e] * f, x[e + 1] * f);
+    for (int e = 0; e < kPer; e += 2) dst[e / 2] = any ? pack2<BF16>(x[e] * f, x[e + 1] * f) : 0u;
     if (lane == 0) p.lse[row] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
@@ -562,14 +773,13 @@ template <int D, bool Q8, bool BF16, int NT>
 cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
     using C = GqaCfg<D, Q8>;
     auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT>;
-    GqaParams q = p;
-    q.stages = C::kStages;
-    const int smem = C::smem_bytes(q.stages);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = C::kRingBytes + 1024 + (kGqaMaxSequences + 1) * 4;
+    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT>>(kern, smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)p.splits, (unsigned)(p.Hk * p.q_blocks), (unsigned)p.B);
-    return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)smem, s, q)
-                   : launch_kernel(kern, grid, dim3(kWarps * 32), (size_t)smem, s, q);
+    const int here = C::kRingBytes + 1024 + (p.B + 1) * 4;
+    const dim3 grid((unsigned)(p.warps / kWarps * p.rounds));
+    return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)here, s, p)
+                   : launch_kernel(kern, grid, dim3(kWarps * 32), (size_t)here, s, p);
 }
 
 template <int D, bool Q8, bool BF16>
@@ -583,33 +793,43 @@ cudaError_t launch_d(const GqaParams& p, bool bf16, bool q8, cudaStream_t s) {
     return bf16 ? launch_n<D, false, true>(p, s) : launch_n<D, false, false>(p, s);
 }
 
+template <int D, bool BF16>
+cudaError_t launch_m(const MergeParams& p, cudaStream_t s) {
+    // Eight warps per row while a wave of CTAs holds the rows, else a warp per row.
+    if (p.rows <= 4 * kGqaSms)
+        return launch_kernel_early(fa_merge_kernel<D, BF16, 8>, dim3((unsigned)p.rows), dim3(256), 0, s, p);
+    return launch_kernel_early(fa_merge_kernel<D, BF16, 1>, dim3((unsigned)((p.rows + 7) / 8)), dim3(256), 0,
+                               s, p);
+}
+
 }  // namespace
 
-int gqa_q_blocks(int group) { return group <= 8 ? 1 : (group + 15) / 16; }
+int gqa_q_rows(int group) { return group <= 8 ? 8 : 16; }
 
-int gqa_splits(int B, int Hk, int group, int max_pages) {
-    // About four CTAs per SM of a 152-SM part (a fixed target, so that the workspace size does not
-    // depend on the device), each split at least 16 pages (four per warp).
-    const long long units = (long long)B * Hk * gqa_q_blocks(group);
-    const long long target = 4LL * 152;
-    if (units <= 0 || units >= target || max_pages <= 16) return 1;
-    long long splits = (target + units - 1) / units;
-    if (splits > (max_pages + 15) / 16) splits = (max_pages + 15) / 16;
-    const int per = (int)((max_pages + splits - 1) / splits);
-    return (max_pages + per - 1) / per;
+int gqa_warps(int B, int Hk, int group, int max_pages) {
+    const long long q_blocks = (group + gqa_q_rows(group) - 1) / gqa_q_rows(group);
+    const long long ctas = ((long long)B * Hk * q_blocks * max_pages + kWarps * kGqaMinPages - 1) /
+                           (kWarps * kGqaMinPages);
+    return kWarps * (int)(ctas < 1 ? 1 : ctas < 4 * kGqaSms ? ctas : 4 * kGqaSms);
+}
+
+int gqa_rounds(int B, int Hk, int group) {
+    const long long units = (long long)B * Hk * ((group + gqa_q_rows(group) - 1) / gqa_q_rows(group));
+    return units >= 2LL * 4 * kGqaSms * kWarps ? 3 : 1;
+}
+
+int gqa_launched_warps(int warps, int D, bool q8, int group) {
+    const int most = gqa_occupancy(D, q8, group <= 8 ? 1 : 2) * kGqaSms * kWarps;
+    return warps < most ? warps : most;
 }
 
 cudaError_t launch_decode_gqa(const GqaParams& p, int D, bool bf16, bool q8, cudaStream_t s) {
     return D == 64 ? launch_d<64>(p, bf16, q8, s) : launch_d<128>(p, bf16, q8, s);
 }
 
-cudaError_t launch_merge_parts(const MergeParams& p, int D, bool bf16, cudaStream_t s) {
-    const dim3 grid((unsigned)((p.rows + 3) / 4)), block(128);
-    if (D == 64)
-        return bf16 ? launch_kernel_early(fa_merge_parts_kernel<64, true>, grid, block, 0, s, p)
-                    : launch_kernel_early(fa_merge_parts_kernel<64, false>, grid, block, 0, s, p);
-    return bf16 ? launch_kernel_early(fa_merge_parts_kernel<128, true>, grid, block, 0, s, p)
-                : launch_kernel_early(fa_merge_parts_kernel<128, false>, grid, block, 0, s, p);
+cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s) {
+    if (D == 64) return bf16 ? launch_m<64, true>(p, s) : launch_m<64, false>(p, s);
+    return bf16 ? launch_m<128, true>(p, s) : launch_m<128, false>(p, s);
 }
 
 }  // namespace fa

@@ -182,32 +182,42 @@ struct CacheReadParams {
     int* status;
 };
 
-// Partial results of attention over parts of the keys, merged by fa_merge_parts_kernel: part i of
-// query row r is o[(r * parts + i) * D ..] (normalised, fp32) and lse2[r * parts + i] (log2
-// domain; -inf: the part holds no key and its o is not written).
-struct PartsRef {
-    const float* o;
-    const float* lse2;
-    int parts;
-};
+// One decode step with grouped heads over a paged cache (fa_decode_gqa.cu).  B is at most
+// kGqaMaxSequences (a longer batch takes several launches).
+constexpr int kGqaMaxSequences = 1024;
 
-// One decode step with grouped heads over a paged cache (fa_decode_paged_ex).
 struct GqaParams {
     CUtensorMap tm_k, tm_v;    // {D, 16, num_pages * Hk}: one box is a page's rows of one head
     const void* q;             // [B, Hq, D] 16-bit
     const uint8_t *k_exp, *v_exp;  // [num_pages, Hk, 16] (e4m3 caches)
     const int* block_tables;   // [B, max_pages]
     const int* seq_lens;       // [B]
-    void* o;                   // [B, Hq, D] 16-bit  (splits == 1 and no other parts)
+    void* o;                   // [B, Hq, D] 16-bit
     float* lse;                // [B, Hq] natural log
-    float* part_o;             // [B*Hq, parts, D] fp32, or null: o and lse are written
-    float* part_lse;           // [B*Hq, parts] log2 domain
-    int parts, part0;          // split i is part part0 + i of a row
+    int2* unit_parts;          // [B, units of a sequence] written: first warp with its pages, and how many
+    float* slot_o;             // [2 * warps * rounds, slot_rows, D] fp32: parts of units that are cut
+    float* slot_lse;           // [2 * warps * rounds, slot_rows] log2 domain
+    float *full_o, *full_lse;  // [B * Hq, D], [B * Hq]: whole units when parts_only
+    int rounds;                // of the split, 1 or 3
+    int slot_rows;             // rows of a slot: the group, at most 8 or (above 8) 16
+    int parts_only;            // rows have other parts (a shared prefix): o, lse are the merge's
     int early;                 // launched before the kernel in front of it has finished
-    int B, Hq, Hk, group, q_blocks, num_pages, max_pages, splits, pages_per_split, stages;
-    float scale_log2;
+    int warps;                 // of a round, a multiple of 4
+    int B, Hq, Hk, group, q_blocks, num_pages, max_pages;
+    float scale_log2;          // scale * log2(e), either sign
     int* status;
     uint64_t timeout_ns;
+};
+
+// Joins the parts of the rows of a decode step (fa_decode_gqa.cu).
+struct MergeParams {
+    const float *prefix_o, *prefix_lse;  // [rows, n_prefix, D], [rows, n_prefix]; LSE = -inf: absent
+    int n_prefix;
+    const float *slot_o, *slot_lse, *full_o, *full_lse;  // as in GqaParams
+    const int2* unit_parts;
+    void* o;     // [rows, D] 16-bit
+    float* lse;  // [rows] natural log
+    int rows, B, Hq, Hk, group, q_rows, q_blocks, slot_rows;
 };
 
 // Attention of all query rows of a batch to one shared prefix (fa_prefix.cu).  A work unit is one
@@ -219,9 +229,9 @@ struct PrefixParams {
     CUtensorMap tm_k, tm_v;    // {D, 16, num_pages * Hk}, box {64, 16, 1}
     CUtensorMap tm_k_tail, tm_v_tail;  // the same with the last page's rows only
     const int* table;          // [ceil(prefix_len / 16)]
-    float* part_o;             // [B*Hq, parts, D] fp32
-    float* part_lse;           // [B*Hq, parts] log2 domain
-    int parts, max_segments;   // parts 0 .. max_segments-1 of a row are the prefix's
+    float* part_o;             // [B*Hq, max_segments, D] fp32
+    float* part_lse;           // [B*Hq, max_segments] log2 domain
+    int max_segments;
     int prefix_len, num_pages;
     int B, Hq, Hk, group;
     int rows_b;                // sequences per query tile (group * rows_b <= 128 rows)
@@ -231,13 +241,6 @@ struct PrefixParams {
     uint32_t s_negate;
     int* status;
     uint64_t timeout_ns;
-};
-
-struct MergeParams {
-    PartsRef parts;
-    void* o;     // [rows, D] 16-bit
-    float* lse;  // [rows] natural log
-    int rows;
 };
 
 // Host-side helpers of the C-ABI layer shared with the other entry-point units.
@@ -308,10 +311,13 @@ cudaError_t launch_decode_gqa(const GqaParams& p, int D, bool bf16, bool q8, cud
 cudaError_t launch_prefix(const PrefixParams& p, int D, bool bf16, cudaStream_t s);
 // The work split of a shared prefix: fills rows_b, n_tiles, n_pairs, key_tiles, grid, max_segments.
 void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p);
-cudaError_t launch_merge_parts(const MergeParams& p, int D, bool bf16, cudaStream_t s);
-// Query blocks of 8 or 16 rows per cache head, and the splits of the page range.
-int gqa_q_blocks(int group);
-int gqa_splits(int B, int Hk, int group, int max_pages);
+cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s);
+// Query rows of a block (8 or 16), the most warps that a step may launch (workspace), and those it
+// does.
+int gqa_q_rows(int group);
+int gqa_warps(int B, int Hk, int group, int max_pages);
+int gqa_rounds(int B, int Hk, int group);
+int gqa_launched_warps(int warps, int D, bool q8, int group);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);
 

@@ -4,7 +4,7 @@
 // Attending to them once per sequence would read them B times; here every cache head's prefix
 // is read once and multiplied with the B * G query rows that use it:
 //     S = scale Q_h K_h^T  [B G, Lp],   part (O_i, LSE_i) of every row over the prefix's tokens,
-// which fa_merge_parts_kernel joins with the part over the sequence's own tokens.
+// which fa_merge_kernel joins with the part over the sequence's own tokens.
 //
 // 4 G B D FLOPs for 4 D bytes of a token and cache head: from B G of about 280 on the tensor cores are the
 // bound, below it HBM is.  tcgen05 kernel on the plan of fa_fwd.cu: two 128-row query tiles
@@ -42,7 +42,6 @@ struct PrefixCfg {
     static constexpr int kStageBytes = 32 * 32 * 4;     // read-out buffer of one softmax warp
     static constexpr int kOffStage = kOffV + kStages * kTileBytes;
     static constexpr int kSmemBytes = kOffStage + 8 * kStageBytes + 1024;
-    static constexpr int kSoftmaxWarps = 8;
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;
     static constexpr int kThreads = 11 * 32;
     static constexpr uint32_t kTmemCols = 512;
@@ -357,12 +356,12 @@ __global__ void __launch_bounds__(PrefixCfg<D, BF16>::kThreads, 1)
             const int b = (2 * sg.pair + t) * p.rows_b + bi;
             const bool valid = bi < p.rows_b && b < p.B;
             const size_t qrow = valid ? (size_t)b * p.Hq + (size_t)sg.hk * p.group + (row - bi * p.group) : 0;
-            const size_t part = qrow * p.parts + sg.part;
+            const size_t part = qrow * p.max_segments + sg.part;
             if (valid) {
                 p.part_lse[part] = l_sum != 0.0f ? m_ref + log2f(l_sum) : -INFINITY;
                 if (sg.last)  // parts that no CTA writes
                     for (int i = sg.part + 1; i < p.max_segments; ++i)
-                        p.part_lse[qrow * p.parts + i] = -INFINITY;
+                        p.part_lse[qrow * p.max_segments + i] = -INFINITY;
             }
             const float inv_l = l_sum != 0.0f ? 1.0f / l_sum : 0.0f;
             // 32 columns at a time through this warp's buffer: 4 rows of 128 bytes per store.
@@ -424,12 +423,14 @@ void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p) {
     p->n_pairs = (p->n_tiles + 1) / 2;
     p->key_tiles = (int)(((long long)prefix_len + kTileRows - 1) / kTileRows);
     const long long units = (long long)Hk * p->n_pairs * p->key_tiles;
-    p->grid = (int)(units < kGrid ? units : kGrid);
-    // CTAs that share one pair's key tiles: at most this many.
+    // One CTA per SM, each with four units at least (a part's read-out costs about as much).
+    const long long want = (units + 3) / 4;
+    p->grid = (int)(want < kGrid ? want : kGrid);
+    // CTAs that share one pair's key tiles: at most this many (a stretch begins every
+    // units / grid units).
     p->max_segments = 0;
     if (units > 0) {
-        const long long per = units / p->grid;  // units of the shortest stretch
-        const long long most = (p->key_tiles + per - 1) / per + 1;
+        const long long most = ((long long)p->key_tiles * p->grid + units - 1) / units + 1;
         p->max_segments = (int)(most < p->key_tiles ? most : p->key_tiles);
     }
 }

@@ -44,8 +44,10 @@ __device__ __forceinline__ int token_position(const RotaryLaunch& p, long long b
 }
 
 // 16-byte units.  Half pairs (rotary_dim a multiple of 16): unit u < rotary_dim/16 is the
-// elements 8u.. and their partners; interleaved (rotary_dim a multiple of 8): unit
-// u < rotary_dim/8 is the elements 8u...  The units after them are copied.
+// elements 8u.. and their partners rotary_dim/2 further, a unit after them 16 elements to copy.
+// Interleaved (rotary_dim a multiple of 8): unit u is the elements 8u.., copied from
+// u = rotary_dim/8 on.  Turned and copied units take the same path (the copy returns what it
+// loaded), since both lie in one warp.
 template <bool BF16, bool INTER>
 __global__ void __launch_bounds__(kThreads) fa_rotary_kernel(const RotaryLaunch p, int units,
                                                              int heads_per_block) {
@@ -61,65 +63,68 @@ __global__ void __launch_bounds__(kThreads) fa_rotary_kernel(const RotaryLaunch 
     const int heads = p.op[0].H + p.op[1].H;
     const int h0 = (int)blockIdx.y * heads_per_block;
     const int h1 = min(heads, h0 + heads_per_block);
-    auto locate = [&](int h, const uint8_t*& src, uint8_t*& dst) {
+    const bool turn = u < n_rot;
+    // Byte offsets of the unit and, for half pairs, of its second 16 bytes.
+    const int lo = (INTER || turn) ? u * 16 : rd * 2 + (u - n_rot) * 32;
+    const int hi = turn ? lo + rd : lo + 16;
+    auto source = [&](int h) {
         const RotaryOperand& o = p.op[h < p.op[0].H ? 0 : 1];
         const int hh = h < p.op[0].H ? h : h - p.op[0].H;
-        src = static_cast<const uint8_t*>(o.x) + 2 * (b * o.sx.b + hh * o.sx.h + l * o.sx.l);
-        dst = static_cast<uint8_t*>(o.y) + 2 * (b * o.sy.b + hh * o.sy.h + l * o.sy.l);
+        return static_cast<const uint8_t*>(o.x) + 2 * (b * o.sx.b + hh * o.sx.h + l * o.sx.l);
     };
-    if (u >= n_rot) {  // an element past rotary_dim: copied
-        const int off = (rd / 8 + u - n_rot) * 16;
-        for (int h = h0; h < h1; ++h) {
-            const uint8_t* src;
-            uint8_t* dst;
-            locate(h, src, dst);
-            *reinterpret_cast<uint4*>(dst + off) = *reinterpret_cast<const uint4*>(src + off);
-        }
-        return;
-    }
-    constexpr int kPairs = INTER ? 4 : 8;
-    float c[kPairs], s[kPairs];
-    const int pos = token_position(p, b, l);
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-        rope_cos_sin(pos, p.rot.freqs[u * kPairs + i], p.rot.mscale, c[i], s[i]);
-        if (p.inverse) s[i] = -s[i];
-    }
-    const int lo = u * 16, hi = lo + rd;  // byte offsets of the unit and its partner (rd/2 elements)
-    for (int h = h0; h < h1; h += kUnroll) {
-        uint4 xa[kUnroll], xb[kUnroll];
-        uint8_t* dst[kUnroll];
+    uint4 xa[kUnroll], xb[kUnroll];
+    auto load = [&](int h) {
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             if (h + j >= h1) break;
-            const uint8_t* src;
-            locate(h + j, src, dst[j]);
+            const uint8_t* src = source(h + j);
             xa[j] = *reinterpret_cast<const uint4*>(src + lo);
             if (!INTER) xb[j] = *reinterpret_cast<const uint4*>(src + hi);
         }
+    };
+    load(h0);  // in flight while the angles are computed
+    constexpr int kPairs = INTER ? 4 : 8;
+    float c[kPairs], s[kPairs];
+    if (turn) {
+        const int pos = token_position(p, b, l);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            rope_cos_sin(pos, p.rot.freqs[u * kPairs + i], p.rot.mscale, c[i], s[i]);
+            if (p.inverse) s[i] = -s[i];
+        }
+    }
+    for (int h = h0; h < h1; h += kUnroll) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             if (h + j >= h1) break;
-            float a[8], y[8];
-            unpack8<BF16>(xa[j], a);
-            if constexpr (INTER) {
+            uint4 ya = xa[j], yb = xb[j];
+            if (turn) {
+                float a[8], y[8];
+                unpack8<BF16>(xa[j], a);
+                if constexpr (INTER) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    y[2 * i] = a[2 * i] * c[i] - a[2 * i + 1] * s[i];
-                    y[2 * i + 1] = a[2 * i + 1] * c[i] + a[2 * i] * s[i];
-                }
-                *reinterpret_cast<uint4*>(dst[j] + lo) = pack8<BF16>(y);
-            } else {
-                float bb[8], z[8];
-                unpack8<BF16>(xb[j], bb);
+                    for (int i = 0; i < 4; ++i) {
+                        y[2 * i] = a[2 * i] * c[i] - a[2 * i + 1] * s[i];
+                        y[2 * i + 1] = a[2 * i + 1] * c[i] + a[2 * i] * s[i];
+                    }
+                } else {
+                    float bb[8], z[8];
+                    unpack8<BF16>(xb[j], bb);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = a[i] * c[i] - bb[i] * s[i];
-                    z[i] = bb[i] * c[i] + a[i] * s[i];
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] = a[i] * c[i] - bb[i] * s[i];
+                        z[i] = bb[i] * c[i] + a[i] * s[i];
+                    }
+                    yb = pack8<BF16>(z);
                 }
-                *reinterpret_cast<uint4*>(dst[j] + lo) = pack8<BF16>(y);
-                *reinterpret_cast<uint4*>(dst[j] + hi) = pack8<BF16>(z);
+                ya = pack8<BF16>(y);
             }
+            const RotaryOperand& o = p.op[h + j < p.op[0].H ? 0 : 1];
+            const int hh = h + j < p.op[0].H ? h + j : h + j - p.op[0].H;
+            uint8_t* dst = static_cast<uint8_t*>(o.y) + 2 * (b * o.sy.b + hh * o.sy.h + l * o.sy.l);
+            *reinterpret_cast<uint4*>(dst + lo) = ya;
+            if (!INTER) *reinterpret_cast<uint4*>(dst + hi) = yb;
         }
     }
 }
@@ -168,7 +173,7 @@ cudaError_t launch_rotary(const RotaryLaunch& p, bool bf16, cudaStream_t s) {
     const int rd = p.rot.rotary_dim, inter = p.rot.interleaved;
     const bool vec = rd % (inter ? 8 : 16) == 0;
     const int n_rot = vec ? (inter ? rd / 8 : rd / 16) : rd / 2;
-    const int units = n_rot + (p.copy_rest ? (vec ? (p.D - rd) / 8 : p.D - rd) : 0);
+    const int units = n_rot + (p.copy_rest ? (vec ? (p.D - rd) / (inter ? 8 : 16) : p.D - rd) : 0);
     const long long blocks = ((long long)p.B * p.L * units + kThreads - 1) / kThreads;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const int heads = p.op[0].H + p.op[1].H;

@@ -92,13 +92,95 @@ fa_status check_decode(int B, int Hq, int Hk, int D, int num_pages, int max_page
     if (st != FA_OK) return st;
     if (B == 0 || Hq == 0) return FA_OK;
     if (Hk == 0 || Hq % Hk != 0) return FA_ERR_INVALID_ARG;
-    if ((long long)Hk * gqa_q_blocks(Hq / Hk) > 65535 || (long long)B * Hq > 0x7fffffffLL ||
-        (long long)num_pages * Hk > 0x7fffffffLL)
+    if ((long long)B * Hq > 0x7fffffffLL || (long long)num_pages * Hk > 0x7fffffffLL ||
+        (long long)B * max_pages > 0x7fffffffLL || Hq > 65535)
         return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 
-size_t parts_bytes(size_t rows, int parts, int D) { return rows * parts * (size_t)(D + 1) * 4u; }
+int q_blocks_of(int group) { return (group + gqa_q_rows(group) - 1) / gqa_q_rows(group); }
+
+int slot_rows_of(int group) { return group < gqa_q_rows(group) ? group : gqa_q_rows(group); }
+
+// Workspace of a decode step, in bytes from its start.
+struct DecodeWorkspace {
+    size_t unit_parts, slot_o, slot_lse, full_o, full_lse, prefix_o, prefix_lse, bytes;
+    int warps;
+};
+DecodeWorkspace decode_workspace(int B, int Hq, int Hk, int D, int max_pages, bool shared,
+                                 int n_prefix) {
+    DecodeWorkspace w;
+    const int chunk = B < kGqaMaxSequences ? B : kGqaMaxSequences;
+    w.warps = gqa_warps(chunk, Hk, Hq / Hk, max_pages);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += (bytes + 15) & ~(size_t)15;
+        return here;
+    };
+    const size_t slots = 2 * (size_t)w.warps * gqa_rounds(chunk, Hk, Hq / Hk) * slot_rows_of(Hq / Hk);
+    const size_t rows = (size_t)B * Hq;
+    w.unit_parts = take((size_t)chunk * Hk * q_blocks_of(Hq / Hk) * 8);
+    w.slot_o = take(slots * D * 4);
+    w.slot_lse = take(slots * 4);
+    w.full_o = take(shared ? rows * D * 4 : 0);
+    w.full_lse = take(shared ? rows * 4 : 0);
+    w.prefix_o = take(rows * n_prefix * D * 4);
+    w.prefix_lse = take(rows * n_prefix * 4);
+    w.bytes = at;
+    return w;
+}
+
+// The decode kernel and the merge for the batch, kGqaMaxSequences at a time.  p holds everything
+// but what depends on the workspace and the chunk; `kernel` counts the traced kernels so far.
+cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* ws,
+                       const DecodeWorkspace& w, int n_prefix, int kernel, cudaStream_t s) {
+    const size_t row_o = (size_t)p.Hq * D;
+    p.q_blocks = q_blocks_of(p.group);
+    p.slot_rows = slot_rows_of(p.group);
+    p.unit_parts = reinterpret_cast<int2*>(ws + w.unit_parts);
+    p.slot_o = reinterpret_cast<float*>(ws + w.slot_o);
+    p.slot_lse = reinterpret_cast<float*>(ws + w.slot_lse);
+    for (int b0 = 0; b0 < B; b0 += kGqaMaxSequences) {
+        GqaParams c = p;
+        c.B = B - b0 < kGqaMaxSequences ? B - b0 : kGqaMaxSequences;
+        c.q = static_cast<const uint16_t*>(p.q) + b0 * row_o;
+        c.o = static_cast<uint16_t*>(p.o) + b0 * row_o;
+        c.lse = p.lse + (size_t)b0 * p.Hq;
+        c.block_tables = p.block_tables ? p.block_tables + (size_t)b0 * p.max_pages : nullptr;
+        c.seq_lens = p.seq_lens + b0;
+        c.full_o = reinterpret_cast<float*>(ws + w.full_o) + b0 * row_o;
+        c.full_lse = reinterpret_cast<float*>(ws + w.full_lse) + (size_t)b0 * p.Hq;
+        c.early = p.early && b0 == 0;
+        c.rounds = gqa_rounds(c.B, p.Hk, p.group);
+        c.warps = gqa_launched_warps(gqa_warps(c.B, p.Hk, p.group, p.max_pages), D, q8, p.group);
+        cudaError_t e = traced_launch(kernel++, s, [&] { return launch_decode_gqa(c, D, bf16, q8, s); });
+        if (e != cudaSuccess) return e;
+        MergeParams m;
+        std::memset(&m, 0, sizeof(m));
+        m.prefix_o = reinterpret_cast<float*>(ws + w.prefix_o) + b0 * row_o * n_prefix;
+        m.prefix_lse = reinterpret_cast<float*>(ws + w.prefix_lse) + (size_t)b0 * p.Hq * n_prefix;
+        m.n_prefix = n_prefix;
+        m.slot_o = c.slot_o;
+        m.slot_lse = c.slot_lse;
+        m.full_o = c.full_o;
+        m.full_lse = c.full_lse;
+        m.unit_parts = c.unit_parts;
+        m.o = c.o;
+        m.lse = c.lse;
+        m.rows = c.B * p.Hq;
+        m.B = c.B;
+        m.Hq = p.Hq;
+        m.Hk = p.Hk;
+        m.group = p.group;
+        m.q_rows = gqa_q_rows(p.group);
+        m.q_blocks = p.q_blocks;
+        m.slot_rows = p.slot_rows;
+        e = traced_launch(kernel++, s, [&] { return launch_merge(m, D, bf16, s); });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 }  // namespace
 
@@ -326,8 +408,7 @@ size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages)
     if (B <= 0 || Hq <= 0 ||
         check_decode(B, Hq, Hk, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK)
         return 0;
-    const int splits = gqa_splits(B, Hk, Hq / Hk, max_pages);
-    return splits > 1 ? parts_bytes((size_t)B * Hq, splits, D) : 0;
+    return decode_workspace(B, Hq, Hk, D, max_pages, false, 0).bytes;
 }
 
 fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_cache,
@@ -348,9 +429,9 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
     GqaParams p;
     std::memset(&p, 0, sizeof(p));
     const size_t rows = (size_t)B * Hq;
-    p.splits = gqa_splits(B, Hk, Hq / Hk, max_pages);
-    const size_t ws_need = p.splits > 1 ? parts_bytes(rows, p.splits, D) : 0;
-    if (ws_need > 0 && (!workspace || workspace_bytes < ws_need || !aligned16(workspace)))
+    const DecodeWorkspace w = decode_workspace(B, Hq, Hk, D, max_pages, false, 0);
+    const size_t ws_need = w.bytes;
+    if (!workspace || workspace_bytes < ws_need || !aligned16(workspace))
         return FA_ERR_INVALID_ARG;
     const size_t cb = cache_bytes(num_pages, Hk, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, Hk) : 0;
     const Range ins[] = {range(q, rows * D * 2u), range(k_cache, cb), range(v_cache, cb),
@@ -375,28 +456,18 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
     p.seq_lens = seq_lens;
     p.o = o;
     p.lse = lse;
-    p.part_o = ws_need ? static_cast<float*>(workspace) : nullptr;
-    p.part_lse = ws_need ? static_cast<float*>(workspace) + rows * p.splits * D : nullptr;
-    p.parts = p.splits;
-    p.B = B;
     p.Hq = Hq;
     p.Hk = Hk;
     p.group = Hq / Hk;
-    p.q_blocks = gqa_q_blocks(p.group);
     p.num_pages = num_pages;
     p.max_pages = max_pages;
-    p.pages_per_split = max_pages > 0 ? (max_pages + p.splits - 1) / p.splits : 1;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status_ptr();
     p.timeout_ns = wait_timeout_ns();
     if (!p.status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool bf16 = dtype == FA_BF16;
-    if (traced_launch(0, s, [&] { return launch_decode_gqa(p, D, bf16, q8, s); }) != cudaSuccess)
-        return FA_ERR_CUDA;
-    if (p.splits == 1) return FA_OK;
-    const MergeParams mp = {{p.part_o, p.part_lse, p.splits}, o, lse, (int)rows};
-    return traced_launch(1, s, [&] { return launch_merge_parts(mp, D, bf16, s); }) == cudaSuccess
+    return run_decode(p, B, D, dtype == FA_BF16, q8, static_cast<uint8_t*>(workspace), w, 0, 0, s) ==
+                   cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -409,8 +480,7 @@ size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix
         return 0;
     PrefixParams pp;
     prefix_plan(B, Hk, Hq / Hk, prefix_len, &pp);
-    const int splits = max_pages > 0 ? gqa_splits(B, Hk, Hq / Hk, max_pages) : 0;
-    return parts_bytes((size_t)B * Hq, pp.max_segments + splits, D);
+    return decode_workspace(B, Hq, Hk, D, max_pages, pp.max_segments > 0, pp.max_segments).bytes;
 }
 
 fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
@@ -439,11 +509,11 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
     prefix_plan(B, Hk, group, prefix_len, &pp);
     GqaParams p;
     std::memset(&p, 0, sizeof(p));
-    p.splits = max_pages > 0 ? gqa_splits(B, Hk, group, max_pages) : 0;
-    const int parts = pp.max_segments + p.splits;
     const size_t rows = (size_t)B * Hq;
-    const size_t ws_need = parts_bytes(rows, parts, D);
-    if (ws_need > 0 && (!workspace || workspace_bytes < ws_need || !aligned16(workspace)))
+    const DecodeWorkspace w =
+        decode_workspace(B, Hq, Hk, D, max_pages, pp.max_segments > 0, pp.max_segments);
+    const size_t ws_need = w.bytes;
+    if (!workspace || workspace_bytes < ws_need || !aligned16(workspace))
         return FA_ERR_INVALID_ARG;
     const size_t cb = cache_bytes(num_pages, Hk, D, FA_CACHE_16BIT);
     const int n_prefix_pages = prefix_len / kPageTokens + (prefix_len % kPageTokens != 0);
@@ -462,8 +532,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
     if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, false) ||
                           !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, false)))
         return FA_ERR_CUDA;
-    float* part_o = static_cast<float*>(workspace);
-    float* part_lse = part_o + rows * parts * D;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
     int* status = status_ptr();
     if (!status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -494,9 +563,8 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
                 return FA_ERR_CUDA;
         }
         pp.table = prefix_table;
-        pp.part_o = part_o;
-        pp.part_lse = part_lse;
-        pp.parts = parts;
+        pp.part_o = reinterpret_cast<float*>(ws + w.prefix_o);
+        pp.part_lse = reinterpret_cast<float*>(ws + w.prefix_lse);
         pp.prefix_len = prefix_len;
         pp.num_pages = num_pages;
         pp.B = B;
@@ -512,34 +580,23 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
         if (traced_launch(n++, s, [&] { return launch_prefix(pp, D, bf16, s); }) != cudaSuccess)
             return FA_ERR_CUDA;
     }
-    if (p.splits > 0) {
-        p.q = q;
-        p.block_tables = block_tables;
-        p.seq_lens = seq_lens;
-        p.part_o = part_o;
-        p.part_lse = part_lse;
-        p.parts = parts;
-        p.part0 = pp.max_segments;
-        p.early = prefix_len > 0;
-        p.B = B;
-        p.Hq = Hq;
-        p.Hk = Hk;
-        p.group = group;
-        p.q_blocks = gqa_q_blocks(group);
-        p.num_pages = num_pages;
-        p.max_pages = max_pages;
-        p.pages_per_split = (max_pages + p.splits - 1) / p.splits;
-        p.scale_log2 = scale * 1.4426950408889634f;
-        p.status = status;
-        p.timeout_ns = wait_timeout_ns();
-        if (traced_launch(n++, s, [&] { return launch_decode_gqa(p, D, bf16, false, s); }) !=
-            cudaSuccess)
-            return FA_ERR_CUDA;
-    }
-    const MergeParams mp = {{part_o, part_lse, parts}, o, lse, (int)rows};
-    return traced_launch(n, s, [&] { return launch_merge_parts(mp, D, bf16, s); }) == cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
+    p.q = q;
+    p.o = o;
+    p.lse = lse;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.parts_only = prefix_len > 0;
+    p.early = prefix_len > 0;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.group = group;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = status;
+    p.timeout_ns = wait_timeout_ns();
+    return run_decode(p, B, D, bf16, false, ws, w, pp.max_segments, n, s) == cudaSuccess ? FA_OK
+                                                                                         : FA_ERR_CUDA;
 }
 
 }  // extern "C"
