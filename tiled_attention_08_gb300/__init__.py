@@ -517,6 +517,7 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
 # the checks below read each property of a tensor once and the calls go straight to the library.
 # ---------------------------------------------------------------------------------------
 _raw_stream = None
+_Strides2, _Strides4 = ctypes.c_int64 * 6, ctypes.c_int64 * 12  # fa_strides[2], fa_strides[4]
 
 
 def _launch(name, index, *args):
@@ -611,21 +612,29 @@ def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
     index = _cuda_index("x", x)
     if x.dim() != 4:
         raise ValueError("rotary operands are [B, H, L, D] views")
+    dtype = x.dtype
     dt = _dtype_code(x)
-    B, H, L, D = x.shape
+    B, H, L, D = shape = x.shape
     if outs is None:
         xs = [_kernel_view(t) for t in xs]
         outs = [torch.empty_like(t) for t in xs]
-    k, k_out, Hk = None, None, 0
-    st = [_row_strides("x", xs[0], x.shape)] * 2 + [_row_strides("out", outs[0], x.shape)] * 2
+    else:
+        for o, t in zip(outs, xs):
+            _row_strides("out", o, t.shape)
+            _same_device("out", o, index)
+            if o.dtype is not dtype:
+                raise TypeError("out must have the dtype of x")
+    sx, sy = _row_strides("x", xs[0], shape), outs[0].stride()[:3]
     if len(xs) == 2:
-        k, k_out, Hk = xs[1], outs[1], xs[1].shape[1]
-        st[1] = _row_strides("k", k, (B, Hk, L, D))
-        st[3] = _row_strides("k's out", k_out, (B, Hk, L, D))
-    for t in (*xs, *outs):
-        if t.dtype is not x.dtype:
+        k, k_out = xs[1], outs[1]
+        Hk = k.shape[1]
+        sk, sk_out = _row_strides("k", k, (B, Hk, L, D)), k_out.stride()[:3]
+        _same_device("k", k, index)
+        if k.dtype is not dtype:
             raise TypeError("the operands must share a dtype")
-        _same_device("an operand", t, index)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    else:
+        Hk, sk, sk_out, kp, kop = 0, sx, sy, None, None
     rotary_dim = _rotary_dim(freqs, index)
     pos, pos_stride = None, 0
     if positions is not None:
@@ -639,11 +648,9 @@ def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
             raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
         pos = positions.data_ptr()
         pos_stride = pst[0] if B > 1 else 0
-    _launch("fa_rotary", index, xs[0].data_ptr(), None if k is None else k.data_ptr(),
-            outs[0].data_ptr(), None if k is None else k_out.data_ptr(),
-            (ctypes.c_int64 * 12)(*st[0], *st[1], *st[2], *st[3]), pos, pos_stride,
-            freqs.data_ptr(), rotary_dim, float(mscale), interleaved, inverse, B, H, Hk, L, D,
-            dt)
+    _launch("fa_rotary", index, xs[0].data_ptr(), kp, outs[0].data_ptr(), kop,
+            _Strides4(*sx, *sk, *sy, *sk_out), pos, pos_stride, freqs.data_ptr(), rotary_dim,
+            float(mscale), interleaved, inverse, B, H, Hk, L, D, dt)
     return outs
 
 
@@ -683,8 +690,12 @@ def _rotary_autograd():
                 want = [i for i, g in enumerate(grads)
                         if g is not None and ctx.needs_input_grad[5 + i]]
                 if want:
-                    turned = _Rotary.apply(positions, freqs, mscale, interleaved, not inverse,
-                                           *[grads[i] for i in want])
+                    args = (mscale, interleaved, not inverse)
+                    gs = [grads[i] for i in want]
+                    if torch.is_grad_enabled():  # a graph of the gradient is wanted
+                        turned = _Rotary.apply(positions, freqs, *args, *gs)
+                    else:
+                        turned = _rotate(gs, positions, freqs, *args)
                     for i, g in zip(want, turned):
                         out[i] = g
                 return (None,) * 5 + tuple(out)
@@ -785,7 +796,7 @@ def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, 
     if freqs is not None:
         rotary_dim = _rotary_dim(freqs, index)
         fp = freqs.data_ptr()
-    _launch("fa_cache_append", index, k.data_ptr(), v.data_ptr(), (ctypes.c_int64 * 6)(*ks, *vs),
+    _launch("fa_cache_append", index, k.data_ptr(), v.data_ptr(), _Strides2(*ks, *vs),
             k_cache.data_ptr(), v_cache.data_ptr(), kep, vep, block_tables.data_ptr(),
             seq_lens.data_ptr(), new, fp, rotary_dim, float(mscale), interleaved, B, H, L, D, num_pages,
             max_pages, dt, kind)
@@ -816,7 +827,7 @@ def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None
     _same_device("out[1]", v, index)
     _launch("fa_cache_read", index, k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
             block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(),
-            (ctypes.c_int64 * 6)(*ks, *vs), B, H, length, D, num_pages, max_pages, dt, kind)
+            _Strides2(*ks, *vs), B, H, length, D, num_pages, max_pages, dt, kind)
     return k, v
 
 

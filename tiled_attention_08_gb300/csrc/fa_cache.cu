@@ -34,8 +34,49 @@ struct RowMap {
     int heads_per_block; // heads that a block walks over
 };
 
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = unpack2<BF16>(w[i]);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+    }
+}
+
+// Writes this thread's 8 elements of a row (its values x, or the 16-bit ones it was given) to
+// row `unit` of a cache; the row's threads are the kTpr lanes around this one.
 template <int D, bool BF16, bool Q8>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void store_unit(void* cache, uint8_t* exps, size_t unit, int chunk,
+                                           const float (&x)[8], const uint4& raw, bool live) {
+    if constexpr (Q8) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int off = D / 16; off > 0; off >>= 1)
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const uint32_t E = row_exponent(mx);
+        const float f = E == kExpNan ? 0.0f : inv_scale(E);
+        if (live) {
+            uint2 q;
+            q.x = e4m3x2(x[0] * f, x[1] * f) | (e4m3x2(x[2] * f, x[3] * f) << 16);
+            q.y = e4m3x2(x[4] * f, x[5] * f) | (e4m3x2(x[6] * f, x[7] * f) << 16);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + unit * D + chunk * 8) = q;
+            if (chunk == 0) exps[unit] = (uint8_t)E;
+        }
+    } else if (live) {
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + (unit * D + chunk * 8) * 2) = raw;
+    }
+}
+
+// The loads of the next head's key and value are in flight while a head is worked on (and the
+// first head's while lengths, page and angles are looked up: whether the row is a new one is
+// known only then).  Without that each thread had one 16-byte load under way and the kernel ran at
+// 2.8 TB/s.
+template <int D, bool BF16, bool Q8>
+__global__ void __launch_bounds__(kThreads, 3)
     fa_cache_append_kernel(const __grid_constant__ CacheAppendParams p, const RowMap m) {
     constexpr int kTpr = D / 8;               // threads per row, 8 elements each
     constexpr int kRows = kThreads / kTpr;    // rows per block
@@ -44,13 +85,25 @@ __global__ void __launch_bounds__(kThreads)
     const int t = (int)blockIdx.x * (1 << m.log_tok) + (row & ((1 << m.log_tok) - 1));
     const int h_step = kRows >> m.log_tok;
     const int h_lane = row >> m.log_tok;
+    const int e0 = chunk * 8;
+    const int h_end = min(p.H, ((int)blockIdx.y + 1) * m.heads_per_block);
+    const int h_first = (int)blockIdx.y * m.heads_per_block;
+    const uint8_t* src_k = static_cast<const uint8_t*>(p.k) + 2 * (b * p.sk.b + t * p.sk.l + e0);
+    const uint8_t* src_v = static_cast<const uint8_t*>(p.v) + 2 * (b * p.sv.b + t * p.sv.l + e0);
+    auto load = [&](const uint8_t* src, long long stride, int h, bool there) {
+        return there && h < h_end ? *reinterpret_cast<const uint4*>(src + 2 * (h * stride))
+                                  : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 next_k = load(src_k, p.sk.h, h_first + h_lane, t < p.L);
+    uint4 next_v = load(src_v, p.sv.h, h_first + h_lane, t < p.L);
+
     const int len = p.seq_lens[b];
     int n_new = p.new_lens ? p.new_lens[b] : (len == 0 ? 0 : p.L);
     if (n_new < 0 || n_new > p.L || len < n_new || len > (long long)p.max_pages * kPageTokens) {
         if (threadIdx.x == 0) bad_arg(p.status);
         n_new = 0;
     }
-    // A block of whole warps leaves together when no row of it is new (uniform over the block).
+    // The block's warps leave together when no row of it is new.
     if ((int)blockIdx.x * (1 << m.log_tok) >= n_new) return;
     bool ok = t < n_new;
     const int pos = len - n_new + t;
@@ -61,8 +114,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int slot = pos % kPageTokens;
 
-    // This thread's rotation: element i of its unit pairs with element i + partner.
-    const int rd = p.rot.rotary_dim, half = rd / 2, e0 = chunk * 8;
+    // This thread's rotation: element i of its unit and its partner, y = x c + partner s.
+    const int rd = p.rot.rotary_dim, half = rd / 2;
     const bool inter = p.rot.interleaved != 0;
     float c[8], s[8];
     if (rd > 0) {
@@ -71,84 +124,61 @@ __global__ void __launch_bounds__(kThreads)
             const int e = e0 + i;
             c[i] = 1.0f;
             s[i] = 0.0f;
-            if (ok && e < rd) {
+            if (inter && (i & 1)) {  // the pair's second element: the same angle
+                c[i] = c[i - 1];
+                s[i] = -s[i - 1];
+            } else if (ok && e < rd) {
                 const int f = inter ? e >> 1 : (e < half ? e : e - half);
-                const bool second = inter ? (e & 1) : e >= half;
                 rope_cos_sin(pos, p.rot.freqs[f], p.rot.mscale, c[i], s[i]);
-                if (!second) s[i] = -s[i];  // y = x c + partner s
+                if (inter || e < half) s[i] = -s[i];
             }
         }
     }
-    const int h_end = min(p.H, ((int)blockIdx.y + 1) * m.heads_per_block);
-    // Every lane of a warp takes the same number of steps (the shuffles below need all lanes).
-    for (int h0 = (int)blockIdx.y * m.heads_per_block; h0 < h_end; h0 += h_step) {
+    // Lane of the unit that holds the partners of half pairs (rotary_dim a multiple of 16).
+    const int d = rd / 16;
+    const int partner = (threadIdx.x & 31) + (e0 < half ? d : (e0 < rd ? -d : 0));
+    // Every lane of a warp takes the same number of steps (the shuffles need all lanes).
+    for (int h0 = h_first; h0 < h_end; h0 += h_step) {
         const int h = h0 + h_lane;
         const bool live = ok && h < h_end;
+        uint4 raw_k = next_k;
+        const uint4 raw_v = next_v;
+        next_k = load(src_k, p.sk.h, h + h_step, ok);
+        next_v = load(src_v, p.sv.h, h + h_step, ok);
+        const size_t unit = ((size_t)page * p.H + h) * kPageTokens + slot;  // row of the cache
+        float x[8];
+        unpack8<BF16>(raw_k, x);
+        if (rd > 0) {
+            float o[8];  // the partners
+            if (inter) {
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const Strides& st = which ? p.sv : p.sk;
-            const uint8_t* src = static_cast<const uint8_t*>(which ? p.v : p.k) +
-                                 2 * (b * st.b + h * st.h + t * st.l);
-            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-            if (live) raw = *reinterpret_cast<const uint4*>(src + e0 * 2);
-            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-            float x[8];
+                for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
+            } else if (rd % 16 == 0) {
+                uint4 r;
+                r.x = __shfl_sync(0xffffffffu, raw_k.x, partner);
+                r.y = __shfl_sync(0xffffffffu, raw_k.y, partner);
+                r.z = __shfl_sync(0xffffffffu, raw_k.z, partner);
+                r.w = __shfl_sync(0xffffffffu, raw_k.w, partner);
+                unpack8<BF16>(r, o);
+            } else {  // pairs that do not fall on 16-byte units
+                const uint16_t* row16 = reinterpret_cast<const uint16_t*>(src_k + 2 * (h * p.sk.h)) - e0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = unpack2<BF16>(w[i]);
-                x[2 * i] = v.x;
-                x[2 * i + 1] = v.y;
-            }
-            if (which == 0 && rd > 0) {
-                float o[8];  // the partners
-                if (inter) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
-                } else if (rd % 16 == 0) {  // the partner unit is another lane's
-                    const int d = rd / 16;
-                    const int src_chunk = e0 < half ? chunk + d : (e0 < rd ? chunk - d : chunk);
-                    const int lane = (threadIdx.x & 31) - chunk + src_chunk;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], lane);
-                } else {
-                    const uint16_t* row16 = reinterpret_cast<const uint16_t*>(src);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = e0 + i;
-                        const int q = e < half ? e + half : (e < rd ? e - half : e);
-                        o[i] = live ? unpack2<BF16>(row16[q]).x : 0.0f;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    const int e = e0 + i;
+                    const int q = e < half ? e + half : (e < rd ? e - half : e);
+                    o[i] = live ? unpack2<BF16>(row16[q]).x : 0.0f;
                 }
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (e0 + i < rd) x[i] = x[i] * c[i] + o[i] * s[i];
             }
-            const size_t unit = ((size_t)page * p.H + h) * kPageTokens + slot;  // row of the cache
-            if constexpr (Q8) {
-                uint32_t mx = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-                for (int off = kTpr / 2; off > 0; off >>= 1)
-                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const uint32_t E = row_exponent(mx);
-                const float f = E == kExpNan ? 0.0f : inv_scale(E);
-                if (live) {
-                    uint2 q;
-                    q.x = e4m3x2(x[0] * f, x[1] * f) | (e4m3x2(x[2] * f, x[3] * f) << 16);
-                    q.y = e4m3x2(x[4] * f, x[5] * f) | (e4m3x2(x[6] * f, x[7] * f) << 16);
-                    uint8_t* dst = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache);
-                    *reinterpret_cast<uint2*>(dst + unit * D + e0) = q;
-                    if (chunk == 0) (which ? p.v_exp : p.k_exp)[unit] = (uint8_t)E;
-                }
-            } else if (live) {
-                uint8_t* dst = static_cast<uint8_t*>(which ? p.v_cache : p.k_cache);
-                if (which == 0 && rd > 0)
-                    raw = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]),
-                                     pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
-                *reinterpret_cast<uint4*>(dst + (unit * D + e0) * 2) = raw;
-            }
+            for (int i = 0; i < 8; ++i)
+                if (e0 + i < rd) x[i] = x[i] * c[i] + o[i] * s[i];
+            if constexpr (!Q8)
+                raw_k = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]),
+                                   pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
         }
+        store_unit<D, BF16, Q8>(p.k_cache, p.k_exp, unit, chunk, x, raw_k, live);
+        unpack8<BF16>(raw_v, x);
+        store_unit<D, BF16, Q8>(p.v_cache, p.v_exp, unit, chunk, x, raw_v, live);
     }
 }
 
