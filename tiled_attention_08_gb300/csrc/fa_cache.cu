@@ -12,6 +12,8 @@
 // page) and, when a call adds fewer tokens than a block has rows (decoding adds one), along heads.
 // The page lookup and the rotation angles depend on the token only, so a thread computes them
 // once and walks over the heads of its chunk.
+#include <type_traits>
+
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -45,57 +47,95 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     }
 }
 
-// Writes this thread's 8 elements of a row (its values x, or the 16-bit ones it was given) to
-// row `unit` of a cache; the row's threads are the kTpr lanes around this one.
-template <int D, bool BF16, bool Q8>
-__device__ __forceinline__ void store_unit(void* cache, uint8_t* exps, size_t unit, int chunk,
-                                           const float (&x)[8], const uint4& raw, bool live) {
-    if constexpr (Q8) {
-        uint32_t mx = 0;
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
+                      pack2<BF16>(x[6], x[7]));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b, float c) {  // a NaN operand wins
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// fp32 pattern of the largest magnitude of a row (a NaN's if it holds one) from this thread's 16
+// values; the row's threads are the D / 16 lanes around this one.
+template <int D>
+__device__ __forceinline__ uint32_t row_amax(const float (&a)[8], const float (&b)[8]) {
+    float mx = max_nan(fabsf(a[0]), fabsf(b[0]), fabsf(a[1]));
+    mx = max_nan(mx, fabsf(b[1]), fabsf(a[2]));
+    mx = max_nan(mx, fabsf(b[2]), fabsf(a[3]));
+    mx = max_nan(mx, fabsf(b[3]), fabsf(a[4]));
+    mx = max_nan(mx, fabsf(b[4]), fabsf(a[5]));
+    mx = max_nan(mx, fabsf(b[5]), fabsf(a[6]));
+    mx = max_nan(mx, fabsf(b[6]), fabsf(a[7]));
+    mx = max_nan(mx, mx, fabsf(b[7]));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int off = D / 16; off > 0; off >>= 1)
-            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const uint32_t E = row_exponent(mx);
-        const float f = E == kExpNan ? 0.0f : inv_scale(E);
-        if (live) {
-            uint2 q;
-            q.x = e4m3x2(x[0] * f, x[1] * f) | (e4m3x2(x[2] * f, x[3] * f) << 16);
-            q.y = e4m3x2(x[4] * f, x[5] * f) | (e4m3x2(x[6] * f, x[7] * f) << 16);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + unit * D + chunk * 8) = q;
-            if (chunk == 0) exps[unit] = (uint8_t)E;
-        }
-    } else if (live) {
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(cache) + (unit * D + chunk * 8) * 2) = raw;
+    for (int off = D / 32; off > 0; off >>= 1)
+        mx = max_nan(mx, mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    return __float_as_uint(mx) & 0x7fffffffu;
+}
+
+// Eight values as e4m3 under the row's exponent.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float f) {
+    return make_uint2(e4m3x2(x[0] * f, x[1] * f) | (e4m3x2(x[2] * f, x[3] * f) << 16),
+                      e4m3x2(x[4] * f, x[5] * f) | (e4m3x2(x[6] * f, x[7] * f) << 16));
+}
+
+// Writes a row's 16 values of this thread (a and b, at elements ea and eb of row `dst`) as e4m3, and
+// the row's exponent.  Called by all lanes of a warp.
+template <int D>
+__device__ __forceinline__ void store_e4m3(uint8_t* dst, uint8_t* exp, int ea, int eb, bool first,
+                                           const float (&a)[8], const float (&b)[8], bool live) {
+    const uint32_t E = row_exponent(row_amax<D>(a, b));
+    const float f = E == kExpNan ? 0.0f : inv_scale(E);
+    if (live) {
+        *reinterpret_cast<uint2*>(dst + ea) = quantise8(a, f);
+        *reinterpret_cast<uint2*>(dst + eb) = quantise8(b, f);
+        if (first) *exp = (uint8_t)E;
     }
 }
 
-// The loads of the next head's key and value are in flight while a head is worked on (and the
-// first head's while lengths, page and angles are looked up: whether the row is a new one is
-// known only then).  Without that each thread had one 16-byte load under way and the kernel ran at
-// 2.8 TB/s.
-template <int D, bool BF16, bool Q8>
+// A thread has two 16-byte units of a row, its key's and its value's: for half pairs on unit
+// borders (rotary_dim a multiple of 16) a unit and its partner, so that the turn needs no other
+// lane, else two neighbours.  The next head's four loads are in flight while a head is written (and
+// the first head's while lengths, page and angles are looked up: whether the row is a new one is
+// known only then); with one 16-byte load under way per thread the kernel ran at 2.8 TB/s.
+// MODE: how keys are turned: 0 not at all, 1 half pairs on unit borders, 2 interleaved, 3 half pairs
+// anywhere.
+template <int D, bool BF16, bool Q8, int MODE>
 __global__ void __launch_bounds__(kThreads, 3)
     fa_cache_append_kernel(const __grid_constant__ CacheAppendParams p, const RowMap m) {
-    constexpr int kTpr = D / 8;               // threads per row, 8 elements each
+    constexpr int kTpr = D / 16;              // threads per row, 16 elements each
     constexpr int kRows = kThreads / kTpr;    // rows per block
     const int b = blockIdx.z;
-    const int chunk = threadIdx.x % kTpr, row = threadIdx.x / kTpr;
+    const int j = threadIdx.x % kTpr, row = threadIdx.x / kTpr;
     const int t = (int)blockIdx.x * (1 << m.log_tok) + (row & ((1 << m.log_tok) - 1));
     const int h_step = kRows >> m.log_tok;
     const int h_lane = row >> m.log_tok;
-    const int e0 = chunk * 8;
+    const int rd = p.rot.rotary_dim, half = rd / 2;
+    int ea = 16 * j, eb = ea + 8;  // this thread's elements
+    if (MODE == 1 && 16 * j < rd) {
+        ea = 8 * j;
+        eb = ea + half;
+    }
     const int h_end = min(p.H, ((int)blockIdx.y + 1) * m.heads_per_block);
     const int h_first = (int)blockIdx.y * m.heads_per_block;
-    const uint8_t* src_k = static_cast<const uint8_t*>(p.k) + 2 * (b * p.sk.b + t * p.sk.l + e0);
-    const uint8_t* src_v = static_cast<const uint8_t*>(p.v) + 2 * (b * p.sv.b + t * p.sv.l + e0);
-    auto load = [&](const uint8_t* src, long long stride, int h, bool there) {
-        return there && h < h_end ? *reinterpret_cast<const uint4*>(src + 2 * (h * stride))
-                                  : make_uint4(0u, 0u, 0u, 0u);
+    const uint8_t* src_k = static_cast<const uint8_t*>(p.k) + 2 * (b * p.sk.b + t * p.sk.l);
+    const uint8_t* src_v = static_cast<const uint8_t*>(p.v) + 2 * (b * p.sv.b + t * p.sv.l);
+    uint4 next[4];
+    auto load = [&](int h, bool there) {
+        if (there && h < h_end) {
+            const uint8_t *k = src_k + 2 * (h * p.sk.h), *v = src_v + 2 * (h * p.sv.h);
+            next[0] = *reinterpret_cast<const uint4*>(k + 2 * ea);
+            next[1] = *reinterpret_cast<const uint4*>(k + 2 * eb);
+            next[2] = *reinterpret_cast<const uint4*>(v + 2 * ea);
+            next[3] = *reinterpret_cast<const uint4*>(v + 2 * eb);
+        }
     };
-    uint4 next_k = load(src_k, p.sk.h, h_first + h_lane, t < p.L);
-    uint4 next_v = load(src_v, p.sv.h, h_first + h_lane, t < p.L);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) next[i] = make_uint4(0u, 0u, 0u, 0u);
+    load(h_first + h_lane, t < p.L);
 
     const int len = p.seq_lens[b];
     int n_new = p.new_lens ? p.new_lens[b] : (len == 0 ? 0 : p.L);
@@ -114,82 +154,112 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     const int slot = pos % kPageTokens;
 
-    // This thread's rotation: element i of its unit and its partner, y = x c + partner s.
-    const int rd = p.rot.rotary_dim, half = rd / 2;
-    const bool inter = p.rot.interleaved != 0;
-    float c[8], s[8];
-    if (rd > 0) {
+    // Angles: pair i of (a, b) (half pairs), or of a, then of b (interleaved).
+    constexpr int kAngles = (MODE == 1 || MODE == 2) ? 8 : 1;
+    float c[kAngles], s[kAngles];
+    if constexpr (MODE == 1 || MODE == 2) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
+            const int f = 8 * j + i;
             c[i] = 1.0f;
             s[i] = 0.0f;
-            if (inter && (i & 1)) {  // the pair's second element: the same angle
-                c[i] = c[i - 1];
-                s[i] = -s[i - 1];
-            } else if (ok && e < rd) {
-                const int f = inter ? e >> 1 : (e < half ? e : e - half);
-                rope_cos_sin(pos, p.rot.freqs[f], p.rot.mscale, c[i], s[i]);
-                if (inter || e < half) s[i] = -s[i];
-            }
+            if (ok && f < half) rope_cos_sin(pos, p.rot.freqs[f], p.rot.mscale, c[i], s[i]);
         }
     }
-    // Lane of the unit that holds the partners of half pairs (rotary_dim a multiple of 16).
-    const int d = rd / 16;
-    const int partner = (threadIdx.x & 31) + (e0 < half ? d : (e0 < rd ? -d : 0));
+    // Row of the cache of this token's first head here; heads are kPageTokens rows apart.
+    constexpr int kRowBytes = D * (Q8 ? 1 : 2);
+    const size_t unit0 = ((size_t)page * p.H + h_first + h_lane) * kPageTokens + slot;
+    const size_t step = (size_t)h_step * kPageTokens;
+    uint8_t* dst_k = static_cast<uint8_t*>(p.k_cache) + unit0 * kRowBytes;
+    uint8_t* dst_v = static_cast<uint8_t*>(p.v_cache) + unit0 * kRowBytes;
+    uint8_t *exp_k = p.k_exp + unit0, *exp_v = p.v_exp + unit0;
     // Every lane of a warp takes the same number of steps (the shuffles need all lanes).
     for (int h0 = h_first; h0 < h_end; h0 += h_step) {
         const int h = h0 + h_lane;
         const bool live = ok && h < h_end;
-        uint4 raw_k = next_k;
-        const uint4 raw_v = next_v;
-        next_k = load(src_k, p.sk.h, h + h_step, ok);
-        next_v = load(src_v, p.sv.h, h + h_step, ok);
-        const size_t unit = ((size_t)page * p.H + h) * kPageTokens + slot;  // row of the cache
-        float x[8];
-        unpack8<BF16>(raw_k, x);
-        if (rd > 0) {
-            float o[8];  // the partners
-            if (inter) {
+        uint4 raw[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
-            } else if (rd % 16 == 0) {
-                uint4 r;
-                r.x = __shfl_sync(0xffffffffu, raw_k.x, partner);
-                r.y = __shfl_sync(0xffffffffu, raw_k.y, partner);
-                r.z = __shfl_sync(0xffffffffu, raw_k.z, partner);
-                r.w = __shfl_sync(0xffffffffu, raw_k.w, partner);
-                unpack8<BF16>(r, o);
-            } else {  // pairs that do not fall on 16-byte units
-                const uint16_t* row16 = reinterpret_cast<const uint16_t*>(src_k + 2 * (h * p.sk.h)) - e0;
+        for (int i = 0; i < 4; ++i) raw[i] = next[i];
+        load(h + h_step, ok);
+        float a[8], bb[8];
+        if (Q8 || MODE != 0) {
+            unpack8<BF16>(raw[0], a);
+            unpack8<BF16>(raw[1], bb);
+        }
+        if constexpr (MODE == 1) {
+            if (16 * j < rd) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int e = e0 + i;
-                    const int q = e < half ? e + half : (e < rd ? e - half : e);
-                    o[i] = live ? unpack2<BF16>(row16[q]).x : 0.0f;
+                    const float y = a[i] * c[i] - bb[i] * s[i];
+                    bb[i] = bb[i] * c[i] + a[i] * s[i];
+                    a[i] = y;
                 }
             }
+        } else if constexpr (MODE == 2) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (e0 + i < rd) x[i] = x[i] * c[i] + o[i] * s[i];
-            if constexpr (!Q8)
-                raw_k = make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]),
-                                   pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+            for (int i = 0; i < 4; ++i) {
+                if (ea + 2 * i < rd) {
+                    const float y = a[2 * i] * c[i] - a[2 * i + 1] * s[i];
+                    a[2 * i + 1] = a[2 * i + 1] * c[i] + a[2 * i] * s[i];
+                    a[2 * i] = y;
+                }
+                if (eb + 2 * i < rd) {
+                    const float y = bb[2 * i] * c[i + 4] - bb[2 * i + 1] * s[i + 4];
+                    bb[2 * i + 1] = bb[2 * i + 1] * c[i + 4] + bb[2 * i] * s[i + 4];
+                    bb[2 * i] = y;
+                }
+            }
+        } else if constexpr (MODE == 3) {
+            const uint16_t* row16 = reinterpret_cast<const uint16_t*>(src_k + 2 * (h * p.sk.h));
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const int e = ea + i;
+                if (!live || e >= rd) break;
+                const bool second = e >= half;
+                float cc, ss;
+                rope_cos_sin(pos, p.rot.freqs[second ? e - half : e], p.rot.mscale, cc, ss);
+                const float mine = unpack2<BF16>(row16[e]).x;
+                const float other = unpack2<BF16>(row16[second ? e - half : e + half]).x;
+                const float y = mine * cc + (second ? other : -other) * ss;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {  // (registers have no index)
+                    if (k == i) a[k] = y;
+                    if (k + 8 == i) bb[k] = y;
+                }
+            }
         }
-        store_unit<D, BF16, Q8>(p.k_cache, p.k_exp, unit, chunk, x, raw_k, live);
-        unpack8<BF16>(raw_v, x);
-        store_unit<D, BF16, Q8>(p.v_cache, p.v_exp, unit, chunk, x, raw_v, live);
+        if constexpr (Q8) {
+            store_e4m3<D>(dst_k, exp_k, ea, eb, j == 0, a, bb, live);
+            unpack8<BF16>(raw[2], a);
+            unpack8<BF16>(raw[3], bb);
+            store_e4m3<D>(dst_v, exp_v, ea, eb, j == 0, a, bb, live);
+        } else if (live) {
+            if (MODE != 0) {
+                raw[0] = pack8<BF16>(a);
+                raw[1] = pack8<BF16>(bb);
+            }
+            *reinterpret_cast<uint4*>(dst_k + 2 * ea) = raw[0];
+            *reinterpret_cast<uint4*>(dst_k + 2 * eb) = raw[1];
+            *reinterpret_cast<uint4*>(dst_v + 2 * ea) = raw[2];
+            *reinterpret_cast<uint4*>(dst_v + 2 * eb) = raw[3];
+        }
+        dst_k += step * kRowBytes;
+        dst_v += step * kRowBytes;
+        exp_k += step;
+        exp_v += step;
     }
 }
 
-// A thread's unit is 8 elements: 16 bytes of the output (8 bytes of an e4m3 cache).
+// A thread's unit is 8 elements: 16 bytes of the output (and 8 or 16 of the cache), so that a warp's
+// stores are whole rows; two heads' keys and values are loaded together.  (16 elements per thread,
+// in one load and two stores 32 bytes apart, took 72 us where this takes 60.)
 template <int D, bool BF16, bool Q8>
 __global__ void __launch_bounds__(kThreads)
     fa_cache_read_kernel(const __grid_constant__ CacheReadParams p, const RowMap m) {
     constexpr int kTpr = D / 8;
     constexpr int kRows = kThreads / kTpr;
     const int b = blockIdx.z;
-    const int chunk = threadIdx.x % kTpr, row = threadIdx.x / kTpr;
+    const int row = threadIdx.x / kTpr, e0 = (threadIdx.x % kTpr) * 8;
     const int t = (int)blockIdx.x * (1 << m.log_tok) + (row & ((1 << m.log_tok) - 1));
     const int h_step = kRows >> m.log_tok;
     const int h_lane = row >> m.log_tok;
@@ -205,42 +275,52 @@ __global__ void __launch_bounds__(kThreads)
         page = p.block_tables[(size_t)b * p.max_pages + t / kPageTokens];
         if (page < 0 || page >= p.num_pages) live = bad_arg(p.status);
     }
-    const int slot = t % kPageTokens, e0 = chunk * 8;
+    const int slot = t % kPageTokens;
     const int h_end = min(p.H, ((int)blockIdx.y + 1) * m.heads_per_block);
-    for (int h = (int)blockIdx.y * m.heads_per_block + h_lane; h < h_end; h += h_step) {
-        const size_t unit = ((size_t)page * p.H + h) * kPageTokens + slot;
+    using In = typename std::conditional<Q8, uint2, uint4>::type;  // 8 elements of the cache
+    const In *kc = static_cast<const In*>(p.k_cache), *vc = static_cast<const In*>(p.v_cache);
+    uint8_t* out_k = static_cast<uint8_t*>(p.k) + 2 * (b * p.sk.b + t * p.sk.l + e0);
+    uint8_t* out_v = static_cast<uint8_t*>(p.v) + 2 * (b * p.sv.b + t * p.sv.l + e0);
+    for (int h = (int)blockIdx.y * m.heads_per_block + h_lane; h < h_end; h += 2 * h_step) {
+        In q[4];     // key and value of this head, of the next
+        float f[4];
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const uint8_t* src = static_cast<const uint8_t*>(which ? p.v_cache : p.k_cache);
+        for (int i = 0; i < 4; ++i) {
+            const int hh = h + (i >> 1) * h_step;
+            if (live && hh < h_end) {
+                const size_t unit = ((size_t)page * p.H + hh) * kPageTokens + slot;
+                q[i] = ((i & 1) ? vc : kc)[unit * (D / 8) + e0 / 8];
+                if constexpr (Q8) f[i] = row_scale(((i & 1) ? p.v_exp : p.k_exp)[unit]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int hh = h + (i >> 1) * h_step;
+            if (hh >= h_end) break;
             uint4 out = make_uint4(0u, 0u, 0u, 0u);
             if (live) {
                 if constexpr (Q8) {
-                    const uint2 q = *reinterpret_cast<const uint2*>(src + unit * D + e0);
-                    const float f = row_scale((which ? p.v_exp : p.k_exp)[unit]);
-                    const uint32_t two[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
+                    const uint32_t two[4] = {q[i].x & 0xffffu, q[i].x >> 16, q[i].y & 0xffffu, q[i].y >> 16};
                     uint32_t r[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 x = unpack2<false>(e4m3x2_to_f16x2(two[i]));
-                        r[i] = pack2<BF16>(x.x * f, x.y * f);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = unpack2<false>(e4m3x2_to_f16x2(two[k]));
+                        r[k] = pack2<BF16>(x.x * f[i], x.y * f[i]);
                     }
                     out = make_uint4(r[0], r[1], r[2], r[3]);
                 } else {
-                    out = *reinterpret_cast<const uint4*>(src + (unit * D + e0) * 2);
+                    out = q[i];
                 }
             }
-            const Strides& st = which ? p.sv : p.sk;
-            uint8_t* dst = static_cast<uint8_t*>(which ? p.v : p.k) +
-                           2 * (b * st.b + h * st.h + t * st.l);
-            *reinterpret_cast<uint4*>(dst + e0 * 2) = out;
+            uint8_t* dst = (i & 1) ? out_v + 2 * (hh * p.sv.h) : out_k + 2 * (hh * p.sk.h);
+            *reinterpret_cast<uint4*>(dst) = out;
         }
     }
 }
 
 // Tokens per block: a power of two up to the block's rows that covers L.  Heads per block: up to
 // `most`, fewer while the grid has under four blocks per SM.
-bool row_map(int B, int H, int L, int D, int most, RowMap* m, dim3* grid) {
-    const int rows = kThreads / (D / 8);
+bool row_map(int B, int H, int L, int rows, int most, RowMap* m, dim3* grid) {
     m->log_tok = 0;
     while ((1 << m->log_tok) < rows && (1 << m->log_tok) < L) ++m->log_tok;
     const int tok = 1 << m->log_tok, h_step = rows / tok;
@@ -256,26 +336,34 @@ bool row_map(int B, int H, int L, int D, int most, RowMap* m, dim3* grid) {
 
 }  // namespace
 
-cudaError_t launch_cache_append(const CacheAppendParams& p, bool bf16, bool q8, cudaStream_t s) {
+namespace {
+template <int D, bool BF16, bool Q8>
+cudaError_t launch_append(const CacheAppendParams& p, cudaStream_t s) {
     RowMap m;
     dim3 grid;
-    if (!row_map(p.B, p.H, p.L, p.D, 8, &m, &grid)) return cudaErrorInvalidConfiguration;
+    if (!row_map(p.B, p.H, p.L, kThreads / (D / 16), 8, &m, &grid))
+        return cudaErrorInvalidConfiguration;
     auto go = [&](auto kern) { return launch_kernel(kern, grid, dim3(kThreads), 0, s, p, m); };
-    if (q8)
-        return p.D == 64 ? (bf16 ? go(fa_cache_append_kernel<64, true, true>)
-                                 : go(fa_cache_append_kernel<64, false, true>))
-                         : (bf16 ? go(fa_cache_append_kernel<128, true, true>)
-                                 : go(fa_cache_append_kernel<128, false, true>));
-    return p.D == 64 ? (bf16 ? go(fa_cache_append_kernel<64, true, false>)
-                             : go(fa_cache_append_kernel<64, false, false>))
-                     : (bf16 ? go(fa_cache_append_kernel<128, true, false>)
-                             : go(fa_cache_append_kernel<128, false, false>));
+    if (p.rot.rotary_dim == 0) return go(fa_cache_append_kernel<D, BF16, Q8, 0>);
+    if (p.rot.interleaved) return go(fa_cache_append_kernel<D, BF16, Q8, 2>);
+    return p.rot.rotary_dim % 16 == 0 ? go(fa_cache_append_kernel<D, BF16, Q8, 1>)
+                                      : go(fa_cache_append_kernel<D, BF16, Q8, 3>);
+}
+template <int D, bool BF16>
+cudaError_t launch_append_q(const CacheAppendParams& p, bool q8, cudaStream_t s) {
+    return q8 ? launch_append<D, BF16, true>(p, s) : launch_append<D, BF16, false>(p, s);
+}
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheAppendParams& p, bool bf16, bool q8, cudaStream_t s) {
+    if (p.D == 64) return bf16 ? launch_append_q<64, true>(p, q8, s) : launch_append_q<64, false>(p, q8, s);
+    return bf16 ? launch_append_q<128, true>(p, q8, s) : launch_append_q<128, false>(p, q8, s);
 }
 
 cudaError_t launch_cache_read(const CacheReadParams& p, bool bf16, bool q8, cudaStream_t s) {
     RowMap m;
     dim3 grid;
-    if (!row_map(p.B, p.H, p.L, p.D, 8, &m, &grid)) return cudaErrorInvalidConfiguration;
+    if (!row_map(p.B, p.H, p.L, kThreads / (p.D / 8), 8, &m, &grid)) return cudaErrorInvalidConfiguration;
     auto go = [&](auto kern) { return launch_kernel(kern, grid, dim3(kThreads), 0, s, p, m); };
     if (q8)
         return p.D == 64 ? (bf16 ? go(fa_cache_read_kernel<64, true, true>)
