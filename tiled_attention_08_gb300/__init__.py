@@ -516,22 +516,24 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
 # Operators around attention.  The smallest of these calls run for a few microseconds on the GPU, so
 # the checks below read each property of a tensor once and the calls go straight to the library.
 # ---------------------------------------------------------------------------------------
-_raw_stream = None
+_raw_stream = _current_device = None
 _Strides2, _Strides4 = ctypes.c_int64 * 6, ctypes.c_int64 * 12  # fa_strides[2], fa_strides[4]
 
 
 def _launch(name, index, *args):
     """The library's entry point ``name`` on the current stream of CUDA device ``index`` (made
     current for the call where it is not); raises on a status other than FA_OK."""
-    global _raw_stream
-    import torch
+    global _raw_stream, _current_device
     if _raw_stream is None:
+        import torch
+        _current_device = torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
     fn = getattr(_lib or load_library(), name)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
+        import torch
         with torch.cuda.device(index):
             status = fn(*args, _raw_stream(index))
     if status != FA_OK:
@@ -726,16 +728,17 @@ def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index):
     """(cache_dtype, num_pages, H, D, k_exp pointer, v_exp pointer) of a checked pair of caches."""
     import torch
     shape = k_cache.shape
+    kind = k_cache.dtype
     if len(shape) != 4 or shape[2] != FA_PAGE_TOKENS or v_cache.shape != shape:
         raise ValueError("caches must be [num_pages, H, FA_PAGE_TOKENS, D]")
-    num_pages, H, _, D = shape
-    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("the caches must be contiguous")
-    _same_device("k_cache", k_cache, index)
-    _same_device("v_cache", v_cache, index)
-    kind = k_cache.dtype
+    if not k_cache.get_device() == v_cache.get_device() == index:
+        raise ValueError(f"the caches are on {k_cache.device} and {v_cache.device}, expected "
+                         f"cuda:{index}")
     if v_cache.dtype is not kind:
         raise TypeError("k_cache and v_cache must share a dtype")
+    num_pages, H, _, D = shape
     if k_exp is None and v_exp is None:
         if kind is not dtype:
             raise TypeError(f"the cache holds {kind}, the call's tensors {dtype}; an e4m3 cache "
@@ -743,27 +746,30 @@ def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index):
         return FA_CACHE_16BIT, num_pages, H, D, None, None
     if kind is not torch.float8_e4m3fn:
         raise TypeError("a cache with exponents must be float8_e4m3fn")
-    for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-        if t is None or t.dtype is not torch.uint8 or t.shape != shape[:3] or \
-                not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous uint8 [num_pages, H, FA_PAGE_TOKENS] "
-                             "tensor")
-        _same_device(name, t, index)
+    es = (num_pages, H, FA_PAGE_TOKENS)
+    u8 = torch.uint8
+    if k_exp is None or v_exp is None or not (
+            k_exp.dtype is u8 and v_exp.dtype is u8 and k_exp.shape == es and v_exp.shape == es and
+            k_exp.is_contiguous() and v_exp.is_contiguous() and
+            k_exp.get_device() == v_exp.get_device() == index):
+        raise ValueError("k_exp and v_exp must be contiguous uint8 [num_pages, H, FA_PAGE_TOKENS] "
+                         "tensors on the cache's device")
     return FA_CACHE_E4M3, num_pages, H, D, k_exp.data_ptr(), v_exp.data_ptr()
 
 
 def _tables(block_tables, seq_lens, B, index):
     """max_pages of a checked block table and its lengths."""
     import torch
-    if block_tables.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or seq_lens.dtype is not i32:
         raise TypeError("block_tables and seq_lens must be int32")
     shape = block_tables.shape
     if len(shape) != 2 or shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("block_tables must be [B, max_pages] and seq_lens [B]")
-    if not block_tables.is_contiguous() or not seq_lens.is_contiguous():
+    if not (block_tables.is_contiguous() and seq_lens.is_contiguous()):
         raise ValueError("block_tables and seq_lens must be contiguous")
-    _same_device("block_tables", block_tables, index)
-    _same_device("seq_lens", seq_lens, index)
+    if not block_tables.get_device() == seq_lens.get_device() == index:
+        raise ValueError(f"block_tables and seq_lens must be on cuda:{index}")
     return shape[1]
 
 
@@ -816,15 +822,17 @@ def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None
     max_pages = _tables(block_tables, seq_lens, B, index)
     shape = (B, H, length, D)
     if out is None:
-        out = (torch.empty(shape, device=k_cache.device, dtype=dtype),
-               torch.empty(shape, device=k_cache.device, dtype=dtype))
-    k, v = out
+        k = torch.empty(shape, device=k_cache.device, dtype=dtype)
+        v = torch.empty_like(k)
+        ks = vs = k.stride()[:3]
+    else:
+        k, v = out
+        if k.dtype is not dtype or v.dtype is not dtype:
+            raise TypeError("out must have the call's dtype")
+        ks, vs = _row_strides("out[0]", k, shape), _row_strides("out[1]", v, shape)
+        _same_device("out[0]", k, index)
+        _same_device("out[1]", v, index)
     dt = _dtype_code(k)
-    if k.dtype is not dtype or v.dtype is not dtype:
-        raise TypeError("out must have the call's dtype")
-    ks, vs = _row_strides("out[0]", k, shape), _row_strides("out[1]", v, shape)
-    _same_device("out[0]", k, index)
-    _same_device("out[1]", v, index)
     _launch("fa_cache_read", index, k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
             block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(),
             _Strides2(*ks, *vs), B, H, length, D, num_pages, max_pages, dt, kind)
