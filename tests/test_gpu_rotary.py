@@ -176,6 +176,11 @@ def test_rotary_second_derivative_and_unused_branches():
     k = randn(1, 2, 8, 64, dtype=torch.bfloat16, seed=1)
     qo, ko = fa.rotary(q, k, None, freqs, mscale)
     assert not ko.requires_grad or ko.grad_fn is not None
+    k2 = randn(1, 3, 8, 64, dtype=torch.bfloat16, seed=5).requires_grad_()
+    q2, k2o = fa.rotary(q.detach(), k2, None, freqs, mscale)  # keys alone need a gradient
+    g2 = randn(1, 3, 8, 64, dtype=torch.bfloat16, seed=6)
+    (dk2,) = torch.autograd.grad((q2, k2o), k2, (torch.ones_like(q2), g2))
+    assert torch.equal(dk2, fa.rotary_apply(g2, None, freqs, mscale, inverse=True))
     g = randn(1, 2, 8, 64, dtype=torch.bfloat16, seed=2).requires_grad_()
     (dq,) = torch.autograd.grad(qo, q, g, create_graph=True)
     h = randn(1, 2, 8, 64, dtype=torch.bfloat16, seed=3)

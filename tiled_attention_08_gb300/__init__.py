@@ -607,36 +607,15 @@ def _kernel_view(t):
     return t.contiguous()
 
 
-def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
-    """The library call for one or two [B, H, L, D] views; returns the outputs."""
+def _rotary_plan(x, positions, freqs, mscale, interleaved):
+    """What a rotation of [B, H, L, D] views like x needs apart from them, checked: (device index,
+    shape, dtype, trailing arguments of fa_rotary by name)."""
     import torch
-    x = xs[0]
     index = _cuda_index("x", x)
     if x.dim() != 4:
         raise ValueError("rotary operands are [B, H, L, D] views")
-    dtype = x.dtype
     dt = _dtype_code(x)
-    B, H, L, D = shape = x.shape
-    if outs is None:
-        xs = [_kernel_view(t) for t in xs]
-        outs = [torch.empty_like(t) for t in xs]
-    else:
-        for o, t in zip(outs, xs):
-            _row_strides("out", o, t.shape)
-            _same_device("out", o, index)
-            if o.dtype is not dtype:
-                raise TypeError("out must have the dtype of x")
-    sx, sy = _row_strides("x", xs[0], shape), outs[0].stride()[:3]
-    if len(xs) == 2:
-        k, k_out = xs[1], outs[1]
-        Hk = k.shape[1]
-        sk, sk_out = _row_strides("k", k, (B, Hk, L, D)), k_out.stride()[:3]
-        _same_device("k", k, index)
-        if k.dtype is not dtype:
-            raise TypeError("the operands must share a dtype")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    else:
-        Hk, sk, sk_out, kp, kop = 0, sx, sy, None, None
+    B, _, L, _ = shape = x.shape
     rotary_dim = _rotary_dim(freqs, index)
     pos, pos_stride = None, 0
     if positions is not None:
@@ -650,9 +629,39 @@ def _rotate(xs, positions, freqs, mscale, interleaved, inverse, outs=None):
             raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
         pos = positions.data_ptr()
         pos_stride = pst[0] if B > 1 else 0
-    _launch("fa_rotary", index, xs[0].data_ptr(), kp, outs[0].data_ptr(), kop,
-            _Strides4(*sx, *sk, *sy, *sk_out), pos, pos_stride, freqs.data_ptr(), rotary_dim,
-            float(mscale), interleaved, inverse, B, H, Hk, L, D, dt)
+    return index, shape, x.dtype, dt, pos, pos_stride, freqs.data_ptr(), rotary_dim, \
+        float(mscale), interleaved
+
+
+def _rotate(xs, plan, inverse, outs=None):
+    """The library call for one or two views that ``plan`` fits; returns the outputs."""
+    import torch
+    index, (B, H, L, D), dtype, dt, pos, pos_stride, freqs, rotary_dim, mscale, interleaved = plan
+    if outs is None:
+        xs = [_kernel_view(t) for t in xs]
+        outs = [torch.empty_like(t) for t in xs]
+    else:
+        for o, t in zip(outs, xs):
+            _row_strides("out", o, t.shape)
+            _same_device("out", o, index)
+            if o.dtype is not dtype:
+                raise TypeError("out must have the dtype of x")
+    x, y = xs[0], outs[0]
+    if x.shape[1] != H:  # (the keys alone: their gradient where the queries have none)
+        H = x.shape[1]
+    sx, sy = _row_strides("x", x, (B, H, L, D)), y.stride()[:3]
+    if len(xs) == 2:
+        k, k_out = xs[1], outs[1]
+        Hk = k.shape[1]
+        sk, sk_out = _row_strides("k", k, (B, Hk, L, D)), k_out.stride()[:3]
+        if k.dtype is not dtype or k.get_device() != index:
+            raise TypeError("the operands must share a dtype and a device")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    else:
+        Hk, sk, sk_out, kp, kop = 0, sx, sy, None, None
+    _launch("fa_rotary", index, x.data_ptr(), kp, y.data_ptr(), kop,
+            _Strides4(*sx, *sk, *sy, *sk_out), pos, pos_stride, freqs, rotary_dim, mscale,
+            interleaved, inverse, B, H, Hk, L, D, dt)
     return outs
 
 
@@ -662,7 +671,7 @@ def rotary_apply(x, positions, freqs, mscale: float = 1.0, interleaved: bool = F
     autograd.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale``
     from ``rotary_freqs``.  ``out`` may be ``x`` (in place); ``inverse`` turns backwards.  The other
     arguments as in fa_rotary (fa.h)."""
-    return _rotate([x], positions, freqs, mscale, interleaved, inverse,
+    return _rotate([x], _rotary_plan(x, positions, freqs, mscale, interleaved), inverse,
                    None if out is None else [out])[0]
 
 
@@ -679,28 +688,24 @@ def _rotary_autograd():
             (and can itself be differentiated)."""
 
             @staticmethod
-            def forward(ctx, positions, freqs, mscale, interleaved, inverse, *xs):
-                ctx.save_for_backward(positions, freqs)
-                ctx.args = (mscale, interleaved, inverse)
-                return tuple(_rotate(list(xs), positions, freqs, mscale, interleaved, inverse))
+            def forward(ctx, positions, freqs, plan, inverse, *xs):
+                ctx.save_for_backward(positions, freqs)  # (the plan holds their addresses)
+                ctx.plan, ctx.inverse = plan, inverse
+                return tuple(_rotate(xs, plan, inverse))
 
             @staticmethod
             def backward(ctx, *grads):
                 positions, freqs = ctx.saved_tensors
-                mscale, interleaved, inverse = ctx.args
-                out = [None] * len(grads)
-                want = [i for i, g in enumerate(grads)
-                        if g is not None and ctx.needs_input_grad[5 + i]]
-                if want:
-                    args = (mscale, interleaved, not inverse)
-                    gs = [grads[i] for i in want]
-                    if torch.is_grad_enabled():  # a graph of the gradient is wanted
-                        turned = _Rotary.apply(positions, freqs, *args, *gs)
-                    else:
-                        turned = _rotate(gs, positions, freqs, *args)
-                    for i, g in zip(want, turned):
-                        out[i] = g
-                return (None,) * 5 + tuple(out)
+                want = [g is not None and n for g, n in zip(grads, ctx.needs_input_grad[4:])]
+                gs = [g for g, w in zip(grads, want) if w]
+                if not gs:
+                    turned = ()
+                elif torch.is_grad_enabled():  # a graph of the gradient is wanted
+                    turned = _Rotary.apply(positions, freqs, ctx.plan, not ctx.inverse, *gs)
+                else:
+                    turned = _rotate(gs, ctx.plan, not ctx.inverse)
+                turned = iter(turned)
+                return (None, None, None, None, *[next(turned) if w else None for w in want])
 
         _rotary_function = _Rotary
     return _rotary_function
@@ -716,9 +721,10 @@ def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = Fals
     import torch
     if k.dim() != 4:
         raise ValueError("rotary operands are [B, H, L, D] views")
+    plan = _rotary_plan(q, positions, freqs, mscale, interleaved)
     if (q.requires_grad or k.requires_grad) and torch.is_grad_enabled():
-        return _rotary_autograd().apply(positions, freqs, mscale, interleaved, False, q, k)
-    return tuple(_rotate([q, k], positions, freqs, mscale, interleaved, False))
+        return _rotary_autograd().apply(positions, freqs, plan, False, q, k)
+    return tuple(_rotate((q, k), plan, False))
 
 
 # ---------------------------------------------------------------------------------------

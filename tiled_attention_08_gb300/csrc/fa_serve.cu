@@ -284,7 +284,6 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out,
     p.D = D;
     p.inverse = inverse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!bind_context()) return FA_ERR_CUDA;
     return traced_launch(0, s, [&] { return launch_rotary(p, dtype == FA_BF16, s); }) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
@@ -342,7 +341,6 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
     p.D = D;
     p.num_pages = num_pages;
     p.max_pages = max_pages;
-    if (!bind_context()) return FA_ERR_CUDA;
     p.status = status_ptr();
     if (!p.status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -394,7 +392,6 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
     p.D = D;
     p.num_pages = num_pages;
     p.max_pages = max_pages;
-    if (!bind_context()) return FA_ERR_CUDA;
     p.status = status_ptr();
     if (!p.status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
