@@ -1,10 +1,9 @@
 """Rotary positions (fa_rotary) against the definition in 64 bits, through the public calls.
 
-Tolerance.  The kernel forms an angle in [-pi, pi] with a relative error of at most 2^-23 (the
-exact reduction leaves under 2^-33 turns for positions below 2^31, the conversion to fp32 and
-the multiplication by 2 pi each half a step) and takes the hardware's sine and cosine, each within
-2^-21.  A result y = x1 c - x2 s is therefore off by at most
-(|x1| + |x2|) mscale (pi 2^-22 + 2^-21 + 2^-22) < 1.5e-6 (|x1| + |x2|) mscale before its one
+Tolerance.  The exact reduction leaves under 2^-33 turns for positions below 2^31; the angle, at
+most an eighth of a turn once the nearest quarter is split off, and its sine and cosine are each
+within a few units of 2^-24, and so are the products and the sum.  A result y = x1 c - x2 s is
+therefore off by well under 1.5e-6 (|x1| + |x2|) mscale (25 units of 2^-24) before its one
 rounding to 16 bits, which is off by half a step: eps/2 of the value (and half the smallest
 subnormal, 2^-25, in fp16).
 """

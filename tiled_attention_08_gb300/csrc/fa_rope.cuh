@@ -9,16 +9,21 @@ namespace fa {
 // 64-bit fixed-point fraction (freq = theta / (2 pi) * 2^64), so the wrapped 64-bit product
 // position * freq is the angle reduced modulo one turn, exactly: for |position| < 2^31 the error
 // left is that of freq's rounding, under 2^-33 turns, where a 32-bit product would have lost
-// 2^-24 of up to 2^31 radians.  Its top 32 bits, as a signed fraction of a turn in [-1/2, 1/2),
-// become an fp32 angle in [-pi, pi] (relative error 2^-23), where the hardware's sine and cosine
-// are within 2^-21: far below half a step of the 16-bit (2^-9, 2^-12) and 8-bit results.
+// 2^-24 of up to 2^31 radians.  The nearest quarter turn is split off in integers too, so that
+// the rest, at most an eighth of a turn, becomes an fp32 with an error of 2^-27 half turns.  The
+// hardware's sine and cosine (2^-21) would do for 16-bit results, but move eight times as many
+// values of an 8-bit cache over a rounding border as fp32's own rounding; sincospif costs a
+// few more instructions per angle, which all heads of a token share.
 __device__ __forceinline__ void rope_cos_sin(int position, long long freq, float mscale, float& c,
                                              float& s) {
-    const long long turns = (long long)position * freq;  // wraps modulo one turn
-    const float a = (float)(int)(turns >> 32) * 1.4629180792671596e-09f;  // 2 pi / 2^32
-    __sincosf(a, &s, &c);
-    c *= mscale;
-    s *= mscale;
+    const uint32_t turns = (uint32_t)(((long long)position * freq) >> 32);  // 2^32 = one turn
+    const uint32_t quarter = (turns + 0x20000000u) >> 30;
+    float sn, cs;
+    sincospif((float)(int)(turns - (quarter << 30)) * 4.656612873077393e-10f, &sn, &cs);  // 2^-31
+    c = ((quarter & 1u) ? sn : cs) * mscale;
+    s = ((quarter & 1u) ? cs : sn) * mscale;
+    if (((quarter + 1u) & 2u)) c = -c;  // quarters 1 and 2
+    if (quarter & 2u) s = -s;           // quarters 2 and 3
 }
 
 }  // namespace fa
