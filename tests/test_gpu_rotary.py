@@ -216,6 +216,34 @@ def test_rotary_streams_graph_and_empty():
     assert fa.rotary_apply(x[:0], None, freqs, mscale).shape == (0, 2, 16, 64)
 
 
+def test_rotary_forward_and_backward_in_a_graph():
+    """Both directions captured and replayed on new values (no eager graph of the leaves is alive:
+    torch refuses such a capture, whatever the operation)."""
+    freqs, mscale = fa.rotary_freqs(64)
+    q = randn(1, 2, 32, 64, dtype=torch.bfloat16).requires_grad_()
+    k = randn(1, 1, 32, 64, dtype=torch.bfloat16, seed=1).requires_grad_()
+    gq, gk = randn(1, 2, 32, 64, dtype=torch.bfloat16, seed=2), randn(1, 1, 32, 64, dtype=torch.bfloat16, seed=3)
+
+    def step():
+        out = fa.rotary(q, k, None, freqs, mscale)
+        return torch.autograd.grad(out, (q, k), (gq, gk))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dq, dk = step()
+    gq.mul_(-2.0)
+    gk.add_(1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dq, fa.rotary_apply(gq, None, freqs, mscale, inverse=True))
+    assert torch.equal(dk, fa.rotary_apply(gk, None, freqs, mscale, inverse=True))
+
+
 def test_rotary_then_attention_depends_on_distances_only():
     """Shifting every position by the same amount leaves attention as it is (relative positions):
     O moves by the 16-bit rounding of the rotated operands alone."""
