@@ -18,7 +18,6 @@ TFLOPS to FlashAttention", sections 4.2-4.3).
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -514,64 +513,32 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
 
 # ---------------------------------------------------------------------------------------
 # Operators around attention.  The smallest of these calls run for a few microseconds on the GPU, so
-# the checks below read each property of a tensor once and the calls go straight to the library.
+# argument checks, allocation and the autograd node are in C++ (csrc/fa_torch.cpp), over the same
+# C ABI.
 # ---------------------------------------------------------------------------------------
-_raw_stream = _current_device = None
-_Strides2, _Strides4 = ctypes.c_int64 * 6, ctypes.c_int64 * 12  # fa_strides[2], fa_strides[4]
+_binding = None
 
 
-def _launch(name, index, *args):
-    """The library's entry point ``name`` on the current stream of CUDA device ``index`` (made
-    current for the call where it is not); raises on a status other than FA_OK."""
-    global _raw_stream, _current_device
-    if _raw_stream is None:
-        import torch
-        _current_device = torch.cuda.current_device
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda i: torch.cuda.current_stream(i).cuda_stream)
-    fn = getattr(_lib or load_library(), name)
-    if index == _current_device():
-        status = fn(*args, _raw_stream(index))
-    else:
-        import torch
-        with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
-    if status != FA_OK:
-        raise FaError(name, status)
+def _ops():
+    """The torch binding of these calls (raises if it was not built)."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are what the binding links to)
+        load_library()
+        path = os.path.join(os.path.dirname(_LIB_PATH), "fa_torch.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"fa_torch.so not built ({path}); run "
+                               "`python -m tiled_attention_08_gb300.build` first")
+        spec = importlib.util.spec_from_file_location("fa_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(FaError)
+        _binding = module
+    return _binding
 
 
-def _cuda_index(name, t):
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return index
-
-
-def _same_device(name, t, index):
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
-
-
-def _row_strides(name, t, shape):
-    """(batch, head, row) element strides of a view of the given [B, H, L, D] shape."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    if st[3] != 1:
-        raise ValueError(f"{name}: the last (D) dimension must be contiguous")
-    return st[:3]
-
-
-def _int32_vector(name, t, n, index):
-    import torch
-    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
-    _same_device(name, t, index)
-
-
-# ---------------------------------------------------------------------------------------
-# Rotary positions
-# ---------------------------------------------------------------------------------------
 def rotary_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
                  factor: float = 1.0, original_len: float = 0.0, device="cuda"):
     """The frequency table of ``rotary`` and ``cache_append`` and the factor ``mscale``:
@@ -588,127 +555,13 @@ def rotary_freqs(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
     return torch.tensor(freqs, dtype=torch.int64, device=device), mscale
 
 
-def _rotary_dim(freqs, index):
-    import torch
-    if freqs.dtype is not torch.int64 or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise TypeError("freqs must be a contiguous one-dimensional int64 tensor (rotary_freqs)")
-    _same_device("freqs", freqs, index)
-    return 2 * freqs.shape[0]
-
-
-def _kernel_view(t):
-    """`t` itself where the kernels can read its strides, else a contiguous copy (an expanded
-    gradient, for one, has strides of 0)."""
-    B, H, _, _ = t.shape
-    b, h, l, d = t.stride()
-    if d == 1 and not (b | h | l) & 7 and l > 0 and (h > 0 or H == 1) and (b > 0 or B == 1) and \
-            not t.data_ptr() & 15:
-        return t
-    return t.contiguous()
-
-
-def _rotary_plan(x, positions, freqs, mscale, interleaved):
-    """What a rotation of [B, H, L, D] views like x needs apart from them, checked: (device index,
-    shape, dtype, trailing arguments of fa_rotary by name)."""
-    import torch
-    index = _cuda_index("x", x)
-    if x.dim() != 4:
-        raise ValueError("rotary operands are [B, H, L, D] views")
-    dt = _dtype_code(x)
-    B, _, L, _ = shape = x.shape
-    rotary_dim = _rotary_dim(freqs, index)
-    pos, pos_stride = None, 0
-    if positions is not None:
-        if positions.dtype is not torch.int32:
-            raise TypeError("positions must be int32")
-        _same_device("positions", positions, index)
-        ps, pst = positions.shape, positions.stride()
-        if ps == (L,):
-            ps, pst = (B, L), (0, *pst)
-        if ps != (B, L) or (L > 1 and pst[1] != 1):
-            raise ValueError(f"positions must be [L] or [B, L] = ({B}, {L}) with contiguous rows")
-        pos = positions.data_ptr()
-        pos_stride = pst[0] if B > 1 else 0
-    return index, shape, x.dtype, dt, pos, pos_stride, freqs.data_ptr(), rotary_dim, \
-        float(mscale), interleaved
-
-
-def _rotate(xs, plan, inverse, outs=None):
-    """The library call for one or two views that ``plan`` fits; returns the outputs."""
-    import torch
-    index, (B, H, L, D), dtype, dt, pos, pos_stride, freqs, rotary_dim, mscale, interleaved = plan
-    if outs is None:
-        xs = [_kernel_view(t) for t in xs]
-        outs = [torch.empty_like(t) for t in xs]
-    else:
-        for o, t in zip(outs, xs):
-            _row_strides("out", o, t.shape)
-            _same_device("out", o, index)
-            if o.dtype is not dtype:
-                raise TypeError("out must have the dtype of x")
-    x, y = xs[0], outs[0]
-    if x.shape[1] != H:  # (the keys alone: their gradient where the queries have none)
-        H = x.shape[1]
-    sx, sy = _row_strides("x", x, (B, H, L, D)), y.stride()[:3]
-    if len(xs) == 2:
-        k, k_out = xs[1], outs[1]
-        Hk = k.shape[1]
-        sk, sk_out = _row_strides("k", k, (B, Hk, L, D)), k_out.stride()[:3]
-        if k.dtype is not dtype or k.get_device() != index:
-            raise TypeError("the operands must share a dtype and a device")
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    else:
-        Hk, sk, sk_out, kp, kop = 0, sx, sy, None, None
-    _launch("fa_rotary", index, x.data_ptr(), kp, y.data_ptr(), kop,
-            _Strides4(*sx, *sk, *sy, *sk_out), pos, pos_stride, freqs, rotary_dim, mscale,
-            interleaved, inverse, B, H, Hk, L, D, dt)
-    return outs
-
-
 def rotary_apply(x, positions, freqs, mscale: float = 1.0, interleaved: bool = False,
                  inverse: bool = False, out=None):
     """Rotary positions on one [B, H, L, D] view (bf16 or fp16, contiguous last dimension), outside
     autograd.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale``
     from ``rotary_freqs``.  ``out`` may be ``x`` (in place); ``inverse`` turns backwards.  The other
     arguments as in fa_rotary (fa.h)."""
-    return _rotate([x], _rotary_plan(x, positions, freqs, mscale, interleaved), inverse,
-                   None if out is None else [out])[0]
-
-
-_rotary_function = None
-
-
-def _rotary_autograd():
-    global _rotary_function
-    if _rotary_function is None:
-        import torch
-
-        class _Rotary(torch.autograd.Function):
-            """Linear in its tensors, so the backward is the same function turned the other way
-            (and can itself be differentiated)."""
-
-            @staticmethod
-            def forward(ctx, positions, freqs, plan, inverse, *xs):
-                ctx.save_for_backward(positions, freqs)  # (the plan holds their addresses)
-                ctx.plan, ctx.inverse = plan, inverse
-                return tuple(_rotate(xs, plan, inverse))
-
-            @staticmethod
-            def backward(ctx, *grads):
-                positions, freqs = ctx.saved_tensors
-                want = [g is not None and n for g, n in zip(grads, ctx.needs_input_grad[4:])]
-                gs = [g for g, w in zip(grads, want) if w]
-                if not gs:
-                    turned = ()
-                elif torch.is_grad_enabled():  # a graph of the gradient is wanted
-                    turned = _Rotary.apply(positions, freqs, ctx.plan, not ctx.inverse, *gs)
-                else:
-                    turned = _rotate(gs, ctx.plan, not ctx.inverse)
-                turned = iter(turned)
-                return (None, None, None, None, *[next(turned) if w else None for w in want])
-
-        _rotary_function = _Rotary
-    return _rotary_function
+    return (_binding or _ops()).rotary_apply(x, positions, freqs, mscale, interleaved, inverse, out)
 
 
 def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = False):
@@ -717,66 +570,9 @@ def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = Fals
     [B, L, H, D] tensors transposed, or the parts of a packed [B, L, 3, H, D] tensor, are read in
     place.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale`` from
     ``rotary_freqs``.  The rotated tensors go to ``attention`` (or, one row per sequence, to
-    ``decode_paged``)."""
-    import torch
-    if k.dim() != 4:
-        raise ValueError("rotary operands are [B, H, L, D] views")
-    plan = _rotary_plan(q, positions, freqs, mscale, interleaved)
-    if (q.requires_grad or k.requires_grad) and torch.is_grad_enabled():
-        return _rotary_autograd().apply(positions, freqs, plan, False, q, k)
-    return tuple(_rotate((q, k), plan, False))
-
-
-# ---------------------------------------------------------------------------------------
-# The paged cache: writing rows and reading them back
-# ---------------------------------------------------------------------------------------
-def _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index):
-    """(cache_dtype, num_pages, H, D, k_exp pointer, v_exp pointer) of a checked pair of caches."""
-    import torch
-    shape = k_cache.shape
-    kind = k_cache.dtype
-    if len(shape) != 4 or shape[2] != FA_PAGE_TOKENS or v_cache.shape != shape:
-        raise ValueError("caches must be [num_pages, H, FA_PAGE_TOKENS, D]")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("the caches must be contiguous")
-    if not k_cache.get_device() == v_cache.get_device() == index:
-        raise ValueError(f"the caches are on {k_cache.device} and {v_cache.device}, expected "
-                         f"cuda:{index}")
-    if v_cache.dtype is not kind:
-        raise TypeError("k_cache and v_cache must share a dtype")
-    num_pages, H, _, D = shape
-    if k_exp is None and v_exp is None:
-        if kind is not dtype:
-            raise TypeError(f"the cache holds {kind}, the call's tensors {dtype}; an e4m3 cache "
-                            "needs k_exp and v_exp")
-        return FA_CACHE_16BIT, num_pages, H, D, None, None
-    if kind is not torch.float8_e4m3fn:
-        raise TypeError("a cache with exponents must be float8_e4m3fn")
-    es = (num_pages, H, FA_PAGE_TOKENS)
-    u8 = torch.uint8
-    if k_exp is None or v_exp is None or not (
-            k_exp.dtype is u8 and v_exp.dtype is u8 and k_exp.shape == es and v_exp.shape == es and
-            k_exp.is_contiguous() and v_exp.is_contiguous() and
-            k_exp.get_device() == v_exp.get_device() == index):
-        raise ValueError("k_exp and v_exp must be contiguous uint8 [num_pages, H, FA_PAGE_TOKENS] "
-                         "tensors on the cache's device")
-    return FA_CACHE_E4M3, num_pages, H, D, k_exp.data_ptr(), v_exp.data_ptr()
-
-
-def _tables(block_tables, seq_lens, B, index):
-    """max_pages of a checked block table and its lengths."""
-    import torch
-    i32 = torch.int32
-    if block_tables.dtype is not i32 or seq_lens.dtype is not i32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    shape = block_tables.shape
-    if len(shape) != 2 or shape[0] != B or seq_lens.shape != (B,):
-        raise ValueError("block_tables must be [B, max_pages] and seq_lens [B]")
-    if not (block_tables.is_contiguous() and seq_lens.is_contiguous()):
-        raise ValueError("block_tables and seq_lens must be contiguous")
-    if not block_tables.get_device() == seq_lens.get_device() == index:
-        raise ValueError(f"block_tables and seq_lens must be on cuda:{index}")
-    return shape[1]
+    ``decode_paged``).  As for any operation, torch refuses to capture a backward into a CUDA
+    graph while an eager graph of the same leaves is alive."""
+    return (_binding or _ops()).rotary(q, k, positions, freqs, mscale, interleaved)
 
 
 def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, k_exp=None,
@@ -787,31 +583,8 @@ def cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens=None, 
     float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` (uint8 [num_pages, H, FA_PAGE_TOKENS]),
     into which rows are quantised.  With ``freqs`` (``rotary_freqs``) each key is first rotated by
     its token index.  See fa_cache_append in fa.h."""
-    index = _cuda_index("k", k)
-    dt = _dtype_code(k)
-    shape = k.shape
-    if len(shape) != 4:
-        raise ValueError("k and v must be [B, H, L, D] views")
-    B, H, L, D = shape
-    ks, vs = _row_strides("k", k, shape), _row_strides("v", v, shape)
-    if v.dtype is not k.dtype:
-        raise TypeError("k and v must share a dtype")
-    _same_device("v", v, index)
-    kind, num_pages, Hc, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, k.dtype, index)
-    if Hc != H or Dc != D:
-        raise ValueError(f"the cache has {Hc} heads of {Dc}, k has {H} of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, index)
-    new, fp, rotary_dim = None, None, 0
-    if new_lens is not None:
-        _int32_vector("new_lens", new_lens, B, index)
-        new = new_lens.data_ptr()
-    if freqs is not None:
-        rotary_dim = _rotary_dim(freqs, index)
-        fp = freqs.data_ptr()
-    _launch("fa_cache_append", index, k.data_ptr(), v.data_ptr(), _Strides2(*ks, *vs),
-            k_cache.data_ptr(), v_cache.data_ptr(), kep, vep, block_tables.data_ptr(),
-            seq_lens.data_ptr(), new, fp, rotary_dim, float(mscale), interleaved, B, H, L, D, num_pages,
-            max_pages, dt, kind)
+    (_binding or _ops()).cache_append(k, v, k_cache, v_cache, block_tables, seq_lens, new_lens, k_exp,
+                                      v_exp, freqs, mscale, interleaved)
 
 
 def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None, v_exp=None,
@@ -819,93 +592,16 @@ def cache_read(k_cache, v_cache, block_tables, seq_lens, length: int, k_exp=None
     """Tokens 0 .. length-1 of every sequence of a paged cache as dense (k, v), each
     [B, H, length, D] of ``dtype`` (bf16 or fp16; the cache's own when it is 16-bit); rows past a
     sequence's end are zeros.  ``out``: an optional pair of views to write.  See fa_cache_read."""
-    import torch
-    index = _cuda_index("k_cache", k_cache)
-    if dtype is None:
-        dtype = out[0].dtype if out is not None else k_cache.dtype
-    kind, num_pages, H, D, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, dtype, index)
-    B = seq_lens.shape[0]
-    max_pages = _tables(block_tables, seq_lens, B, index)
-    shape = (B, H, length, D)
-    if out is None:
-        k = torch.empty(shape, device=k_cache.device, dtype=dtype)
-        v = torch.empty_like(k)
-        ks = vs = k.stride()[:3]
-    else:
-        k, v = out
-        if k.dtype is not dtype or v.dtype is not dtype:
-            raise TypeError("out must have the call's dtype")
-        ks, vs = _row_strides("out[0]", k, shape), _row_strides("out[1]", v, shape)
-        _same_device("out[0]", k, index)
-        _same_device("out[1]", v, index)
-    dt = _dtype_code(k)
-    _launch("fa_cache_read", index, k_cache.data_ptr(), v_cache.data_ptr(), kep, vep,
-            block_tables.data_ptr(), seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(),
-            _Strides2(*ks, *vs), B, H, length, D, num_pages, max_pages, dt, kind)
-    return k, v
+    k, v = out if out is not None else (None, None)
+    return (_binding or _ops()).cache_read(k_cache, v_cache, block_tables, seq_lens, length, k_exp,
+                                           v_exp, dtype, k, v)
 
 
-# ---------------------------------------------------------------------------------------
-# Decode with grouped heads, and with a shared prefix
-# ---------------------------------------------------------------------------------------
-@functools.lru_cache(maxsize=256)
-def _decode_need(B, Hq, Hk, D, max_pages):
-    return fa_decode_workspace_bytes_ex(B, Hq, Hk, D, max_pages)
-
-
-@functools.lru_cache(maxsize=256)
-def _prefix_need(B, Hq, Hk, D, prefix_len, max_pages):
-    return fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages)
-
-
-def _decode_outputs(q, out, lse):
-    """Checked (device index, B, Hq, D, dtype code, o, lse) of a decode step."""
-    import torch
-    index = _cuda_index("q", q)
-    shape = q.shape
-    if len(shape) != 3 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous [B, H, D] tensor")
-    dt = _dtype_code(q)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        if out.dtype is not q.dtype or out.shape != shape or not out.is_contiguous():
-            raise ValueError("out must be a contiguous tensor like q")
-        _same_device("out", out, index)
-    if lse is None:
-        lse = torch.empty(shape[:2], device=q.device, dtype=torch.float32)
-    else:
-        if lse.dtype is not torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 [B, H] tensor")
-        _same_device("lse", lse, index)
-    return index, *shape, dt, out, lse
-
-
-def _workspace(workspace, need, q, index):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a new one where any is needed; the
-    tensor keeps it alive until the call has been enqueued."""
-    import torch
-    if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
-    else:
-        _same_device("workspace", workspace, index)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace, k_exp,
-                     v_exp):
-    index, B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
-    kind, num_pages, Hk, Dc, kep, vep = _paged_cache(k_cache, v_cache, k_exp, v_exp, q.dtype, index)
-    if Dc != D:
-        raise ValueError(f"the cache has heads of {Dc}, q of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, index)
-    wp, wb, keep = _workspace(workspace, _decode_need(B, Hq, Hk, D, max_pages), q, index)
-    _launch("fa_decode_paged_ex", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kep,
-            vep, block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), l.data_ptr(), wp, wb, B,
-            Hq, Hk, D, num_pages, max_pages, 1.0 / math.sqrt(D) if scale is None else float(scale), dt, kind)
-    return o, l
+def _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale=None, out=None, lse=None,
+                     workspace=None, k_exp=None, v_exp=None):
+    """decode_paged through fa_decode_paged_ex, whatever the caches."""
+    return (_binding or _ops()).decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out,
+                                                lse, workspace, k_exp, v_exp)
 
 
 def decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, block_tables, seq_lens,
@@ -916,23 +612,5 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, blo
     ``block_tables[b]``), over 16-bit caches [num_pages, Hk, FA_PAGE_TOKENS, D].  The prefix is read
     once for the whole batch.  Returns O [B, Hq, D] and LSE [B, Hq] (fp32).  See
     fa_decode_shared_prefix in fa.h."""
-    import torch
-    index, B, Hq, D, dt, o, l = _decode_outputs(q, out, lse)
-    _, num_pages, Hk, Dc, _, _ = _paged_cache(k_cache, v_cache, None, None, q.dtype, index)
-    if Dc != D:
-        raise ValueError(f"the cache has heads of {Dc}, q of {D}")
-    max_pages = _tables(block_tables, seq_lens, B, index)
-    if prefix_table.dtype is not torch.int32 or prefix_table.dim() != 1 or \
-            not prefix_table.is_contiguous():
-        raise TypeError("prefix_table must be a contiguous one-dimensional int32 tensor")
-    _same_device("prefix_table", prefix_table, index)
-    prefix_len = int(prefix_len)
-    if prefix_len < 0 or prefix_len > FA_PAGE_TOKENS * prefix_table.shape[0]:
-        raise ValueError(f"prefix_table has room for {FA_PAGE_TOKENS * prefix_table.shape[0]} tokens, "
-                         f"not {prefix_len}")
-    wp, wb, keep = _workspace(workspace, _prefix_need(B, Hq, Hk, D, prefix_len, max_pages), q, index)
-    _launch("fa_decode_shared_prefix", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            prefix_table.data_ptr(), prefix_len, block_tables.data_ptr(), seq_lens.data_ptr(),
-            o.data_ptr(), l.data_ptr(), wp, wb, B, Hq, Hk, D, num_pages, max_pages,
-            1.0 / math.sqrt(D) if scale is None else float(scale), dt)
-    return o, l
+    return (_binding or _ops()).decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len,
+                                                     block_tables, seq_lens, scale, out, lse, workspace)
