@@ -229,7 +229,7 @@ def test_grouped_decode_workspace():
         q_rows = 8 if g <= 8 else 16
         chunk = min(B, 1024)
         units = chunk * Hk * -(-g // q_rows)
-        ctas = min(4 * 152, max(1, -(-units * max_pages // 16)))
+        ctas = min(4 * 152, max(1, -(-units * max_pages // 4)))
         up = lambda n: (n + 15) // 16 * 16  # noqa: E731
         slots = 2 * 4 * ctas * min(g, q_rows) * (3 if units >= 2 * 4 * 152 * 4 else 1)
         return up(8 * units) + up(slots * D * 4) + up(slots * 4)
@@ -256,7 +256,7 @@ def test_grouped_decode_split_model(lens, per_seq, warps, rounds):
     for n in pages:
         cum.append(cum[-1] + n)
     total = cum[-1] * per_seq
-    workers = max(1, min(total // 4, 128 * len(lens) * per_seq, warps))
+    workers = max(1, min(total if total <= 1024 else total // 4, 128 * len(lens) * per_seq, warps))
     if total < 16 * workers:
         rounds = 1
     at = [0, total // 64 * 52, total // 64 * 60, total] if rounds == 3 else [0, total]
@@ -350,7 +350,7 @@ def test_shared_prefix_workspace():
         rows_b = min(128, pairs_b)
         n_pairs = ((pairs_b + rows_b - 1) // rows_b + 1) // 2
         units = Hk * n_pairs * tiles
-        grid = min(152, (units + 3) // 4)
+        grid = min(152, max((units + 3) // 4, min(units, 38)))
         first = [units * c // grid for c in range(grid + 1)]
         most = 0
         for item in range(Hk * n_pairs):

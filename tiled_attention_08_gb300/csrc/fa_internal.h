@@ -313,11 +313,11 @@ cudaError_t launch_prefix(const PrefixParams& p, int D, bool bf16, cudaStream_t 
 void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p);
 cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s);
 // Query rows of a block (8 or 16), the most warps that a step may launch (workspace), and those it
-// does.
+// does (busy_sms: SMs that an earlier kernel still holds).
 int gqa_q_rows(int group);
 int gqa_warps(int B, int Hk, int group, int max_pages);
 int gqa_rounds(int B, int Hk, int group);
-int gqa_launched_warps(int warps, int D, bool q8, int group);
+int gqa_launched_warps(int B, int Hk, int group, int max_pages, int D, bool q8, int busy_sms);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);
 

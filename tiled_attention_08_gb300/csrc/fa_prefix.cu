@@ -101,6 +101,9 @@ __global__ void __launch_bounds__(PrefixCfg<D, BF16>::kThreads, 1)
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
         abort_flag = 0;
         mbar_init(&bar_qf, 1);
         mbar_init(&bar_qe, 1);
@@ -423,9 +426,11 @@ void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p) {
     p->n_pairs = (p->n_tiles + 1) / 2;
     p->key_tiles = (int)(((long long)prefix_len + kTileRows - 1) / kTileRows);
     const long long units = (long long)Hk * p->n_pairs * p->key_tiles;
-    // One CTA per SM, each with four units at least (a part's read-out costs about as much).
-    const long long want = (units + 3) / 4;
-    p->grid = (int)(want < kGrid ? want : kGrid);
+    // One CTA per SM, each with four units at least (a part's read-out costs about as much, and the
+    // merge reads it again), but a quarter of the SMs at least where there are so many units: a unit
+    // takes 2 us, which is all that counts in a short call.
+    const long long want = (units + 3) / 4, least = units < kGrid / 4 ? units : kGrid / 4;
+    p->grid = (int)(want > kGrid ? kGrid : want < least ? least : want);
     // CTAs that share one pair's key tiles: at most this many (a stretch begins every
     // units / grid units).
     p->max_segments = 0;

@@ -134,7 +134,7 @@ DecodeWorkspace decode_workspace(int B, int Hq, int Hk, int D, int max_pages, bo
 // The decode kernel and the merge for the batch, kGqaMaxSequences at a time.  p holds everything
 // but what depends on the workspace and the chunk; `kernel` counts the traced kernels so far.
 cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* ws,
-                       const DecodeWorkspace& w, int n_prefix, int kernel, cudaStream_t s) {
+                       const DecodeWorkspace& w, int n_prefix, int busy_sms, int kernel, cudaStream_t s) {
     const size_t row_o = (size_t)p.Hq * D;
     p.q_blocks = q_blocks_of(p.group);
     p.slot_rows = slot_rows_of(p.group);
@@ -153,7 +153,7 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         c.full_lse = reinterpret_cast<float*>(ws + w.full_lse) + (size_t)b0 * p.Hq;
         c.early = p.early && b0 == 0;
         c.rounds = gqa_rounds(c.B, p.Hk, p.group);
-        c.warps = gqa_launched_warps(gqa_warps(c.B, p.Hk, p.group, p.max_pages), D, q8, p.group);
+        c.warps = gqa_launched_warps(c.B, p.Hk, p.group, p.max_pages, D, q8, c.early ? busy_sms : 0);
         cudaError_t e = traced_launch(kernel++, s, [&] { return launch_decode_gqa(c, D, bf16, q8, s); });
         if (e != cudaSuccess) return e;
         MergeParams m;
@@ -463,7 +463,8 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
     p.timeout_ns = wait_timeout_ns();
     if (!p.status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return run_decode(p, B, D, dtype == FA_BF16, q8, static_cast<uint8_t*>(workspace), w, 0, 0, s) ==
+    return run_decode(p, B, D, dtype == FA_BF16, q8, static_cast<uint8_t*>(workspace), w, 0, 0, 0,
+                      s) ==
                    cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
@@ -592,7 +593,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status;
     p.timeout_ns = wait_timeout_ns();
-    return run_decode(p, B, D, bf16, false, ws, w, pp.max_segments, n, s) == cudaSuccess ? FA_OK
+    return run_decode(p, B, D, bf16, false, ws, w, pp.max_segments, pp.grid, n, s) == cudaSuccess ? FA_OK
                                                                                          : FA_ERR_CUDA;
 }
 
