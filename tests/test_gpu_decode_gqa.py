@@ -166,6 +166,34 @@ def test_query_rows_of_any_magnitude(power):
     check(o, lse, q, ks, vs, scale, dtype, True)
 
 
+@pytest.mark.parametrize("q8", [True, False], ids=["e4m3", "16bit"])
+def test_scores_of_any_size(q8):
+    """Scores around -1e33 and 1e33 (far outside the exponentials' range) and rows of one huge key."""
+    D, dtype, Hk = 64, torch.bfloat16, 1
+    kc, vc, ke, ve = make_cache(2, Hk, D, dtype, q8)
+    k = torch.zeros((2, Hk, 16, D), device="cuda", dtype=dtype)
+    k[:, :, :, 0] = 2.0 ** 40
+    k[:, :, 5, 0] = 2.0 ** 40 * 1.25   # the one key that counts (sign of q decides)
+    v = randn(2, Hk, 16, D, dtype=dtype)
+    bt = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    sl = torch.tensor([16, 1], dtype=torch.int32, device="cuda")
+    fa.cache_append(k, v, kc, vc, bt, torch.full_like(sl, 16), k_exp=ke, v_exp=ve)
+    held_v = gh.f64(fa.cache_read(kc, vc, bt, torch.full_like(sl, 16), 16, k_exp=ke, v_exp=ve, dtype=dtype)[1])
+    q = torch.zeros((2, 2, D), device="cuda", dtype=dtype)
+    q[:, 0, 0], q[:, 1, 0] = 2.0 ** 70, -(2.0 ** 70)
+    o, lse = fa._decode_paged_ex(q, kc, vc, bt, sl, 1.0, None, None, None, ke, ve)
+    assert status() == fa.FA_OK
+    big = 2.0 ** 110
+    o, lse = gh.f64(o), gh.f64(lse)
+    assert np.array_equal(o[0, 0], held_v[0, 0, 5]) and abs(lse[0, 0] / big - 1.25) <= 2.0 ** -22
+    # the others tie: the mean of 15 rows (P is exact: 1 and 0)
+    mean = held_v[0, 0][[i for i in range(16) if i != 5]].mean(0)
+    assert np.all(np.abs(o[0, 1] - mean) <= 2.0 ** -8 * np.abs(mean) + 2.0 ** -18)
+    assert abs(lse[0, 1] / big + 1.0) <= 2.0 ** -22
+    for h, s in ((0, 1.0), (1, -1.0)):  # one key alone, whatever its score
+        assert np.array_equal(o[1, h], held_v[1, 0, 0]) and abs(lse[1, h] / big - s) <= 2.0 ** -22
+
+
 def test_a_bad_row_stays_with_its_sequence_and_head():
     """A NaN key, an infinite value: the results of that sequence's head, no others'."""
     D, dtype, lens, Hk = 64, torch.bfloat16, [40, 40, 40], 2

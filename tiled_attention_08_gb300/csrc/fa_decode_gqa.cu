@@ -35,12 +35,12 @@
 //
 // Softmax in the log2 domain.  The reference of a column is only raised when a score exceeds it
 // by more than 2^8 (a warp vote), so the maximum over the lanes is rarely taken.  An e4m3 cache
-// needs two references: the sum of weights takes p_j = 2^(y_j - m); the products take
-// a_j = 2^(y_j + ev_j - mo) with the value row's exponent ev_j, so that a weight times its row's
-// scale neither overflows nor is lost in fp16, whatever the rows' magnitudes.  P is rounded to the
+// needs a second one: the sum of weights takes p_j = 2^(y_j - m); the products take
+// a_j = 2^((y_j - m) + (ev_j - eo)) with the value row's exponent ev_j, so that a weight times its
+// row's scale neither overflows nor is lost in fp16, whatever the rows' magnitudes.  (eo is relative
+// to m: added to y_j itself, ev_j would be lost behind a large score.)  P is rounded to the
 // cache's 16-bit type (fp16 for e4m3: 2^-12), as in the prefill kernels; sums stay fp32.
 #include <atomic>
-#include <cstdlib>
 #include <type_traits>
 
 #include "fa_e4m3.cuh"
@@ -66,15 +66,17 @@ constexpr int kGqaFewPages = 1024;  // ... where there are more than this many
 // parts (142 -> 158 us for 48 sequences of up to 16384 tokens with groups of 8), so three rounds
 // need at least two units per warp.
 struct GqaSplit {
-    long long at[4];  // round r has the pages [at[r], at[r + 1])
+    long long second, third, total;  // first pages of rounds 1 and 2 (total: there is none), the end
     int workers, rounds;
+    __device__ __forceinline__ long long at(int r) const {
+        return r == 0 ? 0 : r == 1 ? second : r == 2 ? third : total;
+    }
     __device__ __forceinline__ long long start(int r, int i) const {
-        return at[r] + (at[r + 1] - at[r]) * i / workers;
+        return at(r) + (at(r + 1) - at(r)) * i / workers;
     }
     __device__ __forceinline__ int worker_of(long long x) const {  // the one that has page x
-        int r = 0;
-        while (r + 1 < rounds && x >= at[r + 1]) ++r;
-        return r * workers + (int)(((x - at[r] + 1) * workers - 1) / (at[r + 1] - at[r]));
+        const int r = x >= third ? 2 : x >= second ? 1 : 0;
+        return r * workers + (int)(((x - at(r) + 1) * workers - 1) / (at(r + 1) - at(r)));
     }
 };
 // A page for each warp while there are few (latency is all: 13.1 -> 10.1 us for one sequence of 333
@@ -86,10 +88,9 @@ __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int ro
     GqaSplit s;
     s.workers = m < 1 ? 1 : m < warps ? (int)m : warps;
     s.rounds = total >= 16LL * s.workers ? rounds : 1;
-    s.at[0] = 0;
-    s.at[1] = s.rounds > 1 ? total / 64 * 52 : total;
-    s.at[2] = s.rounds > 1 ? total / 64 * 60 : total;
-    s.at[3] = total;
+    s.second = s.rounds > 1 ? total / 64 * 52 : total;
+    s.third = s.rounds > 1 ? total / 64 * 60 : total;
+    s.total = total;
     return s;
 }
 
@@ -145,13 +146,13 @@ template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     if constexpr (BF16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
             "{%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -176,10 +177,14 @@ __device__ __forceinline__ float column_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
+// A reference before any score: below every finite one, and finite, so that no difference of it is
+// a NaN (a masked -inf minus it is -inf).
+constexpr float kNoRef = -3.4028234663852886e38f;  // -FLT_MAX
+
 // Raises a reference to the column's maximum; returns the factor of what was summed under it.
 __device__ __forceinline__ float raise(float& ref, float top) {
     const float next = fmaxf(ref, column_max(top));
-    const float f = next == -INFINITY ? 1.0f : ex2_approx(ref - next);
+    const float f = ex2_approx(ref - next);
     ref = next;
     return f;
 }
@@ -296,14 +301,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     };
     const uint64_t policy = policy_evict_first();
     Batch prod = lookup(0), cons = prod, next = lookup(32);
-    auto issue = [&](int i) {  // page i of this warp into slot i % stages; the whole warp calls it
+    auto issue = [&](int i, int st) {  // page i of this warp into slot st = i % stages; the whole warp calls it
         if (i > 0 && (i & 31) == 0) {
             prod = next;
             next = lookup(i + 32);
         }
         const int ph = __shfl_sync(0xffffffffu, prod.page_head, i & 31);
         if (lane == 0) {
-            const int st = i % stages;
             uint64_t* bar = &bar_full[warp][st];
             uint8_t* dst = ring + st * (2 * C::kPageBytes);
             mbar_arrive_expect_tx(bar, 2 * C::kPageBytes + (Q8 ? 32 : 0));
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 tma_load_page(dst + C::kPageBytes + x * C::kBoxBytes, &p.tm_v, bar, x * 64, ph, policy);
         }
     };
-    for (int i = 0; i < min(stages, mine); ++i) issue(i);
+    for (int i = 0; i < min(stages, mine); ++i) issue(i, i);
 
     // Q fragments (B operand).  Step s of lane t covers elements elem(s) .. + 3: the order in
     // which the K rows are read below.
@@ -374,12 +378,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     };
 
     float acc[C::kTiles][NT][4];
-    float m[NT][2], mo[NT][2], l[NT][2];
+    float m[NT][2], eo[NT][2], l[NT][2];
     size_t row0 = 0;       // first query row of the unit
     int n_q = 0;           // queries of its block
     bool cut = false;      // the unit began in an earlier warp's stretch
     bool ok = true;
-    int done = 0;
+    int done = 0, st = 0;  // pages behind this one, and this one's slot
+    uint32_t parity = 0;   // of the slot's phase
     for (; done < mine; ++done) {
         if (done > 0 && (done & 31) == 0) cons = prod;  // (the ring is less than a batch ahead)
         const int flags = __shfl_sync(0xffffffffu, cons.flags, done & 31);
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    m[nt][j] = mo[nt][j] = -INFINITY;
+                    m[nt][j] = eo[nt][j] = kNoRef;
                     l[nt][j] = 0.0f;
                 }
 #pragma unroll
@@ -409,64 +414,97 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                     for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
             }
         }
-        const int st = done % stages;
-        ok = wait_warp(&bar_full[warp][st], (uint32_t)(done / stages) & 1u, nullptr, p.timeout_ns);
+        ok = wait_warp(&bar_full[warp][st], parity, nullptr, p.timeout_ns);
         if (!ok) break;
         const uint8_t* kp = ring + st * (2 * C::kPageBytes);
         const uint8_t* vp = kp + C::kPageBytes;
         const uint32_t ks = smem_u32(kp), vs = smem_u32(vp);
-        float c[NT][4];
+        constexpr bool kSmall = Q8 && D == 64;  // 64-byte rows
+        // ---- S^T = K Q^T: rows g and g + 8 of the page, even and odd steps apart ----
+        // (One accumulator where two query blocks already take turns.)
+        constexpr bool kTwo = NT == 1;
+        float c[NT][4], c2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[nt][j] = 0.0f;
-        // ---- S^T = K Q^T: rows g and g + 8 of the page ----
+            for (int j = 0; j < 4; ++j) c[nt][j] = c2[nt][j] = 0.0f;
         if constexpr (!Q8) {
+            uint4 lo[C::kBoxes][2], hi[C::kBoxes][2];
 #pragma unroll
-            for (int x = 0; x < C::kBoxes; ++x) {
+            for (int x = 0; x < C::kBoxes; ++x)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t u = (uint32_t)((2 * t + hf) ^ g) * 16;
-                    const uint4 lo = lds_u32x4(ks + x * C::kBoxBytes + g * 128 + u);
-                    const uint4 hi = lds_u32x4(ks + x * C::kBoxBytes + (g + 8) * 128 + u);
+                    const uint32_t u = ks + x * C::kBoxBytes + (uint32_t)((2 * t + hf) ^ g) * 16;
+                    lo[x][hf] = lds_u32x4(u + g * 128);
+                    hi[x][hf] = lds_u32x4(u + (g + 8) * 128);
+                }
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const int s = 4 * x + 2 * hf;
-                        mma16816<kMmaBf16>(c[nt], lo.x, hi.x, lo.y, hi.y, qf[s][nt][0], qf[s][nt][1]);
-                        mma16816<kMmaBf16>(c[nt], lo.z, hi.z, lo.w, hi.w, qf[s + 1][nt][0],
+                        const uint4 &a = lo[x][hf], &b = hi[x][hf];
+                        mma16816<kMmaBf16>(c[nt], a.x, b.x, a.y, b.y, qf[s][nt][0], qf[s][nt][1]);
+                        mma16816<kMmaBf16>(kTwo ? c2[nt] : c[nt], a.z, b.z, a.w, b.w, qf[s + 1][nt][0],
                                            qf[s + 1][nt][1]);
                     }
-                }
-            }
         } else {
             constexpr int kUnits = D / 64;  // 16-byte units of a row per lane
+            uint4 lo[kUnits], hi[kUnits];
 #pragma unroll
             for (int hf = 0; hf < kUnits; ++hf) {
-                uint32_t alo, ahi;
-                if constexpr (D == 128) {
-                    const uint32_t u = (uint32_t)((2 * t + hf) ^ g) * 16;
-                    alo = ks + g * 128 + u;
-                    ahi = ks + (g + 8) * 128 + u;
-                } else {  // 64-byte rows: unit index XOR (row / 2) % 4
-                    alo = ks + g * 64 + (uint32_t)(t ^ ((g >> 1) & 3)) * 16;
-                    ahi = alo + 8 * 64;
-                }
-                const uint4 lo = lds_u32x4(alo), hi = lds_u32x4(ahi);
-                const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+                // (64-byte rows: unit index XOR (row / 2) % 4)
+                const uint32_t u = D == 128 ? ks + g * 128 + (uint32_t)((2 * t + hf) ^ g) * 16
+                                            : ks + g * 64 + (uint32_t)(t ^ ((g >> 1) & 3)) * 16;
+                lo[hf] = lds_u32x4(u);
+                hi[hf] = lds_u32x4(u + 8 * C::kRowBytes);
+            }
+#pragma unroll
+            for (int hf = 0; hf < kUnits; ++hf) {
+                const uint32_t wl[4] = {lo[hf].x, lo[hf].y, lo[hf].z, lo[hf].w};
+                const uint32_t wh[4] = {hi[hf].x, hi[hf].y, hi[hf].z, hi[hf].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a0 = e4m3x2_to_f16x2(wl[i] & 0xffffu), a2 = e4m3x2_to_f16x2(wl[i] >> 16);
                     const uint32_t a1 = e4m3x2_to_f16x2(wh[i] & 0xffffu), a3 = e4m3x2_to_f16x2(wh[i] >> 16);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma16816<false>(c[nt], a0, a1, a2, a3, qf[4 * hf + i][nt][0], qf[4 * hf + i][nt][1]);
+                        mma16816<false>(kTwo && (i & 1) ? c2[nt] : c[nt], a0, a1, a2, a3, qf[4 * hf + i][nt][0],
+                                        qf[4 * hf + i][nt][1]);
                 }
             }
         }
-        // ---- online softmax over the page ----
+        // ---- V into registers, the slot to the page `stages` further on ----
+        // Unit g of keys 2t, 2t+1, 2t+8, 2t+9 (64-byte rows: half a unit).  Two query blocks leave no
+        // registers for that: they read V below, and free the slot after it.
+        // Slots past the sequence's end hold anything: their values count as zeros (their weights
+        // are zero, but zero times a NaN is not).
+        constexpr bool kEarly = NT == 1 && !Q8;
         const int left = flags & 31;  // tokens of this page
         const bool partial = left < kPageTokens;
-        float fk[2] = {1.0f, 1.0f}, ev[2] = {0.0f, 0.0f};  // rows g, g + 8
+        uint4 vq[kSmall ? 1 : C::kBoxes][4];
+        uint2 vh[4];
+        auto read_v = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+                const bool there = !partial || key < left;
+                if constexpr (kSmall) {
+                    vh[k] = lds_u32x2(vs + key * 64 + (uint32_t)((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
+                    if (!there) vh[k] = make_uint2(0u, 0u);
+                } else {
+                    vq[x][k] = lds_u32x4(vs + x * C::kBoxBytes + key * 128 + (uint32_t)(g ^ (key & 7)) * 16);
+                    if (!there) vq[x][k] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        };
+        auto release = [&]() __attribute__((always_inline)) {
+            __syncwarp();  // every lane has read the slot
+            if (done + stages < mine) issue(done + stages, st);
+        };
+        float fk[2] = {1.0f, 1.0f}, ev[2] = {0.0f, 0.0f};  // rows g, g + 8: factor of K, exponent of V
         if constexpr (Q8) {
             const uint8_t* ex = exps + st * 32;
 #pragma unroll
@@ -476,21 +514,38 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 ev[r] = E == kExpNan ? __uint_as_float(0x7fc00000u) : (float)((int)E - 127);
             }
         }
-        float z[NT][4];
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int x = 0; x < (kSmall ? 1 : C::kBoxes); ++x) read_v(x);
+            release();
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[nt][j] += c2[nt][j];
+        // ---- online softmax over the page ----
         bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = j >> 1;
-                float y = c[nt][j] * q_factor[nt][j & 1];
-                if constexpr (Q8) y *= fk[r];
-                float zz = Q8 ? y + ev[r] : y;
-                if (partial && g + 8 * r >= left) y = zz = -INFINITY;
-                c[nt][j] = y;
-                z[nt][j] = zz;
-                up |= y > m[nt][j & 1] + kRaise;
-                if constexpr (Q8) up |= zz > mo[nt][j & 1] + kRaise;
+            for (int j = 0; j < 4; ++j) c[nt][j] *= Q8 ? fk[j >> 1] * q_factor[nt][j & 1] : q_factor[nt][j & 1];
+        }
+        if (partial) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (g + 8 * r < left) continue;
+                ev[r] = 0.0f;  // (a slot's byte may be anything)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) c[nt][2 * r] = c[nt][2 * r + 1] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                up |= fmaxf(c[nt][j], c[nt][j + 2]) > m[nt][j] + kRaise;
+                if constexpr (Q8)
+                    up |= fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]) > eo[nt][j] + kRaise;
             }
         }
         if (__any_sync(0xffffffffu, up)) {
@@ -498,9 +553,14 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                    const float old = m[nt][j];
                     const float f = raise(m[nt][j], fmaxf(c[nt][j], c[nt][j + 2]));
                     l[nt][j] *= f;
-                    const float fo = Q8 ? raise(mo[nt][j], fmaxf(z[nt][j], z[nt][j + 2])) : f;
+                    float fo = f;
+                    if constexpr (Q8) {
+                        eo[nt][j] = fmaxf(eo[nt][j] + (old - m[nt][j]), kNoRef);  // under the new m
+                        fo = raise(eo[nt][j], fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]));
+                    }
 #pragma unroll
                     for (int i = 0; i < C::kTiles; ++i) {
                         acc[i][nt][j] *= fo;
@@ -515,87 +575,62 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             float a[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float ref = m[nt][j & 1];
-                const float pj = ex2_approx(c[nt][j] - (ref == -INFINITY ? 0.0f : ref));
+                const float d = c[nt][j] - m[nt][j & 1];
+                const float pj = ex2_approx(d);
                 l[nt][j & 1] += pj;
-                a[j] = pj;
-                if constexpr (Q8) {
-                    const float ro = mo[nt][j & 1];
-                    a[j] = ex2_approx(z[nt][j] - (ro == -INFINITY ? 0.0f : ro));
-                }
+                a[j] = Q8 ? ex2_approx(d + (ev[j >> 1] - eo[nt][j & 1])) : pj;
             }
             pf[nt][0] = transpose8x8(pack2<kMmaBf16>(a[0], a[1]));
             pf[nt][1] = transpose8x8(pack2<kMmaBf16>(a[2], a[3]));
         }
         // ---- O^T += V^T P^T: keys 2t, 2t+1, 2t+8, 2t+9 of the page ----
-        // Slots past the sequence's end hold anything: their values count as zeros (their weights
-        // are zero, but zero times a NaN is not).
-        const bool dead[4] = {partial && 2 * t >= left, partial && 2 * t + 1 >= left,
-                              partial && 2 * t + 8 >= left, partial && 2 * t + 9 >= left};
-        if constexpr (!Q8 || D == 128) {
+        // Words of the four keys: pairs of keys side by side are an operand register.
+        auto pv8 = [&](int tile, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {  // 4 elements, e4m3
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t lo = __byte_perm(w0, w1, hf ? 0x7362 : 0x5140);
+                const uint32_t hi = __byte_perm(w2, w3, hf ? 0x7362 : 0x5140);
+                const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16);
+                const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xffffu), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma16816<false>(acc[tile + hf][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+            }
+        };
+        auto pv16 = [&](int tile, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {  // 2 elements
+            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma16816<kMmaBf16>(acc[tile][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+        };
+        if constexpr (kSmall) {
+            if constexpr (!kEarly) read_v(0);
+            pv8(0, vh[0].x, vh[1].x, vh[2].x, vh[3].x);
+            pv8(2, vh[0].y, vh[1].y, vh[2].y, vh[3].y);
+        } else {
 #pragma unroll
             for (int x = 0; x < C::kBoxes; ++x) {
-                uint4 v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = 2 * t + (k & 1) + 8 * (k >> 1);
-                    v[k] = lds_u32x4(vs + x * C::kBoxBytes + key * 128 + (uint32_t)(g ^ (key & 7)) * 16);
-                    if (dead[k]) v[k] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w},
-                                          {v[1].x, v[1].y, v[1].z, v[1].w},
-                                          {v[2].x, v[2].y, v[2].z, v[2].w},
-                                          {v[3].x, v[3].y, v[3].z, v[3].w}};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (!Q8) {
-                        const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
-                        const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
-                        const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<kMmaBf16>(acc[4 * x + i][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                    } else {
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t lo = __byte_perm(w[0][i], w[1][i], hf ? 0x7362 : 0x5140);
-                            const uint32_t hi = __byte_perm(w[2][i], w[3][i], hf ? 0x7362 : 0x5140);
-                            const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16);
-                            const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xffffu), a3 = e4m3x2_to_f16x2(hi >> 16);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816<false>(acc[2 * i + hf][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
-                        }
-                    }
-                }
-            }
-        } else {  // e4m3, 64-byte rows: 8 elements per lane and key
-            uint2 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = 2 * t + (k & 1) + 8 * (k >> 1);
-                const uint32_t at = vs + key * 64 + (uint32_t)((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8;
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[k].x), "=r"(v[k].y) : "r"(at) : "memory");
-                if (dead[k]) v[k] = make_uint2(0u, 0u);
-            }
-            const uint32_t w[4][2] = {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const uint32_t lo = __byte_perm(w[0][i], w[1][i], hf ? 0x7362 : 0x5140);
-                    const uint32_t hi = __byte_perm(w[2][i], w[3][i], hf ? 0x7362 : 0x5140);
-                    const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xffffu), a1 = e4m3x2_to_f16x2(lo >> 16);
-                    const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xffffu), a3 = e4m3x2_to_f16x2(hi >> 16);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<false>(acc[2 * i + hf][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                if constexpr (!kEarly) read_v(x);
+                const uint4(&v)[4] = vq[x];
+                if constexpr (Q8) {
+                    pv8(0, v[0].x, v[1].x, v[2].x, v[3].x);
+                    pv8(2, v[0].y, v[1].y, v[2].y, v[3].y);
+                    pv8(4, v[0].z, v[1].z, v[2].z, v[3].z);
+                    pv8(6, v[0].w, v[1].w, v[2].w, v[3].w);
+                } else {
+                    pv16(4 * x, v[0].x, v[1].x, v[2].x, v[3].x);
+                    pv16(4 * x + 1, v[0].y, v[1].y, v[2].y, v[3].y);
+                    pv16(4 * x + 2, v[0].z, v[1].z, v[2].z, v[3].z);
+                    pv16(4 * x + 3, v[0].w, v[1].w, v[2].w, v[3].w);
                 }
             }
         }
-        __syncwarp();  // every lane has read the slot
-        if (done + stages < mine) issue(done + stages);
+        if constexpr (!kEarly) release();
+        if (++st == stages) {
+            st = 0;
+            parity ^= 1u;
+        }
         const bool ends = (flags & kLast) != 0;
         if (!ends && done + 1 < mine) continue;
         // ---- the unit, or this warp's part of it, is done ----
@@ -621,12 +656,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 const float L = column_sum(l[nt][j]);
                 const int qi = nt * 8 + 2 * t + j;
                 if (qi >= n_q) continue;
-                // (L = 0: every score is -inf, as if the row saw no key.)  The two references'
-                // distance is taken in two steps: 2^(mo - m) alone may be below fp32's range.
+                // (L = 0: every score is -inf, as if the row saw no key.)  2^eo in two steps: alone it
+                // may be below fp32's range.
                 const float f = L == 0.0f ? 0.0f : 1.0f / L;
-                const float hop = (!Q8 || mo[nt][j] == -INFINITY || m[nt][j] == -INFINITY)
-                                      ? 1.0f
-                                      : ex2_approx(0.5f * (mo[nt][j] - m[nt][j]));
+                const float hop = Q8 ? ex2_approx(0.5f * eo[nt][j]) : 1.0f;
                 const float lse2 = m[nt][j] + log2f(L);
                 if (g == 0) {
                     if (whole) p.lse[row0 + qi] = lse2 * kLn2;
