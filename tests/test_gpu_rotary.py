@@ -141,6 +141,24 @@ def test_rotary_layouts_and_in_place():
         fa.rotary_apply(yq[:, :, :-1], None, freqs, mscale, out=yq[:, :, 1:])
 
 
+def test_both_parts_of_packed_rows_in_one_call():
+    """Queries and keys of one packed row in place, by one call: [B, L, heads, D], and [B, heads, D] (a
+    decode step, where the row stride of a single row means nothing)."""
+    D, Hq, Hk = 64, 4, 2
+    freqs, mscale = fa.rotary_freqs(D)
+    for B, L, row in ((2, 5, (Hq + 2 * Hk) * D), (3, 1, D), (1, 1, D)):
+        x = randn(B, L, Hq + 2 * Hk, D, dtype=torch.bfloat16)
+        q, k = x[:, :, :Hq].transpose(1, 2), x[:, :, Hq:Hq + Hk].transpose(1, 2)
+        want = fa.rotary(q.contiguous(), k.contiguous(), None, freqs, mscale)
+        held = x[:, :, Hq + Hk:].clone()
+        st = (L * (Hq + 2 * Hk) * D, D, row)
+        assert fa.fa_rotary(q.data_ptr(), k.data_ptr(), q.data_ptr(), k.data_ptr(), [st] * 4, None, 0,
+                            freqs.data_ptr(), D, mscale, 0, 0, B, Hq, Hk, L, D, fa.FA_BF16,
+                            torch.cuda.current_stream().cuda_stream) == fa.FA_OK
+        assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+        assert torch.equal(x[:, :, Hq + Hk:], held)
+
+
 @pytest.mark.parametrize("inter,rd", [(False, 128), (True, 64), (False, 24)])
 def test_rotary_gradient(inter, rd):
     """The gradient against its formula, against differences, and of broadcast gradients."""

@@ -22,7 +22,9 @@ bool packed_parts(const void* a, int Ha, const void* b, int Hb, const Strides& s
     const long long delta = (pa < pb ? pb - pa : pa - pb) / 2;
     const long long first = (long long)(pa < pb ? Ha : Hb) * D;
     const long long second = (long long)(pa < pb ? Hb : Ha) * D;
-    return s.h == D && delta >= first && delta + second <= s.l && s.b >= (long long)L * s.l;
+    if (s.h != D || delta < first) return false;
+    if (L == 1) return delta + second <= s.b;  // one row per sequence: its own stride means nothing
+    return delta + second <= s.l && s.b >= (long long)L * s.l;
 }
 bool same(const Strides& a, const Strides& b) { return a.b == b.b && a.h == b.h && a.l == b.l; }
 
