@@ -145,6 +145,7 @@ COMMON = [
     (dict(B=65536), UNS),
     (dict(H=65536), UNS),
     (dict(maxp=1 << 28), UNS),                   # 16 * max_pages past 31 bits
+    (dict(L=(1 << 31) - 1), UNS),                # the last tile's rows past 31 bits
     (dict(k=0), BAD),
     (dict(v=A + MB + 2), BAD),
     (dict(kc=0), BAD),
@@ -203,6 +204,7 @@ def _decode(B=2, Hq=4, Hk=2, D=64, pages=8, maxp=4, scale=0.125, dtype=0, cdtype
     (dict(B=65536), UNS),
     (dict(Hq=65536 * 20, Hk=65536), UNS),
     (dict(Hq=1 << 20, Hk=4, B=1 << 12), UNS),
+    (dict(B=1, Hq=65535, Hk=65535, maxp=(1 << 27) - 1), UNS),  # a warp's pages past 31 bits
     (dict(q=0), BAD),
     (dict(lse=0), BAD),
     (dict(ve=0), BAD),
@@ -314,6 +316,7 @@ def _prefix(B=2, Hq=4, Hk=2, D=64, prefix=100, pages=8, maxp=4, scale=0.125, dty
 
 @pytest.mark.parametrize("kw,status", [
     (dict(prefix=-1), BAD),
+    (dict(prefix=(1 << 31) - 1), UNS),
     (dict(dtype=2), BAD),
     (dict(D=72), UNS),
     (dict(Hq=3), BAD),

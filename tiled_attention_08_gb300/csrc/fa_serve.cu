@@ -47,6 +47,9 @@ size_t cache_bytes(int num_pages, int H, int D, int cache_dtype) {
 }
 size_t exp_bytes(int num_pages, int H) { return (size_t)num_pages * H * kPageTokens; }
 
+// The kernels count rows up to the end of the last tile in 32 bits.
+constexpr int kMaxTokens = 0x7fffffff - 1023;
+
 // Sizes and flags shared by the calls on a paged cache.
 fa_status check_cache(int B, int H, int L, int D, int num_pages, int max_pages, int dtype,
                       int cache_dtype) {
@@ -55,7 +58,8 @@ fa_status check_cache(int B, int H, int L, int D, int num_pages, int max_pages, 
     if (B < 0 || H < 0 || L < 0 || D <= 0 || num_pages < 0 || max_pages < 0)
         return FA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
-    if (B > 65535 || H > 65535 || max_pages > 0x7fffffff / kPageTokens) return FA_ERR_UNSUPPORTED;
+    if (B > 65535 || H > 65535 || max_pages > 0x7fffffff / kPageTokens || L > kMaxTokens)
+        return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 
@@ -97,6 +101,8 @@ fa_status check_decode(int B, int Hq, int Hk, int D, int num_pages, int max_page
     if ((long long)B * Hq > 0x7fffffffLL || (long long)num_pages * Hk > 0x7fffffffLL ||
         (long long)B * max_pages > 0x7fffffffLL || Hq > 65535)
         return FA_ERR_UNSUPPORTED;
+    // A warp counts its pages in 32 bits (units of one query block at least 8 wide).
+    if ((long long)B * max_pages * ((Hq + 7) / 8 + Hk) > 1LL << 40) return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 
@@ -474,7 +480,7 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
 
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
                                         int max_pages) {
-    if (B <= 0 || Hq <= 0 || prefix_len < 0 ||
+    if (B <= 0 || Hq <= 0 || prefix_len < 0 || prefix_len > kMaxTokens ||
         check_decode(B, Hq, Hk, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK ||
         Hq / Hk > kTileRows)
         return 0;
@@ -491,6 +497,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
                                   int dtype, void* stream) {
     TraceDisarm disarm;
     if (prefix_len < 0) return FA_ERR_INVALID_ARG;
+    if (prefix_len > kMaxTokens) return FA_ERR_UNSUPPORTED;
     fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, FA_CACHE_16BIT);
     if (st != FA_OK) return st;
     if (B == 0 || Hq == 0) return FA_OK;
