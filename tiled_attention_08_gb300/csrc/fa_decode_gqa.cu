@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     for (size_t at = ((size_t)blockIdx.x * (kWarps * 32) + threadIdx.x) * 128;
          at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.q) + at));
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && p.num_pages > 0) {
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
@@ -724,7 +724,9 @@ __global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
     const int hk = h / p.group, gi = h - hk * p.group;
     const int qb = gi / p.q_rows, qi = gi - qb * p.q_rows;
     const int2 own = p.unit_parts[((size_t)b * p.Hk + hk) * p.q_blocks + qb];
-    const int w_first = own.x, n_own = own.y;
+    // (A kernel that gave up on a wait may have left an entry as it found it: no part, then.)
+    const bool there = own.x >= 0 && own.y >= 0 && own.x < p.workers && own.y <= p.workers - own.x;
+    const int w_first = own.x, n_own = there ? own.y : 0;
     const int n_parts = p.n_prefix + n_own;
     if (p.n_prefix == 0 && n_own == 1) return;  // written whole
     const float* pre_o = p.prefix_o + (size_t)row * p.n_prefix * D;

@@ -218,6 +218,7 @@ struct MergeParams {
     void* o;     // [rows, D] 16-bit
     float* lse;  // [rows] natural log
     int rows, B, Hq, Hk, group, q_rows, q_blocks, slot_rows;
+    int workers;  // warps that may have left parts, over all rounds
 };
 
 // Attention of all query rows of a batch to one shared prefix (fa_prefix.cu).  A work unit is one

@@ -184,6 +184,7 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         m.q_rows = gqa_q_rows(p.group);
         m.q_blocks = p.q_blocks;
         m.slot_rows = p.slot_rows;
+        m.workers = c.warps * c.rounds;
         e = traced_launch(kernel++, s, [&] { return launch_merge(m, D, bf16, s); });
         if (e != cudaSuccess) return e;
     }
