@@ -478,10 +478,9 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
     The caches may have fewer heads than q (a divisor: each is shared by a group of query heads),
     and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote."""
     import torch
-    if k_exp is not None or v_exp is not None or (k_cache.dim() == 4 and q.dim() == 3 and
-                                                  k_cache.shape[1] != q.shape[1]):
-        return _decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse,
-                                workspace, k_exp, v_exp)
+    if k_exp is not None or v_exp is not None or k_cache.shape[1:2] != q.shape[1:2]:
+        return (_binding or _ops()).decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale,
+                                                    out, lse, workspace, k_exp, v_exp)
     for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
                     ("block_tables", block_tables), ("seq_lens", seq_lens)):
         if not t.is_cuda or not t.is_contiguous():
