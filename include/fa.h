@@ -324,7 +324,7 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
                         int num_pages, int max_pages, int dtype, int cache_dtype, void* stream);
 
 /* Bytes of device workspace fa_decode_paged_ex needs (the parts of rows whose pages are
- * split, fp32: at D = 128 at most 2.5 MB, from 4864 (sequence, cache head) pairs on 7.5 MB, for every
+ * split, fp32: at D = 128 at most 2.5 MB, from 2048 (sequence, cache head) pairs on 7.5 MB, for every
  * query head of a group up to 16).  Calls that may
  * overlap on the GPU need a workspace each.  0 for invalid sizes. */
 size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages);

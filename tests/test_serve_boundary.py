@@ -233,11 +233,11 @@ def test_grouped_decode_workspace():
         units = chunk * Hk * -(-g // q_rows)
         ctas = min(4 * 152, max(1, -(-units * max_pages // 4)))
         up = lambda n: (n + 15) // 16 * 16  # noqa: E731
-        slots = 2 * 4 * ctas * min(g, q_rows) * (3 if units >= 2 * 4 * 152 * 4 else 1)
+        slots = 2 * 4 * ctas * min(g, q_rows) * (3 if units >= 2048 else 1)
         return up(8 * units) + up(slots * D * 4) + up(slots * 4)
 
     for args in ((256, 32, 8, 128, 256), (1, 8, 1, 128, 16), (1, 8, 1, 128, 1024), (5, 40, 2, 64, 9),
-                 (2, 4, 2, 64, 0), (3000, 2, 2, 64, 1), (256, 32, 32, 128, 256)):
+                 (2, 4, 2, 64, 0), (3000, 2, 2, 64, 1), (256, 32, 32, 128, 256), (255, 64, 8, 64, 9)):
         assert fa.fa_decode_workspace_bytes_ex(*args) == need(*args), args
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 3, 128, 1024) == 0     # invalid
     assert fa.fa_decode_workspace_bytes_ex(1, 8, 1, 96, 1024) == 0

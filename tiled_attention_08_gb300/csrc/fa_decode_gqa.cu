@@ -57,14 +57,17 @@ constexpr int kGqaSms = 152;     // the grid is sized for this many SMs on any d
                                  // workspace does not depend on it
 constexpr int kGqaMinPages = 4;  // pages of a warp's stretch at least ...
 constexpr int kGqaFewPages = 1024;  // ... where there are more than this many
+constexpr int kGqaManyUnits = 2048;  // from so many on the line is dealt out in three rounds
 
 // The split of the line of `total` pages.  One round: `workers` warps take equal stretches.  Not
 // all SMs get the same share of the memory's bandwidth, so equal stretches end up to 15% apart;
 // with three rounds the line's first 52/64 are dealt out like that, the next 8/64 and the last 4/64
 // again in stretches so much shorter, to CTAs that start as earlier ones end (735 -> 641 us for 256
 // sequences of 1..4096 tokens, 32 heads of 128, e4m3).  Short stretches cut long units into many
-// parts (142 -> 158 us for 48 sequences of up to 16384 tokens with groups of 8), so three rounds
-// need at least two units per warp.
+// parts and each begins with an empty ring, so three rounds need kGqaManyUnits: with 2048 to 4096
+// units they took -12% to +1% over e4m3 and 16-bit caches, heads of 64 and 128, groups of 1 to 4; with
+// 1024 (groups of 8) +1% to +18%, with 384 +3% to +25% (142 -> 158 us for 48 sequences of up to
+// 16384 tokens, e4m3, heads of 128).
 struct GqaSplit {
     long long second, third, total;  // first pages of rounds 1 and 2 (total: there is none), the end
     int workers, rounds;
@@ -859,7 +862,7 @@ int gqa_warps(int B, int Hk, int group, int max_pages) {
 
 int gqa_rounds(int B, int Hk, int group) {
     const long long units = (long long)B * Hk * ((group + gqa_q_rows(group) - 1) / gqa_q_rows(group));
-    return units >= 2LL * 4 * kGqaSms * kWarps ? 3 : 1;
+    return units >= kGqaManyUnits ? 3 : 1;
 }
 
 int gqa_launched_warps(int B, int Hk, int group, int max_pages, int D, bool q8, int busy_sms) {
