@@ -14,6 +14,12 @@ allocation and the current CUDA stream come from torch); queries and keys may di
 tensor, the layouts of the flash_attn_func and flash_attn_qkvpacked_func interfaces the pages
 use ("FlashAttention data-flow optimisation", section 4.1, step 3; "AIInfra notes 01: from
 TFLOPS to FlashAttention", sections 4.2-4.3).
+
+Around attention: ``rotary`` (differentiable), ``rotary_apply`` and ``rotary_freqs`` turn queries
+and keys by their positions; ``cache_append`` and ``cache_read`` write and read a paged cache of
+16-bit or e4m3 rows; ``decode_paged`` attends to such a cache with equal or grouped heads and
+``decode_shared_prefix`` does so for a batch whose sequences begin alike.  These go through
+``fa_torch.so``, a C++ binding over the same C ABI.
 """
 from __future__ import annotations
 

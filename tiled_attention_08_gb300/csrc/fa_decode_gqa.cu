@@ -40,6 +40,12 @@
 // row's scale neither overflows nor is lost in fp16, whatever the rows' magnitudes.  (eo is relative
 // to m: added to y_j itself, ev_j would be lost behind a large score.)  P is rounded to the
 // cache's 16-bit type (fp16 for e4m3: 2^-12), as in the prefill kernels; sums stay fp32.
+//
+// Measured.  256 sequences of 1..4096 tokens, 32 heads of 128, e4m3: 620 us (6.9 TB/s); 16-bit
+// caches of long batches 6.8 to 7.0 TB/s.  48 sequences of 1..16384, 64 queries on 8 cache heads of 128,
+// e4m3: 140 us (5.8 TB/s; no SM idle until the first stretches end).  Heads of 64, e4m3: 4.0 to 4.6
+// TB/s: an SM turns over 10 to 12 pages per us whatever their size, with 377 instructions a page and warp
+// and 16 warps' registers.  One sequence of 333 tokens: 5 us and 3 for the merge, latency alone.
 #include <atomic>
 #include <type_traits>
 

