@@ -335,8 +335,9 @@ size_t fa_decode_workspace_bytes_ex(int B, int Hq, int Hk, int D, int max_pages)
  * [num_pages, Hk, FA_PAGE_TOKENS] (FA_CACHE_E4M3; ignored otherwise).  Hq is a multiple of Hk and
  * query head h reads cache head h / (Hq / Hk).  Everything else is as for fa_decode_paged: empty
  * sequences get O = 0, LSE = -inf, slots past a sequence's end may hold anything, a bad length or
- * page index is reported by fa_get_device_status().  Enqueues two kernels for every 1024 sequences
- * (the second may start before the first has finished).  B * max_pages, B * Hq and num_pages * Hk
+ * page index is reported by fa_get_device_status().  Enqueues one kernel for a short step (few
+ * sequences and cache heads, tables of up to 256 pages, groups of up to 8), else two for every 1024
+ * sequences (the second may start before the first has finished).  B * max_pages, B * Hq and num_pages * Hk
  * are below 2^31.
  */
 fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_cache,

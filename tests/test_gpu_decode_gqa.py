@@ -29,12 +29,29 @@ def _gpu():
     gh.require_gpu()
 
 
+EXTRA = 0
+
+
+@pytest.fixture(scope="module", autouse=True, params=[0, 300], ids=["narrow", "wide"])
+def _extra(request):
+    """Everything with tables as long as they need to be (short steps take a cluster per head), and
+    with 300 more columns, which no kernel may read (all steps take the split over all warps)."""
+    global EXTRA
+    EXTRA = request.param
+    yield
+
+
+def widen(bt, extra=None):
+    n = EXTRA if extra is None else extra
+    return torch.cat([bt, torch.full((bt.shape[0], n), -7, dtype=torch.int32, device="cuda")], 1).contiguous()
+
+
 def fill(rng, lens, Hk, D, dtype, q8, scale_rows=None):
     """A cache whose pages hold the sequences' rows and NaN everywhere else, and the rows as held:
     lists of [Hk, n, D] in 64 bits."""
     t, pages = tables(rng, lens)
     kc, vc, ke, ve = make_cache(pages, Hk, D, dtype, q8)
-    bt = torch.from_numpy(t).cuda()
+    bt = widen(torch.from_numpy(t).cuda())
     L = max(max(lens), 1)
     k = torch.from_numpy(rng.standard_normal((len(lens), Hk, L, D), dtype=np.float32))
     v = torch.from_numpy(rng.standard_normal((len(lens), Hk, L, D), dtype=np.float32))
@@ -175,7 +192,7 @@ def test_scores_of_any_size(q8):
     k[:, :, :, 0] = 2.0 ** 40
     k[:, :, 5, 0] = 2.0 ** 40 * 1.25   # the one key that counts (sign of q decides)
     v = randn(2, Hk, 16, D, dtype=dtype)
-    bt = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    bt = widen(torch.tensor([[0], [1]], dtype=torch.int32, device="cuda"))
     sl = torch.tensor([16, 1], dtype=torch.int32, device="cuda")
     fa.cache_append(k, v, kc, vc, bt, torch.full_like(sl, 16), k_exp=ke, v_exp=ve)
     held_v = gh.f64(fa.cache_read(kc, vc, bt, torch.full_like(sl, 16), 16, k_exp=ke, v_exp=ve, dtype=dtype)[1])
@@ -278,6 +295,28 @@ def test_repeated_captured_and_on_another_stream():
               1.0 / math.sqrt(D), dtype, True)
 
 
+@pytest.mark.parametrize("B,Hk,G,D,q8,width", [
+    (72, 1, 2, 128, True, 20), (73, 1, 2, 128, True, 20), (48, 1, 1, 128, False, 20), (49, 1, 1, 128, False, 20),
+    (36, 2, 3, 64, False, 20), (9, 8, 8, 64, True, 20), (4, 1, 8, 128, True, 128), (4, 1, 8, 128, True, 129),
+    (8, 4, 1, 64, False, 256), (8, 4, 1, 64, False, 257), (31, 1, 4, 64, True, 129), (4, 1, 9, 64, True, 20)])
+def test_either_side_of_the_short_step(B, Hk, G, D, q8, width):
+    """Sizes at which the step changes its kernel: most units, longest tables, largest groups."""
+    rng = np.random.default_rng(B + width)
+    lens = [int(x) for x in rng.integers(0, 17 * 16, B)]
+    lens[0], lens[-1] = 17 * 16, 0
+    if width >= 128:
+        lens[1] = 16 * 126 + 5
+    dtype = torch.bfloat16
+    kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, lens, Hk, D, dtype, q8)
+    bt = widen(bt[:, :-EXTRA] if EXTRA else bt, width - (bt.shape[1] - EXTRA))
+    assert bt.shape[1] == width
+    q = randn(B, Hk * G, D, dtype=dtype)
+    scale = 1.0 / math.sqrt(D)
+    o, lse = fa._decode_paged_ex(q, kc, vc, bt, sl, scale, None, None, None, ke, ve)
+    assert status() == fa.FA_OK
+    check(o, lse, q, ks, vs, scale, dtype, q8)
+
+
 def test_many_sequences():
     """More sequences than one launch takes (1024), most of them short, some empty."""
     D, dtype, Hk = 64, torch.float16, 1
@@ -314,7 +353,7 @@ def test_serving_steps_from_a_prompt():
     k, v, q = (randn(2, h, n0 + steps, D, dtype=dtype, seed=i) for i, h in enumerate((Hk, Hk, Hq)))
     rng = np.random.default_rng(12)
     t, pages = tables(rng, [n0 + steps] * 2)
-    bt = torch.from_numpy(t).cuda()
+    bt = widen(torch.from_numpy(t).cuda())
     kc, vc, ke, ve = make_cache(pages, Hk, D, dtype, True)
     sl = torch.full((2,), n0, dtype=torch.int32, device="cuda")
     fa.cache_append(k[:, :, :n0], v[:, :, :n0], kc, vc, bt, sl, k_exp=ke, v_exp=ve, freqs=freqs, mscale=mscale)
@@ -342,7 +381,7 @@ def test_far_pages_of_a_large_cache():
     vc = torch.zeros_like(kc.view(torch.uint8)).view(torch.float8_e4m3fn)
     ke = torch.zeros((pages, Hk, PAGE), dtype=torch.uint8, device="cuda")
     ve = torch.zeros_like(ke)
-    bt = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    bt = widen(torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda"))
     sl = torch.tensor([40], dtype=torch.int32, device="cuda")
     k, v = randn(1, Hk, 40, D, dtype=dtype), randn(1, Hk, 40, D, dtype=dtype, seed=1)
     fa.cache_append(k, v, kc, vc, bt, sl, k_exp=ke, v_exp=ve)

@@ -33,6 +33,16 @@
 //    g of its four keys; bytes (or halves) of two keys are paired by byte permutes.
 // The TMA's 128-byte (64-byte) swizzle spreads these reads over all banks.
 //
+// Short steps.  With few units and short tables (gqa_short) the split above is mostly overhead: the
+// scan, a search per page, parts through memory and a second kernel.  There a cluster of eight CTAs takes
+// one unit, its 32 warps an equal share of the unit's pages each, and the parts are joined through
+// distributed shared memory: CTA r joins query row r, and writes O and LSE.  One sequence of 512 tokens, 8
+// cache heads, group 4, e4m3: 8.2 -> 6.6 us; 17 sequences of 500, 4 heads: 11.3 -> 8.8; a sequence of 4096
+// among eight of 16: 15.1 -> 12.1.  It loses where the clusters do not all fit at once (72 fit with
+// four CTAs per SM and 48 with three; 76 and 52 took 9.1 -> 11.6 and 10.4 -> 12.0 us), where a few
+// units are long (one unit of 4096 tokens: 10.4 -> 11.8 us; 32 units of 8192, all but one head's short: 16.7 ->
+// 17.8), and with groups above 8 (three CTAs per SM: 14.7 -> 22.0 us for 52 units).
+//
 // Softmax in the log2 domain.  The reference of a column is only raised when a score exceeds it
 // by more than 2^8 (a warp vote), so the maximum over the lanes is rarely taken.  An e4m3 cache
 // needs a second one: the sum of weights takes p_j = 2^(y_j - m); the products take
@@ -45,7 +55,7 @@
 // caches of long batches 6.8 to 7.0 TB/s.  48 sequences of 1..16384, 64 queries on 8 cache heads of 128,
 // e4m3: 140 us (5.8 TB/s; no SM idle until the first stretches end).  Heads of 64, e4m3: 4.0 to 4.6
 // TB/s: an SM turns over 10 to 12 pages per us whatever their size, with 377 instructions a page and warp
-// and 16 warps' registers.  One sequence of 333 tokens: 5 us and 3 for the merge, latency alone.
+// and 16 warps' registers.
 #include <atomic>
 #include <type_traits>
 
@@ -63,6 +73,7 @@ constexpr int kGqaSms = 152;     // the grid is sized for this many SMs on any d
                                  // workspace does not depend on it
 constexpr int kGqaMinPages = 4;  // pages of a warp's stretch at least ...
 constexpr int kGqaFewPages = 1024;  // ... where there are more than this many
+constexpr int kClusterCtas = 8;  // of a unit in a short step
 constexpr int kGqaManyUnits = 2048;  // from so many on the line is dealt out in three rounds
 
 // The split of the line of `total` pages.  One round: `workers` warps take equal stretches.  Not
@@ -88,8 +99,8 @@ struct GqaSplit {
         return r * workers + (int)(((x - at(r) + 1) * workers - 1) / (at(r + 1) - at(r)));
     }
 };
-// A page for each warp while there are few (latency is all: 13.1 -> 10.1 us for one sequence of 333
-// tokens, 8 cache heads), else at least kGqaMinPages; and a unit is cut into no more than 128 parts on
+// A page for each warp while there are few (latency is all: 13.1 -> 10.1 us for a token written and
+// attended to behind 333, 8 cache heads, with this split), else at least kGqaMinPages; and a unit is cut into no more than 128 parts on
 // average.
 __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int rounds, int units) {
     const long long a = total <= kGqaFewPages ? total : total / kGqaMinPages, b = 128LL * units;
@@ -104,7 +115,7 @@ __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int ro
 }
 
 // cudaFuncSetAttribute once per kernel and device (the calls below repeat every few microseconds).
-template <int D, bool Q8, bool BF16, int NT>
+template <int D, bool Q8, bool BF16, int NT, bool SHORT>
 struct kGqaKernelId {};
 template <typename Id, typename K>
 cudaError_t allow_shared(K kern, int bytes) {
@@ -206,8 +217,25 @@ struct Batch {
 };
 constexpr int kFirst = 1 << 8, kLast = 1 << 9;
 
-// BF16: the type of q and o (and of a 16-bit cache).  NT: blocks of 8 queries.
-template <int D, bool Q8, bool BF16, int NT>
+// Thread-block clusters of short steps: the value at shared::cta address `addr` of CTA `rank`.
+__device__ __forceinline__ float lds_cluster(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// BF16: the type of q and o (and of a 16-bit cache).  NT: blocks of 8 queries.  SHORT: a cluster per
+// unit, whose warps share the unit's pages and join their parts through distributed shared memory.
+template <int D, bool Q8, bool BF16, int NT, bool SHORT>
 __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     fa_decode_gqa_kernel(const __grid_constant__ GqaParams p) {
     using C = GqaCfg<D, Q8>;
@@ -221,10 +249,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     int* cum = reinterpret_cast<int*>(smem + C::kRingBytes);  // [B + 1] pages before sequence b
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
+    const int per_seq = p.Hk * p.q_blocks;  // units of a sequence
+    const int unit_id = (int)blockIdx.x / kClusterCtas, short_b = unit_id / per_seq;  // (SHORT)
+    const int short_unit = unit_id - short_b * per_seq, rank = (int)blockIdx.x % kClusterCtas;
     pdl_launch_dependents();
     // The queries into L2 (they are read when a warp begins a unit, behind the stream of pages).
     for (size_t at = ((size_t)blockIdx.x * (kWarps * 32) + threadIdx.x) * 128;
-         at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
+         !SHORT && at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.q) + at));
     if (threadIdx.x == 0 && p.num_pages > 0) {
         tma_prefetch_desc(&p.tm_k);
@@ -233,54 +264,74 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     if (lane < stages) mbar_init(&bar_full[warp][lane], 1);
     mbar_fence_init();
     // ---- pages before each sequence: every thread sums a run of sequences ----
+    const int n_seqs = SHORT ? 0 : p.B;
     const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32);
-    const int s0 = min((int)threadIdx.x * run, p.B), s1 = min(s0 + run, p.B);
+    const int s0 = min((int)threadIdx.x * run, n_seqs), s1 = min(s0 + run, n_seqs);
     auto pages_of = [&](int b) {
         const int n = p.seq_lens[b];
         if (n < 0 || n > (long long)p.max_pages * kPageTokens || (n > 0 && p.num_pages == 0)) {
-            if (blockIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
+            if (SHORT || blockIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
             return 0;  // counts as empty
         }
         return (n + kPageTokens - 1) / kPageTokens;
     };
-    int sum = 0;
-    for (int b = s0; b < s1; ++b) sum += pages_of(b);
-    int scan = sum;
+    GqaSplit split;
+    int w = 0, mine = 0;  // this worker, and its pages x0 .. x0 + mine - 1 of the line (SHORT: of the unit)
+    long long x0 = 0, total = 0;
+    if constexpr (SHORT) {
+        const int n_pages = pages_of(short_b), i = warp * kClusterCtas + rank;  // neighbours on different SMs
+        constexpr int kWorkers = kClusterCtas * kWarps;
+        x0 = n_pages * (long long)i / kWorkers;
+        mine = (int)(n_pages * (long long)(i + 1) / kWorkers - x0);
+        __syncthreads();  // (the barriers are initialised)
+    } else {
+        int sum = 0;
+        for (int b = s0; b < s1; ++b) sum += pages_of(b);
+        int scan = sum;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, off);
-        if (lane >= off) scan += v;
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, off);
+            if (lane >= off) scan += v;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        int before = scan - sum;
+        for (int w = 0; w < warp; ++w) before += warp_sum[w];
+        for (int b = s0; b < s1; ++b) {
+            cum[b] = before;
+            before += pages_of(b);
+        }
+        if (threadIdx.x == kWarps * 32 - 1) cum[p.B] = before;
+        __syncthreads();
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+            if (cum[b] == cum[b + 1])
+                for (int i = threadIdx.x; i < per_seq; i += kWarps * 32)
+                    p.unit_parts[(size_t)b * per_seq + i] = make_int2(0, 0);  // no key, no part
+        total = (long long)cum[p.B] * per_seq;
+        split = gqa_split(total, p.warps, p.rounds, p.B * per_seq);
+        const int ctas = p.warps / kWarps;  // of a round
+        const int r = (int)blockIdx.x / ctas;
+        const int wi = warp * ctas + (int)blockIdx.x - r * ctas;  // neighbours on different SMs
+        const bool works = r < split.rounds && wi < split.workers;
+        w = r * split.workers + wi;
+        x0 = works ? split.start(r, wi) : 0;
+        mine = works ? (int)(split.start(r, wi + 1) - x0) : 0;
     }
-    if (lane == 31) warp_sum[warp] = scan;
-    __syncthreads();
-    int before = scan - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
-    for (int b = s0; b < s1; ++b) {
-        cum[b] = before;
-        before += pages_of(b);
-    }
-    if (threadIdx.x == kWarps * 32 - 1) cum[p.B] = before;
-    __syncthreads();
-    const int per_seq = p.Hk * p.q_blocks;  // units of a sequence
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-        if (cum[b] == cum[b + 1])
-            for (int i = threadIdx.x; i < per_seq; i += kWarps * 32)
-                p.unit_parts[(size_t)b * per_seq + i] = make_int2(0, 0);  // no key, no part
-    const long long total = (long long)cum[p.B] * per_seq;
-    const GqaSplit split = gqa_split(total, p.warps, p.rounds, p.B * per_seq);
-    const int ctas = p.warps / kWarps;  // of a round
-    const int r = (int)blockIdx.x / ctas;
-    const int wi = warp * ctas + (int)blockIdx.x - r * ctas;  // neighbours on different SMs
-    const bool works = r < split.rounds && wi < split.workers;
-    const int w = r * split.workers + wi;
-    const long long x0 = works ? split.start(r, wi) : 0;
-    const int mine = works ? (int)(split.start(r, wi + 1) - x0) : 0;
 
     uint8_t* ring = smem + (size_t)warp * stages * (2 * C::kPageBytes);
     uint8_t* exps = smem + (size_t)kWarps * stages * (2 * C::kPageBytes) + warp * stages * 32;
     auto lookup = [&](int first) {  // pages first .. first + 31 of this warp
         Batch r = {0, 0, 0, 0};
-        if (first + lane < mine) {
+        if (SHORT && first + lane < mine) {
+            const int pg = (int)x0 + first + lane;
+            int page = p.block_tables[(size_t)short_b * p.max_pages + pg];
+            if (page < 0 || page >= p.num_pages) {  // as below
+                atomicCAS(p.status, 0, (int)kDevBadArg);
+                page = 0;
+            }
+            r.page_head = page * p.Hk + short_unit / p.q_blocks;
+            r.flags = min(p.seq_lens[short_b] - pg * kPageTokens, kPageTokens);
+        } else if (!SHORT && first + lane < mine) {
             const long long x = x0 + first + lane;
             // (64-bit quotients cost ten times 32-bit ones)
             const bool small = total <= 0x7fffffffLL;
@@ -398,14 +449,14 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         if (done > 0 && (done & 31) == 0) cons = prod;  // (the ring is less than a batch ahead)
         const int flags = __shfl_sync(0xffffffffu, cons.flags, done & 31);
         if (done == 0 || (flags & kFirst)) {  // a new unit
-            const int b = __shfl_sync(0xffffffffu, cons.b, done & 31);
-            const int unit = __shfl_sync(0xffffffffu, cons.unit, done & 31);
+            const int b = SHORT ? short_b : __shfl_sync(0xffffffffu, cons.b, done & 31);
+            const int unit = SHORT ? short_unit : __shfl_sync(0xffffffffu, cons.unit, done & 31);
             const int hk = unit / p.q_blocks, q0 = (unit - hk * p.q_blocks) * (NT * 8);
             n_q = min(NT * 8, p.group - q0);
             row0 = (size_t)b * p.Hq + (size_t)hk * p.group + q0;
             cut = !(flags & kFirst);
             load_q(row0, n_q);
-            if (!cut && lane == 0) {  // for the merge: the warps that have the unit's pages
+            if (!SHORT && !cut && lane == 0) {  // for the merge: the warps that have the unit's pages
                 const long long last = x0 + done + (cum[b + 1] - cum[b]) - 1;
                 const int n = done + (cum[b + 1] - cum[b]) <= mine ? 1 : split.worker_of(last) - w + 1;
                 p.unit_parts[(size_t)b * per_seq + unit] = make_int2(w, n);
@@ -645,10 +696,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         // ---- the unit, or this warp's part of it, is done ----
         // Lane (g, t) holds, for queries 2t and 2t+1, whole runs of elements: e4m3 D/8 from
         // D/8 g on, 16-bit 8 from 64 x + 8 g on for each box x.
-        const bool whole = !cut && ends && !p.parts_only;
+        const bool whole = !SHORT && !cut && ends && !p.parts_only;
         float* part_o = nullptr;
         float* part_lse = nullptr;
-        if (!whole) {
+        if constexpr (SHORT) {  // into this warp's ring, which is empty now
+            part_o = reinterpret_cast<float*>(ring);
+            part_lse = part_o + NT * 8 * D;
+        } else if (!whole) {
             const size_t slot = (cut || !ends) ? 2 * (size_t)w + (cut ? 0 : 1) : 0;
             if (!cut && ends) {  // a whole unit of a row that has other parts
                 part_o = p.full_o + row0 * D;
@@ -707,6 +761,42 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         // No copy may still be landing when the CTA exits.
         for (int i = done; i < min(mine, done + stages); ++i)
             wait_bounded(&bar_full[warp][i % stages], (uint32_t)(i / stages) & 1u, nullptr, p.timeout_ns);
+    }
+    if constexpr (SHORT) {
+        static_assert((NT * 8 * (D + 1)) * 4 <= stages * 2 * C::kPageBytes, "a warp's part in its ring");
+        if ((mine == 0 || !ok) && lane < NT * 8) reinterpret_cast<float*>(ring)[NT * 8 * D + lane] = -INFINITY;
+        cluster_sync();
+        const int hk = short_unit / p.q_blocks, q0 = (short_unit - hk * p.q_blocks) * (NT * 8);
+        const int rows = min(NT * 8, p.group - q0);
+        const size_t row = (size_t)short_b * p.Hq + (size_t)hk * p.group + q0;
+        const uint32_t part0 = smem_u32(smem);
+        constexpr uint32_t kPart = stages * 2 * C::kPageBytes;  // between two warps' parts
+        for (int qi = rank; qi < rows; qi += kClusterCtas) {
+            // Lane i: part i, of warp i % 4 in CTA i / 4.
+            const float y = lds_cluster(part0 + lane % kWarps * kPart + (NT * 8 * D + qi) * 4, lane / kWarps);
+            const uint32_t there = __ballot_sync(0xffffffffu, y != -INFINITY);  // (else nothing was written)
+            float top = y;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float wi = y == -INFINITY ? 0.0f : ex2_approx(y - top);
+            float sum = wi;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            float x = 0.0f;
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+                const float wv = __shfl_sync(0xffffffffu, wi, i);
+                if (threadIdx.x < D && (there >> i & 1u))
+                    x = fmaf(wv, lds_cluster(part0 + i % kWarps * kPart + (qi * D + threadIdx.x) * 4, i / kWarps), x);
+            }
+            const bool any = sum != 0.0f;  // (true of a NaN)
+            if (threadIdx.x < D)
+                static_cast<uint16_t*>(p.o)[(row + qi) * D + threadIdx.x] =
+                    any ? (uint16_t)pack2<BF16>(x / sum, 0.0f) : (uint16_t)0;
+            if (threadIdx.x == 0) p.lse[row + qi] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        }
+        cluster_sync();  // the parts have been read
+        return;
     }
     // Launched early behind a kernel that writes other parts of the same rows, this grid ends only
     // after that one (one CTA waits; the others make room), so that the merge waits for both by
@@ -822,13 +912,16 @@ __global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
     if (lane == 0) p.lse[row] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool Q8, bool BF16, int NT>
+template <int D, bool Q8, bool BF16, int NT, bool SHORT>
 cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
     using C = GqaCfg<D, Q8>;
-    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT>;
+    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT>;
     const int smem = C::kRingBytes + 1024 + (kGqaMaxSequences + 1) * 4;
-    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT>>(kern, smem);
+    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT>>(kern, smem);
     if (e != cudaSuccess) return e;
+    if constexpr (SHORT)
+        return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * kClusterCtas)),
+                                     dim3(kWarps * 32), (size_t)C::kRingBytes + 1024, kClusterCtas, s, p);
     const int here = C::kRingBytes + 1024 + (p.B + 1) * 4;
     const dim3 grid((unsigned)(p.warps / kWarps * p.rounds));
     return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)here, s, p)
@@ -837,7 +930,8 @@ cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
 
 template <int D, bool Q8, bool BF16>
 cudaError_t launch_n(const GqaParams& p, cudaStream_t s) {
-    return p.group <= 8 ? launch_t<D, Q8, BF16, 1>(p, s) : launch_t<D, Q8, BF16, 2>(p, s);
+    if (p.short_step) return launch_t<D, Q8, BF16, 1, true>(p, s);
+    return p.group <= 8 ? launch_t<D, Q8, BF16, 1, false>(p, s) : launch_t<D, Q8, BF16, 2, false>(p, s);
 }
 
 template <int D>
@@ -864,6 +958,12 @@ int gqa_warps(int B, int Hk, int group, int max_pages) {
     const long long ctas = ((long long)B * Hk * q_blocks * max_pages + kWarps - 1) /
                            kWarps;
     return kWarps * (int)(ctas < 1 ? 1 : ctas < 4 * kGqaSms ? ctas : 4 * kGqaSms);
+}
+
+bool gqa_short(int B, int Hk, int group, int max_pages, int D, bool q8) {
+    if (group > 8) return false;
+    const long long units = (long long)B * Hk;
+    return units <= (gqa_occupancy(D, q8, 1) == 4 ? 72 : 48) && max_pages <= (units < 32 ? 128 : 256);
 }
 
 int gqa_rounds(int B, int Hk, int group) {

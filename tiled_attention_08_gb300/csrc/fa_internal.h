@@ -201,6 +201,7 @@ struct GqaParams {
     int rounds;                // of the split, 1 or 3
     int slot_rows;             // rows of a slot: the group, at most 8 or (above 8) 16
     int parts_only;            // rows have other parts (a shared prefix): o, lse are the merge's
+    int short_step;            // a cluster per unit and no merge (gqa_short)
     int early;                 // launched before the kernel in front of it has finished
     int warps;                 // of a round, a multiple of 4
     int B, Hq, Hk, group, q_blocks, num_pages, max_pages;
@@ -287,6 +288,24 @@ cudaError_t launch_kernel_early(void (*kern)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// A launch in clusters of `ctas` neighbouring CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int ctas,
+                                  cudaStream_t s, Args&&... args) {
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 // Launchers (one per kernel unit).  Return the launch error, if any.
 cudaError_t launch_fwd(const FwdParams& p, int D, bool bf16, bool causal, bool drop,
                        cudaStream_t s);
@@ -318,6 +337,8 @@ cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s)
 int gqa_q_rows(int group);
 int gqa_warps(int B, int Hk, int group, int max_pages);
 int gqa_rounds(int B, int Hk, int group);
+// Whether a step takes a cluster per unit (and no merge).
+bool gqa_short(int B, int Hk, int group, int max_pages, int D, bool q8);
 int gqa_launched_warps(int B, int Hk, int group, int max_pages, int D, bool q8, int busy_sms);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);

@@ -160,10 +160,12 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         c.full_o = reinterpret_cast<float*>(ws + w.full_o) + b0 * row_o;
         c.full_lse = reinterpret_cast<float*>(ws + w.full_lse) + (size_t)b0 * p.Hq;
         c.early = p.early && b0 == 0;
+        c.short_step = !p.parts_only && gqa_short(c.B, p.Hk, p.group, p.max_pages, D, q8);
         c.rounds = gqa_rounds(c.B, p.Hk, p.group);
         c.warps = gqa_launched_warps(c.B, p.Hk, p.group, p.max_pages, D, q8, c.early ? busy_sms : 0);
         cudaError_t e = traced_launch(kernel++, s, [&] { return launch_decode_gqa(c, D, bf16, q8, s); });
         if (e != cudaSuccess) return e;
+        if (c.short_step) continue;  // (its clusters have joined their parts)
         MergeParams m;
         std::memset(&m, 0, sizeof(m));
         m.prefix_o = reinterpret_cast<float*>(ws + w.prefix_o) + b0 * row_o * n_prefix;
