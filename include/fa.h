@@ -363,8 +363,8 @@ size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix
  *   caches of dtype (16-bit), Hq a multiple of Hk with Hq / Hk <= 128; prefix_len >= 0 (a host
  *   integer; 0: no prefix), prefix_table int32, device, ceil(prefix_len / 16) entries; max_pages 0:
  *   no sequence has tokens of its own.  A row with no token at all gets O = 0, LSE = -inf.
- * Bad page indexes and lengths are reported as for fa_decode_paged_ex.  Enqueues three kernels (two
- * without a prefix, two more for every further 1024 sequences); each may start before the one in
+ * Bad page indexes and lengths are reported as for fa_decode_paged_ex.  Enqueues three kernels (without
+ * a prefix those of fa_decode_paged_ex; two more for every further 1024 sequences); each may start before the one in
  * front has finished.
  */
 fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
