@@ -100,8 +100,8 @@ struct GqaSplit {
     }
 };
 // A page for each warp while there are few (latency is all: 13.1 -> 10.1 us for a token written and
-// attended to behind 333, 8 cache heads, with this split), else at least kGqaMinPages; and a unit is cut into no more than 128 parts on
-// average.
+// attended to behind 333, 8 cache heads, with this split), else at least kGqaMinPages; and a unit is cut
+// into no more than 128 parts on average.
 __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int rounds, int units) {
     const long long a = total <= kGqaFewPages ? total : total / kGqaMinPages, b = 128LL * units;
     const long long m = a < b ? a : b;
@@ -787,7 +787,9 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             for (int i = 0; i < 32; ++i) {
                 const float wv = __shfl_sync(0xffffffffu, wi, i);
                 if (threadIdx.x < D && (there >> i & 1u))
-                    x = fmaf(wv, lds_cluster(part0 + i % kWarps * kPart + (qi * D + threadIdx.x) * 4, i / kWarps), x);
+                    x = fmaf(wv,
+                             lds_cluster(part0 + i % kWarps * kPart + (qi * D + threadIdx.x) * 4, i / kWarps),
+                             x);
             }
             const bool any = sum != 0.0f;  // (true of a NaN)
             if (threadIdx.x < D)

@@ -431,8 +431,8 @@ void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p) {
     const long long units = (long long)Hk * p->n_pairs * p->key_tiles;
     // One CTA per SM, each with four units at least (a part's read-out costs about as much, and the
     // merge reads it again; 64 sequences of up to 512 tokens behind 4096, 8 cache heads of 128: 33, 33,
-    // 30, 26, 25, 27, 29 us with 1, 2, 3, 4, 5, 6, 8 units), but a quarter of the SMs at least where there are so many units: a unit
-    // takes 2 us, which is all that counts in a short call.
+    // 30, 26, 25, 27, 29 us with 1, 2, 3, 4, 5, 6, 8 units), but a quarter of the SMs at least where
+    // there are so many units: a unit takes 2 us, which is all that counts in a short call.
     const long long want = (units + 3) / 4, least = units < kGrid / 4 ? units : kGrid / 4;
     p->grid = (int)(want > kGrid ? kGrid : want < least ? least : want);
     // CTAs that share one pair's key tiles: at most this many (a stretch begins every
