@@ -478,42 +478,13 @@ def attention_qkvpacked(qkv, causal: bool = False, scale: float | None = None):
 def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | None = None,
                  out=None, lse=None, workspace=None, k_exp=None, v_exp=None):
     """One decode step over a paged cache: q [B, H, D]; k_cache, v_cache
-    [num_pages, H, FA_PAGE_TOKENS, D] (bf16 or fp16, contiguous); block_tables [B, max_pages] and
+    [num_pages, H, FA_PAGE_TOKENS, D] (of q's dtype, contiguous); block_tables [B, max_pages] and
     seq_lens [B] int32 CUDA tensors.  Returns O [B, H, D] and LSE [B, H] (fp32).
 
     The caches may have fewer heads than q (a divisor: each is shared by a group of query heads),
     and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote."""
-    import torch
-    if k_exp is not None or v_exp is not None or k_cache.shape[1:2] != q.shape[1:2]:
-        return (_binding or _ops()).decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale,
-                                                    out, lse, workspace, k_exp, v_exp)
-    for name, t in (("q", q), ("k_cache", k_cache), ("v_cache", v_cache),
-                    ("block_tables", block_tables), ("seq_lens", seq_lens)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    B, H, D = q.shape
-    num_pages = k_cache.shape[0]
-    if tuple(k_cache.shape) != (num_pages, H, FA_PAGE_TOKENS, D) or v_cache.shape != k_cache.shape:
-        raise ValueError("caches must be [num_pages, H, FA_PAGE_TOKENS, D]")
-    max_pages = block_tables.shape[1] if block_tables.dim() == 2 else 0
-    dt = _dtype_code(q)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    o = out if out is not None else torch.empty_like(q)
-    l = lse if lse is not None else torch.empty((B, H), device=q.device, dtype=torch.float32)
-    ws_bytes = fa_decode_workspace_bytes(B, H, D, max_pages)
-    if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), device=q.device, dtype=torch.uint8)
-    status = fa_decode_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                             block_tables.data_ptr(), seq_lens.data_ptr(), o.data_ptr(),
-                             l.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), B, H, D, num_pages,
-                             max_pages, float(scale), dt, _stream_handle(q.device))
-    if status != FA_OK:
-        raise FaError("fa_decode_paged", status)
-    return o, l
+    return (_binding or _ops()).decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse,
+                                             workspace, k_exp, v_exp)
 
 
 # ---------------------------------------------------------------------------------------

@@ -407,6 +407,31 @@ std::tuple<Tensor, Tensor> decode_paged_ex(const Tensor& q, const Tensor& k_cach
     return {s.o, s.lse};
 }
 
+// decode_paged: the kernel of equal heads over a 16-bit cache where the call has that form, else
+// fa_decode_paged_ex.
+std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, const Tensor& v_cache,
+                                        const Tensor& block_tables, const Tensor& seq_lens,
+                                        std::optional<double> scale, const OptTensor& out,
+                                        const OptTensor& lse, const OptTensor& workspace,
+                                        const OptTensor& k_exp, const OptTensor& v_exp) {
+    if (given(k_exp) || given(v_exp) || q.dim() != 3 || k_cache.dim() != 4 || k_cache.size(1) != q.size(1))
+        return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
+                               k_exp, v_exp);
+    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
+    const Step s = decode_outputs(q, out, lse);
+    const Cache c = check_cache(k_cache, v_cache, {}, {}, q.scalar_type(), s.index);
+    TORCH_CHECK_VALUE(c.D == s.D, "the cache has heads of ", c.D, ", q of ", s.D);
+    const int max_pages = check_tables(block_tables, seq_lens, s.B, s.index);
+    const Tensor ws =
+        workspace_of(workspace, fa_decode_workspace_bytes(s.B, s.Hq, s.D, max_pages), q, s.index);
+    check_status("fa_decode_paged",
+                 fa_decode_paged(ptr(q), c.k, c.v, ptr<int32_t>(block_tables), ptr<int32_t>(seq_lens),
+                                 ptr(s.o), ptr<float>(s.lse), ptr(ws), ws.nbytes(), s.B, s.Hq, s.D,
+                                 c.num_pages, max_pages, scale_of(scale, s.D), s.dt,
+                                 stream_of(s.index)));
+    return {s.o, s.lse};
+}
+
 std::tuple<Tensor, Tensor> decode_shared_prefix(const Tensor& q, const Tensor& k_cache,
                                                 const Tensor& v_cache, const Tensor& prefix_table,
                                                 int64_t prefix_len, const Tensor& block_tables,
@@ -457,6 +482,7 @@ PYBIND11_MODULE(fa_torch, m) {
     m.def("rotary_apply", &rotary_apply);
     m.def("cache_append", &cache_append);
     m.def("cache_read", &cache_read);
+    m.def("decode_paged", &decode_paged);
     m.def("decode_paged_ex", &decode_paged_ex);
     m.def("decode_shared_prefix", &decode_shared_prefix);
 }
