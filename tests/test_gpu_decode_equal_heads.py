@@ -9,6 +9,7 @@ import torch
 import gpu_helpers as gh
 import tiled_attention_08_gb300 as fa
 from test_gpu_cache import make_cache, status
+from test_gpu_decode_gqa import check, fill
 from test_gpu_rotary import randn
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,22 @@ def test_refusals_before_anything_is_read():
     with pytest.raises(fa.FaError):
         fa.decode_paged(q, kc, vc, bt, sl, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert fa.fa_launch_count() == launched and status() == fa.FA_OK
+
+
+@pytest.mark.parametrize("D,dtype", [(64, torch.float16), (128, torch.bfloat16), (64, torch.bfloat16),
+                                     (128, torch.float16)], ids=str)
+@pytest.mark.parametrize("lens,H", [([0, 1, 15, 16, 17, 63, 64, 129, 300, 1000], 3), ([1], 1), ([3000], 2),
+                                    ([17, 2001, 0], 4), ([5] * 700, 1)],
+                         ids=["mixed", "one", "long", "split", "many"])
+def test_unused_slots_may_hold_anything(D, dtype, lens, H):
+    """Pages that cache_append wrote in part, all other slots NaN: one CTA per row and split rows."""
+    rng = np.random.default_rng(D + len(lens))
+    kc, vc, _, _, bt, sl, ks, vs = fill(rng, lens, H, D, dtype, False)
+    q = randn(len(lens), H, D, dtype=dtype, seed=H)
+    o, lse = fa.decode_paged(q, kc, vc, bt, sl)
+    assert status() == fa.FA_OK
+    check(o, lse, q, ks, vs, 1.0 / math.sqrt(D), dtype, False)
+    for c in (kc, vc):  # infinities there instead
+        c.nan_to_num_(math.inf)
+    o2, lse2 = fa.decode_paged(q, kc, vc, bt, sl)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)

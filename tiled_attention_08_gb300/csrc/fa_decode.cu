@@ -156,11 +156,11 @@ __global__ void __launch_bounds__(DecCfg<D>::kThreads) fa_decode_kernel(const De
                 for (int tt = 0; tt < C::kTokPerWarp; ++tt)
                     s[tt] += __shfl_xor_sync(0xffffffffu, s[tt], off);
             }
+            const int left = n - (pg * kPageTokens + warp * C::kTokPerWarp);  // tokens from here on
             float mx = -INFINITY;
 #pragma unroll
             for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
-                const int token = pg * kPageTokens + warp * C::kTokPerWarp + tt;
-                if (token >= n) s[tt] = -INFINITY;  // past the sequence's last token
+                if (tt >= left) s[tt] = -INFINITY;  // past the sequence's last token
                 mx = fmaxf(mx, s[tt]);
             }
             const float m_new = fmaxf(m, mx);
@@ -177,6 +177,8 @@ __global__ void __launch_bounds__(DecCfg<D>::kThreads) fa_decode_kernel(const De
                 for (int e = 0; e < C::kPer; ++e) o[e] *= alpha;
 #pragma unroll
                 for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
+                    // Slots past the end hold anything, and their weight of zero times a NaN is one.
+                    if (tt >= left) break;
                     const int t = warp * C::kTokPerWarp + tt;
                     float vv[C::kPer];
                     load_row16<BF16, C::kPer>(vp + (t * D + lane * C::kPer) * 2, vv);
