@@ -73,3 +73,50 @@ def test_unused_slots_may_hold_anything(D, dtype, lens, H):
         c.nan_to_num_(math.inf)
     o2, lse2 = fa.decode_paged(q, kc, vc, bt, sl)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens,at", [([40, 40, 1], (1, 35)), ([40, 1, 40], (1, 0)), ([16, 2000, 5], (1, 999)),
+                                     ([4, 3000, 4], (1, 0)), ([4, 1, 3000], (1, 0))], ids=str)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_key_makes_its_row_nan(lens, at, bad):
+    """A NaN score is in every weight of its row: O and LSE are NaN, even where it is the row's only
+    score, or a warp's or a split's; as in the kernel of grouped heads.  Other rows keep their bits."""
+    D, H, dtype = 64, 2, torch.bfloat16
+    rng = np.random.default_rng(len(lens))
+    kc, vc, _, _, bt, sl, _, _ = fill(rng, lens, H, D, dtype, False)
+    q = randn(len(lens), H, D, dtype=dtype)
+    q[:, :, 7] = 1.0  # (an infinity is a score of +inf: inf - inf in every weight)
+    good, good_lse = fa.decode_paged(q, kc, vc, bt, sl)
+    b, t = at
+    kc[int(bt[b, t // 16]), 1, t % 16, 7] = bad
+    o, lse = fa.decode_paged(q, kc, vc, bt, sl)
+    o2, lse2 = fa._decode_paged_ex(q, kc, vc, bt, sl)
+    assert status() == fa.FA_OK
+    for x, l in ((o, lse), (o2, lse2)):
+        assert torch.isnan(x[b, 1]).all() and torch.isnan(l[b, 1])
+    keep = torch.ones(len(lens), H, dtype=torch.bool)
+    keep[b, 1] = False
+    assert torch.equal(o[keep], good[keep]) and torch.equal(lse[keep], good_lse[keep])
+
+
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_scores_of_minus_infinity_weigh_nothing(n):
+    """Scores of -inf beside finite ones count for nothing; alone they leave O = 0, LSE = -inf, as a row
+    without a key."""
+    D, dtype = 64, torch.bfloat16
+    rng = np.random.default_rng(n)
+    kc, vc, _, _, bt, sl, ks, vs = fill(rng, [n, n], 1, D, dtype, False)
+    q = randn(2, 1, D, dtype=dtype)
+    q[:, :, 0] = 1.0
+    table = bt.long()
+    for t in range(n):
+        if t != 20:  # (sequence 1 keeps one finite score, where it is long enough)
+            kc[table[1, t // 16], 0, t % 16, 0] = -math.inf
+        kc[table[0, t // 16], 0, t % 16, 0] = -math.inf
+    o, lse = fa.decode_paged(q, kc, vc, bt, sl)
+    assert status() == fa.FA_OK
+    assert not o[0].any() and lse[0, 0] == -math.inf
+    if n <= 20:
+        assert not o[1].any() and lse[1, 0] == -math.inf
+    else:
+        check(o[1:], lse[1:], q[1:], [ks[1][:, 20:21]], [vs[1][:, 20:21]], 1.0 / math.sqrt(D), dtype, False)

@@ -164,29 +164,29 @@ __global__ void __launch_bounds__(DecCfg<D>::kThreads) fa_decode_kernel(const De
                 mx = fmaxf(mx, s[tt]);
             }
             const float m_new = fmaxf(m, mx);
-            if (m_new != -INFINITY) {  // (all of this warp's tokens so far may be masked)
-                const float alpha = (m == -INFINITY) ? 0.0f : ex2_approx(m - m_new);
-                float pr[C::kTokPerWarp], psum = 0.0f;
+            // (-inf while every token of this warp is masked or a NaN: a maximum passes NaN over, the
+            // sum keeps it.)
+            const float ref = (m_new == -INFINITY) ? 0.0f : m_new;
+            const float alpha = (m == -INFINITY) ? 0.0f : ex2_approx(m - ref);
+            float pr[C::kTokPerWarp], psum = 0.0f;
 #pragma unroll
-                for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
-                    pr[tt] = ex2_approx(s[tt] - m_new);
-                    psum += pr[tt];
-                }
-                l = l * alpha + psum;
-#pragma unroll
-                for (int e = 0; e < C::kPer; ++e) o[e] *= alpha;
-#pragma unroll
-                for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
-                    // Slots past the end hold anything, and their weight of zero times a NaN is one.
-                    if (tt >= left) break;
-                    const int t = warp * C::kTokPerWarp + tt;
-                    float vv[C::kPer];
-                    load_row16<BF16, C::kPer>(vp + (t * D + lane * C::kPer) * 2, vv);
-#pragma unroll
-                    for (int e = 0; e < C::kPer; ++e) o[e] = fmaf(pr[tt], vv[e], o[e]);
-                }
-                m = m_new;
+            for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
+                pr[tt] = ex2_approx(s[tt] - ref);
+                psum += pr[tt];
             }
+            l = l * alpha + psum;
+#pragma unroll
+            for (int e = 0; e < C::kPer; ++e) o[e] *= alpha;
+#pragma unroll
+            for (int tt = 0; tt < C::kTokPerWarp; ++tt) {
+                const int t = warp * C::kTokPerWarp + tt;
+                float vv[C::kPer];
+                load_row16<BF16, C::kPer>(vp + (t * D + lane * C::kPer) * 2, vv);
+                // Slots past the end hold anything, and their weight of zero times a NaN is one.
+#pragma unroll
+                for (int e = 0; e < C::kPer; ++e) o[e] = fmaf(pr[tt], tt < left ? vv[e] : 0.0f, o[e]);
+            }
+            m = m_new;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_empty[st]);  // this warp is done with the stage
         }
@@ -204,16 +204,15 @@ __global__ void __launch_bounds__(DecCfg<D>::kThreads) fa_decode_kernel(const De
 #pragma unroll
             for (int w = 0; w < C::kComputeWarps; ++w) M = fmaxf(M, red_m[w]);
             float L = 0.0f, O = 0.0f;
-            if (M != -INFINITY) {
 #pragma unroll
-                for (int w = 0; w < C::kComputeWarps; ++w) {
-                    const float f = (red_m[w] == -INFINITY) ? 0.0f : ex2_approx(red_m[w] - M);
-                    L = fmaf(red_l[w], f, L);
-                    O = fmaf(red_o[w][tid], f, O);
-                }
+            for (int w = 0; w < C::kComputeWarps; ++w) {
+                // (a warp without a token has a sum of 0; one with NaN scores alone keeps its NaN)
+                const float f = (red_m[w] == -INFINITY) ? 1.0f : ex2_approx(red_m[w] - M);
+                L = fmaf(red_l[w], f, L);
+                O = fmaf(red_o[w][tid], f, O);
             }
-            const float out = L > 0.0f ? O / L : 0.0f;
-            const float lse2 = L > 0.0f ? M + log2f(L) : -INFINITY;  // log2 domain
+            const float out = L != 0.0f ? O / L : 0.0f;  // (L != 0 is true of a NaN)
+            const float lse2 = L != 0.0f ? M + log2f(L) : -INFINITY;  // log2 domain
             const size_t row = (size_t)b * p.H + h;
             if (p.splits == 1) {
                 uint16_t* dst = reinterpret_cast<uint16_t*>(p.o) + row * D + tid;
@@ -241,17 +240,15 @@ __global__ void __launch_bounds__(D) fa_decode_combine_kernel(const DecodeParams
     float M = -INFINITY;
     for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_lse[base + s]);
     float W = 0.0f, O = 0.0f;
-    if (M != -INFINITY) {
-        for (int s = 0; s < p.splits; ++s) {
-            const float l2 = p.part_lse[base + s];
-            const float w = (l2 == -INFINITY) ? 0.0f : ex2_approx(l2 - M);
-            W += w;
-            O = fmaf(w, p.part_o[(base + s) * D + tid], O);
-        }
+    for (int s = 0; s < p.splits; ++s) {
+        const float l2 = p.part_lse[base + s];  // (a NaN, which the maximum passes over, makes W one)
+        const float w = (l2 == -INFINITY) ? 0.0f : ex2_approx(l2 - M);
+        W += w;
+        O = fmaf(w, p.part_o[(base + s) * D + tid], O);
     }
     uint16_t* dst = reinterpret_cast<uint16_t*>(p.o) + row * D + tid;
-    *dst = (uint16_t)(pack2<BF16>(W > 0.0f ? O / W : 0.0f, 0.0f) & 0xffffu);
-    if (tid == 0) p.lse[row] = W > 0.0f ? (M + log2f(W)) * kLn2 : -INFINITY;
+    *dst = (uint16_t)(pack2<BF16>(W != 0.0f ? O / W : 0.0f, 0.0f) & 0xffffu);
+    if (tid == 0) p.lse[row] = W != 0.0f ? (M + log2f(W)) * kLn2 : -INFINITY;
 }
 
 template <int D, bool BF16>
