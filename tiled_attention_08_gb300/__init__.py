@@ -542,9 +542,9 @@ def rotary_apply(x, positions, freqs, mscale: float = 1.0, interleaved: bool = F
 
 def rotary(q, k, positions, freqs, mscale: float = 1.0, interleaved: bool = False):
     """Rotary positions on queries [B, Hq, L, D] and keys [B, Hk, L, D] in one launch,
-    differentiable; returns the rotated (q, k).  Any strides with a contiguous last dimension:
-    [B, L, H, D] tensors transposed, or the parts of a packed [B, L, 3, H, D] tensor, are read in
-    place.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale`` from
+    differentiable (in reverse and in forward mode); returns the rotated (q, k).  Any strides with
+    a contiguous last dimension: [B, L, H, D] tensors transposed, or the parts of a packed
+    [B, L, 3, H, D] tensor, are read in place.  ``positions``: int32 [L] or [B, L], or None for 0 .. L-1; ``freqs``, ``mscale`` from
     ``rotary_freqs``.  The rotated tensors go to ``attention`` (or, one row per sequence, to
     ``decode_paged``).  As for any operation, torch refuses to capture a backward into a CUDA
     graph while an eager graph of the same leaves is alive."""

@@ -7,6 +7,7 @@
 // than FA_OK raises FaError(call, status).
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
+#include <ATen/ops/_make_dual.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -217,12 +218,36 @@ struct Rotary : torch::autograd::Function<Rotary> {
     }
 };
 
+// The operands that are there, turned; a node of the graph where one of them needs a gradient.
+std::vector<Tensor> turned(const OptTensor& q, const OptTensor& k, const Rotation& r) {
+    if (at::GradMode::is_enabled() && ((given(q) && q->requires_grad()) || (given(k) && k->requires_grad())))
+        return Rotary::apply(q, k, r.positions, r.freqs, r.mscale, r.interleaved, false);
+    std::vector<Tensor> xs;
+    for (const OptTensor* x : {&q, &k})
+        if (given(*x)) xs.push_back(**x);
+    return rotate(xs, r, false);
+}
+
+// The tangent of a dual tensor (torch has one level of them).
+OptTensor tangent_of(const Tensor& x) {
+    const Tensor& t = x._fw_grad(0);
+    return t.defined() && !t._is_zerotensor() ? OptTensor(t) : OptTensor();
+}
+
 std::tuple<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const OptTensor& positions,
                                   const Tensor& freqs, double mscale, bool interleaved) {
-    const auto out = at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad())
-                         ? Rotary::apply(OptTensor(q), OptTensor(k), positions, freqs, mscale,
-                                         interleaved, false)
-                         : rotate({q, k}, {positions, freqs, mscale, interleaved}, false);
+    const Rotation r = {positions, freqs, mscale, interleaved};
+    const OptTensor tq = tangent_of(q), tk = tangent_of(k);
+    if (!tq && !tk) {
+        const auto out = turned(q, k, r);
+        return {out[0], out[1]};
+    }
+    // Forward mode: the map is linear, so the tangents are turned like the values.
+    auto out = turned(q._fw_primal(0), k._fw_primal(0), r);
+    const auto t = turned(tq, tk, r);
+    size_t n = 0;
+    if (tq) out[0] = at::_make_dual(out[0], t[n++], 0);
+    if (tk) out[1] = at::_make_dual(out[1], t[n], 0);
     return {out[0], out[1]};
 }
 
