@@ -8,6 +8,7 @@ import torch.autograd.forward_ad as fwd
 
 import gpu_helpers as gh
 import tiled_attention_08_gb300 as fa
+from test_gpu_cache import make_cache, status
 from test_gpu_rotary import randn
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +59,41 @@ def test_broadcast_and_differentiable_tangents():
         assert torch.equal(dt, back.sum(1, keepdim=True))
         dq, = torch.autograd.grad(primal, q, g)
         assert torch.equal(dq, back)
+
+
+def test_writes_are_seen_by_autograd():
+    """Every call that writes a caller's tensor raises its version, so that a backward which saved the
+    old values is refused; tensors of inference mode, which have no version, can be written too."""
+    q, k, x, _, freqs, mscale = operands()
+    w = torch.ones_like(x, requires_grad=True)
+    y = (w * x).sum()  # saves x
+    fa.rotary_apply(x, None, freqs, mscale, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    for quant in (False, True):
+        kc, vc, ke, ve = make_cache(B, HK, D, q.dtype, quant)
+        bt = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+        sl = torch.full((B,), L, dtype=torch.int32, device="cuda")
+        dense = tuple(torch.empty_like(k) for _ in range(2))
+        row = q[:, :, 0].contiguous()
+        o, lse = torch.empty_like(row), torch.empty((B, HQ), device="cuda")
+        ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        calls = [((kc, vc, ke, ve), lambda: fa.cache_append(k, k, kc, vc, bt, sl, k_exp=ke, v_exp=ve)),
+                 (dense, lambda: fa.cache_read(kc, vc, bt, sl, L, k_exp=ke, v_exp=ve, out=dense)),
+                 ((o, lse, ws), lambda: fa.decode_paged(row, kc, vc, bt, sl, out=o, lse=lse, workspace=ws,
+                                                        k_exp=ke, v_exp=ve))]
+        if not quant:
+            calls.append(((o, lse, ws), lambda: fa.decode_shared_prefix(
+                row, kc, vc, bt[0], 1, bt, sl, out=o, lse=lse, workspace=ws)))
+            one, one_lse = o[:, :1].contiguous(), lse[:, :1].contiguous()
+            calls.append(((one, one_lse, ws), lambda: fa.decode_paged(
+                row[:, :1].contiguous(), kc, vc, bt, sl, out=one, lse=one_lse, workspace=ws)))
+        for tensors, call in calls:
+            tensors = [t for t in tensors if t is not None]
+            before = [t._version for t in tensors]
+            call()
+            assert all(t._version > v for t, v in zip(tensors, before))
+    with torch.inference_mode():
+        z = x.clone()
+    assert torch.equal(fa.rotary_apply(z, None, freqs, mscale, out=z), fa.rotary_apply(x, None, freqs, mscale))
+    assert status() == fa.FA_OK

@@ -87,6 +87,14 @@ T* ptr(const OptTensor& t) {
 }
 bool given(const OptTensor& t) { return t && t->defined(); }
 
+// Tells autograd that a caller's tensor is being written: a backward that saved it is then refused.
+void written(const Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const OptTensor& t) {
+    if (given(t)) written(*t);
+}
+
 // ---------------------------------------------------------------------------------------
 // Rotary positions
 // ---------------------------------------------------------------------------------------
@@ -253,6 +261,7 @@ std::tuple<Tensor, Tensor> rotary(const Tensor& q, const Tensor& k, const OptTen
 
 Tensor rotary_apply(const Tensor& x, const OptTensor& positions, const Tensor& freqs, double mscale,
                     bool interleaved, bool inverse, const OptTensor& out) {
+    written(out);
     return rotate({x.detach()}, {positions, freqs, mscale, interleaved}, inverse,
                   given(out) ? std::vector<Tensor>{*out} : std::vector<Tensor>{})[0];
 }
@@ -325,6 +334,10 @@ void cache_append(const Tensor& k, const Tensor& v, const Tensor& k_cache, const
     const int max_pages = check_tables(block_tables, seq_lens, B, index);
     if (given(new_lens)) int32_vector("new_lens", *new_lens, B, index);
     const int rd = given(freqs) ? rotary_dim_of(*freqs, index) : 0;
+    written(k_cache);
+    written(v_cache);
+    written(k_exp);
+    written(v_exp);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
     check_status("fa_cache_append",
                  fa_cache_append(ptr(k), ptr(v), st, c.k, c.v, c.k_exp, c.v_exp,
@@ -357,6 +370,8 @@ std::tuple<Tensor, Tensor> cache_read(const Tensor& k_cache, const Tensor& v_cac
     same_device("out[1]", v, index);
     TORCH_CHECK_VALUE(k.dim() == 4 && v.dim() == 4, "out must be [B, H, length, D] views");
     const fa_strides st[2] = {row_strides("out[0]", k, sizes), row_strides("out[1]", v, sizes)};
+    written(out_k);
+    written(out_v);
     check_status("fa_cache_read",
                  fa_cache_read(c.k, c.v, c.k_exp, c.v_exp, ptr<int32_t>(block_tables),
                                ptr<int32_t>(seq_lens), ptr(k), ptr(v), st, as_int("B", B), c.H,
@@ -382,6 +397,7 @@ Step decode_outputs(const Tensor& q, const OptTensor& out, const OptTensor& lse)
                               out->is_contiguous(),
                           "out must be a contiguous tensor like q");
         same_device("out", *out, index);
+        written(*out);
         s.o = *out;
     } else {
         s.o = at::empty(q.sizes(), q.options());
@@ -391,6 +407,7 @@ Step decode_outputs(const Tensor& q, const OptTensor& out, const OptTensor& lse)
                               lse->is_contiguous(),
                           "lse must be a contiguous fp32 [B, H] tensor");
         same_device("lse", *lse, index);
+        written(*lse);
         s.lse = *lse;
     } else {
         s.lse = at::empty(q.sizes().slice(0, 2), q.options().dtype(at::kFloat));
@@ -403,6 +420,7 @@ Tensor workspace_of(const OptTensor& workspace, size_t need, const Tensor& q, in
     if (given(workspace)) {
         same_device("workspace", *workspace, index);
         TORCH_CHECK_VALUE(workspace->is_contiguous(), "workspace must be contiguous");
+        written(*workspace);
         return *workspace;
     }
     return at::empty({(int64_t)need}, q.options().dtype(at::kByte));
