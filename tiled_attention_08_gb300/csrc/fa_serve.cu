@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "fa_host.h"
+#include "fa_overlap.h"
 
 using namespace fa;
 
@@ -15,18 +16,19 @@ namespace {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
-// Rows of two operands with the same strides whose extents overlap but whose elements do not:
-// parts of one packed tensor (a row's heads lie together, one part's before the other's).
-bool packed_parts(const void* a, int Ha, const void* b, int Hb, const Strides& s, int L, int D) {
-    const intptr_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
-    const long long delta = (pa < pb ? pb - pa : pa - pb) / 2;
-    const long long first = (long long)(pa < pb ? Ha : Hb) * D;
-    const long long second = (long long)(pa < pb ? Hb : Ha) * D;
-    if (s.h != D || delta < first) return false;
-    if (L == 1) return delta + second <= s.b;  // one row per sequence: its own stride means nothing
-    return delta + second <= s.l && s.b >= (long long)L * s.l;
+// The same layout: equal strides of the dimensions that have more than one entry.
+bool same(const Strides& a, const Strides& b, int B, int H, int L) {
+    return (B <= 1 || a.b == b.b) && (H <= 1 || a.h == b.h) && (L <= 1 || a.l == b.l);
 }
-bool same(const Strides& a, const Strides& b) { return a.b == b.b && a.h == b.h && a.l == b.l; }
+// Parts of one packed tensor: the same layout, extents that overlap, no element in common.
+bool packed_parts(const void* a, const Strides& sa, int Ha, const void* b, const Strides& sb, int Hb, int B,
+                  int L, int D) {
+    const intptr_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
+    if (!same(sa, sb, B, Ha < Hb ? Ha : Hb, L)) return false;
+    const long long h = Ha > 1 ? sa.h : sb.h;
+    return pa < pb ? interleave_apart((pb - pa) / 2, B, Ha, Hb, L, D, sa.b, h, sa.l)
+                   : interleave_apart((pa - pb) / 2, B, Hb, Ha, L, D, sa.b, h, sa.l);
+}
 
 // The rotation of fa_rotary and fa_cache_append; freqs may be null only with rotary_dim = 0.
 fa_status check_rotation(const int64_t* freqs, int rotary_dim, float mscale, int interleaved, int D,
@@ -276,11 +278,10 @@ fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out,
             if (H[j] == 0) continue;
             const RotaryOperand &a = p.op[i], &b = p.op[j];
             // An output may be its own input (in place); parts of one packed tensor may interleave.
-            if (overlap(rout[i], rin[j]) && !(i == j && a.y == b.x && same(a.sy, b.sx)) &&
-                !(same(a.sy, b.sx) && packed_parts(a.y, a.H, b.x, b.H, a.sy, L, D)))
+            if (overlap(rout[i], rin[j]) && !(i == j && a.y == b.x && same(a.sy, b.sx, B, a.H, L)) &&
+                !packed_parts(a.y, a.sy, a.H, b.x, b.sx, b.H, B, L, D))
                 return FA_ERR_INVALID_ARG;
-            if (i < j && overlap(rout[i], rout[j]) &&
-                !(same(a.sy, b.sy) && packed_parts(a.y, a.H, b.y, b.H, a.sy, L, D)))
+            if (i < j && overlap(rout[i], rout[j]) && !packed_parts(a.y, a.sy, a.H, b.y, b.sy, b.H, B, L, D))
                 return FA_ERR_INVALID_ARG;
         }
     }
@@ -386,9 +387,7 @@ fa_status fa_cache_read(const void* k_cache, const void* v_cache, const void* k_
     for (const Range& o : outs)
         for (const Range& i : ins)
             if (overlap(o, i)) return FA_ERR_INVALID_ARG;
-    if (overlap(outs[0], outs[1]) &&
-        !(same(p.sk, p.sv) && packed_parts(k, H, v, H, p.sk, L, D)))
-        return FA_ERR_INVALID_ARG;
+    if (overlap(outs[0], outs[1]) && !packed_parts(k, p.sk, H, v, p.sv, H, B, L, D)) return FA_ERR_INVALID_ARG;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.k_exp = q8 ? static_cast<const uint8_t*>(k_exp) : nullptr;
