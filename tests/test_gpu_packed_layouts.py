@@ -60,3 +60,42 @@ def test_read_back_into_a_packed_tensor(name, B, H, L):
     if L > 1:  # parts that meet are still refused
         with pytest.raises(fa.FaError):
             fa.cache_read(kc, vc, bt, sl, L - 1, k_exp=ke, v_exp=ve, out=(out[0][:, :, 1:], out[0][:, :, :-1]))
+
+
+def _odd_ones():
+    """[B, H, L, D] views whose dimensions of size 1 have strides that no row could be read by, and one
+    that starts inside a 16-byte unit."""
+    n = torch.randn(3 * 5 * D + 8, device="cuda").bfloat16()
+    for shape, strides in (((3, 1, 5, D), (5 * D, 1, D)), ((1, 3, 5, D), (3, 5 * D, D)),
+                           ((3, 5, 1, D), (5 * D, D, 7)), ((1, 1, 1, D), (1, 2, 3)), ((3, 1, 5, D), (5 * D, 0, D)),
+                           ((3, 5, 1, D), (5 * D, D, 0))):
+        yield torch.as_strided(n, shape, (*strides, 1))
+    yield torch.as_strided(n, (3, 5, 1, D), (5 * D, D, D, 1), 1)
+
+
+@pytest.mark.parametrize("i", range(7))
+def test_strides_of_single_entries_mean_nothing(i):
+    x = list(_odd_ones())[i]
+    plain = x.clone(memory_format=torch.contiguous_format)
+    B, H, L, _ = x.shape
+    freqs, mscale = fa.rotary_freqs(D)
+    pos = torch.arange(7, 7 + L, dtype=torch.int32, device="cuda")
+    want = fa.rotary_apply(plain, pos, freqs, mscale)
+    assert torch.equal(fa.rotary_apply(x, pos, freqs, mscale), want)
+    q, k = x.detach().requires_grad_(), plain.detach().requires_grad_()
+    qo, ko = fa.rotary(q, k, pos, freqs, mscale)
+    assert torch.equal(qo, want) and torch.equal(ko, want)
+    gq, = torch.autograd.grad(qo, q, x, retain_graph=True)  # the gradient has that layout too
+    gk, = torch.autograd.grad(ko, k, plain)
+    assert torch.equal(gq, gk)
+    if i < 6:
+        fa.rotary_apply(x, pos, freqs, mscale, out=x)  # in place
+        assert torch.equal(x, want)
+        kc, vc, ke, ve = make_cache(B, H, D, torch.bfloat16, False)
+        bt = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+        sl = torch.full((B,), L, dtype=torch.int32, device="cuda")
+        fa.cache_append(x, plain, kc, vc, bt, sl)
+        v2 = torch.empty_like(plain)
+        x.zero_()
+        fa.cache_read(kc, vc, bt, sl, L, out=(x, v2))
+        assert status() == fa.FA_OK and torch.equal(x, want) and torch.equal(v2, plain)

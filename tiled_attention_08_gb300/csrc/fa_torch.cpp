@@ -69,11 +69,16 @@ int as_int(const char* name, int64_t v) {
     return (int)v;
 }
 
-// (batch, head, row) element strides of a [B, H, L, D] view.
+// Whether the kernels can step by a view's stride of dimension i.
+bool usable_stride(const Tensor& t, int i) { return t.stride(i) > 0 && (t.stride(i) & 7) == 0; }
+
+// (batch, head, row) element strides of a [B, H, L, D] view.  The stride of a dimension of size 1 means
+// nothing and may be anything: one that the library would refuse is replaced.
 fa_strides row_strides(const char* name, const Tensor& t, at::IntArrayRef shape) {
     TORCH_CHECK_VALUE(t.sizes() == shape, name, " has shape ", t.sizes(), ", expected ", shape);
     TORCH_CHECK_VALUE(t.stride(3) == 1, name, ": the last (D) dimension must be contiguous");
-    return {t.stride(0), t.stride(1), t.stride(2)};
+    auto stride = [&](int i) { return t.size(i) > 1 || usable_stride(t, i) ? t.stride(i) : 8; };
+    return {stride(0), stride(1), stride(2)};
 }
 
 void* stream_of(int index) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream(); }
@@ -105,15 +110,13 @@ int rotary_dim_of(const Tensor& freqs, int index) {
     return as_int("rotary_dim", 2 * freqs.size(0));
 }
 
-// `t` itself where the kernels can read its strides, else a contiguous copy (an expanded gradient,
-// for one, has strides of 0).
+// `t` itself where the kernels can read its rows, else a contiguous copy (an expanded gradient, for
+// one, has strides of 0).
 Tensor kernel_view(const Tensor& t) {
     if (t.dim() != 4) return t;
-    const auto st = t.strides();
-    const bool ok = st[3] == 1 && !((st[0] | st[1] | st[2]) & 7) && st[2] > 0 &&
-                    (st[1] > 0 || t.size(1) == 1) && (st[0] > 0 || t.size(0) == 1) &&
-                    !(reinterpret_cast<uintptr_t>(t.data_ptr()) & 15);
-    return ok ? t : t.contiguous();
+    bool ok = t.stride(3) == 1 && !(reinterpret_cast<uintptr_t>(t.data_ptr()) & 15);
+    for (int i = 0; i < 3; ++i) ok = ok && (t.size(i) <= 1 || usable_stride(t, i));
+    return ok ? t : t.clone(at::MemoryFormat::Contiguous);
 }
 
 struct Rotation {
