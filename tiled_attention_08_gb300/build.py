@@ -57,10 +57,11 @@ def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
     return src, r.stdout + r.stderr
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """Where torch is installed, or None."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("fa_torch.so needs an installed torch")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
@@ -87,14 +88,16 @@ def _link_torch(obj: str) -> None:
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Compiles and links the library and the torch binding; returns the path of libfa.so."""
+    """Compiles and links the library and, where torch is installed, its binding; returns the path
+    of libfa.so."""
     os.makedirs(BUILD, exist_ok=True)
     headers = _headers()
     torch_obj = os.path.join(BUILD, "fa_torch.o")
-    # Compiled by another torch than this one: its headers are part of the object's inputs.
-    version = os.path.join(_torch_dir(), "version.py")
+    torch_dir = _torch_dir()
     torch_job = None
-    if force or _stale(torch_obj, TORCH_SRC, [os.path.join(ROOT, "include", "fa.h"), version]):
+    # Compiled by another torch than this one: its headers are part of the object's inputs.
+    if torch_dir and (force or _stale(torch_obj, TORCH_SRC, [os.path.join(ROOT, "include", "fa.h"),
+                                                             os.path.join(torch_dir, "version.py")])):
         torch_pool = cf.ThreadPoolExecutor(max_workers=1)
         torch_job = torch_pool.submit(_compile_torch, torch_obj)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -116,6 +119,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    if not torch_dir:
+        print("torch is not installed: fa_torch.so (decode_paged, rotary and the calls on a cache for torch "
+              "tensors) is not built", file=sys.stderr)
+        return LIB
     if torch_job is not None:
         torch_job.result()
     if torch_job is not None or not os.path.exists(TORCH_LIB):
