@@ -61,3 +61,43 @@ def test_library_without_torch(tools, capsys):
     assert tools.since() == ["fa_torch.o", "fa_torch.so"]
     fa_build.build()
     assert tools.since() == []
+
+
+def test_binding_follows_the_installed_torch(tools):
+    """Another torch is noticed by its version, however old its files are."""
+    fa_build.build()
+    assert "fa_torch.so" in tools.since()
+    version = tools.torch / "version.py"
+    version.write_text("__version__ = '1.1'\n")
+    os.utime(version, (1, 1))
+    fa_build.build()
+    assert tools.since() == ["fa_torch.o", "fa_torch.so"]
+    os.utime(version)  # touched, but the same
+    fa_build.build()
+    assert tools.since() == []
+
+
+@pytest.mark.parametrize("broken", ["fa_fwd.o", "libfa.so", "fa_torch.o", "fa_torch.so"])
+def test_a_build_that_failed_half_way_is_taken_up_again(tools, broken):
+    """Whatever step fails, nothing torn is left in its place, and the next build ends with libraries that
+    are newer than all objects."""
+    fa_build.build()
+    tools.since()
+    before = {name: (tools.dir / name).read_text() for name in os.listdir(tools.dir)}
+    for name in os.listdir(tools.dir):  # everything is older than the sources
+        os.utime(tools.dir / name, (1, 1))
+    tools.failing = (broken,)
+    with pytest.raises(RuntimeError):
+        fa_build.build()
+    assert (tools.dir / broken).read_text() == before[broken]
+    assert all("torn" not in (tools.dir / name).read_text() for name in os.listdir(tools.dir))
+    tools.failing = ()
+    tools.since()
+    fa_build.build()
+    assert broken in tools.since()
+    for lib in ("libfa.so", "fa_torch.so"):
+        t = os.path.getmtime(tools.dir / lib)
+        objs = [n for n in os.listdir(tools.dir) if n.endswith(".o") and (n == "fa_torch.o") == (lib == "fa_torch.so")]
+        assert t > 1 and all(os.path.getmtime(tools.dir / n) <= t for n in objs)
+    fa_build.build()
+    assert tools.since() == []

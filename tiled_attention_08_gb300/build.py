@@ -3,7 +3,10 @@ fa_torch.so, the torch binding of the small calls (csrc/fa_torch.cpp, host code)
 
 Usage: ``python -m tiled_attention_08_gb300.build [--verbose]``.  Object files and the
 library go to ``tiled_attention_08_gb300/_build/`` (git-ignored).  A unit is recompiled when
-it or any header it may include is newer than its object file.
+it or any header it may include is newer than its object file (the binding also when the
+installed torch is not the one it was compiled for), and a library is linked again when an
+object is newer than it.  Objects and libraries are put in place whole, so that an interrupted
+build leaves none that looks fresh.
 """
 from __future__ import annotations
 
@@ -47,14 +50,23 @@ def _stale(obj: str, src: str, headers: list[str]) -> bool:
     return any(os.path.getmtime(f) > t for f in [src, *headers])
 
 
+def _run(cmd: list[str], out: str, what: str) -> str:
+    """Runs a command that writes ``out``, which appears whole or not at all; returns its messages."""
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return r.stdout + r.stderr
+
+
 def _compile(src: str, obj: str, verbose: bool) -> tuple[str, str]:
-    cmd = [_nvcc(), *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]
+    cmd = [_nvcc(), *ARCH, *NVCC_FLAGS, "-c", src]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
-    return src, r.stdout + r.stderr
+    return src, _run(cmd, obj, f"nvcc failed for {os.path.basename(src)}")
 
 
 def _torch_dir() -> str | None:
@@ -65,26 +77,36 @@ def _torch_dir() -> str | None:
     return list(spec.submodule_search_locations)[0]
 
 
-def _compile_torch(obj: str) -> None:
+def _torch_id() -> str:
+    """The installed torch that an object was compiled for: its place and its version file."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return _torch_dir() + "\n" + f.read()
+
+
+def _other_torch(note: str) -> bool:
+    """Whether the note beside the object names another torch than the installed one."""
+    if not os.path.exists(note):
+        return True
+    with open(note) as f:
+        return f.read() != _torch_id()
+
+
+def _compile_torch(obj: str, note: str) -> None:
     inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", inc, "-I",
-           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I",
-           sysconfig.get_paths()["include"], "-c", TORCH_SRC, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for fa_torch.cpp:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(note):  # (no note: compiled again, should this end half way)
+        os.remove(note)
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", inc, "-I",
+          os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I",
+          sysconfig.get_paths()["include"], "-c", TORCH_SRC], obj, "g++ failed for fa_torch.cpp")
+    with open(note, "w") as f:
+        f.write(_torch_id())
 
 
 def _link_torch(obj: str) -> None:
-    tmp = TORCH_LIB + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch",
-           "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libfa.so",
-           "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of fa_torch.so failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, TORCH_LIB)
+    _run(["g++", "-shared", obj, "-L", os.path.join(_torch_dir(), "lib"), "-ltorch", "-ltorch_cpu",
+          "-ltorch_python", "-lc10", "-lc10_cuda", "-L", BUILD, "-l:libfa.so", "-Wl,-rpath,$ORIGIN"],
+         TORCH_LIB, "link of fa_torch.so failed")
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -93,13 +115,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = _headers()
     torch_obj = os.path.join(BUILD, "fa_torch.o")
+    torch_note = torch_obj + ".torch"
     torch_dir = _torch_dir()
     torch_job = None
-    # Compiled by another torch than this one: its headers are part of the object's inputs.
-    if torch_dir and (force or _stale(torch_obj, TORCH_SRC, [os.path.join(ROOT, "include", "fa.h"),
-                                                             os.path.join(torch_dir, "version.py")])):
+    if torch_dir and (force or _other_torch(torch_note) or
+                      _stale(torch_obj, TORCH_SRC, [os.path.join(ROOT, "include", "fa.h")])):
         torch_pool = cf.ThreadPoolExecutor(max_workers=1)
-        torch_job = torch_pool.submit(_compile_torch, torch_obj)
+        torch_job = torch_pool.submit(_compile_torch, torch_obj, torch_note)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     jobs = []
     for src in srcs:
@@ -112,20 +134,15 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 if verbose and log.strip():
                     print(f"== {os.path.basename(src)}\n{log}")
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in srcs]
-    if jobs or not os.path.exists(LIB):
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
+    if _stale(LIB, objs[0], objs):
+        _run([_nvcc(), *ARCH, "-shared", *objs], LIB, "link failed")
     if not torch_dir:
         print("torch is not installed: fa_torch.so (decode_paged, rotary and the calls on a cache for torch "
               "tensors) is not built", file=sys.stderr)
         return LIB
     if torch_job is not None:
         torch_job.result()
-    if torch_job is not None or not os.path.exists(TORCH_LIB):
+    if _stale(TORCH_LIB, torch_obj, []):
         _link_torch(torch_obj)
     return LIB
 
