@@ -49,7 +49,10 @@
 // a_j = 2^((y_j - m) + (ev_j - eo)) with the value row's exponent ev_j, so that a weight times its
 // row's scale neither overflows nor is lost in fp16, whatever the rows' magnitudes.  (eo is relative
 // to m: added to y_j itself, ev_j would be lost behind a large score.)  P is rounded to the
-// cache's 16-bit type (fp16 for e4m3: 2^-12), as in the prefill kernels; sums stay fp32.
+// cache's 16-bit type (fp16 for e4m3: 2^-12), as in the prefill kernels; sums stay fp32.  The reference
+// of weights in fp16 stays 2^7 below the largest, which with the 2^8 keeps them below 2^15: fp16's range
+// of normal numbers then begins 2^-21 below the largest instead of 2^-14, and many small weights behind a
+// large one, which the sum of weights has in full, are not rounded away in the products.
 //
 // Measured.  256 sequences of 1..4096 tokens, 32 heads of 128, e4m3: 620 us (6.9 TB/s); 16-bit
 // caches of long batches 6.8 to 7.0 TB/s.  48 sequences of 1..16384, 64 queries on 8 cache heads of 128,
@@ -68,6 +71,7 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.0f;  // log2 headroom of the references
+constexpr float kLift = 7.0f;   // a reference of fp16 weights stays this far below the largest score
 constexpr int kWarps = 4;
 constexpr int kGqaSms = 152;     // the grid is sized for this many SMs on any device, so that the
                                  // workspace does not depend on it
@@ -201,9 +205,9 @@ __device__ __forceinline__ float column_sum(float v) {
 // a NaN (a masked -inf minus it is -inf).
 constexpr float kNoRef = -3.4028234663852886e38f;  // -FLT_MAX
 
-// Raises a reference to the column's maximum; returns the factor of what was summed under it.
-__device__ __forceinline__ float raise(float& ref, float top) {
-    const float next = fmaxf(ref, column_max(top));
+// Raises a reference to the column's maximum less `lift`; returns the factor of what was summed under it.
+__device__ __forceinline__ float raise(float& ref, float top, float lift) {
+    const float next = fmaxf(ref, column_max(top) - lift);
     const float f = ex2_approx(ref - next);
     ref = next;
     return f;
@@ -240,6 +244,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     fa_decode_gqa_kernel(const __grid_constant__ GqaParams p) {
     using C = GqaCfg<D, Q8>;
     constexpr bool kMmaBf16 = BF16 && !Q8;  // e4m3 values are exact in fp16
+    constexpr float kLiftM = Q8 || BF16 ? 0.0f : kLift;  // (over e4m3 m is the reference of the sum alone)
     constexpr int stages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -603,9 +608,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                up |= fmaxf(c[nt][j], c[nt][j + 2]) > m[nt][j] + kRaise;
+                up |= fmaxf(c[nt][j], c[nt][j + 2]) > m[nt][j] + (kRaise + kLiftM);
                 if constexpr (Q8)
-                    up |= fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]) > eo[nt][j] + kRaise;
+                    up |= fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]) >
+                          eo[nt][j] + (kRaise + kLift);
             }
         }
         if (__any_sync(0xffffffffu, up)) {
@@ -614,12 +620,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float old = m[nt][j];
-                    const float f = raise(m[nt][j], fmaxf(c[nt][j], c[nt][j + 2]));
+                    const float f = raise(m[nt][j], fmaxf(c[nt][j], c[nt][j + 2]), kLiftM);
                     l[nt][j] *= f;
                     float fo = f;
                     if constexpr (Q8) {
                         eo[nt][j] = fmaxf(eo[nt][j] + (old - m[nt][j]), kNoRef);  // under the new m
-                        fo = raise(eo[nt][j], fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]));
+                        fo = raise(eo[nt][j], fmaxf(c[nt][j] - m[nt][j] + ev[0], c[nt][j + 2] - m[nt][j] + ev[1]),
+                                   kLift);
                     }
 #pragma unroll
                     for (int i = 0; i < C::kTiles; ++i) {
