@@ -120,3 +120,21 @@ def test_scores_of_minus_infinity_weigh_nothing(n):
         assert not o[1].any() and lse[1, 0] == -math.inf
     else:
         check(o[1:], lse[1:], q[1:], [ks[1][:, 20:21]], [vs[1][:, 20:21]], 1.0 / math.sqrt(D), dtype, False)
+
+
+def test_buffers_made_for_a_larger_batch():
+    """Tables, lengths and outputs with more rows than q, or of another shape: the first B rows are used,
+    as they always were."""
+    D, H, dtype = 64, 2, torch.float16
+    rng = np.random.default_rng(1)
+    lens = [40, 7, 300, 16, 90]
+    kc, vc, _, _, bt, sl, _, _ = fill(rng, lens, H, D, dtype, False)
+    q = randn(len(lens), H, D, dtype=dtype)
+    want, want_lse = fa.decode_paged(q[:3].contiguous(), kc, vc, bt[:3].contiguous(), sl[:3].contiguous())
+    o, lse = fa.decode_paged(q[:3].contiguous(), kc, vc, bt, sl)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    out, out_lse = torch.full((5, H * D), 7.0, device="cuda", dtype=dtype), torch.full((5, H, 1), 7.0, device="cuda")
+    o, lse = fa.decode_paged(q[:3].contiguous(), kc, vc, bt, sl[:, None], out=out, lse=out_lse)
+    assert o is out and lse is out_lse and status() == fa.FA_OK
+    assert torch.equal(out[:3].view(3, H, D), want) and torch.equal(out_lse[:3, :, 0], want_lse)
+    assert torch.all(out[3:] == 7.0) and torch.all(out_lse[3:] == 7.0)

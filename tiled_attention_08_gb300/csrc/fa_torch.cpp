@@ -453,8 +453,16 @@ std::tuple<Tensor, Tensor> decode_paged_ex(const Tensor& q, const Tensor& k_cach
     return {s.o, s.lse};
 }
 
+// A caller's buffer that holds at least n elements of a type.
+void check_room(const char* name, const Tensor& t, at::ScalarType type, int64_t n, int index) {
+    same_device(name, t, index);
+    TORCH_CHECK_VALUE(t.scalar_type() == type && t.is_contiguous() && t.numel() >= n, name,
+                      " must be a contiguous ", type, " tensor of at least ", n, " elements");
+}
+
 // decode_paged: the kernel of equal heads over a 16-bit cache where the call has that form, else
-// fa_decode_paged_ex.
+// fa_decode_paged_ex.  That form also takes buffers made for more sequences than q has: tables, lengths
+// and outputs with more rows, of which the first B are used, in any shape.
 std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, const Tensor& v_cache,
                                         const Tensor& block_tables, const Tensor& seq_lens,
                                         std::optional<double> scale, const OptTensor& out,
@@ -464,18 +472,31 @@ std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, 
         return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
                                k_exp, v_exp);
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
-    const Step s = decode_outputs(q, out, lse);
-    const Cache c = check_cache(k_cache, v_cache, {}, {}, q.scalar_type(), s.index);
-    TORCH_CHECK_VALUE(c.D == s.D, "the cache has heads of ", c.D, ", q of ", s.D);
-    const int max_pages = check_tables(block_tables, seq_lens, s.B, s.index);
+    const int index = cuda_index("q", q);
+    TORCH_CHECK_VALUE(q.is_contiguous(), "q must be contiguous");
+    const int dt = dtype_code(q);
+    const Cache c = check_cache(k_cache, v_cache, {}, {}, q.scalar_type(), index);
+    const int B = as_int("B", q.size(0)), D = as_int("D", q.size(2));
+    TORCH_CHECK_VALUE(c.D == D, "the cache has heads of ", c.D, ", q of ", D);
+    TORCH_CHECK_TYPE(block_tables.scalar_type() == at::kInt && seq_lens.scalar_type() == at::kInt,
+                     "block_tables and seq_lens must be int32");
+    TORCH_CHECK_VALUE(block_tables.dim() == 2, "block_tables must be [B, max_pages]");
+    const int max_pages = as_int("max_pages", block_tables.size(1));
+    check_room("block_tables", block_tables, at::kInt, (int64_t)B * max_pages, index);
+    check_room("seq_lens", seq_lens, at::kInt, B, index);
+    if (given(out)) check_room("out", *out, q.scalar_type(), q.numel(), index);
+    if (given(lse)) check_room("lse", *lse, at::kFloat, (int64_t)B * c.H, index);
+    const Tensor o = given(out) ? *out : at::empty(q.sizes(), q.options());
+    const Tensor l = given(lse) ? *lse : at::empty({B, c.H}, q.options().dtype(at::kFloat));
+    written(out);
+    written(lse);
     const Tensor ws =
-        workspace_of(workspace, fa_decode_workspace_bytes(s.B, s.Hq, s.D, max_pages), q, s.index);
+        workspace_of(workspace, fa_decode_workspace_bytes(B, c.H, D, max_pages), q, index);
     check_status("fa_decode_paged",
                  fa_decode_paged(ptr(q), c.k, c.v, ptr<int32_t>(block_tables), ptr<int32_t>(seq_lens),
-                                 ptr(s.o), ptr<float>(s.lse), ptr(ws), ws.nbytes(), s.B, s.Hq, s.D,
-                                 c.num_pages, max_pages, scale_of(scale, s.D), s.dt,
-                                 stream_of(s.index)));
-    return {s.o, s.lse};
+                                 ptr(o), ptr<float>(l), ptr(ws), ws.nbytes(), B, c.H, D, c.num_pages,
+                                 max_pages, scale_of(scale, D), dt, stream_of(index)));
+    return {o, l};
 }
 
 std::tuple<Tensor, Tensor> decode_shared_prefix(const Tensor& q, const Tensor& k_cache,
