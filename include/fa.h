@@ -226,7 +226,8 @@ size_t fa_decode_workspace_bytes(int B, int H, int D, int max_pages);
  *   block_tables:     [B, max_pages] int32, device; entries past a sequence's pages are unread;
  *   seq_lens:         [B] int32, device, 0 <= seq_lens[b] <= 16 * max_pages;
  *   lse:              [B, H] fp32; workspace: fa_decode_workspace_bytes(B, H, D, max_pages).
- * A sequence with no cached token gets O = 0 and LSE = -inf.  Host-side argument errors return
+ * A sequence with no cached token gets O = 0 and LSE = -inf.  Slots past a sequence's end may hold
+ * anything.  A row with a NaN score gets NaN in O and LSE.  Host-side argument errors return
  * before anything is enqueued; a page index outside [0, num_pages) or a length outside its range
  * (device data, checked by the kernel before any copy) is skipped and reported by
  * fa_get_device_status() as FA_ERR_INVALID_ARG, with the outputs of that call undefined.
@@ -248,7 +249,8 @@ fa_status fa_decode_paged(const void* q, const void* k_cache, const void* v_cach
  *   q, q_out: [B, Hq, L, D], k, k_out: [B, Hk, L, D] views (strides[0..3] = q, k, q_out, k_out;
  *             Hk = 0 or Hq = 0: that operand is absent and its pointers are ignored);
  *             D in {64, 128}; an output may be its own input (same pointer and strides), or
- *             interleave with another operand as a part of one packed tensor; no other overlap;
+ *             interleave with another operand as a part of one packed tensor (of equal strides,
+ *             the parts at any place among its dimensions); no other overlap;
  *   positions: [B, L] int32, device, rows position_stride elements apart (0: one row for all
  *             sequences; negative positions turn backwards), or null: position l;
  *   freqs:    [rotary_dim / 2] int64, device: theta_i as a fraction of a turn, theta_i / (2 pi)
@@ -292,7 +294,7 @@ typedef enum { FA_CACHE_16BIT = 0, FA_CACHE_E4M3 = 1 } fa_cache_dtype;
 /*
  * Writes new keys and values into a paged cache.  Sequence b adds new_lens[b] rows (rows
  * 0 .. new_lens[b]-1 of k[b], v[b]), which become its last tokens seq_lens[b] - new_lens[b] ..
- * seq_lens[b] - 1; rows of k and v behind them are not read, other slots keep what they hold.
+ * seq_lens[b] - 1; rows of k and v behind them count for nothing, other slots keep what they hold.
  *   k, v:        [B, H, L, D] views of dtype (strides[0..1]);
  *   k_cache, v_cache: [num_pages, H, FA_PAGE_TOKENS, D], k_exp, v_exp: [num_pages, H,
  *                FA_PAGE_TOKENS] bytes (ignored for a 16-bit cache), 16-byte aligned, contiguous;
@@ -314,7 +316,7 @@ fa_status fa_cache_append(const void* k, const void* v, const fa_strides* stride
  * Reads a paged cache back: rows 0 .. L-1 of every sequence as dense k, v [B, H, L, D] views of
  * dtype (strides[0..1]); rows at or past seq_lens[b] are written as zeros.  An e4m3 row is
  * its values times 2^e, rounded to dtype (exact in bf16, but for a value that quantising rounded up
- * to 2^128).  For a prompt that continues behind
+ * to 2^128).  k and v may be parts of one packed tensor, as in fa_rotary.  For a prompt that continues behind
  * cached tokens: the dense rows are the keys and values of fa_fwd_ex with Lk > Lq.  Bad device data
  * is reported as for fa_cache_append; those rows are written as zeros.
  */

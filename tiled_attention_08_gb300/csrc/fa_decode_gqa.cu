@@ -5,8 +5,9 @@
 // over the seq_lens[b] tokens of the sequence, token t in page block_tables[b][t / 16] at slot
 // t % 16.  A cached e4m3 row is its values times a power of two (fa_e4m3.cuh).
 //
-// Bound by HBM: every cached row is read once per cache head and used by G query rows, 4 G D FLOPs
-// for 2 D or 4 D bytes.  On the FMA pipes the products alone would cost G instructions per value
+// Bound by HBM: every cached row is read once per cache head and used by G query rows (up to 16: a
+// larger group is cut into blocks of 16, each of which reads the rows again), 4 G D FLOPs for 2 D or
+// 4 D bytes.  On the FMA pipes the products alone would cost G instructions per value
 // and lane, over the issue rate from G = 4 on, so they run on the tensor cores.  tcgen05's
 // smallest tile has 64 rows and reads its operands from shared memory, where e4m3 rows would
 // first have to be written back as 16-bit; mma.sync m16n8k16 takes its operands from registers,
@@ -41,7 +42,11 @@
 // among eight of 16: 15.1 -> 12.1.  It loses where the clusters do not all fit at once (72 fit with
 // four CTAs per SM and 48 with three; 76 and 52 took 9.1 -> 11.6 and 10.4 -> 12.0 us), where a few
 // units are long (one unit of 4096 tokens: 10.4 -> 11.8 us; 32 units of 8192, all but one head's short: 16.7 ->
-// 17.8), and with groups above 8 (three CTAs per SM: 14.7 -> 22.0 us for 52 units).
+// 17.8), and with groups above 8 (three CTAs per SM: 14.7 -> 22.0 us for 52 units).  Tables' width, in pages,
+// all sequences that long, group 4, line against cluster: 8 units over e4m3, heads of 128, of 128 pages 11.4 and
+// 9.6 us, 192 11.9 and 11.4, 256 12.4 and 12.7, 512 14.7 and 18.6; 32 units 256 17.6 and 14.9, 384 21.7 and 18.2,
+// 512 23.7 and 21.4 (lengths spread from a quarter up: 20.6 and 20.6).  So 128 for fewer than 32 units, else
+// 256.  Both are careful: 16-bit caches still gain there (8 units of 256 pages, heads of 64: 10.4 and 9.9).
 //
 // Softmax in the log2 domain.  The reference of a column is only raised when a score exceeds it
 // by more than 2^8 (a warp vote), so the maximum over the lanes is rarely taken.  An e4m3 cache
@@ -59,6 +64,9 @@
 // e4m3: 140 us (5.8 TB/s; no SM idle until the first stretches end).  Heads of 64, e4m3: 4.0 to 4.6
 // TB/s: an SM turns over 10 to 12 pages per us whatever their size, with 377 instructions a page and warp
 // and 16 warps' registers.
+// 32 sequences of 8192, 4 cache heads, groups of 8, 16, 32, 64: heads of 128 e4m3 62, 74, 128, 234 us,
+// 16-bit 97, 105, 181, 343; heads of 64 e4m3 43, 53, 88, 159, 16-bit 59, 59, 97, 178.  Two query blocks at
+// heads of 128 spill 36 words of 168 registers.
 #include <atomic>
 #include <type_traits>
 
@@ -84,7 +92,9 @@ constexpr int kGqaManyUnits = 2048;  // from so many on the line is dealt out in
 // all SMs get the same share of the memory's bandwidth, so equal stretches end up to 15% apart;
 // with three rounds the line's first 52/64 are dealt out like that, the next 8/64 and the last 4/64
 // again in stretches so much shorter, to CTAs that start as earlier ones end (735 -> 641 us for 256
-// sequences of 1..4096 tokens, 32 heads of 128, e4m3).  Short stretches cut long units into many
+// sequences of 1..4096 tokens, 32 heads of 128, e4m3; borders at 40/56 to 60/62 of 64 take 603 to 634 us
+// there, and 52/60 is within 1% of the best of them over four other batches of 2048 and more units).  Short
+// stretches cut long units into many
 // parts and each begins with an empty ring, so three rounds need kGqaManyUnits: with 2048 to 4096
 // units they took -12% to +1% over e4m3 and 16-bit caches, heads of 64 and 128, groups of 1 to 4; with
 // 1024 (groups of 8) +1% to +18%, with 384 +3% to +25% (142 -> 158 us for 48 sequences of up to
@@ -105,7 +115,9 @@ struct GqaSplit {
 };
 // A page for each warp while there are few (latency is all: 13.1 -> 10.1 us for a token written and
 // attended to behind 333, 8 cache heads, with this split), else at least kGqaMinPages; and a unit is cut
-// into no more than 128 parts on average.
+// into no more than 128 parts on average, which one CTA joins.  Limits of 32, 64, 128, 256, 512 for
+// one unit, groups of 8: of 16384 tokens (e4m3, heads of 128) 32, 21, 16, 16, 19 us; two of 32768 (16-bit, heads of
+// 64) 34, 21, 16, 17, 20; longer units would gain from 256 (one of 65536, e4m3: 109, 58, 34, 25, 25).
 __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int rounds, int units) {
     const long long a = total <= kGqaFewPages ? total : total / kGqaMinPages, b = 128LL * units;
     const long long m = a < b ? a : b;
@@ -985,7 +997,10 @@ int gqa_launched_warps(int B, int Hk, int group, int max_pages, int D, bool q8, 
     const int warps = gqa_warps(B, Hk, group, max_pages);
     // Beside a kernel that holds busy_sms SMs: the warps that find room at once, if the step is so
     // short (16 pages a warp at most) that a second wave behind that kernel would be its tail
-    // (28.5 -> 24.5 us for 64 sequences of up to 512 tokens beside a prefix of 4096 on 64 SMs).
+    // (28.5 -> 24.5 us for 64 sequences of up to 512 tokens beside a prefix of 4096 on 64 SMs).  All SMs
+    // against those left, 64 sequences, 8 cache heads of 128, group 4: beside 4096 tokens, sequences of up to
+    // 256 24.5 and 22.2 us, 512 29.5 and 27.7, 768 (over the limit) 34.3 and 33.9, 2048 56.0 and 58.3; beside
+    // 8192, which leaves 24 SMs (most over the limit), 128 29.3 and 28.0, 256 31.1 and 40.9, 512 36.0 and 60.6.
     const int beside = (kGqaSms - busy_sms) * per_sm;
     const long long q_blocks = (group + gqa_q_rows(group) - 1) / gqa_q_rows(group);
     if (busy_sms > 0 && beside > 0 && (long long)B * Hk * q_blocks * max_pages <= 16LL * beside)

@@ -22,8 +22,8 @@
 //    tail (a grid of whole splits per head would idle up to half of the last wave);
 //  * output: fp32 parts, each row 64 or 128 contiguous floats, staged through shared memory.
 //
-// 256 sequences, 32 heads of 128, a prefix of 16384 tokens: 62 us, of which 15 do not depend on the
-// prefix's length (start, queries, read-out, the join's share); each further token at 1577 TFLOP/s.
+// 256 sequences, 32 heads of 128, a prefix of 16384 tokens: 62 us, 1108 TFLOP/s.  Doubling the prefix
+// adds 43 us (1580 TFLOP/s), so that 19 do not depend on its length (start, queries, read-out).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 
