@@ -377,6 +377,41 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
                                   int dtype, void* stream);
 
 /*
+ * Attention under a sliding window with first tokens that stay visible, with grouped heads.  Query row i
+ * of head h stands at position t = i + Lk - Lq (as under fa_fwd_ex's causal mask) and sees key j of
+ * head h / (Hq / Hk) iff
+ *     0 <= j <= t  and  (j > t - window or j < sinks),
+ * that is its own and the window - 1 keys in front of it, and the first `sinks` keys.  window >= 1,
+ * sinks >= 0; a window of Lk or more is the causal mask.  q, o: [B, Hq, Lq, D], k, v: [B, Hk, Lk, D]
+ * views (strides[0..3] = q, k, v, o) with Hq a multiple of Hk, lse contiguous [B, Hq, Lq]; Lq, Lk <= 2^30 - 1024.
+ * A row that sees no key (t < 0, only when Lq > Lk) gets O = 0 and LSE = -inf.  Lk = 0 with Lq > 0
+ * is FA_ERR_UNSUPPORTED, as are more than 2^31 - 1 tiles.  o may be another part of one packed tensor
+ * with an input of the same length (as in fa_rotary), else their extents must not overlap.  An infinity or NaN in V reaches every row of a tile
+ * that some row of it sees.
+ * Enqueues one kernel (two when Lq > Lk).
+ */
+fa_status fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
+                        const fa_strides* strides, int B, int Hq, int Hk, int Lq, int Lk, int D,
+                        int window, int sinks, float scale, int dtype, void* stream);
+
+/* Bytes of device workspace fa_window_bwd needs: two fp32 vectors per query head padded to whole tiles,
+ * and, where the first tokens' keys are seen by far more queries than a window's, fp32 parts of their
+ * gradients (at most 65 MB at D = 128).  0 for an empty problem or invalid sizes. */
+size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hk, int Lq, int Lk, int D, int window, int sinks);
+
+/*
+ * Its backward: given the forward's o and lse and the output gradient dout, writes dq, dk, dv (dk and dv
+ * summed over the heads of a group; zeros where no query sees a key).  strides[0..7] = q, k, v, o,
+ * dout, dq, dk, dv; a gradient may be another part of one packed tensor with operands of its length.  Every
+ * call gives the same bits.  Lq = Lk = 0 returns FA_OK; only one of them 0 returns FA_ERR_UNSUPPORTED.  Calls
+ * that may overlap on the GPU need a workspace each.  Enqueues three or four kernels.
+ */
+fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                        size_t workspace_bytes, const fa_strides* strides, int B, int Hq, int Hk, int Lq,
+                        int Lk, int D, int window, int sinks, float scale, int dtype, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the current device's status word.  Returns
  * FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last call,
  * FA_ERR_INVALID_ARG if a decode kernel found a page index or sequence length out of range, or

@@ -39,6 +39,8 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
            "FA_CACHE_16BIT", "FA_CACHE_E4M3", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "decode_shared_prefix",
+           "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes", "window_forward",
+           "window_backward", "attention_window",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_BF16", "FA_FP16"]
 
@@ -59,7 +61,8 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_launch_count", "fa_status_string", "fa_bwd_noalloc", "fa_decode_paged",
             "fa_decode_workspace_bytes", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
             "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
-            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes")
+            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "fa_window_fwd",
+            "fa_window_bwd", "fa_window_bwd_workspace_bytes")
 
 
 class FaStrides(ctypes.Structure):
@@ -131,6 +134,13 @@ def load_library():
         lib.fa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, sz, i, i, i,
                                                 i, i, i, f, i, vp]
         lib.fa_decode_shared_prefix.restype = i
+        lib.fa_window_fwd.argtypes = [vp, vp, vp, vp, vp, sp, i, i, i, i, i, i, i, i, f, i, vp]
+        lib.fa_window_fwd.restype = i
+        lib.fa_window_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
+        lib.fa_window_bwd_workspace_bytes.restype = sz
+        lib.fa_window_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sp, i, i, i, i, i,
+                                      i, i, i, f, i, vp]
+        lib.fa_window_bwd.restype = i
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, i,
                                        vp]
         lib.fa_bwd_noalloc.restype = i
@@ -256,6 +266,25 @@ def fa_decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len, block
                                                   block_tables, seq_lens, o, lse, workspace,
                                                   workspace_bytes, B, Hq, Hk, D, num_pages,
                                                   max_pages, scale, dtype, stream)
+
+
+def fa_window_fwd(q, k, v, o, lse, strides, B, Hq, Hk, Lq, Lk, D, window, sinks, scale, dtype,
+                  stream) -> int:
+    """``strides``: four (batch, head, row) tuples for q, k, v, o."""
+    return load_library().fa_window_fwd(q, k, v, o, lse, _strides_array(strides), B, Hq, Hk, Lq, Lk,
+                                        D, window, sinks, scale, dtype, stream)
+
+
+def fa_window_bwd_workspace_bytes(B, Hq, Hk, Lq, Lk, D, window, sinks) -> int:
+    return int(load_library().fa_window_bwd_workspace_bytes(B, Hq, Hk, Lq, Lk, D, window, sinks))
+
+
+def fa_window_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, strides, B, Hq, Hk,
+                  Lq, Lk, D, window, sinks, scale, dtype, stream) -> int:
+    """``strides``: eight (batch, head, row) tuples for q, k, v, o, dout, dq, dk, dv."""
+    return load_library().fa_window_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace,
+                                        workspace_bytes, _strides_array(strides), B, Hq, Hk, Lq, Lk,
+                                        D, window, sinks, scale, dtype, stream)
 
 
 def fa_bwd_workspace_bytes(B, H, L, D) -> int:
@@ -590,3 +619,29 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, blo
     fa_decode_shared_prefix in fa.h."""
     return (_binding or _ops()).decode_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len,
                                                      block_tables, seq_lens, scale, out, lse, workspace)
+
+
+def window_forward(q, k, v, window: int, sinks: int = 0, scale: float | None = None, out=None,
+                   lse=None):
+    """O, LSE of attention under a sliding window: q [B, Hq, Lq, D], k and v [B, Hk, Lk, D] views (bf16
+    or fp16, contiguous last dimension, Hq a multiple of Hk).  The query at position t (row i of Lq is at
+    i + Lk - Lq) sees the ``window`` keys up to its own and the first ``sinks``.  O is like q, LSE
+    contiguous [B, Hq, Lq] fp32.  See fa_window_fwd in fa.h."""
+    return (_binding or _ops()).window_forward(q, k, v, window, sinks, scale, out, lse)
+
+
+def window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
+                    workspace=None, grads=None):
+    """dQ, dK, dV for ``window_forward`` (dK and dV summed over the query heads that share a key head).
+    ``grads`` optionally gives the three output views.  See fa_window_bwd in fa.h."""
+    dq, dk, dv = grads if grads is not None else (None, None, None)
+    return (_binding or _ops()).window_backward(q, k, v, o, lse, dout, window, sinks, scale,
+                                                workspace, dq, dk, dv)
+
+
+def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None):
+    """Differentiable attention under a sliding window with first tokens that stay visible and grouped
+    heads (``window_forward``, ``window_backward``); returns O like q.  Differentiable once, in reverse
+    mode.  [B, L, H, D] tensors transposed, or the parts of a packed tensor, are read in place;
+    tensors that the kernels cannot step through (expanded ones, for example) are copied."""
+    return (_binding or _ops()).attention_window(q, k, v, window, sinks, scale)

@@ -6,10 +6,13 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_overlap.h"
 
 namespace fa {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 struct Range {
     uintptr_t lo, hi;  // [lo, hi)
@@ -35,6 +38,20 @@ bool take_strides(const fa_strides& in, int B, int H, Strides* out);
 
 // Bytes from the first to one past the last element of a strided [B, H, L, D] 16-bit operand.
 Range extent(const void* p, const Strides& s, int B, int H, int L, int D);
+
+// The same layout: equal strides of the dimensions that have more than one entry.
+inline bool same(const Strides& a, const Strides& b, int B, int H, int L) {
+    return (B <= 1 || a.b == b.b) && (H <= 1 || a.h == b.h) && (L <= 1 || a.l == b.l);
+}
+// Parts of one packed tensor: the same layout, extents that overlap, no element in common.
+inline bool packed_parts(const void* a, const Strides& sa, int Ha, const void* b, const Strides& sb, int Hb, int B,
+                         int L, int D) {
+    const intptr_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
+    if (!same(sa, sb, B, Ha < Hb ? Ha : Hb, L)) return false;
+    const long long h = Ha > 1 ? sa.h : sb.h;
+    return pa < pb ? interleave_apart((pb - pa) / 2, B, Ha, Hb, L, D, sa.b, h, sa.l)
+                   : interleave_apart((pa - pb) / 2, B, Hb, Ha, L, D, sa.b, h, sa.l);
+}
 
 // Tiled tensor map of up to 5 dimensions: sizes and box in elements, strides (of dimensions 1..)
 // in bytes; elements past the sizes read as zeros.

@@ -245,6 +245,47 @@ struct PrefixParams {
     uint64_t timeout_ns;
 };
 
+// Attention with a sliding window and first tokens that stay visible (fa_window_fwd.cu).
+struct WindowFwdParams {
+    CUtensorMap tm_q, tm_k, tm_v;  // 16-bit {D, L, H, B} (strided), box {64, 128, 1, 1}
+    void* o;                       // [B, Hq, Lq, D] 16-bit, strides so
+    Strides so;
+    float* lse;                    // [B*Hq, Lq]
+    int Lq, Lk, Hq, Hk, B;
+    int window, sinks;             // in [1, Lk], [0, Lk]
+    int head_pairs;                // a work item is a query tile of two heads, not two tiles of one
+    int columns;                   // B * Hq, or half of it: heads (or pairs of them)
+    int rows;                      // work items of one of them
+    int sched_group;               // of the columns (tile_coords)
+    float scale_log2;              // |scale| * log2(e)
+    uint32_t s_negate;
+    int* status;
+    uint64_t timeout_ns;
+};
+
+// Its backward (fa_window_bwd.cu).
+constexpr int kWindowSms = 152;  // the split is made for this many SMs on any device, so that the
+                                 // workspace does not depend on it
+struct WindowBwdParams {
+    CUtensorMap tm_q, tm_k, tm_v, tm_do;
+    const void* dout;
+    Strides sdo;
+    const float *nlse2_pad, *delta_pad;  // [B*Hq, Lqpad]: -LSE * log2(e), rowsum(dO * O)
+    void *dq, *dk, *dv;
+    Strides sdq, sdk, sdv;
+    int Lq, Lk, Lqpad, Hq, Hk, B, n_qtiles, n_ktiles;
+    int window, sinks;
+    int q_first;                         // query tiles in front of it see no key
+    int sched_group_k, sched_group_q;    // heads per schedule group of the two passes
+    int split_tiles, parts;              // the first split_tiles key tiles are cut into parts ...
+    float* part;                         // ... [B*Hk, split_tiles, parts, 2 (dK, dV), D/4, 128, 4]
+    int dkdv_items;
+    float scale, scale_log2;
+    int* sched;                          // work counters: [0] dK/dV pass, [1] dQ pass
+    int* status;
+    uint64_t timeout_ns;
+};
+
 // Host-side helpers of the C-ABI layer shared with the other entry-point units.
 // Consumes the fa_trace_next_call arming of the calling thread (every public call ends so).
 void trace_disarm();
@@ -331,6 +372,12 @@ cudaError_t launch_decode_gqa(const GqaParams& p, int D, bool bf16, bool q8, cud
 cudaError_t launch_prefix(const PrefixParams& p, int D, bool bf16, cudaStream_t s);
 // The work split of a shared prefix: fills rows_b, n_tiles, n_pairs, key_tiles, grid, max_segments.
 void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p);
+cudaError_t launch_window_fwd(const WindowFwdParams& p, int D, bool bf16, cudaStream_t s);
+// The split of the first tokens' key tiles: fills split_tiles, parts, dkdv_items from the sizes.
+void window_bwd_plan(WindowBwdParams* p);
+cudaError_t launch_window_dkdv(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_window_dq(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_window_join(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s);
 // Query rows of a block (8 or 16), the most warps that a step may launch (workspace), and those it
 // does (busy_sms: SMs that an earlier kernel still holds).

@@ -7,28 +7,12 @@
 #include <cstring>
 
 #include "fa_host.h"
-#include "fa_overlap.h"
 
 using namespace fa;
 
 namespace {
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
-// The same layout: equal strides of the dimensions that have more than one entry.
-bool same(const Strides& a, const Strides& b, int B, int H, int L) {
-    return (B <= 1 || a.b == b.b) && (H <= 1 || a.h == b.h) && (L <= 1 || a.l == b.l);
-}
-// Parts of one packed tensor: the same layout, extents that overlap, no element in common.
-bool packed_parts(const void* a, const Strides& sa, int Ha, const void* b, const Strides& sb, int Hb, int B,
-                  int L, int D) {
-    const intptr_t pa = reinterpret_cast<intptr_t>(a), pb = reinterpret_cast<intptr_t>(b);
-    if (!same(sa, sb, B, Ha < Hb ? Ha : Hb, L)) return false;
-    const long long h = Ha > 1 ? sa.h : sb.h;
-    return pa < pb ? interleave_apart((pb - pa) / 2, B, Ha, Hb, L, D, sa.b, h, sa.l)
-                   : interleave_apart((pa - pb) / 2, B, Hb, Ha, L, D, sa.b, h, sa.l);
-}
 
 // The rotation of fa_rotary and fa_cache_append; freqs may be null only with rotary_dim = 0.
 fa_status check_rotation(const int64_t* freqs, int rotary_dim, float mscale, int interleaved, int D,

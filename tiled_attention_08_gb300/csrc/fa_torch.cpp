@@ -15,6 +15,7 @@
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <cmath>
 #include <optional>
 #include <string>
@@ -529,6 +530,147 @@ std::tuple<Tensor, Tensor> decode_shared_prefix(const Tensor& q, const Tensor& k
     return {s.o, s.lse};
 }
 
+// ---------------------------------------------------------------------------------------
+// Attention under a sliding window with first tokens that stay visible
+// ---------------------------------------------------------------------------------------
+struct Window {
+    int64_t window, sinks;
+    std::optional<double> scale;
+};
+// Windows and counts of first tokens are ints in the C interface; beyond its lengths they mean the same.
+int as_span(int64_t v) { return (int)std::clamp<int64_t>(v, INT32_MIN, INT32_MAX); }
+
+struct WindowSizes {
+    int index, dt, B, Hq, Hk, Lq, Lk, D;
+    fa_strides q, k, v;
+};
+WindowSizes window_sizes(const Tensor& q, const Tensor& k, const Tensor& v) {
+    const int index = cuda_index("q", q);
+    TORCH_CHECK_VALUE(q.dim() == 4 && k.dim() == 4, "q, k and v must be [B, H, L, D] views");
+    TORCH_CHECK_VALUE(k.size(0) == q.size(0) && k.size(3) == q.size(3), "q and k must agree in B and D: ",
+                      q.sizes(), " and ", k.sizes());
+    TORCH_CHECK_TYPE(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(),
+                     "q, k, v must share a dtype");
+    same_device("k", k, index);
+    same_device("v", v, index);
+    return {index, dtype_code(q), as_int("B", q.size(0)), as_int("Hq", q.size(1)), as_int("Hk", k.size(1)),
+            as_int("Lq", q.size(2)), as_int("Lk", k.size(2)), as_int("D", q.size(3)),
+            row_strides("q", q, q.sizes()), row_strides("k", k, k.sizes()), row_strides("v", v, k.sizes())};
+}
+
+// An output like `like`: the caller's or a new one.
+Tensor output_like(const char* name, const OptTensor& out, const Tensor& like) {
+    if (!given(out)) return at::empty_like(like);
+    TORCH_CHECK_TYPE(out->scalar_type() == like.scalar_type(), name, " must have the dtype of q");
+    same_device(name, *out, like.get_device());
+    written(*out);
+    return *out;
+}
+
+void check_lse(const Tensor& lse, const WindowSizes& w) {
+    const int64_t shape[3] = {w.B, w.Hq, w.Lq};
+    TORCH_CHECK_VALUE(lse.scalar_type() == at::kFloat && lse.sizes() == at::IntArrayRef(shape, 3) &&
+                          lse.is_contiguous(),
+                      "lse must be a contiguous fp32 [B, Hq, Lq] tensor");
+    same_device("lse", lse, w.index);
+}
+
+std::tuple<Tensor, Tensor> window_fwd(const Tensor& q_, const Tensor& k_, const Tensor& v_, const Window& win,
+                                      const OptTensor& out, const OptTensor& lse) {
+    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
+    const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_);
+    const WindowSizes w = window_sizes(q, k, v);
+    const Tensor o = output_like("out", out, q);
+    const Tensor l = given(lse) ? *lse : at::empty({w.B, w.Hq, w.Lq}, q.options().dtype(at::kFloat));
+    check_lse(l, w);
+    written(lse);
+    const fa_strides st[4] = {w.q, w.k, w.v, row_strides("out", o, q.sizes())};
+    check_status("fa_window_fwd",
+                 fa_window_fwd(ptr(q), ptr(k), ptr(v), ptr(o), ptr<float>(l), st, w.B, w.Hq, w.Hk, w.Lq, w.Lk, w.D,
+                               as_span(win.window), as_span(win.sinks), scale_of(win.scale, w.D), w.dt,
+                               stream_of(w.index)));
+    return {o, l};
+}
+
+std::tuple<Tensor, Tensor, Tensor> window_bwd(const Tensor& q_, const Tensor& k_, const Tensor& v_,
+                                              const Tensor& o_, const Tensor& lse, const Tensor& dout_,
+                                              const Window& win, const OptTensor& workspace,
+                                              const OptTensor& dq_, const OptTensor& dk_, const OptTensor& dv_) {
+    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
+    const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_), o = kernel_view(o_),
+                 dout = kernel_view(dout_);
+    const WindowSizes w = window_sizes(q, k, v);
+    check_lse(lse, w);
+    for (const Tensor* t : {&o, &dout}) {
+        TORCH_CHECK_TYPE(t->scalar_type() == q.scalar_type(), "o and dout must have the dtype of q");
+        same_device("o or dout", *t, w.index);
+    }
+    const Tensor dq = output_like("dq", dq_, q), dk = output_like("dk", dk_, k), dv = output_like("dv", dv_, v);
+    const fa_strides st[8] = {w.q, w.k, w.v, row_strides("o", o, q.sizes()), row_strides("dout", dout, q.sizes()),
+                              row_strides("dq", dq, q.sizes()), row_strides("dk", dk, k.sizes()),
+                              row_strides("dv", dv, k.sizes())};
+    if (w.Lq == 0 && w.Lk > 0) {  // no query: the keys have no gradient
+        dk.zero_();
+        dv.zero_();
+        return {dq, dk, dv};
+    }
+    const int window = as_span(win.window), sinks = as_span(win.sinks);
+    const Tensor ws = workspace_of(
+        workspace, fa_window_bwd_workspace_bytes(w.B, w.Hq, w.Hk, w.Lq, w.Lk, w.D, window, sinks), q, w.index);
+    check_status("fa_window_bwd",
+                 fa_window_bwd(ptr(q), ptr(k), ptr(v), ptr(o), ptr(dout), ptr<float>(lse), ptr(dq), ptr(dk), ptr(dv),
+                               ptr(ws), ws.nbytes(), st, w.B, w.Hq, w.Hk, w.Lq, w.Lk, w.D, window, sinks,
+                               scale_of(win.scale, w.D), w.dt, stream_of(w.index)));
+    return {dq, dk, dv};
+}
+
+struct WindowAttention : torch::autograd::Function<WindowAttention> {
+    static Tensor forward(torch::autograd::AutogradContext* ctx, const Tensor& q, const Tensor& k, const Tensor& v,
+                          int64_t window, int64_t sinks, std::optional<double> scale) {
+        const auto [o, lse] = window_fwd(q, k, v, {window, sinks, scale}, {}, {});
+        ctx->save_for_backward({q, k, v, o, lse});
+        ctx->saved_data["window"] = window;
+        ctx->saved_data["sinks"] = sinks;
+        ctx->saved_data["scale"] = scale;
+        return o;
+    }
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                   torch::autograd::variable_list grads) {
+        TORCH_CHECK(!at::GradMode::is_enabled(), "attention_window is differentiable once (no create_graph)");
+        const auto s = ctx->get_saved_variables();
+        const auto scale = ctx->saved_data["scale"];
+        const auto [dq, dk, dv] =
+            window_bwd(s[0], s[1], s[2], s[3], s[4], grads[0],
+                       {ctx->saved_data["window"].toInt(), ctx->saved_data["sinks"].toInt(),
+                        scale.isNone() ? std::optional<double>() : scale.toDouble()},
+                       {}, {}, {}, {});
+        return {dq, dk, dv, Tensor(), Tensor(), Tensor()};
+    }
+};
+
+Tensor attention_window(const Tensor& q, const Tensor& k, const Tensor& v, int64_t window, int64_t sinks,
+                        std::optional<double> scale) {
+    for (const Tensor* x : {&q, &k, &v})
+        TORCH_CHECK_NOT_IMPLEMENTED(!tangent_of(*x), "attention_window has no forward-mode derivative");
+    if (at::GradMode::is_enabled() && (q.requires_grad() || k.requires_grad() || v.requires_grad()))
+        return WindowAttention::apply(q, k, v, window, sinks, scale);
+    return std::get<0>(window_fwd(q, k, v, {window, sinks, scale}, {}, {}));
+}
+
+std::tuple<Tensor, Tensor> window_forward(const Tensor& q, const Tensor& k, const Tensor& v, int64_t window,
+                                          int64_t sinks, std::optional<double> scale, const OptTensor& out,
+                                          const OptTensor& lse) {
+    return window_fwd(q, k, v, {window, sinks, scale}, out, lse);
+}
+
+std::tuple<Tensor, Tensor, Tensor> window_backward(const Tensor& q, const Tensor& k, const Tensor& v,
+                                                   const Tensor& o, const Tensor& lse, const Tensor& dout,
+                                                   int64_t window, int64_t sinks, std::optional<double> scale,
+                                                   const OptTensor& workspace, const OptTensor& dq,
+                                                   const OptTensor& dk, const OptTensor& dv) {
+    return window_bwd(q, k, v, o, lse, dout, {window, sinks, scale}, workspace, dq, dk, dv);
+}
+
 PyObject* status_error_class = nullptr;
 
 }  // namespace
@@ -552,4 +694,7 @@ PYBIND11_MODULE(fa_torch, m) {
     m.def("decode_paged", &decode_paged);
     m.def("decode_paged_ex", &decode_paged_ex);
     m.def("decode_shared_prefix", &decode_shared_prefix);
+    m.def("attention_window", &attention_window);
+    m.def("window_forward", &window_forward);
+    m.def("window_backward", &window_backward);
 }
