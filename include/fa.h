@@ -348,6 +348,24 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
                              size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
                              int max_pages, float scale, int dtype, int cache_dtype, void* stream);
 
+/* Bytes of device workspace fa_decode_window needs (no more than fa_decode_paged_ex with such tables).
+ * 0 for invalid sizes. */
+size_t fa_decode_window_workspace_bytes(int B, int Hq, int Hk, int D, int max_pages, int window,
+                                        int sinks);
+
+/*
+ * fa_decode_paged_ex under a sliding window with first tokens that stay visible: the row of a sequence of n
+ * tokens attends to its last `window` (>= 1) and its first `sinks` (>= 0) tokens, no token twice.  The
+ * pages of other tokens, and their entries in block_tables, are not read and may be anything: a cache may
+ * give them to other sequences.  Slots of a page that are read with it but hold other tokens may hold
+ * anything.
+ */
+fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                           const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,
+                           void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                           int Hk, int D, int num_pages, int max_pages, int window, int sinks,
+                           float scale, int dtype, int cache_dtype, void* stream);
+
 /* Bytes of device workspace fa_decode_shared_prefix needs: fa_decode_paged_ex's and fp32 parts of
  * every query row.  0 for invalid sizes. */
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,

@@ -117,3 +117,43 @@ def test_workspace_sizes():
                             rows = 2 * B * Hk * G * L * 4 + 16
                             most = max(most, need(B, Hk * G, Hk, L, L, 128, window, sinks) - rows)
     assert 0 < most <= 65 << 20
+
+
+def _decode(B=2, Hq=4, Hk=2, D=64, num_pages=16, max_pages=4, window=8, sinks=1, scale=0.125, dtype=0, q8=1,
+            ws_bytes=None, **ptrs):
+    names = ("q", "kc", "vc", "ke", "ve", "bt", "sl", "o", "lse", "ws")
+    p = {n: A + i * 16 * MB for i, n in enumerate(names)}
+    p.update(ptrs)
+    need = fa.fa_decode_window_workspace_bytes(B, Hq, Hk, D, max_pages, window, sinks)
+    return fa.fa_decode_window(*(p[n] for n in names), need if ws_bytes is None else ws_bytes, B, Hq, Hk, D,
+                               num_pages, max_pages, window, sinks, scale, dtype, q8, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(window=0), BAD),
+    (dict(window=-1), BAD),
+    (dict(sinks=-1), BAD),
+    (dict(dtype=2), BAD),
+    (dict(q8=2), BAD),
+    (dict(Hq=3), BAD),
+    (dict(D=80), UNS),
+    (dict(scale=math.nan), BAD),
+    (dict(q=0), BAD),
+    (dict(ke=0), BAD),
+    (dict(o=A), BAD),
+    (dict(ws=0), BAD),
+    (dict(ws_bytes=16), BAD),
+    (dict(ws=A + 16 * MB), BAD),
+    (dict(B=0), OK),
+])
+def test_decode_is_refused(kw, status):
+    assert _decode(**kw) == status
+
+
+def test_decode_workspace():
+    need = fa.fa_decode_window_workspace_bytes
+    assert need(4, 8, 2, 64, 4096, 1 << 20, 0) == fa.fa_decode_workspace_bytes_ex(4, 8, 2, 64, 4096)
+    assert 0 < need(4, 8, 2, 64, 1 << 20, 64, 4) <= fa.fa_decode_workspace_bytes_ex(4, 8, 2, 64, 1 << 20)
+    assert need(4, 8, 2, 64, 1 << 20, (1 << 31) - 1, (1 << 31) - 1) == \
+        fa.fa_decode_workspace_bytes_ex(4, 8, 2, 64, 1 << 20)
+    assert need(4, 8, 2, 64, 16, 0, 0) == need(0, 8, 2, 64, 16, 4, 0) == need(4, 8, 3, 64, 16, 4, 0) == 0

@@ -39,6 +39,7 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
            "FA_CACHE_16BIT", "FA_CACHE_E4M3", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "decode_shared_prefix",
+           "fa_decode_window", "fa_decode_window_workspace_bytes",
            "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes", "window_forward",
            "window_backward", "attention_window",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
@@ -62,7 +63,8 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_decode_workspace_bytes", "fa_rotary", "fa_rotary_freqs", "fa_cache_append",
             "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
             "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "fa_window_fwd",
-            "fa_window_bwd", "fa_window_bwd_workspace_bytes")
+            "fa_window_bwd", "fa_window_bwd_workspace_bytes", "fa_decode_window",
+            "fa_decode_window_workspace_bytes")
 
 
 class FaStrides(ctypes.Structure):
@@ -129,6 +131,11 @@ def load_library():
         lib.fa_decode_paged_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i,
                                            i, i, f, i, i, vp]
         lib.fa_decode_paged_ex.restype = i
+        lib.fa_decode_window_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+        lib.fa_decode_window_workspace_bytes.restype = sz
+        lib.fa_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i,
+                                         i, i, f, i, i, vp]
+        lib.fa_decode_window.restype = i
         lib.fa_shared_prefix_workspace_bytes.argtypes = [i, i, i, i, i, i]
         lib.fa_shared_prefix_workspace_bytes.restype = sz
         lib.fa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, sz, i, i, i,
@@ -253,6 +260,18 @@ def fa_decode_paged_ex(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens
                                              seq_lens, o, lse, workspace, workspace_bytes, B, Hq,
                                              Hk, D, num_pages, max_pages, scale, dtype, cache_dtype,
                                              stream)
+
+
+def fa_decode_window_workspace_bytes(B, Hq, Hk, D, max_pages, window, sinks) -> int:
+    return int(load_library().fa_decode_window_workspace_bytes(B, Hq, Hk, D, max_pages, window, sinks))
+
+
+def fa_decode_window(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o, lse, workspace,
+                     workspace_bytes, B, Hq, Hk, D, num_pages, max_pages, window, sinks, scale, dtype,
+                     cache_dtype, stream) -> int:
+    return load_library().fa_decode_window(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o,
+                                           lse, workspace, workspace_bytes, B, Hq, Hk, D, num_pages,
+                                           max_pages, window, sinks, scale, dtype, cache_dtype, stream)
 
 
 def fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages) -> int:
@@ -505,15 +524,19 @@ def attention_qkvpacked(qkv, causal: bool = False, scale: float | None = None):
 
 
 def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | None = None,
-                 out=None, lse=None, workspace=None, k_exp=None, v_exp=None):
+                 out=None, lse=None, workspace=None, k_exp=None, v_exp=None, window: int | None = None,
+                 sinks: int = 0):
     """One decode step over a paged cache: q [B, H, D]; k_cache, v_cache
     [num_pages, H, FA_PAGE_TOKENS, D] (of q's dtype, contiguous); block_tables [B, max_pages] and
     seq_lens [B] int32 CUDA tensors.  Returns O [B, H, D] and LSE [B, H] (fp32).
 
     The caches may have fewer heads than q (a divisor: each is shared by a group of query heads),
-    and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote."""
+    and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote.
+
+    With ``window`` a sequence attends to its last ``window`` and its first ``sinks`` tokens alone; pages of
+    other tokens are not looked up (fa_decode_window in fa.h).  ``sinks`` counts with a window only."""
     return (_binding or _ops()).decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse,
-                                             workspace, k_exp, v_exp)
+                                             workspace, k_exp, v_exp, window, sinks)
 
 
 # ---------------------------------------------------------------------------------------

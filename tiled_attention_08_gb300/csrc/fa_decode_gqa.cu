@@ -131,7 +131,7 @@ __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int ro
 }
 
 // cudaFuncSetAttribute once per kernel and device (the calls below repeat every few microseconds).
-template <int D, bool Q8, bool BF16, int NT, bool SHORT>
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
 struct kGqaKernelId {};
 template <typename Id, typename K>
 cudaError_t allow_shared(K kern, int bytes) {
@@ -229,9 +229,33 @@ __device__ __forceinline__ float raise(float& ref, float top, float lift) {
 struct Batch {
     int page_head;  // page * Hk + head in the cache
     int b, unit;    // sequence, and (cache head, query block) in it
-    int flags;      // tokens that count (1..16) | first page of its unit << 8 | last << 9
+    int flags;      // tokens that count (1..16) | first page of its unit << 8 | last << 9, and under a
+                    // window bit 16 + i: slot i counts
 };
 constexpr int kFirst = 1 << 8, kLast = 1 << 9;
+
+// The pages that a sequence of n tokens reads under a window: those of the first tokens, then those of
+// the last `window` (no page twice).
+struct WindowPages {
+    int n, lo;          // tokens; the window's first
+    int lead, lo_page;  // pages of first tokens in front of it; the page that it begins in
+    __device__ __forceinline__ int count() const { return lead + (n + kPageTokens - 1) / kPageTokens - lo_page; }
+    __device__ __forceinline__ int page(int i) const { return i < lead ? i : lo_page + (i - lead); }
+};
+__device__ __forceinline__ WindowPages window_pages(int n, int window, int sinks) {
+    WindowPages w;
+    w.n = n;
+    w.lo = max(n - window, 0);
+    w.lo_page = w.lo / kPageTokens;
+    w.lead = min((sinks + kPageTokens - 1) / kPageTokens, w.lo_page);
+    return w;
+}
+// Slots of page pg that count.
+__device__ __forceinline__ int window_slots(const WindowPages& w, int pg, int sinks) {
+    auto first = [](int k) { return k <= 0 ? 0 : k >= kPageTokens ? 0xffff : (1 << k) - 1; };  // slots 0 .. k-1
+    const int t0 = pg * kPageTokens;
+    return first(w.n - t0) & (~first(w.lo - t0) | first(sinks - t0)) & 0xffff;
+}
 
 // Thread-block clusters of short steps: the value at shared::cta address `addr` of CTA `rank`.
 __device__ __forceinline__ float lds_cluster(uint32_t addr, uint32_t rank) {
@@ -251,7 +275,8 @@ __device__ __forceinline__ void cluster_sync() {
 
 // BF16: the type of q and o (and of a 16-bit cache).  NT: blocks of 8 queries.  SHORT: a cluster per
 // unit, whose warps share the unit's pages and join their parts through distributed shared memory.
-template <int D, bool Q8, bool BF16, int NT, bool SHORT>
+// WIN: the pages of the window and of the first tokens alone; nothing else of a sequence's table is read.
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
 __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     fa_decode_gqa_kernel(const __grid_constant__ GqaParams p) {
     using C = GqaCfg<D, Q8>;
@@ -290,6 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             if (SHORT || blockIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
             return 0;  // counts as empty
         }
+        if constexpr (WIN) return window_pages(n, p.window, p.sinks).count();
         return (n + kPageTokens - 1) / kPageTokens;
     };
     GqaSplit split;
@@ -340,14 +366,18 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     auto lookup = [&](int first) {  // pages first .. first + 31 of this warp
         Batch r = {0, 0, 0, 0};
         if (SHORT && first + lane < mine) {
-            const int pg = (int)x0 + first + lane;
+            int pg = (int)x0 + first + lane;
+            const int n = p.seq_lens[short_b];
+            if constexpr (WIN) pg = window_pages(n, p.window, p.sinks).page(pg);
             int page = p.block_tables[(size_t)short_b * p.max_pages + pg];
             if (page < 0 || page >= p.num_pages) {  // as below
                 atomicCAS(p.status, 0, (int)kDevBadArg);
                 page = 0;
             }
             r.page_head = page * p.Hk + short_unit / p.q_blocks;
-            r.flags = min(p.seq_lens[short_b] - pg * kPageTokens, kPageTokens);
+            r.flags = min(n - pg * kPageTokens, kPageTokens);
+            if constexpr (WIN)
+                r.flags |= window_slots(window_pages(n, p.window, p.sinks), pg, p.sinks) << 16;
         } else if (!SHORT && first + lane < mine) {
             const long long x = x0 + first + lane;
             // (64-bit quotients cost ten times 32-bit ones)
@@ -363,7 +393,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             const long long rest = x - (long long)cum[lo] * per_seq;
             r.b = lo;
             r.unit = small ? (int)((uint32_t)rest / (uint32_t)n_pages) : (int)(rest / n_pages);
-            const int pg = (int)(rest - (long long)r.unit * n_pages);
+            const int at_page = (int)(rest - (long long)r.unit * n_pages);
+            const int n = p.seq_lens[lo];
+            int pg = at_page;
+            if constexpr (WIN) pg = window_pages(n, p.window, p.sinks).page(at_page);
             int page = p.block_tables[(size_t)lo * p.max_pages + pg];
             if (page < 0 || page >= p.num_pages) {
                 // Reported; page 0 is read instead: nothing outside the cache is touched.
@@ -371,8 +404,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 page = 0;
             }
             r.page_head = page * p.Hk + r.unit / p.q_blocks;
-            r.flags = min(p.seq_lens[lo] - pg * kPageTokens, kPageTokens) | (pg == 0 ? kFirst : 0) |
-                      (pg == n_pages - 1 ? kLast : 0);
+            r.flags = min(n - pg * kPageTokens, kPageTokens) | (at_page == 0 ? kFirst : 0) |
+                      (at_page == n_pages - 1 ? kLast : 0);
+            if constexpr (WIN)
+                r.flags |= window_slots(window_pages(n, p.window, p.sinks), pg, p.sinks) << 16;
         }
         return r;
     };
@@ -560,14 +595,16 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         // are zero, but zero times a NaN is not).
         constexpr bool kEarly = NT == 1 && !Q8;
         const int left = flags & 31;  // tokens of this page
-        const bool partial = left < kPageTokens;
+        const uint32_t slots = WIN ? (uint32_t)flags >> 16 : 0xffffu;  // (WIN) its slots that count
+        const bool partial = WIN ? slots != 0xffffu : left < kPageTokens;
+        auto counts = [&](int slot) { return WIN ? (slots >> slot & 1u) != 0u : slot < left; };
         uint4 vq[kSmall ? 1 : C::kBoxes][4];
         uint2 vh[4];
         auto read_v = [&](int x) __attribute__((always_inline)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int key = 2 * t + (k & 1) + 8 * (k >> 1);
-                const bool there = !partial || key < left;
+                const bool there = !partial || counts(key);
                 if constexpr (kSmall) {
                     vh[k] = lds_u32x2(vs + key * 64 + (uint32_t)((g >> 1) ^ ((key >> 1) & 3)) * 16 + (g & 1) * 8);
                     if (!there) vh[k] = make_uint2(0u, 0u);
@@ -610,7 +647,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         if (partial) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                if (g + 8 * r < left) continue;
+                if (counts(g + 8 * r)) continue;
                 ev[r] = 0.0f;  // (a slot's byte may be anything)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) c[nt][2 * r] = c[nt][2 * r + 1] = -INFINITY;
@@ -933,12 +970,12 @@ __global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
     if (lane == 0) p.lse[row] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool Q8, bool BF16, int NT, bool SHORT>
-cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
+cudaError_t launch_w(const GqaParams& p, cudaStream_t s) {
     using C = GqaCfg<D, Q8>;
-    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT>;
+    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT, WIN>;
     const int smem = C::kRingBytes + 1024 + (kGqaMaxSequences + 1) * 4;
-    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT>>(kern, smem);
+    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT, WIN>>(kern, smem);
     if (e != cudaSuccess) return e;
     if constexpr (SHORT)
         return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * kClusterCtas)),
@@ -947,6 +984,12 @@ cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
     const dim3 grid((unsigned)(p.warps / kWarps * p.rounds));
     return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)here, s, p)
                    : launch_kernel(kern, grid, dim3(kWarps * 32), (size_t)here, s, p);
+}
+
+template <int D, bool Q8, bool BF16, int NT, bool SHORT>
+cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
+    return p.window > 0 ? launch_w<D, Q8, BF16, NT, SHORT, true>(p, s)
+                        : launch_w<D, Q8, BF16, NT, SHORT, false>(p, s);
 }
 
 template <int D, bool Q8, bool BF16>

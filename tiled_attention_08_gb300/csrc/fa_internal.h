@@ -203,6 +203,9 @@ struct GqaParams {
     int parts_only;            // rows have other parts (a shared prefix): o, lse are the merge's
     int short_step;            // a cluster per unit and no merge (gqa_short)
     int early;                 // launched before the kernel in front of it has finished
+    int window, sinks;         // window > 0: each sequence reads its last `window` tokens and its first
+                               // `sinks` alone
+    int span;                  // pages that a sequence reads at most (max_pages without a window)
     int warps;                 // of a round, a multiple of 4
     int B, Hq, Hk, group, q_blocks, num_pages, max_pages;
     float scale_log2;          // scale * log2(e), either sign

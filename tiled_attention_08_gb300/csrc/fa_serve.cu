@@ -101,11 +101,10 @@ struct DecodeWorkspace {
     size_t unit_parts, slot_o, slot_lse, full_o, full_lse, prefix_o, prefix_lse, bytes;
     int warps;
 };
-DecodeWorkspace decode_workspace(int B, int Hq, int Hk, int D, int max_pages, bool shared,
-                                 int n_prefix) {
+DecodeWorkspace decode_workspace(int B, int Hq, int Hk, int D, int span, bool shared, int n_prefix) {
     DecodeWorkspace w;
     const int chunk = B < kGqaMaxSequences ? B : kGqaMaxSequences;
-    w.warps = gqa_warps(chunk, Hk, Hq / Hk, max_pages);
+    w.warps = gqa_warps(chunk, Hk, Hq / Hk, span);
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -146,9 +145,9 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         c.full_o = reinterpret_cast<float*>(ws + w.full_o) + b0 * row_o;
         c.full_lse = reinterpret_cast<float*>(ws + w.full_lse) + (size_t)b0 * p.Hq;
         c.early = p.early && b0 == 0;
-        c.short_step = !p.parts_only && gqa_short(c.B, p.Hk, p.group, p.max_pages, D, q8);
+        c.short_step = !p.parts_only && gqa_short(c.B, p.Hk, p.group, p.span, D, q8);
         c.rounds = gqa_rounds(c.B, p.Hk, p.group);
-        c.warps = gqa_launched_warps(c.B, p.Hk, p.group, p.max_pages, D, q8, c.early ? busy_sms : 0);
+        c.warps = gqa_launched_warps(c.B, p.Hk, p.group, p.span, D, q8, c.early ? busy_sms : 0);
         cudaError_t e = traced_launch(kernel++, s, [&] { return launch_decode_gqa(c, D, bf16, q8, s); });
         if (e != cudaSuccess) return e;
         if (c.short_step) continue;  // (its clusters have joined their parts)
@@ -177,6 +176,82 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+// Pages that a sequence reads at most: the whole table, or those of the first tokens and of the window
+// (which may begin anywhere in a page).
+int window_span(int max_pages, int window, int sinks) {
+    if (window == 0) return max_pages;
+    const long long pages = ((long long)sinks + kPageTokens - 1) / kPageTokens +
+                            ((long long)window + kPageTokens - 2) / kPageTokens + 1;
+    return pages < max_pages ? (int)pages : max_pages;
+}
+
+// One decode step; window = 0: over all tokens.
+fa_status decode_step(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                      const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens, void* o,
+                      float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hk, int D,
+                      int num_pages, int max_pages, int window, int sinks, float scale, int dtype,
+                      int cache_dtype, void* stream) {
+    TraceDisarm disarm;
+    fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0) return FA_OK;
+    const bool q8 = cache_dtype == FA_CACHE_E4M3;
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse))
+        return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages,
+                           max_pages, cache_dtype))
+        return FA_ERR_INVALID_ARG;
+    GqaParams p;
+    std::memset(&p, 0, sizeof(p));
+    const size_t rows = (size_t)B * Hq;
+    const int span = window_span(max_pages, window, sinks);
+    const DecodeWorkspace w = decode_workspace(B, Hq, Hk, D, span, false, 0);
+    const size_t ws_need = w.bytes;
+    if (!workspace || workspace_bytes < ws_need || !aligned16(workspace))
+        return FA_ERR_INVALID_ARG;
+    const size_t cb = cache_bytes(num_pages, Hk, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, Hk) : 0;
+    const Range ins[] = {range(q, rows * D * 2u), range(k_cache, cb), range(v_cache, cb),
+                         range(k_exp, eb), range(v_exp, eb),
+                         range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u)};
+    const Range outs[] = {range(o, rows * D * 2u), range(lse, rows * 4u), range(workspace, ws_need)};
+    for (int a = 0; a < 3; ++a) {
+        for (const Range& in : ins)
+            if (overlap(outs[a], in)) return FA_ERR_INVALID_ARG;
+        for (int b = a + 1; b < 3; ++b)
+            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
+    }
+    if (!bind_context()) return FA_ERR_CUDA;
+    if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, q8) ||
+                          !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, q8)))
+        return FA_ERR_CUDA;
+    p.q = q;
+    p.k_exp = static_cast<const uint8_t*>(k_exp);
+    p.v_exp = static_cast<const uint8_t*>(v_exp);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.group = Hq / Hk;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.window = window;
+    p.sinks = sinks;
+    p.span = span;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.status = status_ptr();
+    p.timeout_ns = wait_timeout_ns();
+    if (!p.status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return run_decode(p, B, D, dtype == FA_BF16, q8, static_cast<uint8_t*>(workspace), w, 0, 0, 0,
+                      s) ==
+                   cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -407,61 +482,30 @@ fa_status fa_decode_paged_ex(const void* q, const void* k_cache, const void* v_c
                              const int32_t* seq_lens, void* o, float* lse, void* workspace,
                              size_t workspace_bytes, int B, int Hq, int Hk, int D, int num_pages,
                              int max_pages, float scale, int dtype, int cache_dtype, void* stream) {
-    TraceDisarm disarm;
-    fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, cache_dtype);
-    if (st != FA_OK) return st;
-    if (B == 0 || Hq == 0) return FA_OK;
-    const bool q8 = cache_dtype == FA_CACHE_E4M3;
-    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse))
+    return decode_step(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o, lse, workspace,
+                       workspace_bytes, B, Hq, Hk, D, num_pages, max_pages, 0, 0, scale, dtype, cache_dtype,
+                       stream);
+}
+
+size_t fa_decode_window_workspace_bytes(int B, int Hq, int Hk, int D, int max_pages, int window, int sinks) {
+    if (B <= 0 || Hq <= 0 || window < 1 || sinks < 0 ||
+        check_decode(B, Hq, Hk, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK)
+        return 0;
+    return decode_workspace(B, Hq, Hk, D, window_span(max_pages, window, sinks), false, 0).bytes;
+}
+
+fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                           const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens, void* o,
+                           float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int Hk, int D,
+                           int num_pages, int max_pages, int window, int sinks, float scale, int dtype,
+                           int cache_dtype, void* stream) {
+    if (window < 1 || sinks < 0) {
+        trace_disarm();
         return FA_ERR_INVALID_ARG;
-    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages,
-                           max_pages, cache_dtype))
-        return FA_ERR_INVALID_ARG;
-    GqaParams p;
-    std::memset(&p, 0, sizeof(p));
-    const size_t rows = (size_t)B * Hq;
-    const DecodeWorkspace w = decode_workspace(B, Hq, Hk, D, max_pages, false, 0);
-    const size_t ws_need = w.bytes;
-    if (!workspace || workspace_bytes < ws_need || !aligned16(workspace))
-        return FA_ERR_INVALID_ARG;
-    const size_t cb = cache_bytes(num_pages, Hk, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, Hk) : 0;
-    const Range ins[] = {range(q, rows * D * 2u), range(k_cache, cb), range(v_cache, cb),
-                         range(k_exp, eb), range(v_exp, eb),
-                         range(block_tables, (size_t)B * max_pages * 4u),
-                         range(seq_lens, (size_t)B * 4u)};
-    const Range outs[] = {range(o, rows * D * 2u), range(lse, rows * 4u), range(workspace, ws_need)};
-    for (int a = 0; a < 3; ++a) {
-        for (const Range& in : ins)
-            if (overlap(outs[a], in)) return FA_ERR_INVALID_ARG;
-        for (int b = a + 1; b < 3; ++b)
-            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
     }
-    if (!bind_context()) return FA_ERR_CUDA;
-    if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, q8) ||
-                          !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, q8)))
-        return FA_ERR_CUDA;
-    p.q = q;
-    p.k_exp = static_cast<const uint8_t*>(k_exp);
-    p.v_exp = static_cast<const uint8_t*>(v_exp);
-    p.block_tables = block_tables;
-    p.seq_lens = seq_lens;
-    p.o = o;
-    p.lse = lse;
-    p.Hq = Hq;
-    p.Hk = Hk;
-    p.group = Hq / Hk;
-    p.num_pages = num_pages;
-    p.max_pages = max_pages;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.status = status_ptr();
-    p.timeout_ns = wait_timeout_ns();
-    if (!p.status) return FA_ERR_CUDA;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return run_decode(p, B, D, dtype == FA_BF16, q8, static_cast<uint8_t*>(workspace), w, 0, 0, 0,
-                      s) ==
-                   cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
+    return decode_step(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o, lse, workspace,
+                       workspace_bytes, B, Hq, Hk, D, num_pages, max_pages, window, sinks, scale, dtype,
+                       cache_dtype, stream);
 }
 
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
@@ -578,6 +622,7 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
     p.lse = lse;
     p.block_tables = block_tables;
     p.seq_lens = seq_lens;
+    p.span = max_pages;
     p.parts_only = prefix_len > 0;
     p.early = prefix_len > 0;
     p.Hq = Hq;

@@ -70,6 +70,9 @@ int as_int(const char* name, int64_t v) {
     return (int)v;
 }
 
+// Windows and counts of first tokens are ints in the C interface; beyond its lengths they mean the same.
+int as_span(int64_t v) { return (int)std::clamp<int64_t>(v, INT32_MIN, INT32_MAX); }
+
 // Whether the kernels can step by a view's stride of dimension i.
 bool usable_stride(const Tensor& t, int i) { return t.stride(i) > 0 && (t.stride(i) & 7) == 0; }
 
@@ -438,12 +441,24 @@ std::tuple<Tensor, Tensor> decode_paged_ex(const Tensor& q, const Tensor& k_cach
                                            const Tensor& block_tables, const Tensor& seq_lens,
                                            std::optional<double> scale, const OptTensor& out,
                                            const OptTensor& lse, const OptTensor& workspace,
-                                           const OptTensor& k_exp, const OptTensor& v_exp) {
+                                           const OptTensor& k_exp, const OptTensor& v_exp,
+                                           std::optional<int64_t> window = {}, int64_t sinks = 0) {
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
     const Step s = decode_outputs(q, out, lse);
     const Cache c = check_cache(k_cache, v_cache, k_exp, v_exp, q.scalar_type(), s.index);
     TORCH_CHECK_VALUE(c.D == s.D, "the cache has heads of ", c.D, ", q of ", s.D);
     const int max_pages = check_tables(block_tables, seq_lens, s.B, s.index);
+    if (window) {
+        const int w = as_span(*window), n = as_span(sinks);
+        const Tensor ws = workspace_of(
+            workspace, fa_decode_window_workspace_bytes(s.B, s.Hq, c.H, s.D, max_pages, w, n), q, s.index);
+        check_status("fa_decode_window",
+                     fa_decode_window(ptr(q), c.k, c.v, c.k_exp, c.v_exp, ptr<int32_t>(block_tables),
+                                      ptr<int32_t>(seq_lens), ptr(s.o), ptr<float>(s.lse), ptr(ws), ws.nbytes(),
+                                      s.B, s.Hq, c.H, s.D, c.num_pages, max_pages, w, n, scale_of(scale, s.D),
+                                      s.dt, c.kind, stream_of(s.index)));
+        return {s.o, s.lse};
+    }
     const Tensor ws = workspace_of(
         workspace, fa_decode_workspace_bytes_ex(s.B, s.Hq, c.H, s.D, max_pages), q, s.index);
     check_status("fa_decode_paged_ex",
@@ -468,10 +483,12 @@ std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, 
                                         const Tensor& block_tables, const Tensor& seq_lens,
                                         std::optional<double> scale, const OptTensor& out,
                                         const OptTensor& lse, const OptTensor& workspace,
-                                        const OptTensor& k_exp, const OptTensor& v_exp) {
-    if (given(k_exp) || given(v_exp) || q.dim() != 3 || k_cache.dim() != 4 || k_cache.size(1) != q.size(1))
+                                        const OptTensor& k_exp, const OptTensor& v_exp,
+                                        std::optional<int64_t> window, int64_t sinks) {
+    if (window || given(k_exp) || given(v_exp) || q.dim() != 3 || k_cache.dim() != 4 ||
+        k_cache.size(1) != q.size(1))
         return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
-                               k_exp, v_exp);
+                               k_exp, v_exp, window, sinks);
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
     const int index = cuda_index("q", q);
     TORCH_CHECK_VALUE(q.is_contiguous(), "q must be contiguous");
@@ -537,9 +554,6 @@ struct Window {
     int64_t window, sinks;
     std::optional<double> scale;
 };
-// Windows and counts of first tokens are ints in the C interface; beyond its lengths they mean the same.
-int as_span(int64_t v) { return (int)std::clamp<int64_t>(v, INT32_MIN, INT32_MAX); }
-
 struct WindowSizes {
     int index, dt, B, Hq, Hk, Lq, Lk, D;
     fa_strides q, k, v;
@@ -692,7 +706,13 @@ PYBIND11_MODULE(fa_torch, m) {
     m.def("cache_append", &cache_append);
     m.def("cache_read", &cache_read);
     m.def("decode_paged", &decode_paged);
-    m.def("decode_paged_ex", &decode_paged_ex);
+    m.def("decode_paged_ex",
+          [](const Tensor& q, const Tensor& k_cache, const Tensor& v_cache, const Tensor& block_tables,
+             const Tensor& seq_lens, std::optional<double> scale, const OptTensor& out, const OptTensor& lse,
+             const OptTensor& workspace, const OptTensor& k_exp, const OptTensor& v_exp) {
+              return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
+                                     k_exp, v_exp);
+          });
     m.def("decode_shared_prefix", &decode_shared_prefix);
     m.def("attention_window", &attention_window);
     m.def("window_forward", &window_forward);
