@@ -366,6 +366,36 @@ fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cac
                            int Hk, int D, int num_pages, int max_pages, int window, int sinks,
                            float scale, int dtype, int cache_dtype, void* stream);
 
+/* Bytes of device workspace fa_attention_paged needs (fp32 parts of query tiles that several CTAs share; at most
+ * 41 MB at D = 128, whatever the sizes).  0 for an empty problem or invalid sizes. */
+size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, int max_pages);
+
+/*
+ * Attention of a chunk of new tokens over a paged cache: a prompt, or the next part of one, whose keys and
+ * values have been written (fa_cache_append).  Sequence b has seq_lens[b] tokens in the cache, the last
+ * new_lens[b] of them new; row i < new_lens[b] of q[b, h] is token t = seq_lens[b] - new_lens[b] + i and
+ * attends to tokens j <= t of cache head h / (Hq / Hk), with window > 0 to those with j > t - window or
+ * j < sinks alone (window = 0: to all; sinks is ignored).
+ *   q, o:      [B, Hq, L, D] views of dtype (strides[0..1]); o may be another part of one packed tensor with q;
+ *   lse:       [B, Hq, L] fp32, contiguous;
+ *   new_lens:  [B] int32, device, 0 <= new_lens[b] <= min(L, seq_lens[b]); null: L for every sequence, 0 for
+ *              one of length 0;
+ *   caches, exponents, block_tables, seq_lens, scale: as for fa_decode_paged_ex.  An e4m3 row is its values times
+ *              its power of two, rounded to dtype, as fa_cache_read gives it.
+ * Rows new_lens[b] .. L - 1 of o are written as zeros, of lse as -inf.  Pages without a token that some row of a
+ * sequence sees, and their table entries, are not read; slots of other pages that hold no such token may
+ * hold anything.  (An infinity or NaN in V of a token that counts may reach rows of the same chunk that do not see
+ * it.)  Hq / Hk <= 128.  Bad lengths and page indexes (device data) are reported by fa_get_device_status() as
+ * FA_ERR_INVALID_ARG: a sequence with a bad length counts as one without new tokens, a bad page as
+ * zeros.  Calls that may overlap on the GPU need a workspace each.  Enqueues two kernels.
+ */
+fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                             const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,
+                             const int32_t* new_lens, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, const fa_strides* strides, int B, int Hq, int Hk,
+                             int L, int D, int num_pages, int max_pages, int window, int sinks,
+                             float scale, int dtype, int cache_dtype, void* stream);
+
 /* Bytes of device workspace fa_decode_shared_prefix needs: fa_decode_paged_ex's and fp32 parts of
  * every query row.  0 for invalid sizes. */
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,

@@ -157,3 +157,61 @@ def test_decode_workspace():
     assert need(4, 8, 2, 64, 1 << 20, (1 << 31) - 1, (1 << 31) - 1) == \
         fa.fa_decode_workspace_bytes_ex(4, 8, 2, 64, 1 << 20)
     assert need(4, 8, 2, 64, 16, 0, 0) == need(0, 8, 2, 64, 16, 4, 0) == need(4, 8, 3, 64, 16, 4, 0) == 0
+
+
+def _chunk(B=2, Hq=4, Hk=2, L=32, D=64, num_pages=16, max_pages=4, window=0, sinks=0, scale=0.125, dtype=0, q8=1,
+           ws_bytes=None, st=None, **ptrs):
+    names = ("q", "kc", "vc", "ke", "ve", "bt", "sl", "nl", "o", "lse", "ws")
+    p = {n: A + i * 64 * MB for i, n in enumerate(names)}
+    p.update(ptrs)
+    need = fa.fa_attention_paged_workspace_bytes(B, Hq, Hk, L, D, max_pages)
+    s = strides(Hq, L, D)
+    return fa.fa_attention_paged(*(p[n] for n in names), need if ws_bytes is None else ws_bytes, st or [s, s], B,
+                                 Hq, Hk, L, D, num_pages, max_pages, window, sinks, scale, dtype, q8, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(window=-1), BAD),
+    (dict(sinks=-1), BAD),
+    (dict(dtype=2), BAD),
+    (dict(q8=2), BAD),
+    (dict(B=-1), BAD),
+    (dict(L=-1), BAD),
+    (dict(Hq=3), BAD),
+    (dict(Hk=0), BAD),
+    (dict(D=80), UNS),
+    (dict(Hq=258), UNS),                    # a group of 129
+    (dict(max_pages=1 << 26), UNS),
+    (dict(B=1 << 12, L=1 << 24, Hq=2, max_pages=1 << 20), UNS),
+    (dict(scale=math.inf), BAD),
+    (dict(q=0), BAD),
+    (dict(q=A + 8), BAD),
+    (dict(o=0), BAD),
+    (dict(o=A + 1024), BAD),
+    (dict(o=A + 64 * MB), BAD),             # on the keys
+    (dict(lse=A), BAD),
+    (dict(lse=A + 9 * 64 * MB + 2), BAD),
+    (dict(kc=0), BAD),
+    (dict(ke=0), BAD),
+    (dict(bt=0), BAD),
+    (dict(sl=0), BAD),
+    (dict(nl=A + 7 * 64 * MB + 2), BAD),
+    (dict(o=A + 7 * 64 * MB), BAD),         # on the new lengths
+    (dict(ws=0), BAD),
+    (dict(ws_bytes=64), BAD),
+    (dict(ws=A), BAD),
+    (dict(st=[(8192, 2048, 60)] * 2), BAD),
+    (dict(B=0), OK),
+    (dict(L=0), OK),
+    (dict(Hq=0), OK),
+])
+def test_chunk_is_refused(kw, status):
+    assert _chunk(**kw) == status
+
+
+def test_chunk_workspace():
+    need = fa.fa_attention_paged_workspace_bytes
+    assert need(64, 64, 8, 4096, 128, 4096) <= 41_000_000
+    assert 0 < need(1, 8, 8, 16, 128, 4) < need(64, 64, 8, 4096, 128, 4096)
+    for bad in ((0, 4, 2, 32, 64, 4), (2, 4, 3, 32, 64, 4), (2, 4, 2, 0, 64, 4), (2, 4, 2, 32, 96, 4)):
+        assert need(*bad) == 0

@@ -39,7 +39,8 @@ __all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa
            "fa_cache_read", "rotary", "rotary_apply", "rotary_freqs", "cache_append", "cache_read",
            "FA_CACHE_16BIT", "FA_CACHE_E4M3", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
            "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "decode_shared_prefix",
-           "fa_decode_window", "fa_decode_window_workspace_bytes",
+           "fa_decode_window", "fa_decode_window_workspace_bytes", "fa_attention_paged",
+           "fa_attention_paged_workspace_bytes", "attention_paged",
            "fa_window_fwd", "fa_window_bwd", "fa_window_bwd_workspace_bytes", "window_forward",
            "window_backward", "attention_window",
            "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
@@ -64,7 +65,8 @@ EXPORTED = ("fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex", "fa_bwd_workspace_byte
             "fa_cache_read", "fa_decode_paged_ex", "fa_decode_workspace_bytes_ex",
             "fa_decode_shared_prefix", "fa_shared_prefix_workspace_bytes", "fa_window_fwd",
             "fa_window_bwd", "fa_window_bwd_workspace_bytes", "fa_decode_window",
-            "fa_decode_window_workspace_bytes")
+            "fa_decode_window_workspace_bytes", "fa_attention_paged",
+            "fa_attention_paged_workspace_bytes")
 
 
 class FaStrides(ctypes.Structure):
@@ -136,6 +138,11 @@ def load_library():
         lib.fa_decode_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i,
                                          i, i, f, i, i, vp]
         lib.fa_decode_window.restype = i
+        lib.fa_attention_paged_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        lib.fa_attention_paged_workspace_bytes.restype = sz
+        lib.fa_attention_paged.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, sp, i, i, i,
+                                           i, i, i, i, i, i, f, i, i, vp]
+        lib.fa_attention_paged.restype = i
         lib.fa_shared_prefix_workspace_bytes.argtypes = [i, i, i, i, i, i]
         lib.fa_shared_prefix_workspace_bytes.restype = sz
         lib.fa_decode_shared_prefix.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, vp, sz, i, i, i,
@@ -272,6 +279,21 @@ def fa_decode_window(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, 
     return load_library().fa_decode_window(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o,
                                            lse, workspace, workspace_bytes, B, Hq, Hk, D, num_pages,
                                            max_pages, window, sinks, scale, dtype, cache_dtype, stream)
+
+
+def fa_attention_paged_workspace_bytes(B, Hq, Hk, L, D, max_pages) -> int:
+    return int(load_library().fa_attention_paged_workspace_bytes(B, Hq, Hk, L, D, max_pages))
+
+
+def fa_attention_paged(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, new_lens, o, lse,
+                       workspace, workspace_bytes, strides, B, Hq, Hk, L, D, num_pages, max_pages,
+                       window, sinks, scale, dtype, cache_dtype, stream) -> int:
+    """``strides``: two (batch, head, row) tuples for q, o."""
+    return load_library().fa_attention_paged(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens,
+                                             new_lens, o, lse, workspace, workspace_bytes,
+                                             _strides_array(strides), B, Hq, Hk, L, D, num_pages,
+                                             max_pages, window, sinks, scale, dtype, cache_dtype,
+                                             stream)
 
 
 def fa_shared_prefix_workspace_bytes(B, Hq, Hk, D, prefix_len, max_pages) -> int:
@@ -668,3 +690,16 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
     mode.  [B, L, H, D] tensors transposed, or the parts of a packed tensor, are read in place;
     tensors that the kernels cannot step through (expanded ones, for example) are copied."""
     return (_binding or _ops()).attention_window(q, k, v, window, sinks, scale)
+
+
+def attention_paged(q, k_cache, v_cache, block_tables, seq_lens, new_lens=None, window: int | None = None,
+                    sinks: int = 0, scale: float | None = None, out=None, lse=None, workspace=None,
+                    k_exp=None, v_exp=None):
+    """Attention of a chunk of new tokens of every sequence over a paged cache: q [B, Hq, L, D], of which
+    the first ``new_lens[b]`` rows (None: all L) are the last tokens of sequence b, ``seq_lens[b]`` being its
+    length with them; their keys and values have been written (``cache_append``).  A token attends to all
+    up to its own, or with ``window`` to the last ``window`` of them and the first ``sinks`` of the sequence.
+    Caches as for ``decode_paged``, with as many heads as q or a divisor.  Returns O like q and LSE
+    [B, Hq, L] (fp32); rows without a token are zeros and -inf.  See fa_attention_paged in fa.h."""
+    return (_binding or _ops()).attention_paged(q, k_cache, v_cache, block_tables, seq_lens, new_lens,
+                                                window, sinks, scale, out, lse, workspace, k_exp, v_exp)

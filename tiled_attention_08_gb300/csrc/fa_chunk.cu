@@ -1,0 +1,842 @@
+// fa_chunk.cu -- attention of a chunk of new tokens of every sequence over a paged cache (sm_103a).
+//
+// Sequence b of len_b cached tokens adds its last n_b; row i < n_b of q[b, h] is token len_b - n_b + i
+// and attends, causally, to the cached rows of head h / G, all of them or those of a sliding window and
+// the first tokens (fa_window_sched.h):  O = softmax(scale q K^T) V and LSE.  Rows i >= n_b get 0, -inf.
+//
+// 4 G D FLOPs per token pair and cache head: bound by the tensor cores from a few hundred query rows per
+// cache head on, by HBM or latency below.  The pipeline is that of the dense forward: two 128-row query
+// tiles share every 128-key tile; producer warps, one MMA warp, eight softmax warps (a row per
+// thread), P as the TMEM operand of PV.  What differs:
+//  * rows: row r of a tile is token r % T of head r / T of the group, T = 128 / G tokens: short chunks
+//    fill the tensor core with the group's heads, and each cached row is read once for all of them.  One
+//    4-D TMA box {64, T, G, 1} of q brings them in that order.  Rows behind T G hold whatever the slot
+//    held: tensor-core rows do not mix, and they are not written.
+//  * keys: a 128-key tile is 8 pages.  Of a 16-bit cache each is its own TMA box, issued by one lane
+//    each; pages without a token that the pair sees are read at a row outside the map, as zeros, and
+//    slots of other pages that hold none are cleared in V by the MMA warp (0 * NaN).  Of an e4m3 cache
+//    four converter warps read the bytes, multiply by the row's power of two in fp32, round to q's type
+//    (exact in bf16) and write the tile in the swizzled layout that the contraction reads.
+//  * split: lengths are known on the device only, and rows alone seldom fill 152 SMs.  Units (head, pair of
+//    query tiles, key tile) form one line, of which every CTA takes an equal stretch: each CTA first
+//    sums the pairs' key tiles.  A pair that lies whole in a stretch is written as O and LSE; of a cut
+//    one each CTA leaves an fp32 part (two at most), which fa_chunk_join_kernel joins.
+#include "fa_e4m3.cuh"
+#include "fa_internal.h"
+#include "fa_ptx.cuh"
+#include "fa_window_sched.h"
+
+namespace fa {
+namespace {
+
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+// fp16 weights are taken relative to a reference 2^7 below the largest (see fa_decode_gqa.cu).
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
+constexpr int kPagesPerTile = kTileRows / kPageTokens;
+
+template <int D, bool BF16, bool Q8>
+struct ChunkCfg {
+    static constexpr int kChunks = D / kChunkElems;
+    static constexpr int kTileBytes = kTileRows * D * 2;
+    static constexpr int kStages = (D == 128) ? 2 : 4;  // of the K ring and of the V ring
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kStageBytes = 32 * 64 * 2;     // read-out buffer of one softmax warp
+    static constexpr int kOffStage = kOffV + kStages * kTileBytes;
+    static constexpr int kSmemBytes = kOffStage + 8 * kStageBytes + 1024;
+    static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;  // (e4m3: the K warp loads queries alone)
+    static constexpr int kConvWarp = 12;                         // the first of four converter warps
+    static constexpr int kConvThreads = 128;
+    static constexpr int kThreads = Q8 ? 16 * 32 : 11 * 32;
+    // e4m3: registers per thread of the softmax warps, of warps 8-11 and of the converters; 128 at
+    // launch, and 2 * 168 + 64 + 112 = 4 * 128.
+    static constexpr int kRegsSoftmax = 168, kRegsIssue = 64, kRegsConv = 112;
+    static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConv == 4 * 128, "the launch's registers");
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kTmS = 0, kTmO = 256;
+    static_assert(kTmO + 2 * D <= kTmemCols, "TMEM budget");
+    static_assert(kSmemBytes <= 232448 - 1024, "shared memory over the 227 KB per-block limit");
+    static constexpr uint32_t kIdescS = idesc_f16(BF16, 128, 128, false, false);
+    static constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, false, true);
+};
+
+template <int N>
+__device__ __forceinline__ void regs_raise() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_lower() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// New tokens of sequence b and the tokens in front of them; none where the lengths are out of range.
+__device__ __forceinline__ bool sequence(const ChunkParams& p, int b, int& n, int& before) {
+    const int len = p.seq_lens[b];
+    n = p.new_lens ? p.new_lens[b] : (len > 0 ? p.L : 0);
+    before = len - n;
+    const bool ok = len >= 0 && len <= (long long)p.max_pages * kPageTokens && n >= 0 && n <= p.L && n <= len &&
+                    (n == 0 || p.num_pages > 0);
+    if (!ok) n = before = 0;
+    return ok;
+}
+__device__ __forceinline__ int pairs_of(const ChunkParams& p, int n) { return (n + 2 * p.T - 1) / (2 * p.T); }
+
+// Pair i of a sequence: tokens 2 T i .. of its new ones.
+__device__ __forceinline__ KeyTiles pair_tiles(const ChunkParams& p, int n, int before, int i) {
+    const int t0 = 2 * p.T * i;
+    return key_tiles(before + t0, before + imin(t0 + 2 * p.T, n) - 1, p.window, p.sinks);
+}
+
+// A place on the line of units and how many of this CTA's lie from there on.
+struct Walk {
+    int hk, b, pair, j;
+    int left;
+};
+
+// Key tiles j0 .. j0 + n - 1 (of those of `all`) of a pair of query tiles.
+struct Segment {
+    int b, hk, t0;         // first new token of the pair
+    int fresh, before;     // new tokens of the sequence, tokens in front of them
+    KeyTiles all;
+    int n_all, j0, n;
+    int a_end, b_0, b_1;   // A sees tiles j < a_end of `all`, B those of j < b_0 and j >= b_1
+    bool has_b;
+    __device__ __forceinline__ bool active(int t, int j) const { return t ? has_b && (j < b_0 || j >= b_1) : j < a_end; }
+    __device__ __forceinline__ int count(int t) const {  // of the segment's
+        const int e = j0 + n;
+        if (t == 0) return imax(imin(e, a_end) - j0, 0);
+        return has_b ? imax(imin(e, b_0) - j0, 0) + imax(e - imax(j0, b_1), 0) : 0;
+    }
+    __device__ __forceinline__ bool whole() const { return n == n_all; }
+};
+
+__device__ __forceinline__ bool segment_at(const ChunkParams& p, const Walk& w, Segment& s) {
+    if (w.left <= 0) return false;
+    s.b = w.b;
+    s.hk = w.hk;
+    s.t0 = 2 * p.T * w.pair;
+    sequence(p, w.b, s.fresh, s.before);
+    s.all = pair_tiles(p, s.fresh, s.before, w.pair);
+    s.n_all = s.all.count();
+    s.j0 = w.j;
+    s.n = imin(s.n_all - w.j, w.left);
+    const int first = s.before + s.t0, mid = first + p.T, end = s.before + s.fresh;
+    s.has_b = mid < end;
+    // (tile index to its place in the list)
+    const int a_hi = imin(mid, end);  // A's last token + 1
+    s.a_end = s.all.lead + ((a_hi - 1) / 128 + 1 - s.all.lo);
+    s.b_0 = s.b_1 = 0;
+    if (s.has_b) {
+        const KeyTiles kb = key_tiles(mid, imin(mid + p.T, end) - 1, p.window, p.sinks);
+        s.b_1 = s.all.lead + imax(kb.lo - s.all.lo, 0);
+        s.b_0 = kb.lead <= s.all.lead ? kb.lead : s.all.lead + imax(kb.lead - s.all.lo, 0);
+    }
+    return true;
+}
+__device__ __forceinline__ void step(const ChunkParams& p, const Segment& s, Walk& w) {
+    w.left -= s.n;
+    w.j += s.n;
+    if (w.left <= 0 || w.j < s.n_all) return;
+    w.j = 0;
+    ++w.pair;
+    int n = s.fresh, before;
+    while (w.pair >= pairs_of(p, n)) {  // (the line goes on: some sequence has another pair)
+        w.pair = 0;
+        if (++w.b == p.B) {
+            w.b = 0;
+            if (++w.hk == p.Hk) {  // (only if the lengths were changed meanwhile)
+                w.left = 0;
+                return;
+            }
+        }
+        sequence(p, w.b, n, before);
+    }
+}
+
+// Tokens lo .. hi - 1 and those below `lead` are seen by some row of the segment's pair.
+struct Live {
+    int lo, hi, lead;
+    __device__ __forceinline__ bool token(int t) const { return t < hi && (t >= lo || t < lead); }
+    __device__ __forceinline__ bool any(int t, int n) const { return t < hi && (t + n > lo || t < lead); }
+    __device__ __forceinline__ bool every(int t, int n) const { return t + n <= hi && (t >= lo || t + n <= lead); }
+};
+__device__ __forceinline__ Live live_of(const ChunkParams& p, const Segment& s) {
+    return {imax(s.before + s.t0 - p.window + 1, 0), s.before + s.fresh, p.sinks};
+}
+
+// The CTA that has unit u.
+__device__ __forceinline__ int unit_cta(long long units, int grid, long long u) {
+    return (int)(((u + 1) * grid - 1) / units);
+}
+
+template <int D, bool BF16, bool Q8>
+__global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
+    fa_chunk_kernel(const __grid_constant__ ChunkParams p) {
+    using C = ChunkCfg<D, BF16, Q8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+    __shared__ uint64_t bar_qf, bar_qe, bar_kf[C::kStages], bar_ke[C::kStages], bar_vf[C::kStages],
+        bar_ve[C::kStages], bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_flag;
+    __shared__ int warp_sum[C::kThreads / 32];
+    __shared__ Walk start_sh;
+    __shared__ long long total_sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int* abort_v = &abort_flag;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        if (p.num_pages > 0) tma_prefetch_desc(&p.tm_q);
+        if (!Q8 && p.num_pages > 0) {
+            tma_prefetch_desc(&p.tm_k);
+            tma_prefetch_desc(&p.tm_v);
+        }
+        abort_flag = 0;
+        start_sh.left = 0;
+        mbar_init(&bar_qf, 1);
+        mbar_init(&bar_qe, 1);
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&bar_kf[s], Q8 ? C::kConvThreads : 1);
+            mbar_init(&bar_ke[s], 1);
+            mbar_init(&bar_vf[s], Q8 ? C::kConvThreads : 1);
+            mbar_init(&bar_ve[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bar_sf[t], 1);
+            mbar_init(&bar_pf[t], 128);
+            mbar_init(&bar_oready[t], 1);
+        }
+        mbar_init(&bar_fin, 1);
+        mbar_fence_init();
+    }
+    if (warp == C::kMmaWarp) tmem_alloc(&tmem_base_sh, C::kTmemCols);
+    // Query rows behind T G are never written: zeros, so that no leftover score makes a row rescale.
+    for (int e = (int)threadIdx.x; e < 2 * C::kChunks * (kTileRows - p.T * p.group) * 8; e += C::kThreads) {
+        const int box = e / ((kTileRows - p.T * p.group) * 8), at = e - box * (kTileRows - p.T * p.group) * 8;
+        sts_u32x4(smem_u32(smem + C::kOffQ + box * kChunkBytes + p.T * p.group * 128 + at * 16),
+                  make_uint4(0u, 0u, 0u, 0u));
+    }
+    fence_proxy_async_smem();
+    // ---- the line: every thread sums a run of (sequence, pair) ----
+    const int slots = p.B * p.max_pairs;
+    const int run = (slots + C::kThreads - 1) / C::kThreads;
+    const int i0 = imin((int)threadIdx.x * run, slots), i1 = imin(i0 + run, slots);
+    auto walk_run = [&](auto&& f) {  // f(b, pair, key tiles) for the run, until it returns true
+        int b = i0 / p.max_pairs, i = i0 - b * p.max_pairs, n = 0, before = 0, pairs = 0;
+        for (int at = i0; at < i1; ++at) {
+            if (at == i0 || i == 0) {
+                if (!sequence(p, b, n, before) && i == 0 && blockIdx.x == 0)
+                    atomicCAS(p.status, 0, (int)kDevBadArg);
+                pairs = pairs_of(p, n);
+            }
+            if (i < pairs && f(b, i, pair_tiles(p, n, before, i).count())) return;
+            if (++i == p.max_pairs) {
+                i = 0;
+                ++b;
+            }
+        }
+    };
+    int sum = 0;
+    walk_run([&](int, int, int k) {
+        sum += k;
+        return false;
+    });
+    int scan = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int before_me = scan - sum, per_head = 0;
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+        if (i < warp) before_me += warp_sum[i];
+        per_head += warp_sum[i];
+    }
+    const long long total = (long long)per_head * p.Hk;
+    const int workers = (int)(total < p.grid ? total : p.grid);
+    if ((int)blockIdx.x < workers) {
+        const long long u0 = total * blockIdx.x / workers, u1 = total * (blockIdx.x + 1) / workers;
+        const int hk = (int)(u0 / per_head), rest = (int)(u0 - (long long)hk * per_head);
+        if (rest >= before_me && rest < before_me + sum) {
+            int at = before_me;
+            walk_run([&](int b, int i, int k) {
+                if (rest >= at + k) {
+                    at += k;
+                    return false;
+                }
+                start_sh = {hk, b, i, rest - at, (int)(u1 - u0)};
+                total_sh = total;
+                return true;
+            });
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_base_sh;
+    Walk walk = start_sh;
+
+    // (e4m3: each warpgroup sets its registers at the head of its branch, with one instruction)
+    if (warp >= 8 && warp < C::kConvWarp) {
+    if constexpr (Q8) regs_lower<C::kRegsIssue>();
+    if (warp == C::kKWarp || (!Q8 && warp == C::kVWarp)) {
+        // ------------------------------ TMA producers ------------------------------
+        // The K warp brings each segment's query pair, and K's pages of a 16-bit cache; the V warp V's.
+        // Lane 8c + i issues page i of chunk c; table entries are fetched one tile ahead.
+        const bool is_k = warp == C::kKWarp;
+        const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
+        uint64_t* full = is_k ? bar_kf : bar_vf;
+        uint64_t* empty = is_k ? bar_ke : bar_ve;
+        uint8_t* ring = smem + (is_k ? C::kOffK : C::kOffV);
+        const int my_page = lane & (kPagesPerTile - 1), my_chunk = lane / kPagesPerTile;
+        bool ok = true;
+        int issued = 0, n_seg = 0;
+        Segment sg;
+        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+            if (is_k) {
+                if (n_seg > 0) ok = wait_warp(&bar_qe, (uint32_t)(n_seg - 1) & 1u, abort_v, p.timeout_ns);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int nt = sg.has_b ? 2 : 1;
+                    const uint32_t box = (uint32_t)(p.group * p.T) * kChunkElems * 2;
+                    mbar_arrive_expect_tx(&bar_qf, (uint32_t)nt * C::kChunks * box);
+                    for (int t = 0; t < nt; ++t)
+                        for (int c = 0; c < C::kChunks; ++c)
+                            tma_load_4d(smem + C::kOffQ + t * C::kTileBytes + c * kChunkBytes, &p.tm_q, &bar_qf,
+                                        c * kChunkElems, sg.t0 + t * p.T, sg.hk * p.group, sg.b);
+                }
+                __syncwarp();
+                ++n_seg;
+            }
+            if constexpr (!Q8) {
+                const Live live = live_of(p, sg);
+                auto entry = [&](int j) {  // this lane's page of tile j, or -1: nothing of it counts
+                    const int pg = sg.all.tile(j) * kPagesPerTile + my_page;
+                    if (my_chunk >= C::kChunks || !live.any(pg * kPageTokens, kPageTokens)) return -1;
+                    const int page = p.block_tables[(size_t)sg.b * p.max_pages + pg];
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicCAS(p.status, 0, (int)kDevBadArg);
+                        return -1;
+                    }
+                    return page;
+                };
+                int next = entry(sg.j0);
+                for (int j = sg.j0; j < sg.j0 + sg.n; ++j) {
+                    const int page = next;
+                    if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
+                    const int st = issued % C::kStages;
+                    if (issued >= C::kStages) {
+                        ok = wait_warp(&empty[st], ((uint32_t)(issued / C::kStages) & 1u) ^ 1u, abort_v,
+                                       p.timeout_ns);
+                        if (!ok) break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+                    __syncwarp();
+                    if (my_chunk < C::kChunks)  // (outside the map: zeros)
+                        tma_load_3d(ring + st * C::kTileBytes + my_chunk * kChunkBytes +
+                                        my_page * (kPageTokens * 128),
+                                    map, &full[st], my_chunk * kChunkElems, page < 0 ? kPageTokens : 0,
+                                    page < 0 ? 0 : page * p.Hk + sg.hk);
+                    __syncwarp();
+                    ++issued;
+                }
+            }
+        }
+        if (!ok && lane == 0) record_timeout(p.status, abort_v);
+        // Drain: the newest fill of every slot must have landed before the CTA exits.
+        if (is_k && n_seg > 0) wait_bounded(&bar_qf, (uint32_t)(n_seg - 1) & 1u, nullptr, p.timeout_ns);
+        for (int g = issued - 1; g >= 0 && g >= issued - C::kStages; --g)
+            wait_bounded(&full[g % C::kStages], (uint32_t)(g / C::kStages) & 1u, nullptr, p.timeout_ns);
+    } else if (warp == C::kMmaWarp) {
+        // ------------------------------ MMA issuer ------------------------------
+        bool ok = true;
+        int g = 0, n_seg = 0, ps[2] = {0, 0};
+        const uint32_t neg = p.s_negate ? kIdescNegateA : 0u;
+        auto wait_ring = [&](uint64_t* full, int i) -> bool {
+            const bool r = wait_warp(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u, abort_v,
+                                     p.timeout_ns);
+            tc_fence_after_sync();
+            return r;
+        };
+        Segment sg;
+        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+            const Live live = live_of(p, sg);
+            const int j1 = sg.j0 + sg.n;
+            const int n_of[2] = {sg.count(0), sg.count(1)};
+            int done[2] = {0, 0};
+            auto issue_s = [&](int t, int gk) {  // S_t = Q_t K^T for ring fill gk
+                const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + t * C::kTileBytes));
+                const uint64_t kd = sdesc_kmajor_sw128(
+                    smem_u32(smem + C::kOffK + (gk % C::kStages) * C::kTileBytes));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+                    mma_ss_w(tmem + C::kTmS + 128 * t, sdesc_advance(qd, off), sdesc_advance(kd, off),
+                             C::kIdescS | neg, kk > 0 ? 1u : 0u);
+                }
+                mma_commit_w(&bar_sf[t]);
+            };
+            auto issue_pv = [&](int t, int gv) -> bool {  // O_t += P_t V for ring fill gv (landed)
+                if (!wait_warp(&bar_pf[t], (uint32_t)ps[t] & 1u, abort_v, p.timeout_ns)) return false;
+                tc_fence_after_sync();
+                const uint64_t vd = sdesc_mnmajor_sw128(
+                    smem_u32(smem + C::kOffV + (gv % C::kStages) * C::kTileBytes), kChunkBytes);
+#pragma unroll
+                for (int kk = 0; kk < kTileRows / 16; ++kk)
+                    mma_ts_w(tmem + C::kTmO + D * t, tmem + C::kTmS + 128 * t + kk * 8,
+                             sdesc_advance(vd, kk * 2048), C::kIdescO, (done[t] > 0 || kk > 0) ? 1u : 0u);
+                ++ps[t];
+                if (++done[t] == n_of[t]) mma_commit_w(&bar_oready[t]);  // O_t is final
+                return true;
+            };
+            ok = wait_warp(&bar_qf, (uint32_t)n_seg & 1u, abort_v, p.timeout_ns);
+            tc_fence_after_sync();
+            ok = ok && wait_ring(bar_kf, g);
+            if (!ok) break;
+            for (int t = 0; t < 2; ++t)
+                if (sg.active(t, sg.j0)) issue_s(t, g);
+            if (sg.n == 1) mma_commit_w(&bar_qe);  // every S of the segment issued
+            mma_commit_w(&bar_ke[g % C::kStages]);
+            for (int j = sg.j0; ok && j < j1; ++j) {
+                const bool next = j + 1 < j1;
+                const int gj = g + (j - sg.j0);
+                if (!wait_ring(bar_vf, gj) || (next && !wait_ring(bar_kf, gj + 1))) {
+                    ok = false;
+                    break;
+                }
+                if constexpr (!Q8) {
+                    // Slots of a page that were read with it but hold no token that counts: zeros.
+                    const int key0 = sg.all.tile(j) * kTileRows;
+                    if (!live.every(key0, kTileRows)) {
+                        uint8_t* tile = smem + C::kOffV + (gj % C::kStages) * C::kTileBytes;
+                        for (int r = lane; r < kTileRows; r += 32) {
+                            const int token = key0 + r;
+                            if (live.token(token) || !live.any(token & ~(kPageTokens - 1), kPageTokens)) continue;
+#pragma unroll
+                            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    sts_u32x4(smem_u32(tile + c * kChunkBytes + r * 128 + u * 16),
+                                              make_uint4(0u, 0u, 0u, 0u));
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok) break;
+                    if (sg.active(t, j) && !issue_pv(t, gj)) {
+                        ok = false;
+                        break;
+                    }
+                    if (next && sg.active(t, j + 1)) issue_s(t, gj + 1);
+                }
+                if (!ok) break;
+                if (j + 2 == j1) mma_commit_w(&bar_qe);  // the segment's last S issued
+                mma_commit_w(&bar_ve[gj % C::kStages]);
+                if (next) mma_commit_w(&bar_ke[(gj + 1) % C::kStages]);
+            }
+            g += sg.n;
+            ++n_seg;
+        }
+        if (!ok && lane == 0) record_timeout(p.status, abort_v);
+        mma_commit_w(&bar_fin);  // every issued MMA must finish before TMEM is released
+        wait_warp(&bar_fin, 0, nullptr, p.timeout_ns);
+    }
+    } else if (Q8 && warp >= C::kConvWarp) {
+        // ------------------------------ converters ------------------------------
+        // Thread i takes 16-byte units i % 4 (+ 4 for the second chunk) of rows i / 4 + 32 k: eight lanes
+        // write all eight 16-byte places of a line of banks.  The next K tile's bytes are in flight while
+        // V is converted, and the other way round.
+        if constexpr (Q8) {
+            regs_lower<C::kRegsConv>();
+            constexpr int kRows = 4, kUnits = kRows * C::kChunks;
+            const int tid = (warp - C::kConvWarp) * 32 + lane, unit = tid & 3, row0 = tid >> 2;
+            struct Bytes {
+                uint4 x[kUnits];
+                uint32_t e;  // exponent byte of each of the four rows (of a row that does not count: 0, with zeros)
+            };
+            auto load = [&](const Segment& sg, const Live& live, int j, bool v, Bytes& r) {
+                const uint8_t* cache = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache);
+                const uint8_t* ex = v ? p.v_exp : p.k_exp;
+                const int key0 = sg.all.tile(j) * kTileRows;
+                r.e = 0;
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    const int token = key0 + row0 + 32 * k;
+                    bool there = live.token(token);
+                    size_t at = 0;
+                    if (there) {
+                        const int page = p.block_tables[(size_t)sg.b * p.max_pages + token / kPageTokens];
+                        there = page >= 0 && page < p.num_pages;
+                        if (!there) atomicCAS(p.status, 0, (int)kDevBadArg);
+                        else at = ((size_t)page * p.Hk + sg.hk) * kPageTokens + token % kPageTokens;
+                    }
+#pragma unroll
+                    for (int c = 0; c < C::kChunks; ++c)
+                        r.x[k * C::kChunks + c] =
+                            there ? *reinterpret_cast<const uint4*>(cache + at * D + c * 64 + unit * 16)
+                                  : make_uint4(0u, 0u, 0u, 0u);
+                    if (there) r.e |= (uint32_t)ex[at] << (8 * k);
+                }
+            };
+            auto store = [&](const Bytes& r, uint8_t* tile) {
+#pragma unroll
+                for (int k = 0; k < kRows; ++k) {
+                    const int row = row0 + 32 * k;
+                    const float f = row_scale(r.e >> (8 * k) & 0xffu);
+#pragma unroll
+                    for (int c = 0; c < C::kChunks; ++c) {
+                        const uint4& x = r.x[k * C::kChunks + c];
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t y[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float2 a = unpack2<false>(
+                                    e4m3x2_to_f16x2(h ? w[i] >> 16 : w[i] & 0xffffu));
+                                y[2 * i + h] = pack2<BF16>(a.x * f, a.y * f);
+                            }
+                        const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
+                        sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
+                        sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
+                                  make_uint4(y[4], y[5], y[6], y[7]));
+                    }
+                }
+                fence_proxy_async_smem();
+            };
+            bool ok = true;
+            int g = 0;
+            Segment sg;
+            Bytes kb, vb;
+            Live live;
+            int j = 0;
+            bool more = segment_at(p, walk, sg);
+            if (more) {
+                live = live_of(p, sg);
+                j = sg.j0;
+                load(sg, live, j, false, kb);
+                load(sg, live, j, true, vb);
+            }
+            while (ok && more) {
+                const int st = g % C::kStages;
+                const uint32_t ph = ((uint32_t)(g / C::kStages) & 1u) ^ 1u;
+                if (g >= C::kStages) ok = wait_warp(&bar_ke[st], ph, abort_v, p.timeout_ns);
+                if (!ok) break;
+                store(kb, smem + C::kOffK + st * C::kTileBytes);
+                mbar_arrive(&bar_kf[st]);
+                if (++j == sg.j0 + sg.n) {  // the next tile, perhaps of another segment
+                    step(p, sg, walk);
+                    more = segment_at(p, walk, sg);
+                    if (more) {
+                        live = live_of(p, sg);
+                        j = sg.j0;
+                    }
+                }
+                if (more) load(sg, live, j, false, kb);
+                if (g >= C::kStages) ok = wait_warp(&bar_ve[st], ph, abort_v, p.timeout_ns);
+                if (!ok) break;
+                store(vb, smem + C::kOffV + st * C::kTileBytes);
+                mbar_arrive(&bar_vf[st]);
+                if (more) load(sg, live, j, true, vb);
+                ++g;
+            }
+            if (!ok && lane == 0) record_timeout(p.status, abort_v);
+        }
+    } else {
+        // ------------------------------ softmax warps ------------------------------
+        if constexpr (Q8) regs_raise<C::kRegsSoftmax>();
+        const int t = warp / 4, quad = warp % 4;
+        const int row = quad * 32 + lane;  // row inside the tile == TMEM lane
+        const int head = row / p.T, tok = row - head * p.T;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+        const uint32_t s_addr = tmem + lane_off + C::kTmS + 128 * t;
+        const uint32_t o_addr = tmem + lane_off + C::kTmO + D * t;
+        const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
+        const uint32_t stage = smem_u32(smem + C::kOffStage + warp * C::kStageBytes);
+        bool ok = true, cut_behind = false;
+        int ps = 0, n_done = 0;
+        Segment sg;
+        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+            const int j1 = sg.j0 + sg.n, cnt = sg.count(t);
+            const int first = sg.before + sg.t0 + t * p.T, pos = first + tok;
+            const int last = imin(first + p.T, sg.before + sg.fresh) - 1;
+            float m_ref = -INFINITY, l_sum = 0.0f;
+            bool began = false;
+            for (int j = sg.j0; j < j1; ++j) {
+                if (!sg.active(t, j)) continue;
+                ok = wait_warp(&bar_sf[t], (uint32_t)ps & 1u, abort_v, p.timeout_ns);
+                if (!ok) break;
+                ++ps;
+                tc_fence_after_sync();
+                float s[128];
+                {
+                    uint32_t r[128];
+                    tmem_ld_cols<128>(s_addr, r);
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) s[i] = __uint_as_float(r[i]);
+                }
+                const int key0 = sg.all.tile(j) * kTileRows;
+                if (hides_later(key0, kTileRows, first)) {
+                    const int lim = pos - key0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c > lim) s[c] = -INFINITY;
+                }
+                if (hides_earlier(key0, kTileRows, last, p.window, p.sinks)) {
+                    const int lim = pos - p.window - key0, sink = p.sinks - key0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c <= lim && c >= sink) s[c] = -INFINITY;
+                }
+                float m4[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) m4[v] = fmaxf(s[v], s[v + 4]);
+#pragma unroll
+                for (int c = 8; c < 128; c += 8) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) m4[v] = fmax3(m4[v], s[c + v], s[c + 4 + v]);
+                }
+                const float m_cand = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.scale_log2;
+                float m_new = m_ref;
+                if (m_cand > m_ref + (kRescaleThreshold + kLift<BF16>)) m_new = m_cand - kLift<BF16>;
+                const bool rescale = began && (m_new != m_ref);
+                const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
+                const float alpha = rescale ? ex2_approx(m_ref - m_new) : 1.0f;
+                const uint64_t shift2 = f2_make(-m_use, -m_use);
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float y0, y1;
+                        f2_split(f2_fma(f2_make(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1]), scale2, shift2),
+                                 y0, y1);
+                        const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
+                        sum2[i & 1] = f2_add(sum2[i & 1], f2_make(p0, p1));
+                        pk[i] = pack2<BF16>(p0, p1);
+                    }
+                    tmem_st16(s_addr + h * 16, pk);
+                }
+                float sa, sb, sc, sd;
+                f2_split(sum2[0], sa, sb);
+                f2_split(sum2[1], sc, sd);
+                l_sum = l_sum * alpha + ((sa + sb) + (sc + sd));
+                if (__any_sync(0xffffffffu, rescale)) tmem_row_scale<D>(o_addr, alpha);
+                tmem_st_wait();
+                tc_fence_before_sync();
+                mbar_arrive(&bar_pf[t]);
+                m_ref = m_new;
+                began = true;
+            }
+            if (!ok) break;
+            const bool valid = head < p.group && sg.t0 + t * p.T + tok < sg.fresh;
+            const bool whole = sg.whole(), behind = !whole && sg.j0 == 0;  // (behind: it goes on in the next CTA)
+            cut_behind |= behind;
+            if (behind && threadIdx.x == 0) {  // for the join: the pair and the CTAs that have its tiles
+                const long long x = (total_sh * blockIdx.x / workers) + (start_sh.left - walk.left);
+                const int n_parts = unit_cta(total_sh, workers, x + sg.n_all - 1) - (int)blockIdx.x + 1;
+                p.owners[blockIdx.x] = make_int4(sg.b, sg.hk, sg.t0, n_parts);
+            }
+            const size_t slot = 2 * (size_t)blockIdx.x + (behind ? 1 : 0);
+            const size_t part = (slot * 2 + t) * kTileRows + row;
+            if (cnt > 0) {
+                ok = wait_warp(&bar_oready[t], (uint32_t)n_done & 1u, abort_v, p.timeout_ns);
+                if (!ok) break;
+                tc_fence_after_sync();
+                ++n_done;
+            }
+            const float lse2 = l_sum != 0.0f ? m_ref + log2f(l_sum) : -INFINITY;
+            const float inv_l = l_sum != 0.0f ? 1.0f / l_sum : 0.0f;
+            if (whole) {
+                const int h = sg.hk * p.group + head;
+                const size_t orow = (size_t)sg.b * p.Hq + h;
+                const int i = sg.t0 + t * p.T + tok;
+                if (valid) p.lse[orow * p.L + i] = lse2 * kLn2;
+                uint8_t* dst = valid ? reinterpret_cast<uint8_t*>(p.o) +
+                                           row_offset(p.so, (int)orow, p.Hq, i)
+                                     : nullptr;
+                if (cnt > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t r[32];
+                            tmem_ld32(o_addr + 64 * c + 32 * hf, r);
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack2<BF16>(__uint_as_float(r[8 * v + 2 * e]) * inv_l,
+                                                       __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
+                                sts_u32x4(stage + lane * 128 + (((4 * hf + v) ^ (lane & 7)) << 4),
+                                          make_uint4(w[0], w[1], w[2], w[3]));
+                            }
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = 4 * k + (lane >> 3), uu = lane & 7;
+                            const uint4 w = lds_u32x4(stage + rr * 128 + ((uu ^ (rr & 7)) << 4));
+                            uint8_t* d = reinterpret_cast<uint8_t*>(
+                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+                            if (d) *reinterpret_cast<uint4*>(d + c * 128 + uu * 16) = w;
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else {
+                if (valid) p.slot_lse[part] = cnt > 0 ? lse2 : -INFINITY;
+                if (cnt > 0) {
+                    float* dst = valid ? p.slot_o + part * D : nullptr;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(o_addr + 32 * c, r);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) {
+                            uint4 w;
+                            w.x = __float_as_uint(__uint_as_float(r[4 * v + 0]) * inv_l);
+                            w.y = __float_as_uint(__uint_as_float(r[4 * v + 1]) * inv_l);
+                            w.z = __float_as_uint(__uint_as_float(r[4 * v + 2]) * inv_l);
+                            w.w = __float_as_uint(__uint_as_float(r[4 * v + 3]) * inv_l);
+                            sts_u32x4(stage + lane * 128 + ((v ^ (lane & 7)) << 4), w);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int rr = 4 * k + (lane >> 3), uu = lane & 7;
+                            const uint4 w = lds_u32x4(stage + rr * 128 + ((uu ^ (rr & 7)) << 4));
+                            float* d = reinterpret_cast<float*>(
+                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+                            if (d) *reinterpret_cast<uint4*>(d + c * 32 + uu * 4) = w;
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) record_timeout(p.status, abort_v);
+        if (threadIdx.x == 0 && !(cut_behind && ok)) p.owners[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == C::kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Joins the parts of the pairs that are cut: block (c, y) the rows 32 y .. of the pair that goes on behind
+// CTA c, a warp per row.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).  And, before that, the rows
+// without a token: zeros and -inf, 64 rows of a head per warp.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) fa_chunk_join_kernel(const ChunkParams p) {
+    constexpr int kPer = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int blocks_l = (p.L + 63) / 64;
+    const long long items = (long long)p.B * p.Hq * blocks_l;
+    for (long long it = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; it < items;
+         it += (long long)gridDim.x * gridDim.y * 8) {
+        const int bh = (int)(it / blocks_l), i0 = (int)(it - (long long)bh * blocks_l) * 64;
+        int n, ahead;
+        sequence(p, bh / p.Hq, n, ahead);
+        const int from = imax(n, i0), to = imin(i0 + 64, p.L);
+        for (int e = from * (D / 8) + lane; e < to * (D / 8); e += 32) {
+            const int i = e / (D / 8), u = e % (D / 8);
+            reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.o) + row_offset(p.so, bh, p.Hq, i))[u] =
+                make_uint4(0u, 0u, 0u, 0u);
+            if (u == 0) p.lse[(size_t)bh * p.L + i] = -INFINITY;
+        }
+    }
+    pdl_wait();
+    const int4 own = p.owners[blockIdx.x];
+    const int n_parts = own.w;
+    // (A kernel that gave up on a wait may have left an entry as it found it.)
+    if (n_parts < 2 || n_parts > (int)gridDim.x - (int)blockIdx.x || own.x < 0 || own.x >= p.B || own.y < 0 ||
+        own.y >= p.Hk || own.z < 0)
+        return;
+    int fresh, before;
+    sequence(p, own.x, fresh, before);
+    for (int k = 0; k < 4; ++k) {
+        const int r2 = blockIdx.y * 32 + warp * 4 + k;  // row of the two tiles
+        const int t = r2 >> 7, row = r2 & 127, head = row / p.T, tok = row - head * p.T;
+        const int i = own.z + t * p.T + tok;
+        if (head >= p.group || i >= fresh) continue;
+        float top = -INFINITY, sum = 0.0f, x[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
+        for (int c = 0; c < n_parts; ++c) {
+            const size_t slot = 2 * ((size_t)blockIdx.x + c) + (c == 0 ? 1 : 0);
+            const size_t part = (slot * 2 + t) * kTileRows + row;
+            const float y = p.slot_lse[part];
+            if (y == -INFINITY) continue;  // it saw no key there, and left no values
+            const float next = fmaxf(top, y);
+            const float f = ex2_approx(top - next), w = ex2_approx(y - next);
+            const float* src = p.slot_o + part * D + lane * kPer;
+            sum = fmaf(sum, f, w);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[e] = fmaf(x[e], f, w * src[e]);
+            top = next;
+        }
+        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+        const size_t orow = (size_t)own.x * p.Hq + own.y * p.group + head;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.o) +
+                                                    row_offset(p.so, (int)orow, p.Hq, i)) +
+                        lane * (kPer / 2);
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<BF16>(x[e] * inv, x[e + 1] * inv);
+        if (lane == 0) p.lse[orow * p.L + i] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+template <int D, bool BF16, bool Q8>
+cudaError_t launch_t(const ChunkParams& p, cudaStream_t s) {
+    using C = ChunkCfg<D, BF16, Q8>;
+    auto kern = fa_chunk_kernel<D, BF16, Q8>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmemBytes, s, p);
+}
+
+}  // namespace
+
+void chunk_plan(int B, int Hk, int group, int L, int max_pages, ChunkParams* p) {
+    p->T = imin(kTileRows / group, imax(L, 1));
+    p->max_pairs = (L + 2 * p->T - 1) / (2 * p->T);
+    const long long units = (long long)B * Hk * p->max_pairs * ((max_pages + kPagesPerTile - 1) / kPagesPerTile);
+    p->grid = (int)(units < 1 ? 1 : units < kChunkGrid ? units : kChunkGrid);
+}
+
+cudaError_t launch_chunk(const ChunkParams& p, int D, bool bf16, bool q8, cudaStream_t s) {
+    if (D == 64) {
+        if (q8) return bf16 ? launch_t<64, true, true>(p, s) : launch_t<64, false, true>(p, s);
+        return bf16 ? launch_t<64, true, false>(p, s) : launch_t<64, false, false>(p, s);
+    }
+    if (q8) return bf16 ? launch_t<128, true, true>(p, s) : launch_t<128, false, true>(p, s);
+    return bf16 ? launch_t<128, true, false>(p, s) : launch_t<128, false, false>(p, s);
+}
+
+cudaError_t launch_chunk_join(const ChunkParams& p, int D, bool bf16, cudaStream_t s) {
+    const dim3 grid((unsigned)p.grid, 8), block(256);
+    if (D == 64)
+        return bf16 ? launch_kernel_early(fa_chunk_join_kernel<64, true>, grid, block, 0, s, p)
+                    : launch_kernel_early(fa_chunk_join_kernel<64, false>, grid, block, 0, s, p);
+    return bf16 ? launch_kernel_early(fa_chunk_join_kernel<128, true>, grid, block, 0, s, p)
+                : launch_kernel_early(fa_chunk_join_kernel<128, false>, grid, block, 0, s, p);
+}
+
+}  // namespace fa

@@ -289,6 +289,31 @@ struct WindowBwdParams {
     uint64_t timeout_ns;
 };
 
+// Attention of a chunk of new tokens over a paged cache (fa_chunk.cu).
+constexpr int kChunkGrid = 152;  // CTAs at most, on any device, so that the workspace does not depend on it
+struct ChunkParams {
+    CUtensorMap tm_q;            // {D, L, Hq, B} (strided), box {64, T, group, 1}
+    CUtensorMap tm_k, tm_v;      // 16-bit caches: {D, 16, num_pages * Hk}, box {64, 16, 1}
+    const void *k_cache, *v_cache;
+    const uint8_t *k_exp, *v_exp;
+    const int *block_tables, *seq_lens;
+    const int* new_lens;         // [B], or null: L each (0 for an empty sequence)
+    void* o;                     // [B, Hq, L, D] 16-bit, strides so
+    Strides so;
+    float* lse;                  // [B, Hq, L]
+    float *slot_o, *slot_lse;    // [2 * grid, 2 * 128, D], [2 * grid, 2 * 128]: parts of cut pairs (LSE in log2)
+    int4* owners;                // [grid]: sequence, cache head, first token and parts of the pair that goes
+                                 // on behind each CTA
+    int B, Hq, Hk, L, group, num_pages, max_pages;
+    int window, sinks;           // (no window: 2^30, 0)
+    int T, max_pairs;            // tokens of a query tile, pairs of tiles of a sequence at most
+    int grid;
+    float scale_log2;            // |scale| * log2(e)
+    uint32_t s_negate;
+    int* status;
+    uint64_t timeout_ns;
+};
+
 // Host-side helpers of the C-ABI layer shared with the other entry-point units.
 // Consumes the fa_trace_next_call arming of the calling thread (every public call ends so).
 void trace_disarm();
@@ -381,6 +406,10 @@ void window_bwd_plan(WindowBwdParams* p);
 cudaError_t launch_window_dkdv(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_window_dq(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_window_join(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
+// The work split of a chunk: fills T, max_pairs, grid.
+void chunk_plan(int B, int Hk, int group, int L, int max_pages, ChunkParams* p);
+cudaError_t launch_chunk(const ChunkParams& p, int D, bool bf16, bool q8, cudaStream_t s);
+cudaError_t launch_chunk_join(const ChunkParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s);
 // Query rows of a block (8 or 16), the most warps that a step may launch (workspace), and those it
 // does (busy_sms: SMs that an earlier kernel still holds).

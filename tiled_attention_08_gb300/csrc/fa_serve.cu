@@ -7,6 +7,8 @@
 #include <cstring>
 
 #include "fa_host.h"
+#include "fa_ptx.cuh"
+#include "fa_window_sched.h"
 
 using namespace fa;
 
@@ -252,6 +254,36 @@ fa_status decode_step(const void* q, const void* k_cache, const void* v_cache, c
                    cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
+}
+
+// Sizes of a chunk's attention: as of a decode step, and the kernel's line of units in 31 bits per cache
+// head and 37 in all.
+fa_status check_chunk(int B, int Hq, int Hk, int L, int D, int num_pages, int max_pages, float scale, int dtype,
+                      int cache_dtype) {
+    if (L < 0) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_decode(B, Hq, Hk, D, num_pages, max_pages, scale, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0 || L == 0) return FA_OK;
+    if (Hq / Hk > kTileRows || L > kMaxTokens || max_pages > ((1 << 30) - 1024) / kPageTokens)
+        return FA_ERR_UNSUPPORTED;
+    ChunkParams p;
+    chunk_plan(B, Hk, Hq / Hk, L, max_pages, &p);
+    const long long line = (long long)B * p.max_pairs * (max_pages / 8 + 1);
+    if (line > 0x7fffffffLL || line * Hk > 1LL << 37) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// Workspace of a chunk's attention, in bytes from its start (the owners come first).
+struct ChunkWorkspace {
+    size_t slot_lse, slot_o, bytes;
+};
+ChunkWorkspace chunk_workspace(int grid, int D) {
+    ChunkWorkspace w;
+    const size_t rows = 2 * (size_t)grid * 2 * kTileRows;
+    w.slot_lse = (size_t)grid * 16;
+    w.slot_o = w.slot_lse + rows * 4;
+    w.bytes = w.slot_o + rows * D * 4;
+    return w;
 }
 
 }  // namespace
@@ -506,6 +538,98 @@ fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cac
     return decode_step(q, k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, o, lse, workspace,
                        workspace_bytes, B, Hq, Hk, D, num_pages, max_pages, window, sinks, scale, dtype,
                        cache_dtype, stream);
+}
+
+size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, int max_pages) {
+    if (B <= 0 || Hq <= 0 || L <= 0 || check_chunk(B, Hq, Hk, L, D, 0, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) != FA_OK)
+        return 0;
+    ChunkParams p;
+    chunk_plan(B, Hk, Hq / Hk, L, max_pages, &p);
+    return chunk_workspace(p.grid, D).bytes;
+}
+
+fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
+                             const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,
+                             const int32_t* new_lens, void* o, float* lse, void* workspace,
+                             size_t workspace_bytes, const fa_strides* strides, int B, int Hq, int Hk, int L,
+                             int D, int num_pages, int max_pages, int window, int sinks, float scale, int dtype,
+                             int cache_dtype, void* stream) {
+    TraceDisarm disarm;
+    if (window < 0 || sinks < 0) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_chunk(B, Hq, Hk, L, D, num_pages, max_pages, scale, dtype, cache_dtype);
+    if (st != FA_OK) return st;
+    if (B == 0 || Hq == 0 || L == 0) return FA_OK;
+    const bool q8 = cache_dtype == FA_CACHE_E4M3, bf16 = dtype == FA_BF16;
+    if (!q || !o || !lse || !strides || !aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(new_lens))
+        return FA_ERR_INVALID_ARG;
+    if (!cache_pointers_ok(k_cache, v_cache, k_exp, v_exp, block_tables, seq_lens, num_pages, max_pages,
+                           cache_dtype))
+        return FA_ERR_INVALID_ARG;
+    ChunkParams p;
+    std::memset(&p, 0, sizeof(p));
+    chunk_plan(B, Hk, Hq / Hk, L, max_pages, &p);
+    const ChunkWorkspace w = chunk_workspace(p.grid, D);
+    if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    Strides sq;
+    if (!take_strides(strides[0], B, Hq, &sq) || !take_strides(strides[1], B, Hq, &p.so))
+        return FA_ERR_INVALID_ARG;
+    const size_t rows = (size_t)B * Hq * L;
+    const size_t cb = cache_bytes(num_pages, Hk, D, cache_dtype), eb = q8 ? exp_bytes(num_pages, Hk) : 0;
+    const Range ins[] = {extent(q, sq, B, Hq, L, D), range(k_cache, cb), range(v_cache, cb), range(k_exp, eb),
+                         range(v_exp, eb), range(block_tables, (size_t)B * max_pages * 4u),
+                         range(seq_lens, (size_t)B * 4u), range(new_lens, new_lens ? (size_t)B * 4u : 0)};
+    const Range outs[] = {extent(o, p.so, B, Hq, L, D), range(lse, rows * 4u), range(workspace, w.bytes)};
+    for (int a = 0; a < 3; ++a) {
+        for (int i = 0; i < 8; ++i)
+            // o may be another part of one packed tensor with q.
+            if (overlap(outs[a], ins[i]) &&
+                !(a == 0 && i == 0 && packed_parts(o, p.so, Hq, q, sq, Hq, B, L, D)))
+                return FA_ERR_INVALID_ARG;
+        for (int b = a + 1; b < 3; ++b)
+            if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
+    }
+    if (!bind_context()) return FA_ERR_CUDA;
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)Hq, (cuuint64_t)B};
+    const cuuint64_t qs[3] = {(cuuint64_t)sq.l * 2, (cuuint64_t)sq.h * 2, (cuuint64_t)sq.b * 2};
+    const cuuint32_t qb[4] = {(cuuint32_t)kChunkElems, (cuuint32_t)p.T, (cuuint32_t)(Hq / Hk), 1};
+    if (!make_tiled_map(&p.tm_q, type, q, 4, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) return FA_ERR_CUDA;
+    if (!q8 && num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, false) ||
+                                 !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, false)))
+        return FA_ERR_CUDA;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_exp = static_cast<const uint8_t*>(k_exp);
+    p.v_exp = static_cast<const uint8_t*>(v_exp);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.o = o;
+    p.lse = lse;
+    p.slot_o = reinterpret_cast<float*>(ws + w.slot_o);
+    p.slot_lse = reinterpret_cast<float*>(ws + w.slot_lse);
+    p.owners = reinterpret_cast<int4*>(ws);
+    p.B = B;
+    p.Hq = Hq;
+    p.Hk = Hk;
+    p.L = L;
+    p.group = Hq / Hk;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages;
+    p.window = window == 0 ? 1 << 30 : imin(window, 1 << 30);
+    p.sinks = window == 0 ? 0 : imin(sinks, 1 << 30);
+    // (The softmax takes the maximum of the stored scores: a negative scale is moved into the
+    // contraction as an exact sign flip, and the multiplier keeps a masked -inf at -inf.)
+    p.scale_log2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
+    p.s_negate = scale < 0.0f ? 1u : 0u;
+    p.status = status_ptr();
+    p.timeout_ns = wait_timeout_ns();
+    if (!p.status) return FA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (traced_launch(0, s, [&] { return launch_chunk(p, D, bf16, q8, s); }) != cudaSuccess) return FA_ERR_CUDA;
+    return traced_launch(1, s, [&] { return launch_chunk_join(p, D, bf16, s); }) == cudaSuccess ? FA_OK
+                                                                                               : FA_ERR_CUDA;
 }
 
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,

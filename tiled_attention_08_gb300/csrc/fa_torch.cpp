@@ -685,6 +685,46 @@ std::tuple<Tensor, Tensor, Tensor> window_backward(const Tensor& q, const Tensor
     return window_bwd(q, k, v, o, lse, dout, {window, sinks, scale}, workspace, dq, dk, dv);
 }
 
+// ---------------------------------------------------------------------------------------
+// Chunks of new tokens over a paged cache
+// ---------------------------------------------------------------------------------------
+std::tuple<Tensor, Tensor> attention_paged(const Tensor& q_, const Tensor& k_cache, const Tensor& v_cache,
+                                           const Tensor& block_tables, const Tensor& seq_lens,
+                                           const OptTensor& new_lens, std::optional<int64_t> window, int64_t sinks,
+                                           std::optional<double> scale, const OptTensor& out, const OptTensor& lse,
+                                           const OptTensor& workspace, const OptTensor& k_exp,
+                                           const OptTensor& v_exp) {
+    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
+    const int index = cuda_index("q", q_);
+    TORCH_CHECK_VALUE(q_.dim() == 4, "q must be a [B, H, L, D] view");
+    const int dt = dtype_code(q_);
+    const Tensor q = kernel_view(q_);
+    const int B = as_int("B", q.size(0)), Hq = as_int("H", q.size(1)), L = as_int("L", q.size(2)),
+              D = as_int("D", q.size(3));
+    const Cache c = check_cache(k_cache, v_cache, k_exp, v_exp, q.scalar_type(), index);
+    TORCH_CHECK_VALUE(c.D == D, "the cache has heads of ", c.D, ", q of ", D);
+    const int max_pages = check_tables(block_tables, seq_lens, B, index);
+    if (given(new_lens)) int32_vector("new_lens", *new_lens, B, index);
+    TORCH_CHECK_VALUE(!window || *window >= 1, "window must be at least 1 (or None)");
+    const Tensor o = output_like("out", out, q);
+    const Tensor l = given(lse) ? *lse : at::empty({B, Hq, L}, q.options().dtype(at::kFloat));
+    const int64_t shape[3] = {B, Hq, L};
+    TORCH_CHECK_VALUE(l.scalar_type() == at::kFloat && l.sizes() == at::IntArrayRef(shape, 3) && l.is_contiguous(),
+                      "lse must be a contiguous fp32 [B, H, L] tensor");
+    same_device("lse", l, index);
+    written(lse);
+    const fa_strides st[2] = {row_strides("q", q, q.sizes()), row_strides("out", o, q.sizes())};
+    const Tensor ws = workspace_of(
+        workspace, fa_attention_paged_workspace_bytes(B, Hq, c.H, L, D, max_pages), q, index);
+    check_status("fa_attention_paged",
+                 fa_attention_paged(ptr(q), c.k, c.v, c.k_exp, c.v_exp, ptr<int32_t>(block_tables),
+                                    ptr<int32_t>(seq_lens), ptr<int32_t>(new_lens), ptr(o), ptr<float>(l), ptr(ws),
+                                    ws.nbytes(), st, B, Hq, c.H, L, D, c.num_pages, max_pages,
+                                    window ? as_span(*window) : 0, as_span(sinks), scale_of(scale, D), dt, c.kind,
+                                    stream_of(index)));
+    return {o, l};
+}
+
 PyObject* status_error_class = nullptr;
 
 }  // namespace
@@ -715,6 +755,7 @@ PYBIND11_MODULE(fa_torch, m) {
           });
     m.def("decode_shared_prefix", &decode_shared_prefix);
     m.def("attention_window", &attention_window);
+    m.def("attention_paged", &attention_paged);
     m.def("window_forward", &window_forward);
     m.def("window_backward", &window_backward);
 }
