@@ -117,14 +117,17 @@ __device__ __forceinline__ void dkdv_item(const WindowBwdParams& p, int id, Dkdv
 // of four columns lie together for all 128 rows, so that a warp's stores are contiguous.
 template <int N>
 __device__ __forceinline__ void part_out(uint32_t taddr, float* dst, int slice, int row) {
-    uint32_t r[N];
-    tmem_ld<N>(taddr, r);
     float4* d = reinterpret_cast<float4*>(dst) + (size_t)slice * (N / 4) * kTileRows + row;
+#pragma unroll 1
+    for (int h = 0; h < N; h += 16) {
+        uint32_t r[16];
+        tmem_ld16(taddr + h, r);
 #pragma unroll
-    for (int c = 0; c < N / 4; ++c)
-        d[(size_t)c * kTileRows] =
-            make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]),
-                        __uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
+        for (int c = 0; c < 4; ++c)
+            d[(size_t)(h / 4 + c) * kTileRows] =
+                make_float4(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1]),
+                            __uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3]));
+    }
 }
 
 // dK and dV.
@@ -426,24 +429,27 @@ __global__ void __launch_bounds__(DkdvCfg<D, BF16>::kThreads, 1)
         bool ok = true;
         int u = 0;                 // query tiles of earlier items
         uint32_t done_par = 0u;    // phase of the item's done barrier
-        DkdvItem it;
         for (int round = 0; ok; ++round) {
             // The quadrant's warps agree on the outcome before any of them goes on: they meet
             // at named barriers below.
-            const int id = queue_pop_warp(bars.queue, round, abort_v, p.timeout_ns);
+            int id = queue_pop_warp(bars.queue, round, abort_v, p.timeout_ns);
             ok = bar_and(grp_bar, kGrpThreads, id != -2);
             if (!ok || id < 0) break;
-            dkdv_item(p, id, it);
-            const int key = it.kt * kTileRows + row;
-            const int u_end = u + it.n_it;
-            const int off = p.Lk - p.Lq;
-            // Query at position t sees this thread's key iff key <= t < key + window, or t >= key for a
-            // first token.
-            const int seen_until = key < p.sinks ? 1 << 30 : key + p.window;
-            Unit un = it.first;
-            for (int uu = u; uu < u_end; ++uu) {
-                const int qi = un.qi;
-                un.step(it);
+            // The loop is at the limit of 96 registers: it keeps of the item no more than it needs, in units
+            // of the tile's key offset (keys and positions relative to the tile's first query row).
+            int key, qi, q_lo, q_hi, u_end;
+            {
+                DkdvItem it;
+                dkdv_item(p, id, it);
+                key = it.kt * kTileRows + row;
+                qi = it.first.qi;
+                q_lo = it.q.lo;
+                q_hi = it.q.hi;
+                u_end = u + it.n_it;
+            }
+            const bool empty = u_end == u;
+            for (; u < u_end; ++u) {
+                const int uu = u;
                 const int qs = uu % C::kQStages, os = uu % C::kOStages;  // ring slots of Q, dO
                 const uint32_t qph = (uint32_t)(uu / C::kQStages) & 1u;
                 const uint32_t oph = (uint32_t)(uu / C::kOStages) & 1u;
@@ -451,10 +457,12 @@ __global__ void __launch_bounds__(DkdvCfg<D, BF16>::kThreads, 1)
                 const uint32_t nlse2_addr =
                     smem_u32(smem + C::kOffNlse + qs * C::kVecBytes) + c0 * 4;
                 const uint32_t dlt_addr = smem_u32(smem + C::kOffDelta + os * C::kVecBytes) + c0 * 4;
-                const int q0 = qi * kTileRows + c0;
-                const int key0w = key - lane;
-                const bool masked = hides_later(key0w, 32, q0 + off) || q0 + kC > p.Lq ||
-                                    hides_earlier(key0w, 32, q0 + kC - 1 + off, p.window, p.sinks);
+                // This warp's first query row, and its position; a query at position t sees this thread's
+                // key iff key <= t < key + window, or t >= key for a first token.
+                const int q0 = qi * kTileRows + c0, t0 = q0 + (p.Lk - p.Lq);
+                if (++qi == q_hi) qi = q_lo;
+                const bool masked = hides_later(key - lane, 32, t0) || q0 + kC > p.Lq ||
+                                    hides_earlier(key - lane, 32, t0 + kC - 1, p.window, p.sinks);
                 // Phase 1: P^T = exp2(S^T * scale*log2e - LSE*log2e) on this warp's columns;
                 // kept in registers, and the S^T columns are released at once.
                 ok = wait_bounded(&bar_qf[qs], qph, abort_v, p.timeout_ns) &&
@@ -484,7 +492,8 @@ __global__ void __launch_bounds__(DkdvCfg<D, BF16>::kThreads, 1)
                         pv[i + 3] = ex2_approx(y3);
                     }
                     if (masked) {
-                        const int from = key - off - q0, until = imin(seen_until - off, p.Lq) - q0;
+                        const int from = key - t0;
+                        const int until = imin(key < p.sinks ? kC : from + p.window, p.Lq - q0);
 #pragma unroll
                         for (int i = 0; i < kC; ++i)
                             if (i < from || i >= until) pv[i] = 0.0f;
@@ -536,12 +545,15 @@ __global__ void __launch_bounds__(DkdvCfg<D, BF16>::kThreads, 1)
                 mbar_arrive(&bar_ppd);
             }
             if (!ok) break;
+            asm volatile("" : "+r"(id));  // (decoded anew: nothing of the item lives through the loop)
+            DkdvItem it;
+            dkdv_item(p, id, it);
             const int key0 = key - lane;
             const size_t coff = (size_t)part * C::kOutCols * 2;
             const int bhk = it.b * p.Hk + it.hk;
             uint8_t* dv0 = reinterpret_cast<uint8_t*>(p.dv) + row_offset(p.sdv, bhk, p.Hk, key0) + coff;
             uint8_t* dk0 = reinterpret_cast<uint8_t*>(p.dk) + row_offset(p.sdk, bhk, p.Hk, key0) + coff;
-            if (it.n_it == 0) {
+            if (empty) {
                 if (it.part < 0 && key < p.Lk) {  // a row per lane: rare
 #pragma unroll
                     for (int c = 0; c < C::kOutCols / 8; ++c) {
@@ -572,7 +584,6 @@ __global__ void __launch_bounds__(DkdvCfg<D, BF16>::kThreads, 1)
                     tmem + lane_off + C::kTmDK + part * C::kOutCols, dk0, (size_t)p.sdk.l * 2u, p.Lk - key0,
                     p.scale, lane);
             }
-            u = u_end;
         }
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
     }
