@@ -280,7 +280,8 @@ struct WindowBwdParams {
     int window, sinks;
     int q_first;                         // query tiles in front of it see no key
     int sched_group_k, sched_group_q;    // heads per schedule group of the two passes
-    int split_tiles, parts;              // the first split_tiles key tiles are cut into parts ...
+    int split_tiles, parts;              // the first split_tiles key tiles of every head come first, cut into
+                                         // parts where there is more than one ...
     float* part;                         // ... [B*Hk, split_tiles, parts, 2 (dK, dV), D/4, 128, 4]
     int dkdv_items;
     float scale, scale_log2;

@@ -50,11 +50,17 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, int B, int H, int L, int D, 
                           dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Heads per schedule group (tile_coords): the rows that the group's items stream at a time, `bytes` per
-// head, take at most this much of L2.
-int sched_group(long long bytes, int heads) {
-    const long long g = (48LL << 20) / (bytes > 0 ? bytes : 1);
-    return (int)(g < 1 ? 1 : g > heads ? heads : g);
+// Key heads per schedule group (tile_coords).  The items that run at the same time, one per SM, are some
+// consecutive tiles of every head of a group; what they stream is `span` rows of a head and one more tile of
+// them for each further tile, `row_bytes` each.  As many heads as keep that within kStreamed of L2.
+constexpr long long kStreamed = 48LL << 20;
+int sched_group(int row_bytes, int span, int len, int items_per_tile, int heads) {
+    for (int g = heads; g > 1; g = g > 2 * kWindowSms ? g / 2 : g - 1) {
+        const int at_once = imin(g, kWindowSms), tiles = kWindowSms / (g * items_per_tile);
+        const long long rows = imin(len, span + kTileRows * (tiles < 1 ? 1 : tiles));
+        if (at_once * rows * row_bytes <= kStreamed) return g;
+    }
+    return 1;
 }
 
 // The plan of the backward pass and its workspace: the two vectors, the parts, the counters.
@@ -75,7 +81,7 @@ size_t bwd_plan(const Shape& sh, int B, int Hq, int Hk, int Lq, int Lk, int D, W
     window_bwd_plan(p);
     *part_at = 2u * (size_t)B * Hq * sh.Lqpad * 4u;
     *sched_at = *part_at +
-                (p->split_tiles ? (size_t)B * Hk * p->split_tiles * p->parts * 2u * kTileRows * D * 4u : 0u);
+                (p->parts > 1 ? (size_t)B * Hk * p->split_tiles * p->parts * 2u * kTileRows * D * 4u : 0u);
     return *sched_at + kSchedBytes;
 }
 
@@ -133,8 +139,8 @@ fa_status fa_window_fwd(const void* q, const void* k, const void* v, void* o, fl
     p.columns = p.head_pairs ? B * (Hq / 2) : B * Hq;
     p.rows = p.head_pairs ? sh.n_qtiles : (sh.n_qtiles + 1) / 2;
     const int per_key_head = p.columns / (B * Hk);
-    const long long span = imin(Lk, sh.window + sh.sinks + 2 * kTileRows);
-    p.sched_group = imin(sched_group(4 * span * D, B * Hk) * per_key_head, p.columns);
+    const int span = imin(Lk, sh.window + sh.sinks + kTileRows);
+    p.sched_group = per_key_head * sched_group(4 * D, span, Lk, per_key_head, B * Hk);
     // (The softmax takes the maximum of the stored scores: a negative scale is moved into the
     // contraction as an exact sign flip, and the multiplier keeps a masked -inf at -inf.)
     p.scale_log2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, FLT_MIN);
@@ -227,9 +233,9 @@ fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void*
     p.sdq = s8[5];
     p.sdk = s8[6];
     p.sdv = s8[7];
-    const long long span = imin(Lk, sh.window + sh.sinks + 2 * kTileRows);
-    p.sched_group_k = sched_group(4 * imin(Lq, (int)span) * (long long)D * (Hq / Hk), B * Hk);
-    p.sched_group_q = imin(sched_group(4 * span * D, B * Hk) * (Hq / Hk), B * Hq);
+    const int group = Hq / Hk, span = imin(Lk, sh.window + sh.sinks + kTileRows);
+    p.sched_group_k = sched_group(4 * D * group, sh.window + kTileRows, Lq, 1, B * Hk);
+    p.sched_group_q = group * sched_group(4 * D, span, Lk, group, B * Hk);
     p.part = reinterpret_cast<float*>(ws + part_at);
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -262,7 +268,7 @@ fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void*
     if (traced_launch(n++, s, [&] { return launch_bwd_pre(pp, s); }) != cudaSuccess ||
         traced_launch(n++, s, [&] { return launch_window_dkdv(p, D, bf16, s); }) != cudaSuccess)
         return FA_ERR_CUDA;
-    if (p.split_tiles > 0 &&
+    if (p.parts > 1 &&
         traced_launch(n++, s, [&] { return launch_window_join(p, D, bf16, s); }) != cudaSuccess)
         return FA_ERR_CUDA;
     return traced_launch(n++, s, [&] { return launch_window_dq(p, D, bf16, s); }) == cudaSuccess ? FA_OK

@@ -90,13 +90,13 @@ __device__ __forceinline__ void dkdv_item(const WindowBwdParams& p, int id, Dkdv
     const int heads = p.B * p.Hk, cut = heads * p.split_tiles * p.parts;
     int bhk, i = 0, n = 1;
     it.part = -1;
-    if (id < cut) {  // the parts of the first tokens' tiles first: none is smaller than a window's item
+    if (id < cut) {  // the first tokens' tiles (or their parts) first: none is smaller than a window's item
         const int rest = id / heads;
         bhk = id - rest * heads;
         it.kt = rest / p.parts;
         i = rest - it.kt * p.parts;
         n = p.parts;
-        it.part = (bhk * p.split_tiles + it.kt) * p.parts + i;
+        if (n > 1) it.part = (bhk * p.split_tiles + it.kt) * p.parts + i;
     } else {
         tile_coords(id - cut, heads, p.n_ktiles - p.split_tiles, p.sched_group_k, bhk, it.kt);
         it.kt += p.split_tiles;
@@ -1101,12 +1101,8 @@ void window_bwd_plan(WindowBwdParams* p) {
     const long long all = (long long)heads * ((long long)n_sink * heavy + (long long)(p->n_ktiles - n_sink) * usual);
     const long long share = (all + 2 * kWindowSms - 1) / (2 * kWindowSms);
     const int most = (int)(share > usual ? share : usual);
-    p->split_tiles = 0;
-    p->parts = 1;
-    if (n_sink > 0 && 2LL * heavy > 3LL * most) {
-        p->split_tiles = n_sink;
-        p->parts = (heavy + most - 1) / most;
-    }
+    p->split_tiles = 2LL * heavy > 3LL * usual ? n_sink : 0;
+    p->parts = p->split_tiles > 0 && 2LL * heavy > 3LL * most ? (heavy + most - 1) / most : 1;
     p->dkdv_items = heads * (p->split_tiles * p->parts + p->n_ktiles - p->split_tiles);
 }
 
