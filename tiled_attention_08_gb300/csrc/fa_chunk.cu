@@ -44,21 +44,27 @@ struct ChunkCfg {
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 2 * kTileBytes;
     static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    static constexpr int kStageBytes = 32 * 64 * 2;     // read-out buffer of one softmax warp
-    static constexpr int kOffStage = kOffV + kStages * kTileBytes;
-    static constexpr int kSmemBytes = kOffStage + 8 * kStageBytes + 1024;
-    static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;  // (e4m3: the K warp loads queries alone)
+    // e4m3: pieces of 64 tokens as bytes on their way to the converters, K and V in turn, 32 KB of them, and
+    // their exponents.
+    static constexpr int kPieceRows = 64;
+    static constexpr int kPieceBytes = kPieceRows * D;
+    static constexpr int kPieces = Q8 ? 32768 / kPieceBytes : 0;
+    static constexpr int kOffRaw = kOffV + kStages * kTileBytes;
+    static constexpr int kOffExp = kOffRaw + kPieces * kPieceBytes;
+    static constexpr int kSmemBytes = kOffExp + kPieces * kPieceRows + 1024;
+    static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;  // (e4m3: queries, the cache's bytes)
     static constexpr int kConvWarp = 12;                         // the first of four converter warps
-    static constexpr int kConvThreads = 128;
-    static constexpr int kThreads = Q8 ? 16 * 32 : 11 * 32;
-    // e4m3: registers per thread of the softmax warps, of warps 8-11 and of the converters; 128 at
-    // launch, and 2 * 168 + 64 + 112 = 4 * 128.
-    static constexpr int kRegsSoftmax = 168, kRegsIssue = 64, kRegsConv = 112;
-    static_assert(2 * kRegsSoftmax + kRegsIssue + kRegsConv == 4 * 128, "the launch's registers");
+    static constexpr int kThreads = Q8 ? 16 * 32 : 12 * 32;
+    // Registers per thread of the softmax warps, of warps 8-11 and of the converters.  At launch each
+    // thread has kRegs; the sums over the warpgroups are the same.
+    static constexpr int kRegs = Q8 ? 128 : 168;
+    static constexpr int kRegsSoftmax = Q8 ? 176 : 208, kRegsIssue = 88, kRegsConv = 72;
+    static_assert(2 * kRegsSoftmax + kRegsIssue + (Q8 ? kRegsConv : 0) == kThreads / 128 * kRegs,
+                  "the launch's registers");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kTmS = 0, kTmO = 256;
     static_assert(kTmO + 2 * D <= kTmemCols, "TMEM budget");
-    static_assert(kSmemBytes <= 232448 - 1024, "shared memory over the 227 KB per-block limit");
+    static_assert(kSmemBytes <= 232448 - 768, "shared memory over the 227 KB per-block limit");
     static constexpr uint32_t kIdescS = idesc_f16(BF16, 128, 128, false, false);
     static constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, false, true);
 };
@@ -70,6 +76,34 @@ __device__ __forceinline__ void regs_raise() {
 template <int N>
 __device__ __forceinline__ void regs_lower() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Every lane of a warp holds a row's 128 bytes, 8 units of 16, bound for dst (null: not written).  The units
+// are transposed in groups of eight lanes (a butterfly of xor shuffles; see tmem_rows_to_global_xpose), so that
+// each store instruction writes 128 contiguous bytes of four rows.
+__device__ __forceinline__ void rows_out(uint32_t (&m)[8][4], uint8_t* dst, int lane) {
+#pragma unroll
+    for (int s = 4; s >= 1; s /= 2) {
+        const bool upper = (lane & s) != 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e & s) continue;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t send = upper ? m[e][k] : m[e | s][k];
+                const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, s);
+                if (upper) m[e][k] = recv;
+                else m[e | s][k] = recv;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {  // unit lane % 8 of row 8 (lane / 8) + e
+        uint8_t* d = reinterpret_cast<uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), (lane & 24) + e));
+        if (d)
+            *reinterpret_cast<uint4*>(d + (lane & 7) * 16) = make_uint4(m[e][0], m[e][1], m[e][2], m[e][3]);
+    }
 }
 
 // New tokens of sequence b and the tokens in front of them; none where the lengths are out of range.
@@ -181,6 +215,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                                ~uintptr_t(1023));
     __shared__ uint64_t bar_qf, bar_qe, bar_kf[C::kStages], bar_ke[C::kStages], bar_vf[C::kStages],
         bar_ve[C::kStages], bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint64_t bar_rf[Q8 ? C::kPieces : 1], bar_re[Q8 ? C::kPieces : 1];  // pieces landed / read
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ int warp_sum[C::kThreads / 32];
@@ -192,7 +227,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         if (p.num_pages > 0) tma_prefetch_desc(&p.tm_q);
-        if (!Q8 && p.num_pages > 0) {
+        if (p.num_pages > 0) {
             tma_prefetch_desc(&p.tm_k);
             tma_prefetch_desc(&p.tm_v);
         }
@@ -201,15 +236,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         mbar_init(&bar_qf, 1);
         mbar_init(&bar_qe, 1);
         for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&bar_kf[s], Q8 ? C::kConvThreads : 1);
+            mbar_init(&bar_kf[s], Q8 ? 4 : 1);  // (a converter warp each)
             mbar_init(&bar_ke[s], 1);
-            mbar_init(&bar_vf[s], Q8 ? C::kConvThreads : 1);
+            mbar_init(&bar_vf[s], Q8 ? 4 : 1);
             mbar_init(&bar_ve[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar_sf[t], 1);
             mbar_init(&bar_pf[t], 128);
             mbar_init(&bar_oready[t], 1);
+        }
+        for (int s = 0; s < C::kPieces; ++s) {
+            mbar_init(&bar_rf[s], 1);
+            mbar_init(&bar_re[s], 4);
         }
         mbar_init(&bar_fin, 1);
         mbar_fence_init();
@@ -283,9 +322,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     const uint32_t tmem = tmem_base_sh;
     Walk walk = start_sh;
 
-    // (e4m3: each warpgroup sets its registers at the head of its branch, with one instruction)
+    // (Each warpgroup sets its registers at the head of its branch, with one instruction.)
     if (warp >= 8 && warp < C::kConvWarp) {
-    if constexpr (Q8) regs_lower<C::kRegsIssue>();
+    regs_lower<C::kRegsIssue>();
     if (warp == C::kKWarp || (!Q8 && warp == C::kVWarp)) {
         // ------------------------------ TMA producers ------------------------------
         // The K warp brings each segment's query pair, and K's pages of a 16-bit cache; the V warp V's.
@@ -354,6 +393,67 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         if (is_k && n_seg > 0) wait_bounded(&bar_qf, (uint32_t)(n_seg - 1) & 1u, nullptr, p.timeout_ns);
         for (int g = issued - 1; g >= 0 && g >= issued - C::kStages; --g)
             wait_bounded(&full[g % C::kStages], (uint32_t)(g / C::kStages) & 1u, nullptr, p.timeout_ns);
+    } else if (Q8 && warp == C::kVWarp) {
+        // ------------------------------ the cache's bytes ------------------------------
+        // Pieces K lo, K hi, V lo, V hi of each tile; lane i issues page i of a piece and its exponents.
+        if constexpr (Q8) {
+            bool ok = true;
+            int issued = 0;
+            Segment sg;
+            for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+                const Live live = live_of(p, sg);
+                auto entry = [&](int j) {  // page `lane` of tile j, or -1: nothing of it counts
+                    const int pg = sg.all.tile(j) * kPagesPerTile + lane;
+                    if (lane >= kPagesPerTile || !live.any(pg * kPageTokens, kPageTokens)) return -1;
+                    const int page = p.block_tables[(size_t)sg.b * p.max_pages + pg];
+                    if (page < 0 || page >= p.num_pages) {
+                        atomicCAS(p.status, 0, (int)kDevBadArg);
+                        return -1;
+                    }
+                    return page;
+                };
+                int next = entry(sg.j0);
+                for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j) {
+                    const int pages = next;
+                    if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
+#pragma unroll
+                    for (int piece = 0; piece < 4; ++piece) {
+                        const int st = issued % C::kPieces;
+                        if (issued >= C::kPieces) {
+                            ok = wait_warp(&bar_re[st], ((uint32_t)(issued / C::kPieces) & 1u) ^ 1u, abort_v,
+                                           p.timeout_ns);
+                            if (!ok) break;
+                        }
+                        const int page = __shfl_sync(0xffffffffu, pages, (piece & 1) * 4 + (lane & 3));
+                        const uint32_t there = __ballot_sync(0xffffffffu, lane < 4 && page >= 0);
+                        if (lane < 4 && page < 0) {  // no page: zeros, whose exponents are finite
+                            sts_u32x4(smem_u32(smem + C::kOffExp + st * C::kPieceRows + lane * kPageTokens),
+                                      make_uint4(0u, 0u, 0u, 0u));
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&bar_rf[st], C::kPieceBytes + __popc(there) * kPageTokens);
+                        __syncwarp();
+                        if (lane < 4) {
+                            const size_t ph = page < 0 ? 0 : (size_t)page * p.Hk + sg.hk;
+                            tma_load_3d(smem + C::kOffRaw + st * C::kPieceBytes + lane * (kPageTokens * D),
+                                        piece < 2 ? &p.tm_k : &p.tm_v, &bar_rf[st], 0, page < 0 ? kPageTokens : 0,
+                                        (int)ph);
+                            if (page >= 0)
+                                bulk_load(smem + C::kOffExp + st * C::kPieceRows + lane * kPageTokens,
+                                          (piece < 2 ? p.k_exp : p.v_exp) + ph * kPageTokens, kPageTokens,
+                                          &bar_rf[st]);
+                        }
+                        __syncwarp();
+                        ++issued;
+                    }
+                }
+            }
+            if (!ok && lane == 0) record_timeout(p.status, abort_v);
+            for (int g = issued - 1; g >= 0 && g >= issued - C::kPieces; --g)
+                wait_bounded(&bar_rf[g % C::kPieces], (uint32_t)(g / C::kPieces) & 1u, nullptr, p.timeout_ns);
+        }
     } else if (warp == C::kMmaWarp) {
         // ------------------------------ MMA issuer ------------------------------
         bool ok = true;
@@ -453,108 +553,77 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     }
     } else if (Q8 && warp >= C::kConvWarp) {
         // ------------------------------ converters ------------------------------
-        // Thread i takes 16-byte units i % 4 (+ 4 for the second chunk) of rows i / 4 + 32 k: eight lanes
-        // write all eight 16-byte places of a line of banks.  The next K tile's bytes are in flight while
-        // V is converted, and the other way round.
+        // Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of row q ^ 5b of eight rows: the eight lanes of a
+        // shared-memory access then read and write all eight 16-byte places of a line of banks.
         if constexpr (Q8) {
             regs_lower<C::kRegsConv>();
-            constexpr int kRows = 4, kUnits = kRows * C::kChunks;
-            const int tid = (warp - C::kConvWarp) * 32 + lane, unit = tid & 3, row0 = tid >> 2;
-            struct Bytes {
-                uint4 x[kUnits];
-                uint32_t e;  // exponent byte of each of the four rows (of a row that does not count: 0, with zeros)
-            };
-            auto load = [&](const Segment& sg, const Live& live, int j, bool v, Bytes& r) {
-                const uint8_t* cache = static_cast<const uint8_t*>(v ? p.v_cache : p.k_cache);
-                const uint8_t* ex = v ? p.v_exp : p.k_exp;
-                const int key0 = sg.all.tile(j) * kTileRows;
-                r.e = 0;
+            const int unit = lane & 3, row_in = (warp - C::kConvWarp) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
+            bool ok = true;
+            int g = 0, piece = 0;  // tiles and pieces so far
+            auto convert = [&](const Live& live, int key0, uint8_t* tile) {
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int st = piece % C::kPieces;
+                    ok = wait_warp(&bar_rf[st], (uint32_t)(piece / C::kPieces) & 1u, abort_v, p.timeout_ns);
+                    if (!ok) return;
+                    const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
+                    const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
+                    const bool all = live.every(key0 + hf * 64, 64);
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const int token = key0 + row0 + 32 * k;
-                    bool there = live.token(token);
-                    size_t at = 0;
-                    if (there) {
-                        const int page = p.block_tables[(size_t)sg.b * p.max_pages + token / kPageTokens];
-                        there = page >= 0 && page < p.num_pages;
-                        if (!there) atomicCAS(p.status, 0, (int)kDevBadArg);
-                        else at = ((size_t)page * p.Hk + sg.hk) * kPageTokens + token % kPageTokens;
+                    for (int k = 0; k < 2; ++k) {
+                        const int r = row_in + 32 * k, row = hf * 64 + r;
+                        const float f = row_scale(ex[r]);
+                        const bool there = all || live.token(key0 + row);
+#pragma unroll
+                        for (int c = 0; c < C::kChunks; ++c) {
+                            const uint32_t at = D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                                                         : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16;
+                            const uint4 x = lds_u32x4(at);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            uint32_t y[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const float2 a = unpack2<false>(e4m3x2_to_f16x2(h ? w[i] >> 16 : w[i] & 0xffffu));
+                                    y[2 * i + h] = there ? pack2<BF16>(a.x * f, a.y * f) : 0u;
+                                }
+                            const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
+                            sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
+                                      make_uint4(y[0], y[1], y[2], y[3]));
+                            sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
+                                      make_uint4(y[4], y[5], y[6], y[7]));
+                        }
                     }
-#pragma unroll
-                    for (int c = 0; c < C::kChunks; ++c)
-                        r.x[k * C::kChunks + c] =
-                            there ? *reinterpret_cast<const uint4*>(cache + at * D + c * 64 + unit * 16)
-                                  : make_uint4(0u, 0u, 0u, 0u);
-                    if (there) r.e |= (uint32_t)ex[at] << (8 * k);
-                }
-            };
-            auto store = [&](const Bytes& r, uint8_t* tile) {
-#pragma unroll
-                for (int k = 0; k < kRows; ++k) {
-                    const int row = row0 + 32 * k;
-                    const float f = row_scale(r.e >> (8 * k) & 0xffu);
-#pragma unroll
-                    for (int c = 0; c < C::kChunks; ++c) {
-                        const uint4& x = r.x[k * C::kChunks + c];
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t y[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float2 a = unpack2<false>(
-                                    e4m3x2_to_f16x2(h ? w[i] >> 16 : w[i] & 0xffffu));
-                                y[2 * i + h] = pack2<BF16>(a.x * f, a.y * f);
-                            }
-                        const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
-                        sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4), make_uint4(y[0], y[1], y[2], y[3]));
-                        sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
-                                  make_uint4(y[4], y[5], y[6], y[7]));
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_re[st]);
+                    ++piece;
                 }
                 fence_proxy_async_smem();
+                __syncwarp();
             };
-            bool ok = true;
-            int g = 0;
             Segment sg;
-            Bytes kb, vb;
-            Live live;
-            int j = 0;
-            bool more = segment_at(p, walk, sg);
-            if (more) {
-                live = live_of(p, sg);
-                j = sg.j0;
-                load(sg, live, j, false, kb);
-                load(sg, live, j, true, vb);
-            }
-            while (ok && more) {
-                const int st = g % C::kStages;
-                const uint32_t ph = ((uint32_t)(g / C::kStages) & 1u) ^ 1u;
-                if (g >= C::kStages) ok = wait_warp(&bar_ke[st], ph, abort_v, p.timeout_ns);
-                if (!ok) break;
-                store(kb, smem + C::kOffK + st * C::kTileBytes);
-                mbar_arrive(&bar_kf[st]);
-                if (++j == sg.j0 + sg.n) {  // the next tile, perhaps of another segment
-                    step(p, sg, walk);
-                    more = segment_at(p, walk, sg);
-                    if (more) {
-                        live = live_of(p, sg);
-                        j = sg.j0;
-                    }
+            for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+                const Live live = live_of(p, sg);
+                for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j) {
+                    const int key0 = sg.all.tile(j) * kTileRows, st = g % C::kStages;
+                    const uint32_t ph = ((uint32_t)(g / C::kStages) & 1u) ^ 1u;
+                    if (g >= C::kStages) ok = wait_warp(&bar_ke[st], ph, abort_v, p.timeout_ns);
+                    if (ok) convert(live, key0, smem + C::kOffK + st * C::kTileBytes);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&bar_kf[st]);
+                    if (g >= C::kStages) ok = wait_warp(&bar_ve[st], ph, abort_v, p.timeout_ns);
+                    if (ok) convert(live, key0, smem + C::kOffV + st * C::kTileBytes);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&bar_vf[st]);
+                    ++g;
                 }
-                if (more) load(sg, live, j, false, kb);
-                if (g >= C::kStages) ok = wait_warp(&bar_ve[st], ph, abort_v, p.timeout_ns);
-                if (!ok) break;
-                store(vb, smem + C::kOffV + st * C::kTileBytes);
-                mbar_arrive(&bar_vf[st]);
-                if (more) load(sg, live, j, true, vb);
-                ++g;
             }
             if (!ok && lane == 0) record_timeout(p.status, abort_v);
         }
     } else {
         // ------------------------------ softmax warps ------------------------------
-        if constexpr (Q8) regs_raise<C::kRegsSoftmax>();
+        regs_raise<C::kRegsSoftmax>();
         const int t = warp / 4, quad = warp % 4;
         const int row = quad * 32 + lane;  // row inside the tile == TMEM lane
         const int head = row / p.T, tok = row - head * p.T;
@@ -562,7 +631,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         const uint32_t s_addr = tmem + lane_off + C::kTmS + 128 * t;
         const uint32_t o_addr = tmem + lane_off + C::kTmO + D * t;
         const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
-        const uint32_t stage = smem_u32(smem + C::kOffStage + warp * C::kStageBytes);
         bool ok = true, cut_behind = false;
         int ps = 0, n_done = 0;
         Segment sg;
@@ -667,62 +735,33 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                            row_offset(p.so, (int)orow, p.Hq, i)
                                      : nullptr;
                 if (cnt > 0) {
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 64; ++c) {
+                        uint32_t m[8][4];
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             uint32_t r[32];
                             tmem_ld32(o_addr + 64 * c + 32 * hf, r);
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = pack2<BF16>(__uint_as_float(r[8 * v + 2 * e]) * inv_l,
-                                                       __uint_as_float(r[8 * v + 2 * e + 1]) * inv_l);
-                                sts_u32x4(stage + lane * 128 + (((4 * hf + v) ^ (lane & 7)) << 4),
-                                          make_uint4(w[0], w[1], w[2], w[3]));
-                            }
+                            for (int e = 0; e < 16; ++e)
+                                m[4 * hf + e / 4][e % 4] = pack2<BF16>(__uint_as_float(r[2 * e]) * inv_l,
+                                                                       __uint_as_float(r[2 * e + 1]) * inv_l);
                         }
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int rr = 4 * k + (lane >> 3), uu = lane & 7;
-                            const uint4 w = lds_u32x4(stage + rr * 128 + ((uu ^ (rr & 7)) << 4));
-                            uint8_t* d = reinterpret_cast<uint8_t*>(
-                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
-                            if (d) *reinterpret_cast<uint4*>(d + c * 128 + uu * 16) = w;
-                        }
-                        __syncwarp();
+                        rows_out(m, dst ? dst + c * 128 : nullptr, lane);
                     }
                 }
             } else {
                 if (valid) p.slot_lse[part] = cnt > 0 ? lse2 : -INFINITY;
                 if (cnt > 0) {
                     float* dst = valid ? p.slot_o + part * D : nullptr;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
-                        uint32_t r[32];
+                        uint32_t r[32], m[8][4];
                         tmem_ld32(o_addr + 32 * c, r);
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) {
-                            uint4 w;
-                            w.x = __float_as_uint(__uint_as_float(r[4 * v + 0]) * inv_l);
-                            w.y = __float_as_uint(__uint_as_float(r[4 * v + 1]) * inv_l);
-                            w.z = __float_as_uint(__uint_as_float(r[4 * v + 2]) * inv_l);
-                            w.w = __float_as_uint(__uint_as_float(r[4 * v + 3]) * inv_l);
-                            sts_u32x4(stage + lane * 128 + ((v ^ (lane & 7)) << 4), w);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int rr = 4 * k + (lane >> 3), uu = lane & 7;
-                            const uint4 w = lds_u32x4(stage + rr * 128 + ((uu ^ (rr & 7)) << 4));
-                            float* d = reinterpret_cast<float*>(
-                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
-                            if (d) *reinterpret_cast<uint4*>(d + c * 32 + uu * 4) = w;
-                        }
-                        __syncwarp();
+                        for (int e = 0; e < 32; ++e)
+                            m[e / 4][e % 4] = __float_as_uint(__uint_as_float(r[e]) * inv_l);
+                        rows_out(m, dst ? reinterpret_cast<uint8_t*>(dst + c * 32) : nullptr, lane);
                     }
                 }
             }

@@ -294,8 +294,8 @@ struct WindowBwdParams {
 constexpr int kChunkGrid = 152;  // CTAs at most, on any device, so that the workspace does not depend on it
 struct ChunkParams {
     CUtensorMap tm_q;            // {D, L, Hq, B} (strided), box {64, T, group, 1}
-    CUtensorMap tm_k, tm_v;      // 16-bit caches: {D, 16, num_pages * Hk}, box {64, 16, 1}
-    const void *k_cache, *v_cache;
+    CUtensorMap tm_k, tm_v;      // {D, 16, num_pages * Hk}: a box is a page's rows of one head, 128 bytes of
+                                 // each at most
     const uint8_t *k_exp, *v_exp;
     const int *block_tables, *seq_lens;
     const int* new_lens;         // [B], or null: L each (0 for an empty sequence)

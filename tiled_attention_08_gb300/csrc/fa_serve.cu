@@ -594,12 +594,10 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
     const cuuint64_t qs[3] = {(cuuint64_t)sq.l * 2, (cuuint64_t)sq.h * 2, (cuuint64_t)sq.b * 2};
     const cuuint32_t qb[4] = {(cuuint32_t)kChunkElems, (cuuint32_t)p.T, (cuuint32_t)(Hq / Hk), 1};
     if (!make_tiled_map(&p.tm_q, type, q, 4, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B)) return FA_ERR_CUDA;
-    if (!q8 && num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, false) ||
-                                 !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, false)))
+    if (num_pages > 0 && (!make_cache_map(&p.tm_k, k_cache, num_pages, Hk, D, dtype, q8) ||
+                          !make_cache_map(&p.tm_v, v_cache, num_pages, Hk, D, dtype, q8)))
         return FA_ERR_CUDA;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.k_cache = k_cache;
-    p.v_cache = v_cache;
     p.k_exp = static_cast<const uint8_t*>(k_exp);
     p.v_exp = static_cast<const uint8_t*>(v_exp);
     p.block_tables = block_tables;
