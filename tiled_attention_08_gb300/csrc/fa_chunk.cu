@@ -569,25 +569,38 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                     const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
                     const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
                     const bool all = live.every(key0 + hf * 64, 64);
+                    // (All reads first: they and the writes keep their order.)
+                    uint4 x[2][C::kChunks];
+                    uint64_t f2[2];
+                    bool there[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int r = row_in + 32 * k, row = hf * 64 + r;
+                        const int r = row_in + 32 * k;
+#pragma unroll
+                        for (int c = 0; c < C::kChunks; ++c)
+                            x[k][c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                                                         : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
                         const float f = row_scale(ex[r]);
-                        const bool there = all || live.token(key0 + row);
+                        f2[k] = f2_make(f, f);
+                        there[k] = all || live.token(key0 + hf * 64 + r);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_re[st]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int row = hf * 64 + row_in + 32 * k;
 #pragma unroll
                         for (int c = 0; c < C::kChunks; ++c) {
-                            const uint32_t at = D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
-                                                         : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16;
-                            const uint4 x = lds_u32x4(at);
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                            const uint32_t w[4] = {x[k][c].x, x[k][c].y, x[k][c].z, x[k][c].w};
                             uint32_t y[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const float2 a = unpack2<false>(e4m3x2_to_f16x2(h ? w[i] >> 16 : w[i] & 0xffffu));
-                                    y[2 * i + h] = there ? pack2<BF16>(a.x * f, a.y * f) : 0u;
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                const float2 a =
+                                    unpack2<false>(e4m3x2_to_f16x2(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu));
+                                float lo, hi;
+                                f2_split(f2_mul(f2_make(a.x, a.y), f2[k]), lo, hi);
+                                y[i] = there[k] ? pack2<BF16>(lo, hi) : 0u;
+                            }
                             const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
                             sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
                                       make_uint4(y[0], y[1], y[2], y[3]));
@@ -595,8 +608,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                       make_uint4(y[4], y[5], y[6], y[7]));
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_re[st]);
                     ++piece;
                 }
                 fence_proxy_async_smem();
