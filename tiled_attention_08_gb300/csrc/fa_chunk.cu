@@ -106,6 +106,24 @@ __device__ __forceinline__ void rows_out(uint32_t (&m)[8][4], uint8_t* dst, int 
     }
 }
 
+// Four e4m3 bytes times the fp32 factor (twice in f2), rounded to 16 bits.
+template <bool BF16>
+__device__ __forceinline__ void scaled16(uint32_t w, uint64_t f2, uint32_t& y0, uint32_t& y1) {
+    uint32_t h[2], y[2];
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(h[0]), "=r"(h[1])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 a = unpack2<false>(h[i]);
+        float lo, hi;
+        f2_split(f2_mul(f2_make(a.x, a.y), f2), lo, hi);
+        y[i] = pack2<BF16>(lo, hi);
+    }
+    y0 = y[0];
+    y1 = y[1];
+}
+
 // New tokens of sequence b and the tokens in front of them; none where the lengths are out of range.
 __device__ __forceinline__ bool sequence(const ChunkParams& p, int b, int& n, int& before) {
     const int len = p.seq_lens[b];
@@ -560,74 +578,62 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             const int unit = lane & 3, row_in = (warp - C::kConvWarp) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
             bool ok = true;
             int g = 0, piece = 0;  // tiles and pieces so far
-            auto convert = [&](const Live& live, int key0, uint8_t* tile) {
-#pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int st = piece % C::kPieces;
-                    ok = wait_warp(&bar_rf[st], (uint32_t)(piece / C::kPieces) & 1u, abort_v, p.timeout_ns);
-                    if (!ok) return;
-                    const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
-                    const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
-                    const bool all = live.every(key0 + hf * 64, 64);
-                    // (All reads first: they and the writes keep their order.)
-                    uint4 x[2][C::kChunks];
-                    uint64_t f2[2];
-                    bool there[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int r = row_in + 32 * k;
-#pragma unroll
-                        for (int c = 0; c < C::kChunks; ++c)
-                            x[k][c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
-                                                         : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
-                        const float f = row_scale(ex[r]);
-                        f2[k] = f2_make(f, f);
-                        there[k] = all || live.token(key0 + hf * 64 + r);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_re[st]);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int row = hf * 64 + row_in + 32 * k;
-#pragma unroll
-                        for (int c = 0; c < C::kChunks; ++c) {
-                            const uint32_t w[4] = {x[k][c].x, x[k][c].y, x[k][c].z, x[k][c].w};
-                            uint32_t y[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float2 a =
-                                    unpack2<false>(e4m3x2_to_f16x2(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu));
-                                float lo, hi;
-                                f2_split(f2_mul(f2_make(a.x, a.y), f2[k]), lo, hi);
-                                y[i] = there[k] ? pack2<BF16>(lo, hi) : 0u;
-                            }
-                            const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
-                            sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
-                                      make_uint4(y[0], y[1], y[2], y[3]));
-                            sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
-                                      make_uint4(y[4], y[5], y[6], y[7]));
-                        }
-                    }
-                    ++piece;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            };
             Segment sg;
             for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
                 const Live live = live_of(p, sg);
-                for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j) {
-                    const int key0 = sg.all.tile(j) * kTileRows, st = g % C::kStages;
+                for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j, ++g) {
+                    const int key0 = sg.all.tile(j) * kTileRows, slot = g % C::kStages;
                     const uint32_t ph = ((uint32_t)(g / C::kStages) & 1u) ^ 1u;
-                    if (g >= C::kStages) ok = wait_warp(&bar_ke[st], ph, abort_v, p.timeout_ns);
-                    if (ok) convert(live, key0, smem + C::kOffK + st * C::kTileBytes);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(&bar_kf[st]);
-                    if (g >= C::kStages) ok = wait_warp(&bar_ve[st], ph, abort_v, p.timeout_ns);
-                    if (ok) convert(live, key0, smem + C::kOffV + st * C::kTileBytes);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(&bar_vf[st]);
-                    ++g;
+                    // One copy of the code for K and V: with two (and both rows of a thread unrolled) the warps
+                    // of an SM no longer found their instructions in its cache (2.5 of 10.7 cycles per
+                    // instruction; 0.5 in the kernel of 16-bit caches).
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {  // K lo, K hi, V lo, V hi
+                        const bool v = h >= 2;
+                        const int hf = h & 1, st = piece % C::kPieces;
+                        if (hf == 0 && g >= C::kStages)
+                            ok = wait_warp(v ? &bar_ve[slot] : &bar_ke[slot], ph, abort_v, p.timeout_ns);
+                        ok = ok && wait_warp(&bar_rf[st], (uint32_t)(piece / C::kPieces) & 1u, abort_v, p.timeout_ns);
+                        if (!ok) break;
+                        const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
+                        const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
+                        uint8_t* tile = smem + (v ? C::kOffV : C::kOffK) + slot * C::kTileBytes;
+                        const bool all = live.every(key0 + hf * 64, 64);
+#pragma unroll 1
+                        for (int r = row_in; r < 64; r += 32) {
+                            const int row = hf * 64 + r;
+                            uint4 x[C::kChunks];  // (all reads first: they and the writes keep their order)
+#pragma unroll
+                            for (int c = 0; c < C::kChunks; ++c)
+                                x[c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                                                          : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
+                            const float f = row_scale(ex[r]);
+                            const bool there = all || live.token(key0 + row);
+#pragma unroll
+                            for (int c = 0; c < C::kChunks; ++c) {
+                                const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                                uint32_t y[8];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    scaled16<BF16>(w[i], f2_make(f, f), y[2 * i], y[2 * i + 1]);
+                                if (!there)
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) y[i] = 0u;
+                                const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
+                                sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
+                                          make_uint4(y[0], y[1], y[2], y[3]));
+                                sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
+                                          make_uint4(y[4], y[5], y[6], y[7]));
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bar_re[st]);
+                            if (hf) mbar_arrive(v ? &bar_vf[slot] : &bar_kf[slot]);
+                        }
+                        ++piece;
+                    }
                 }
             }
             if (!ok && lane == 0) record_timeout(p.status, abort_v);
@@ -789,8 +795,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     }
 }
 
-// Joins the parts of the pairs that are cut: block (c, y) the rows 32 y .. of the pair that goes on behind
-// CTA c, a warp per row.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).  And, before that, the rows
+// Joins the parts of the pairs that are cut: block (c, y) the rows 16 y .. of the pair that goes on behind
+// CTA c, two rows a warp.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).  And, before that, the rows
 // without a token: zeros and -inf, 64 rows of a head per warp.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) fa_chunk_join_kernel(const ChunkParams p) {
@@ -820,35 +826,71 @@ __global__ void __launch_bounds__(256) fa_chunk_join_kernel(const ChunkParams p)
         return;
     int fresh, before;
     sequence(p, own.x, fresh, before);
-    for (int k = 0; k < 4; ++k) {
-        const int r2 = blockIdx.y * 32 + warp * 4 + k;  // row of the two tiles
+    // Two rows a warp; lane c takes the log-sum-exp of parts c, c + 32, ...
+    int out_i[2];
+    size_t orow[2], part0[2];
+    float top[2], sum[2], x[2][kPer];
+    auto part_at = [&](int r, int c) {  // of row r of the warp
+        return part0[r] + (c == 0 ? 0 : (2 * (size_t)c - 1) * 2 * kTileRows);
+    };
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int r2 = (int)blockIdx.y * 16 + warp * 2 + r;  // row of the two tiles
         const int t = r2 >> 7, row = r2 & 127, head = row / p.T, tok = row - head * p.T;
         const int i = own.z + t * p.T + tok;
-        if (head >= p.group || i >= fresh) continue;
-        float top = -INFINITY, sum = 0.0f, x[kPer];
+        out_i[r] = head < p.group && i < fresh ? i : -1;
+        orow[r] = (size_t)own.x * p.Hq + own.y * p.group + head;
+        part0[r] = ((2 * (size_t)blockIdx.x + 1) * 2 + t) * kTileRows + row;
+        top[r] = -INFINITY;
+        sum[r] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
-        for (int c = 0; c < n_parts; ++c) {
-            const size_t slot = 2 * ((size_t)blockIdx.x + c) + (c == 0 ? 1 : 0);
-            const size_t part = (slot * 2 + t) * kTileRows + row;
-            const float y = p.slot_lse[part];
-            if (y == -INFINITY) continue;  // it saw no key there, and left no values
-            const float next = fmaxf(top, y);
-            const float f = ex2_approx(top - next), w = ex2_approx(y - next);
-            const float* src = p.slot_o + part * D + lane * kPer;
-            sum = fmaf(sum, f, w);
+        for (int e = 0; e < kPer; ++e) x[r][e] = 0.0f;
+    }
+    for (int c0 = 0; c0 < n_parts; c0 += 32) {
+        float y[2], w[2];
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) x[e] = fmaf(x[e], f, w * src[e]);
-            top = next;
+        for (int r = 0; r < 2; ++r)
+            y[r] = out_i[r] >= 0 && c0 + lane < n_parts ? p.slot_lse[part_at(r, c0 + lane)] : -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float m = y[r];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float next = fmaxf(top[r], m), base = next == -INFINITY ? 0.0f : next;
+            const float f = ex2_approx(top[r] - base);
+            w[r] = y[r] == -INFINITY ? 0.0f : ex2_approx(y[r] - base);  // (NaN stays)
+            float s = w[r];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+            sum[r] = fmaf(sum[r], f, s);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[r][e] *= f;
+            top[r] = next;
         }
-        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-        const size_t orow = (size_t)own.x * p.Hq + own.y * p.group + head;
+        const int n = imin(n_parts - c0, 32);
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float wc = __shfl_sync(0xffffffffu, w[r], c);
+                if (wc == 0.0f) continue;  // (of a part without a key nothing was written)
+                const float* src = p.slot_o + part_at(r, c0 + c) * D + lane * kPer;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) x[r][e] = fmaf(wc, src[e], x[r][e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        if (out_i[r] < 0) continue;
+        const float inv = sum[r] != 0.0f ? 1.0f / sum[r] : 0.0f;
         uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.o) +
-                                                    row_offset(p.so, (int)orow, p.Hq, i)) +
+                                                    row_offset(p.so, (int)orow[r], p.Hq, out_i[r])) +
                         lane * (kPer / 2);
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<BF16>(x[e] * inv, x[e + 1] * inv);
-        if (lane == 0) p.lse[orow * p.L + i] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<BF16>(x[r][e] * inv, x[r][e + 1] * inv);
+        if (lane == 0)
+            p.lse[orow[r] * p.L + out_i[r]] = sum[r] != 0.0f ? (top[r] + log2f(sum[r])) * kLn2 : -INFINITY;
     }
 }
 
@@ -881,7 +923,7 @@ cudaError_t launch_chunk(const ChunkParams& p, int D, bool bf16, bool q8, cudaSt
 }
 
 cudaError_t launch_chunk_join(const ChunkParams& p, int D, bool bf16, cudaStream_t s) {
-    const dim3 grid((unsigned)p.grid, 8), block(256);
+    const dim3 grid((unsigned)p.grid, 16), block(256);
     if (D == 64)
         return bf16 ? launch_kernel_early(fa_chunk_join_kernel<64, true>, grid, block, 0, s, p)
                     : launch_kernel_early(fa_chunk_join_kernel<64, false>, grid, block, 0, s, p);
