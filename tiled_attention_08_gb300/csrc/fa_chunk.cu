@@ -40,26 +40,35 @@ template <int D, bool BF16, bool Q8>
 struct ChunkCfg {
     static constexpr int kChunks = D / kChunkElems;
     static constexpr int kTileBytes = kTileRows * D * 2;
-    static constexpr int kStages = (D == 128) ? 2 : 4;  // of the K ring and of the V ring
+    // Tile slots.  16-bit caches: a ring for K and one for V.  e4m3: one ring, K and V in turn, of three
+    // slots at D = 128 (a step reads V_j and K_{j+1} while V_{j+1} is converted), which leaves room for
+    // twice as many bytes in flight (32 KB of them with two rings of two: 1139 us where 64 KB take XXX).
+    static constexpr int kStages = (D == 128) ? 2 : 4;
+    static constexpr int kSlots = Q8 ? ((D == 128) ? 3 : 6) : 2 * kStages;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + 2 * kTileBytes;
-    static constexpr int kOffV = kOffK + kStages * kTileBytes;
-    // e4m3: pieces of 64 tokens as bytes on their way to the converters, K and V in turn, 32 KB of them, and
+    static constexpr int kOffKV = kOffQ + 2 * kTileBytes;
+    // The slot of K (v = 0) or V (v = 1) of the g-th tile, and the how-manieth use of it that is.
+    __host__ __device__ static constexpr int slot(int g, int v) {
+        return Q8 ? (2 * g + v) % kSlots : v * kStages + g % kStages;
+    }
+    __host__ __device__ static constexpr int use(int g, int v) { return Q8 ? (2 * g + v) / kSlots : g / kStages; }
+    // e4m3: pieces of 64 tokens as bytes on their way to the converters, K and V in turn, 64 KB of them, and
     // their exponents.
     static constexpr int kPieceRows = 64;
     static constexpr int kPieceBytes = kPieceRows * D;
-    static constexpr int kPieces = Q8 ? 32768 / kPieceBytes : 0;
-    static constexpr int kOffRaw = kOffV + kStages * kTileBytes;
+    static constexpr int kPieces = Q8 ? 65536 / kPieceBytes : 0;
+    static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffExp = kOffRaw + kPieces * kPieceBytes;
     static constexpr int kSmemBytes = kOffExp + kPieces * kPieceRows + 1024;
-    static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10;  // (e4m3: queries, the cache's bytes)
-    static constexpr int kConvWarp = 12;                         // the first of four converter warps
+    // Warp 8: queries, and K of a 16-bit cache; 9: V, or an e4m3 cache's bytes; 10: MMA; 12 .. 15: converters.
+    static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
+    static constexpr int kConverters = Q8 ? 4 : 0;
     static constexpr int kThreads = Q8 ? 16 * 32 : 12 * 32;
-    // Registers per thread of the softmax warps, of warps 8-11 and of the converters.  At launch each
-    // thread has kRegs; the sums over the warpgroups are the same.
+    // Registers per thread of the softmax warps and of the others.  At launch each thread has kRegs; the sums
+    // over the warpgroups are the same.
     static constexpr int kRegs = Q8 ? 128 : 168;
-    static constexpr int kRegsSoftmax = Q8 ? 176 : 208, kRegsIssue = 88, kRegsConv = 72;
-    static_assert(2 * kRegsSoftmax + kRegsIssue + (Q8 ? kRegsConv : 0) == kThreads / 128 * kRegs,
+    static constexpr int kRegsSoftmax = Q8 ? 176 : 208, kRegsOther = Q8 ? 80 : 88;
+    static_assert(2 * kRegsSoftmax + (kThreads / 128 - 2) * kRegsOther == kThreads / 128 * kRegs,
                   "the launch's registers");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kTmS = 0, kTmO = 256;
@@ -106,22 +115,61 @@ __device__ __forceinline__ void rows_out(uint32_t (&m)[8][4], uint8_t* dst, int 
     }
 }
 
-// Four e4m3 bytes times the fp32 factor (twice in f2), rounded to 16 bits.
+// Sixteen e4m3 bytes times 2^(E - 127), rounded once to 16 bits.
+//
+// In the usual case by a product of the 16-bit type.  bf16: sign, exponent and mantissa of a byte are moved to
+// their places (its exponent field 0 .. 15 becomes bf16's, subnormals included), which gives 2^-120 of its
+// value; the factor makes up for that.  fp16: converted, then scaled.  `usual`: the factor is a number of the
+// type, and no byte is e4m3's NaN (0x7f, 0xff), which the moved bits would lose.
 template <bool BF16>
-__device__ __forceinline__ void scaled16(uint32_t w, uint64_t f2, uint32_t& y0, uint32_t& y1) {
-    uint32_t h[2], y[2];
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(h[0]), "=r"(h[1])
-        : "r"(w));
+__device__ __forceinline__ uint32_t row_factor(uint32_t E) {
+    const uint32_t x = BF16 ? (E + 120u) << 7 : (E - 112u) << 10;
+    return x | x << 16;
+}
+template <bool BF16>
+__device__ __forceinline__ bool usual_exponent(uint32_t E) {
+    return BF16 ? E <= 134u : E - 113u <= 29u;  // 2^(E - 7) and 2^(E - 127) are normal numbers
+}
+// Bit 7 of a byte is set where one of the bytes of x is a NaN.
+__device__ __forceinline__ uint32_t nan_bytes(const uint4& x) {
+    return ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
+}
+template <bool BF16>
+__device__ __forceinline__ void scaled16(const uint4& x, uint32_t f, uint32_t (&y)[8]) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 a = unpack2<false>(h[i]);
-        float lo, hi;
-        f2_split(f2_mul(f2_make(a.x, a.y), f2), lo, hi);
-        y[i] = pack2<BF16>(lo, hi);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (BF16) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t b = __byte_perm(w[i], 0u, h ? 0x3424 : 0x1404);  // each byte on top of a half
+                asm("mul.rn.bf16x2 %0, %1, %2;"
+                    : "=r"(y[2 * i + h])
+                    : "r"((b >> 4 & 0x07f007f0u) | (b & 0x80008000u)), "r"(f));
+            }
+        } else {
+            asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 a, b;\n\tmov.b32 {l, h}, %2;\n\t"
+                "cvt.rn.f16x2.e4m3x2 a, l;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\t"
+                "mul.rn.f16x2 %0, a, %3;\n\tmul.rn.f16x2 %1, b, %3;\n\t}"
+                : "=r"(y[2 * i]), "=r"(y[2 * i + 1])
+                : "r"(w[i]), "r"(f));
+        }
     }
-    y0 = y[0];
-    y1 = y[1];
+}
+// The same for any exponent and any bytes, and zeros where `there` is false; out of line.
+template <bool BF16>
+__device__ __noinline__ void convert_any(uint4 x, uint32_t E, bool there, uint32_t to0, uint32_t to1) {
+    const float f = row_scale(E);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 a = unpack2<false>(e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)) & 0xffffu));
+        y[i] = there ? pack2<BF16>(a.x * f, a.y * f) : 0u;
+    }
+    sts_u32x4(to0, make_uint4(y[0], y[1], y[2], y[3]));
+    sts_u32x4(to1, make_uint4(y[4], y[5], y[6], y[7]));
 }
 
 // New tokens of sequence b and the tokens in front of them; none where the lengths are out of range.
@@ -231,8 +279,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
-    __shared__ uint64_t bar_qf, bar_qe, bar_kf[C::kStages], bar_ke[C::kStages], bar_vf[C::kStages],
-        bar_ve[C::kStages], bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint64_t bar_qf, bar_qe, bar_f[C::kSlots], bar_e[C::kSlots];  // slots full / empty
+    __shared__ uint64_t bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
     __shared__ uint64_t bar_rf[Q8 ? C::kPieces : 1], bar_re[Q8 ? C::kPieces : 1];  // pieces landed / read
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
@@ -253,11 +301,9 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         start_sh.left = 0;
         mbar_init(&bar_qf, 1);
         mbar_init(&bar_qe, 1);
-        for (int s = 0; s < C::kStages; ++s) {
-            mbar_init(&bar_kf[s], Q8 ? 4 : 1);  // (a converter warp each)
-            mbar_init(&bar_ke[s], 1);
-            mbar_init(&bar_vf[s], Q8 ? 4 : 1);
-            mbar_init(&bar_ve[s], 1);
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(&bar_f[s], Q8 ? C::kConverters : 1);
+            mbar_init(&bar_e[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bar_sf[t], 1);
@@ -266,7 +312,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         }
         for (int s = 0; s < C::kPieces; ++s) {
             mbar_init(&bar_rf[s], 1);
-            mbar_init(&bar_re[s], 4);
+            mbar_init(&bar_re[s], C::kConverters);
         }
         mbar_init(&bar_fin, 1);
         mbar_fence_init();
@@ -340,18 +386,15 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     const uint32_t tmem = tmem_base_sh;
     Walk walk = start_sh;
 
-    // (Each warpgroup sets its registers at the head of its branch, with one instruction.)
-    if (warp >= 8 && warp < C::kConvWarp) {
-    regs_lower<C::kRegsIssue>();
+    // (A warpgroup sets its registers with one instruction.)
+    if (warp >= 8) {
+    regs_lower<C::kRegsOther>();
     if (warp == C::kKWarp || (!Q8 && warp == C::kVWarp)) {
         // ------------------------------ TMA producers ------------------------------
         // The K warp brings each segment's query pair, and K's pages of a 16-bit cache; the V warp V's.
         // Lane 8c + i issues page i of chunk c; table entries are fetched one tile ahead.
         const bool is_k = warp == C::kKWarp;
         const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
-        uint64_t* full = is_k ? bar_kf : bar_vf;
-        uint64_t* empty = is_k ? bar_ke : bar_ve;
-        uint8_t* ring = smem + (is_k ? C::kOffK : C::kOffV);
         const int my_page = lane & (kPagesPerTile - 1), my_chunk = lane / kPagesPerTile;
         bool ok = true;
         int issued = 0, n_seg = 0;
@@ -388,18 +431,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                 for (int j = sg.j0; j < sg.j0 + sg.n; ++j) {
                     const int page = next;
                     if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
-                    const int st = issued % C::kStages;
-                    if (issued >= C::kStages) {
-                        ok = wait_warp(&empty[st], ((uint32_t)(issued / C::kStages) & 1u) ^ 1u, abort_v,
-                                       p.timeout_ns);
+                    const int st = C::slot(issued, !is_k), use = C::use(issued, !is_k);
+                    if (use > 0) {
+                        ok = wait_warp(&bar_e[st], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
                         if (!ok) break;
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+                    if (lane == 0) mbar_arrive_expect_tx(&bar_f[st], C::kTileBytes);
                     __syncwarp();
                     if (my_chunk < C::kChunks)  // (outside the map: zeros)
-                        tma_load_3d(ring + st * C::kTileBytes + my_chunk * kChunkBytes +
+                        tma_load_3d(smem + C::kOffKV + st * C::kTileBytes + my_chunk * kChunkBytes +
                                         my_page * (kPageTokens * 128),
-                                    map, &full[st], my_chunk * kChunkElems, page < 0 ? kPageTokens : 0,
+                                    map, &bar_f[st], my_chunk * kChunkElems, page < 0 ? kPageTokens : 0,
                                     page < 0 ? 0 : page * p.Hk + sg.hk);
                     __syncwarp();
                     ++issued;
@@ -410,7 +452,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         // Drain: the newest fill of every slot must have landed before the CTA exits.
         if (is_k && n_seg > 0) wait_bounded(&bar_qf, (uint32_t)(n_seg - 1) & 1u, nullptr, p.timeout_ns);
         for (int g = issued - 1; g >= 0 && g >= issued - C::kStages; --g)
-            wait_bounded(&full[g % C::kStages], (uint32_t)(g / C::kStages) & 1u, nullptr, p.timeout_ns);
+            wait_bounded(&bar_f[C::slot(g, !is_k)], (uint32_t)C::use(g, !is_k) & 1u, nullptr, p.timeout_ns);
     } else if (Q8 && warp == C::kVWarp) {
         // ------------------------------ the cache's bytes ------------------------------
         // Pieces K lo, K hi, V lo, V hi of each tile; lane i issues page i of a piece and its exponents.
@@ -477,9 +519,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         bool ok = true;
         int g = 0, n_seg = 0, ps[2] = {0, 0};
         const uint32_t neg = p.s_negate ? kIdescNegateA : 0u;
-        auto wait_ring = [&](uint64_t* full, int i) -> bool {
-            const bool r = wait_warp(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u, abort_v,
-                                     p.timeout_ns);
+        auto wait_tile = [&](int i, int v) -> bool {  // K or V of the i-th tile is there
+            const bool r = wait_warp(&bar_f[C::slot(i, v)], (uint32_t)C::use(i, v) & 1u, abort_v, p.timeout_ns);
             tc_fence_after_sync();
             return r;
         };
@@ -491,8 +532,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             int done[2] = {0, 0};
             auto issue_s = [&](int t, int gk) {  // S_t = Q_t K^T for ring fill gk
                 const uint64_t qd = sdesc_kmajor_sw128(smem_u32(smem + C::kOffQ + t * C::kTileBytes));
-                const uint64_t kd = sdesc_kmajor_sw128(
-                    smem_u32(smem + C::kOffK + (gk % C::kStages) * C::kTileBytes));
+                const uint64_t kd =
+                    sdesc_kmajor_sw128(smem_u32(smem + C::kOffKV + C::slot(gk, 0) * C::kTileBytes));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
@@ -505,7 +546,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                 if (!wait_warp(&bar_pf[t], (uint32_t)ps[t] & 1u, abort_v, p.timeout_ns)) return false;
                 tc_fence_after_sync();
                 const uint64_t vd = sdesc_mnmajor_sw128(
-                    smem_u32(smem + C::kOffV + (gv % C::kStages) * C::kTileBytes), kChunkBytes);
+                    smem_u32(smem + C::kOffKV + C::slot(gv, 1) * C::kTileBytes), kChunkBytes);
 #pragma unroll
                 for (int kk = 0; kk < kTileRows / 16; ++kk)
                     mma_ts_w(tmem + C::kTmO + D * t, tmem + C::kTmS + 128 * t + kk * 8,
@@ -516,16 +557,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             };
             ok = wait_warp(&bar_qf, (uint32_t)n_seg & 1u, abort_v, p.timeout_ns);
             tc_fence_after_sync();
-            ok = ok && wait_ring(bar_kf, g);
+            ok = ok && wait_tile(g, 0);
             if (!ok) break;
             for (int t = 0; t < 2; ++t)
                 if (sg.active(t, sg.j0)) issue_s(t, g);
             if (sg.n == 1) mma_commit_w(&bar_qe);  // every S of the segment issued
-            mma_commit_w(&bar_ke[g % C::kStages]);
+            mma_commit_w(&bar_e[C::slot(g, 0)]);
             for (int j = sg.j0; ok && j < j1; ++j) {
                 const bool next = j + 1 < j1;
                 const int gj = g + (j - sg.j0);
-                if (!wait_ring(bar_vf, gj) || (next && !wait_ring(bar_kf, gj + 1))) {
+                // (e4m3: K_{j+1}, which may still be on its way, is waited for behind PV_A.)
+                if (!wait_tile(gj, 1) || (!Q8 && next && !wait_tile(gj + 1, 0))) {
                     ok = false;
                     break;
                 }
@@ -533,7 +575,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                     // Slots of a page that were read with it but hold no token that counts: zeros.
                     const int key0 = sg.all.tile(j) * kTileRows;
                     if (!live.every(key0, kTileRows)) {
-                        uint8_t* tile = smem + C::kOffV + (gj % C::kStages) * C::kTileBytes;
+                        uint8_t* tile = smem + C::kOffKV + C::slot(gj, 1) * C::kTileBytes;
                         for (int r = lane; r < kTileRows; r += 32) {
                             const int token = key0 + r;
                             if (live.token(token) || !live.any(token & ~(kPageTokens - 1), kPageTokens)) continue;
@@ -555,12 +597,16 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                         ok = false;
                         break;
                     }
+                    if (Q8 && t == 0 && next && !wait_tile(gj + 1, 0)) {
+                        ok = false;
+                        break;
+                    }
                     if (next && sg.active(t, j + 1)) issue_s(t, gj + 1);
                 }
                 if (!ok) break;
                 if (j + 2 == j1) mma_commit_w(&bar_qe);  // the segment's last S issued
-                mma_commit_w(&bar_ve[gj % C::kStages]);
-                if (next) mma_commit_w(&bar_ke[(gj + 1) % C::kStages]);
+                mma_commit_w(&bar_e[C::slot(gj, 1)]);
+                if (next) mma_commit_w(&bar_e[C::slot(gj + 1, 0)]);
             }
             g += sg.n;
             ++n_seg;
@@ -568,13 +614,12 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
         mma_commit_w(&bar_fin);  // every issued MMA must finish before TMEM is released
         wait_warp(&bar_fin, 0, nullptr, p.timeout_ns);
-    }
     } else if (Q8 && warp >= C::kConvWarp) {
         // ------------------------------ converters ------------------------------
-        // Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of row q ^ 5b of eight rows: the eight lanes of a
-        // shared-memory access then read and write all eight 16-byte places of a line of banks.
+        // Of a piece each warp takes eight of every 32 rows.  Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of
+        // row q ^ 5b of them: the eight lanes of a shared-memory access then read and write all eight 16-byte
+        // places of a line of banks.
         if constexpr (Q8) {
-            regs_lower<C::kRegsConv>();
             const int unit = lane & 3, row_in = (warp - C::kConvWarp) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
             bool ok = true;
             int g = 0, piece = 0;  // tiles and pieces so far
@@ -582,55 +627,67 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
                 const Live live = live_of(p, sg);
                 for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j, ++g) {
-                    const int key0 = sg.all.tile(j) * kTileRows, slot = g % C::kStages;
-                    const uint32_t ph = ((uint32_t)(g / C::kStages) & 1u) ^ 1u;
+                    const int key0 = sg.all.tile(j) * kTileRows;
                     // One copy of the code for K and V: with two (and both rows of a thread unrolled) the warps
                     // of an SM no longer found their instructions in its cache (2.5 of 10.7 cycles per
                     // instruction; 0.5 in the kernel of 16-bit caches).
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {  // K lo, K hi, V lo, V hi
-                        const bool v = h >= 2;
-                        const int hf = h & 1, st = piece % C::kPieces;
-                        if (hf == 0 && g >= C::kStages)
-                            ok = wait_warp(v ? &bar_ve[slot] : &bar_ke[slot], ph, abort_v, p.timeout_ns);
+                        const int v = h >> 1, hf = h & 1, st = piece % C::kPieces;
+                        const int slot = C::slot(g, v), use = C::use(g, v);
+                        if (hf == 0 && use > 0)
+                            ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
                         ok = ok && wait_warp(&bar_rf[st], (uint32_t)(piece / C::kPieces) & 1u, abort_v, p.timeout_ns);
                         if (!ok) break;
                         const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
                         const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
-                        uint8_t* tile = smem + (v ? C::kOffV : C::kOffK) + slot * C::kTileBytes;
-                        const bool all = live.every(key0 + hf * 64, 64);
-#pragma unroll 1
-                        for (int r = row_in; r < 64; r += 32) {
-                            const int row = hf * 64 + r;
-                            uint4 x[C::kChunks];  // (all reads first: they and the writes keep their order)
+                        const uint32_t tile = smem_u32(smem + C::kOffKV + slot * C::kTileBytes);
+                        uint4 x[2][C::kChunks];  // (all reads first: they and the writes keep their order)
+                        uint32_t e[2], nan = 0u;
+                        bool usual = live.every(key0 + hf * 64, 64);
 #pragma unroll
-                            for (int c = 0; c < C::kChunks; ++c)
-                                x[c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
-                                                          : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
-                            const float f = row_scale(ex[r]);
-                            const bool there = all || live.token(key0 + row);
+                        for (int k = 0; k < 2; ++k) {
+                            const int r = row_in + 32 * k;
 #pragma unroll
                             for (int c = 0; c < C::kChunks; ++c) {
-                                const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                                uint32_t y[8];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    scaled16<BF16>(w[i], f2_make(f, f), y[2 * i], y[2 * i + 1]);
-                                if (!there)
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) y[i] = 0u;
-                                const uint32_t line = smem_u32(tile + c * kChunkBytes + row * 128);
-                                sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
-                                          make_uint4(y[0], y[1], y[2], y[3]));
-                                sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
-                                          make_uint4(y[4], y[5], y[6], y[7]));
+                                x[k][c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                                                             : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
+                                if constexpr (BF16) nan |= nan_bytes(x[k][c]);
                             }
+                            e[k] = ex[r];
+                            usual = usual && usual_exponent<BF16>(e[k]);
+                        }
+                        usual = usual && !(nan & 0x80808080u);
+                        auto line = [&](int k, int c, int i) {  // where 16-byte piece i of the unit goes
+                            const int row = hf * 64 + row_in + 32 * k;
+                            return tile + c * kChunkBytes + row * 128 + ((uint32_t)((2 * unit + i) ^ (row & 7)) << 4);
+                        };
+                        // (A branch per unit would keep the units from overlapping: 1010 -> 1629 us.)
+                        if (__all_sync(0xffffffffu, usual)) {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t f = row_factor<BF16>(e[k]);
+#pragma unroll
+                                for (int c = 0; c < C::kChunks; ++c) {
+                                    uint32_t y[8];
+                                    scaled16<BF16>(x[k][c], f, y);
+                                    sts_u32x4(line(k, c, 0), make_uint4(y[0], y[1], y[2], y[3]));
+                                    sts_u32x4(line(k, c, 1), make_uint4(y[4], y[5], y[6], y[7]));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int c = 0; c < C::kChunks; ++c)
+                                    convert_any<BF16>(x[k][c], e[k], live.token(key0 + hf * 64 + row_in + 32 * k),
+                                                      line(k, c, 0), line(k, c, 1));
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
                             mbar_arrive(&bar_re[st]);
-                            if (hf) mbar_arrive(v ? &bar_vf[slot] : &bar_kf[slot]);
+                            if (hf) mbar_arrive(&bar_f[slot]);
                         }
                         ++piece;
                     }
@@ -638,6 +695,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             }
             if (!ok && lane == 0) record_timeout(p.status, abort_v);
         }
+    }
     } else {
         // ------------------------------ softmax warps ------------------------------
         regs_raise<C::kRegsSoftmax>();
@@ -828,7 +886,7 @@ __global__ void __launch_bounds__(256) fa_chunk_join_kernel(const ChunkParams p)
     sequence(p, own.x, fresh, before);
     // Two rows a warp; lane c takes the log-sum-exp of parts c, c + 32, ...
     int out_i[2];
-    size_t orow[2], part0[2];
+    size_t orow[2], part0[2] = {0, 0};
     float top[2], sum[2], x[2][kPer];
     auto part_at = [&](int r, int c) {  // of row r of the warp
         return part0[r] + (c == 0 ? 0 : (2 * (size_t)c - 1) * 2 * kTileRows);
