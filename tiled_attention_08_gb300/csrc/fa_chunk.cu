@@ -52,15 +52,14 @@ struct ChunkCfg {
         return Q8 ? (2 * g + v) % kSlots : v * kStages + g % kStages;
     }
     __host__ __device__ static constexpr int use(int g, int v) { return Q8 ? (2 * g + v) / kSlots : g / kStages; }
-    // e4m3: pieces of 64 tokens as bytes on their way to the converters, K and V in turn, 64 KB of them, and
-    // their exponents.
-    static constexpr int kPieceRows = 64;
-    static constexpr int kPieceBytes = kPieceRows * D;
-    static constexpr int kPieces = Q8 ? 65536 / kPieceBytes : 0;
+    // e4m3: tiles as bytes on their way to the converters, a ring each of K and V, 64 KB in all, and their
+    // exponents.
+    static constexpr int kRawBytes = kTileRows * D;
+    static constexpr int kRaw = Q8 ? 32768 / kRawBytes : 0;
     static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
-    static constexpr int kOffExp = kOffRaw + kPieces * kPieceBytes;
-    static constexpr int kSmemBytes = kOffExp + kPieces * kPieceRows + 1024;
-    // Warp 8: queries, and K of a 16-bit cache; 9: V, or an e4m3 cache's bytes; 10: MMA; 12 .. 15: converters.
+    static constexpr int kOffExp = kOffRaw + 2 * kRaw * kRawBytes;
+    static constexpr int kSmemBytes = kOffExp + 2 * kRaw * kTileRows + 1024;
+    // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 15: converters.
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
     static constexpr int kConverters = Q8 ? 4 : 0;
     static constexpr int kThreads = Q8 ? 16 * 32 : 12 * 32;
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                                ~uintptr_t(1023));
     __shared__ uint64_t bar_qf, bar_qe, bar_f[C::kSlots], bar_e[C::kSlots];  // slots full / empty
     __shared__ uint64_t bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
-    __shared__ uint64_t bar_rf[Q8 ? C::kPieces : 1], bar_re[Q8 ? C::kPieces : 1];  // pieces landed / read
+    __shared__ uint64_t bar_rf[Q8 ? 2 * C::kRaw : 1], bar_re[Q8 ? 2 * C::kRaw : 1];  // bytes landed / read
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ int warp_sum[C::kThreads / 32];
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             mbar_init(&bar_pf[t], 128);
             mbar_init(&bar_oready[t], 1);
         }
-        for (int s = 0; s < C::kPieces; ++s) {
+        for (int s = 0; s < 2 * C::kRaw; ++s) {
             mbar_init(&bar_rf[s], 1);
             mbar_init(&bar_re[s], C::kConverters);
         }
@@ -389,13 +388,19 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     // (A warpgroup sets its registers with one instruction.)
     if (warp >= 8) {
     regs_lower<C::kRegsOther>();
-    if (warp == C::kKWarp || (!Q8 && warp == C::kVWarp)) {
+    if (warp == C::kKWarp || warp == C::kVWarp) {
         // ------------------------------ TMA producers ------------------------------
-        // The K warp brings each segment's query pair, and K's pages of a 16-bit cache; the V warp V's.
-        // Lane 8c + i issues page i of chunk c; table entries are fetched one tile ahead.
+        // The K warp brings each segment's query pair, and K's pages; the V warp V's.  Lane 8c + i issues page i
+        // of chunk c, over e4m3 lane i page i and lane 8 + i its exponents; table entries are fetched one tile ahead.
         const bool is_k = warp == C::kKWarp;
         const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
         const int my_page = lane & (kPagesPerTile - 1), my_chunk = lane / kPagesPerTile;
+        constexpr int kIssuers = Q8 ? 2 : C::kChunks;  // groups of eight lanes
+        uint64_t* full = Q8 ? bar_rf : bar_f;
+        uint64_t* empty = Q8 ? bar_re : bar_e;
+        auto slot_of = [&](int i) { return Q8 ? (is_k ? 0 : C::kRaw) + i % C::kRaw : C::slot(i, !is_k); };
+        auto use_of = [&](int i) { return Q8 ? i / C::kRaw : C::use(i, !is_k); };
+        constexpr int kRing = Q8 ? C::kRaw : C::kStages;
         bool ok = true;
         int issued = 0, n_seg = 0;
         Segment sg;
@@ -415,105 +420,59 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                 __syncwarp();
                 ++n_seg;
             }
-            if constexpr (!Q8) {
-                const Live live = live_of(p, sg);
-                auto entry = [&](int j) {  // this lane's page of tile j, or -1: nothing of it counts
-                    const int pg = sg.all.tile(j) * kPagesPerTile + my_page;
-                    if (my_chunk >= C::kChunks || !live.any(pg * kPageTokens, kPageTokens)) return -1;
-                    const int page = p.block_tables[(size_t)sg.b * p.max_pages + pg];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicCAS(p.status, 0, (int)kDevBadArg);
-                        return -1;
+            const Live live = live_of(p, sg);
+            auto entry = [&](int j) {  // this lane's page of tile j, or -1: nothing of it counts
+                const int pg = sg.all.tile(j) * kPagesPerTile + my_page;
+                if (my_chunk >= kIssuers || !live.any(pg * kPageTokens, kPageTokens)) return -1;
+                const int page = p.block_tables[(size_t)sg.b * p.max_pages + pg];
+                if (page < 0 || page >= p.num_pages) {
+                    atomicCAS(p.status, 0, (int)kDevBadArg);
+                    return -1;
+                }
+                return page;
+            };
+            int next = entry(sg.j0);
+            for (int j = sg.j0; j < sg.j0 + sg.n; ++j, ++issued) {
+                const int page = next;
+                if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
+                const int st = slot_of(issued), use = use_of(issued);
+                if (use > 0) {
+                    ok = wait_warp(&empty[st], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
+                    if (!ok) break;
+                }
+                const size_t ph = page < 0 ? 0 : (size_t)page * p.Hk + sg.hk;
+                const int row = page < 0 ? kPageTokens : 0;  // (outside the map: zeros)
+                if constexpr (Q8) {
+                    uint8_t* ex = smem + C::kOffExp + st * kTileRows + my_page * kPageTokens;
+                    const bool mine = my_chunk == 1 && page >= 0;
+                    const uint32_t n_ex = __popc(__ballot_sync(0xffffffffu, mine));
+                    if (my_chunk == 1 && page < 0) {  // no page: zeros, whose exponents are finite
+                        sts_u32x4(smem_u32(ex), make_uint4(0u, 0u, 0u, 0u));
+                        fence_proxy_async_smem();
                     }
-                    return page;
-                };
-                int next = entry(sg.j0);
-                for (int j = sg.j0; j < sg.j0 + sg.n; ++j) {
-                    const int page = next;
-                    if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
-                    const int st = C::slot(issued, !is_k), use = C::use(issued, !is_k);
-                    if (use > 0) {
-                        ok = wait_warp(&bar_e[st], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
-                        if (!ok) break;
-                    }
-                    if (lane == 0) mbar_arrive_expect_tx(&bar_f[st], C::kTileBytes);
                     __syncwarp();
-                    if (my_chunk < C::kChunks)  // (outside the map: zeros)
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kRawBytes + n_ex * kPageTokens);
+                    __syncwarp();
+                    if (my_chunk == 0)
+                        tma_load_3d(smem + C::kOffRaw + st * C::kRawBytes + my_page * (kPageTokens * D), map,
+                                    &full[st], 0, row, (int)ph);
+                    if (mine) bulk_load(ex, (is_k ? p.k_exp : p.v_exp) + ph * kPageTokens, kPageTokens, &full[st]);
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+                    __syncwarp();
+                    if (my_chunk < kIssuers)
                         tma_load_3d(smem + C::kOffKV + st * C::kTileBytes + my_chunk * kChunkBytes +
                                         my_page * (kPageTokens * 128),
-                                    map, &bar_f[st], my_chunk * kChunkElems, page < 0 ? kPageTokens : 0,
-                                    page < 0 ? 0 : page * p.Hk + sg.hk);
-                    __syncwarp();
-                    ++issued;
+                                    map, &full[st], my_chunk * kChunkElems, row, (int)ph);
                 }
+                __syncwarp();
             }
         }
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
         // Drain: the newest fill of every slot must have landed before the CTA exits.
         if (is_k && n_seg > 0) wait_bounded(&bar_qf, (uint32_t)(n_seg - 1) & 1u, nullptr, p.timeout_ns);
-        for (int g = issued - 1; g >= 0 && g >= issued - C::kStages; --g)
-            wait_bounded(&bar_f[C::slot(g, !is_k)], (uint32_t)C::use(g, !is_k) & 1u, nullptr, p.timeout_ns);
-    } else if (Q8 && warp == C::kVWarp) {
-        // ------------------------------ the cache's bytes ------------------------------
-        // Pieces K lo, K hi, V lo, V hi of each tile; lane i issues page i of a piece and its exponents.
-        if constexpr (Q8) {
-            bool ok = true;
-            int issued = 0;
-            Segment sg;
-            for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
-                const Live live = live_of(p, sg);
-                auto entry = [&](int j) {  // page `lane` of tile j, or -1: nothing of it counts
-                    const int pg = sg.all.tile(j) * kPagesPerTile + lane;
-                    if (lane >= kPagesPerTile || !live.any(pg * kPageTokens, kPageTokens)) return -1;
-                    const int page = p.block_tables[(size_t)sg.b * p.max_pages + pg];
-                    if (page < 0 || page >= p.num_pages) {
-                        atomicCAS(p.status, 0, (int)kDevBadArg);
-                        return -1;
-                    }
-                    return page;
-                };
-                int next = entry(sg.j0);
-                for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j) {
-                    const int pages = next;
-                    if (j + 1 < sg.j0 + sg.n) next = entry(j + 1);
-#pragma unroll
-                    for (int piece = 0; piece < 4; ++piece) {
-                        const int st = issued % C::kPieces;
-                        if (issued >= C::kPieces) {
-                            ok = wait_warp(&bar_re[st], ((uint32_t)(issued / C::kPieces) & 1u) ^ 1u, abort_v,
-                                           p.timeout_ns);
-                            if (!ok) break;
-                        }
-                        const int page = __shfl_sync(0xffffffffu, pages, (piece & 1) * 4 + (lane & 3));
-                        const uint32_t there = __ballot_sync(0xffffffffu, lane < 4 && page >= 0);
-                        if (lane < 4 && page < 0) {  // no page: zeros, whose exponents are finite
-                            sts_u32x4(smem_u32(smem + C::kOffExp + st * C::kPieceRows + lane * kPageTokens),
-                                      make_uint4(0u, 0u, 0u, 0u));
-                            fence_proxy_async_smem();
-                        }
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(&bar_rf[st], C::kPieceBytes + __popc(there) * kPageTokens);
-                        __syncwarp();
-                        if (lane < 4) {
-                            const size_t ph = page < 0 ? 0 : (size_t)page * p.Hk + sg.hk;
-                            tma_load_3d(smem + C::kOffRaw + st * C::kPieceBytes + lane * (kPageTokens * D),
-                                        piece < 2 ? &p.tm_k : &p.tm_v, &bar_rf[st], 0, page < 0 ? kPageTokens : 0,
-                                        (int)ph);
-                            if (page >= 0)
-                                bulk_load(smem + C::kOffExp + st * C::kPieceRows + lane * kPageTokens,
-                                          (piece < 2 ? p.k_exp : p.v_exp) + ph * kPageTokens, kPageTokens,
-                                          &bar_rf[st]);
-                        }
-                        __syncwarp();
-                        ++issued;
-                    }
-                }
-            }
-            if (!ok && lane == 0) record_timeout(p.status, abort_v);
-            for (int g = issued - 1; g >= 0 && g >= issued - C::kPieces; --g)
-                wait_bounded(&bar_rf[g % C::kPieces], (uint32_t)(g / C::kPieces) & 1u, nullptr, p.timeout_ns);
-        }
+        for (int g = issued - 1; g >= 0 && g >= issued - kRing; --g)
+            wait_bounded(&full[slot_of(g)], (uint32_t)use_of(g) & 1u, nullptr, p.timeout_ns);
     } else if (warp == C::kMmaWarp) {
         // ------------------------------ MMA issuer ------------------------------
         bool ok = true;
@@ -616,80 +575,80 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         wait_warp(&bar_fin, 0, nullptr, p.timeout_ns);
     } else if (Q8 && warp >= C::kConvWarp) {
         // ------------------------------ converters ------------------------------
-        // Of a piece each warp takes eight of every 32 rows.  Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of
+        // Each warp takes eight of every 32 rows of a tile.  Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of
         // row q ^ 5b of them: the eight lanes of a shared-memory access then read and write all eight 16-byte
         // places of a line of banks.
         if constexpr (Q8) {
+            constexpr int kUnits = 4 * C::kChunks;
             const int unit = lane & 3, row_in = (warp - C::kConvWarp) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
             bool ok = true;
-            int g = 0, piece = 0;  // tiles and pieces so far
+            int g = 0;  // tiles so far
             Segment sg;
             for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
                 const Live live = live_of(p, sg);
                 for (int j = sg.j0; ok && j < sg.j0 + sg.n; ++j, ++g) {
                     const int key0 = sg.all.tile(j) * kTileRows;
-                    // One copy of the code for K and V: with two (and both rows of a thread unrolled) the warps
-                    // of an SM no longer found their instructions in its cache (2.5 of 10.7 cycles per
-                    // instruction; 0.5 in the kernel of 16-bit caches).
+                    // One copy of the code for K and V: with two (and more of it unrolled) the warps of an SM no
+                    // longer found their instructions in its cache (2.5 of 10.7 cycles per instruction; 0.5 in
+                    // the kernel of 16-bit caches).
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {  // K lo, K hi, V lo, V hi
-                        const int v = h >> 1, hf = h & 1, st = piece % C::kPieces;
-                        const int slot = C::slot(g, v), use = C::use(g, v);
-                        if (hf == 0 && use > 0)
-                            ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
-                        ok = ok && wait_warp(&bar_rf[st], (uint32_t)(piece / C::kPieces) & 1u, abort_v, p.timeout_ns);
+                    for (int v = 0; v < 2; ++v) {
+                        const int slot = C::slot(g, v), use = C::use(g, v), st = v * C::kRaw + g % C::kRaw;
+                        ok = wait_warp(&bar_rf[st], (uint32_t)(g / C::kRaw) & 1u, abort_v, p.timeout_ns);
                         if (!ok) break;
-                        const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kPieceBytes);
-                        const uint8_t* ex = smem + C::kOffExp + st * C::kPieceRows;
+                        const uint32_t raw = smem_u32(smem + C::kOffRaw + st * C::kRawBytes);
+                        const uint8_t* ex = smem + C::kOffExp + st * kTileRows;
                         const uint32_t tile = smem_u32(smem + C::kOffKV + slot * C::kTileBytes);
-                        uint4 x[2][C::kChunks];  // (all reads first: they and the writes keep their order)
-                        uint32_t e[2], nan = 0u;
-                        bool usual = live.every(key0 + hf * 64, 64);
+                        uint4 x[kUnits];  // (all reads first: they and the writes keep their order)
+                        uint32_t e[4], nan = 0u;
+                        bool usual = live.every(key0, kTileRows);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < 4; ++k) {
                             const int r = row_in + 32 * k;
 #pragma unroll
                             for (int c = 0; c < C::kChunks; ++c) {
-                                x[k][c] = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
-                                                             : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
-                                if constexpr (BF16) nan |= nan_bytes(x[k][c]);
+                                uint4& y = x[k * C::kChunks + c];
+                                y = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                                                       : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
+                                if constexpr (BF16) nan |= nan_bytes(y);
                             }
                             e[k] = ex[r];
                             usual = usual && usual_exponent<BF16>(e[k]);
                         }
                         usual = usual && !(nan & 0x80808080u);
-                        auto line = [&](int k, int c, int i) {  // where 16-byte piece i of the unit goes
-                            const int row = hf * 64 + row_in + 32 * k;
+                        usual = __all_sync(0xffffffffu, usual);
+                        if (lane == 0) mbar_arrive(&bar_re[st]);
+                        if (use > 0) ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
+                        if (!ok) break;
+                        auto line = [&](int k, int c, int i) {  // where 16-byte piece i of a unit goes
+                            const int row = row_in + 32 * k;
                             return tile + c * kChunkBytes + row * 128 + ((uint32_t)((2 * unit + i) ^ (row & 7)) << 4);
                         };
                         // (A branch per unit would keep the units from overlapping: 1010 -> 1629 us.)
-                        if (__all_sync(0xffffffffu, usual)) {
+                        if (usual) {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
+                            for (int k = 0; k < 4; ++k) {
                                 const uint32_t f = row_factor<BF16>(e[k]);
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c) {
                                     uint32_t y[8];
-                                    scaled16<BF16>(x[k][c], f, y);
+                                    scaled16<BF16>(x[k * C::kChunks + c], f, y);
                                     sts_u32x4(line(k, c, 0), make_uint4(y[0], y[1], y[2], y[3]));
                                     sts_u32x4(line(k, c, 1), make_uint4(y[4], y[5], y[6], y[7]));
                                 }
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
+                            for (int k = 0; k < 4; ++k)
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c)
-                                    convert_any<BF16>(x[k][c], e[k], live.token(key0 + hf * 64 + row_in + 32 * k),
-                                                      line(k, c, 0), line(k, c, 1));
+                                    convert_any<BF16>(x[k * C::kChunks + c], e[k],
+                                                      live.token(key0 + row_in + 32 * k), line(k, c, 0),
+                                                      line(k, c, 1));
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&bar_re[st]);
-                            if (hf) mbar_arrive(&bar_f[slot]);
-                        }
-                        ++piece;
+                        if (lane == 0) mbar_arrive(&bar_f[slot]);
                     }
                 }
             }
