@@ -59,14 +59,14 @@ struct ChunkCfg {
     static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffExp = kOffRaw + 2 * kRaw * kRawBytes;
     static constexpr int kSmemBytes = kOffExp + 2 * kRaw * kTileRows + 1024;
-    // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 15: converters.
+    // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 19: converters.
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
-    static constexpr int kConverters = Q8 ? 4 : 0;
-    static constexpr int kThreads = Q8 ? 16 * 32 : 12 * 32;
+    static constexpr int kConverters = Q8 ? 8 : 0;
+    static constexpr int kThreads = (12 + kConverters) * 32;
     // Registers per thread of the softmax warps and of the others.  At launch each thread has kRegs; the sums
     // over the warpgroups are the same.
-    static constexpr int kRegs = Q8 ? 128 : 168;
-    static constexpr int kRegsSoftmax = Q8 ? 176 : 208, kRegsOther = Q8 ? 80 : 88;
+    static constexpr int kRegs = Q8 ? 96 : 168;
+    static constexpr int kRegsSoftmax = Q8 ? 168 : 208, kRegsOther = Q8 ? 48 : 88;
     static_assert(2 * kRegsSoftmax + (kThreads / 128 - 2) * kRegsOther == kThreads / 128 * kRegs,
                   "the launch's registers");
     static constexpr uint32_t kTmemCols = 512;
@@ -575,11 +575,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         wait_warp(&bar_fin, 0, nullptr, p.timeout_ns);
     } else if (Q8 && warp >= C::kConvWarp) {
         // ------------------------------ converters ------------------------------
-        // Each warp takes eight of every 32 rows of a tile.  Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of
+        // Each warp takes eight of every 64 rows of a tile.  Lane 8 q + 4 b + i takes 16-byte units i (and 4 + i) of
         // row q ^ 5b of them: the eight lanes of a shared-memory access then read and write all eight 16-byte
         // places of a line of banks.
         if constexpr (Q8) {
-            constexpr int kUnits = 4 * C::kChunks;
+            constexpr int kRows = kTileRows / (8 * C::kConverters), kUnits = kRows * C::kChunks;
             const int unit = lane & 3, row_in = (warp - C::kConvWarp) * 8 + ((lane >> 3) ^ (5 * ((lane >> 2) & 1)));
             bool ok = true;
             int g = 0;  // tiles so far
@@ -600,11 +600,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                         const uint8_t* ex = smem + C::kOffExp + st * kTileRows;
                         const uint32_t tile = smem_u32(smem + C::kOffKV + slot * C::kTileBytes);
                         uint4 x[kUnits];  // (all reads first: they and the writes keep their order)
-                        uint32_t e[4], nan = 0u;
+                        uint32_t e[kRows], nan = 0u;
                         bool usual = live.every(key0, kTileRows);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int r = row_in + 32 * k;
+                        for (int k = 0; k < kRows; ++k) {
+                            const int r = row_in + 8 * C::kConverters * k;
 #pragma unroll
                             for (int c = 0; c < C::kChunks; ++c) {
                                 uint4& y = x[k * C::kChunks + c];
@@ -621,13 +621,13 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                         if (use > 0) ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
                         if (!ok) break;
                         auto line = [&](int k, int c, int i) {  // where 16-byte piece i of a unit goes
-                            const int row = row_in + 32 * k;
+                            const int row = row_in + 8 * C::kConverters * k;
                             return tile + c * kChunkBytes + row * 128 + ((uint32_t)((2 * unit + i) ^ (row & 7)) << 4);
                         };
                         // (A branch per unit would keep the units from overlapping: 1010 -> 1629 us.)
                         if (usual) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < kRows; ++k) {
                                 const uint32_t f = row_factor<BF16>(e[k]);
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c) {
@@ -639,11 +639,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                             }
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
+                            for (int k = 0; k < kRows; ++k)
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c)
                                     convert_any<BF16>(x[k * C::kChunks + c], e[k],
-                                                      live.token(key0 + row_in + 32 * k), line(k, c, 0),
+                                                      live.token(key0 + row_in + 8 * C::kConverters * k), line(k, c, 0),
                                                       line(k, c, 1));
                         }
                         fence_proxy_async_smem();
