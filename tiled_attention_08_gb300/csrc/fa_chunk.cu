@@ -114,61 +114,29 @@ __device__ __forceinline__ void rows_out(uint32_t (&m)[8][4], uint8_t* dst, int 
     }
 }
 
-// Sixteen e4m3 bytes times 2^(E - 127), rounded once to 16 bits.
-//
-// In the usual case by a product of the 16-bit type.  bf16: sign, exponent and mantissa of a byte are moved to
-// their places (its exponent field 0 .. 15 becomes bf16's, subnormals included), which gives 2^-120 of its
-// value; the factor makes up for that.  fp16: converted, then scaled.  `usual`: the factor is a number of the
-// type, and no byte is e4m3's NaN (0x7f, 0xff), which the moved bits would lose.
+// Sixteen e4m3 bytes times an fp32 power of two, rounded once to 16 bits.  By way of fp16 and fp32: five
+// instructions per two values, over the conversion, fp and integer pipes.  (Moving sign, exponent and mantissa to
+// their places in bf16 and one 16-bit product are as many, most of them on the integer pipe, and lose a NaN byte and
+// rows of extreme size, which then have to be looked for: 792 and 829 us against 774 for chunks of 512 behind
+// up to 16384 tokens, 64 heads on 8 of 128.)
 template <bool BF16>
-__device__ __forceinline__ uint32_t row_factor(uint32_t E) {
-    const uint32_t x = BF16 ? (E + 120u) << 7 : (E - 112u) << 10;
-    return x | x << 16;
-}
-template <bool BF16>
-__device__ __forceinline__ bool usual_exponent(uint32_t E) {
-    return BF16 ? E <= 134u : E - 113u <= 29u;  // 2^(E - 7) and 2^(E - 127) are normal numbers
-}
-// Bit 7 of a byte is set where one of the bytes of x is a NaN.
-__device__ __forceinline__ uint32_t nan_bytes(const uint4& x) {
-    return ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
-           ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
-}
-template <bool BF16>
-__device__ __forceinline__ void scaled16(const uint4& x, uint32_t f, uint32_t (&y)[8]) {
+__device__ __forceinline__ void scaled16(const uint4& x, uint64_t f2, uint32_t (&y)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if constexpr (BF16) {
+        uint32_t h[2];
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(h[0]), "=r"(h[1])
+            : "r"(w[i]));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t b = __byte_perm(w[i], 0u, h ? 0x3424 : 0x1404);  // each byte on top of a half
-                asm("mul.rn.bf16x2 %0, %1, %2;"
-                    : "=r"(y[2 * i + h])
-                    : "r"((b >> 4 & 0x07f007f0u) | (b & 0x80008000u)), "r"(f));
-            }
-        } else {
-            asm("{\n\t.reg .b16 l, h;\n\t.reg .b32 a, b;\n\tmov.b32 {l, h}, %2;\n\t"
-                "cvt.rn.f16x2.e4m3x2 a, l;\n\tcvt.rn.f16x2.e4m3x2 b, h;\n\t"
-                "mul.rn.f16x2 %0, a, %3;\n\tmul.rn.f16x2 %1, b, %3;\n\t}"
-                : "=r"(y[2 * i]), "=r"(y[2 * i + 1])
-                : "r"(w[i]), "r"(f));
+        for (int k = 0; k < 2; ++k) {
+            const float2 a = unpack2<false>(h[k]);
+            float lo, hi;
+            f2_split(f2_mul(f2_make(a.x, a.y), f2), lo, hi);
+            y[2 * i + k] = pack2<BF16>(lo, hi);
         }
     }
-}
-// The same for any exponent and any bytes, and zeros where `there` is false; out of line.
-template <bool BF16>
-__device__ __noinline__ void convert_any(uint4 x, uint32_t E, bool there, uint32_t to0, uint32_t to1) {
-    const float f = row_scale(E);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 a = unpack2<false>(e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)) & 0xffffu));
-        y[i] = there ? pack2<BF16>(a.x * f, a.y * f) : 0u;
-    }
-    sts_u32x4(to0, make_uint4(y[0], y[1], y[2], y[3]));
-    sts_u32x4(to1, make_uint4(y[4], y[5], y[6], y[7]));
 }
 
 // New tokens of sequence b and the tokens in front of them; none where the lengths are out of range.
@@ -600,51 +568,45 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                         const uint8_t* ex = smem + C::kOffExp + st * kTileRows;
                         const uint32_t tile = smem_u32(smem + C::kOffKV + slot * C::kTileBytes);
                         uint4 x[kUnits];  // (all reads first: they and the writes keep their order)
-                        uint32_t e[kRows], nan = 0u;
-                        bool usual = live.every(key0, kTileRows);
+                        float f[kRows];
+                        auto row_of = [&](int k) { return row_in + 8 * C::kConverters * k; };
 #pragma unroll
                         for (int k = 0; k < kRows; ++k) {
-                            const int r = row_in + 8 * C::kConverters * k;
+                            const int r = row_of(k);
 #pragma unroll
-                            for (int c = 0; c < C::kChunks; ++c) {
-                                uint4& y = x[k * C::kChunks + c];
-                                y = lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
+                            for (int c = 0; c < C::kChunks; ++c)
+                                x[k * C::kChunks + c] =
+                                    lds_u32x4(D == 128 ? raw + r * 128 + (uint32_t)((c * 4 + unit) ^ (r & 7)) * 16
                                                        : raw + r * 64 + (uint32_t)(unit ^ ((r >> 1) & 3)) * 16);
-                                if constexpr (BF16) nan |= nan_bytes(y);
-                            }
-                            e[k] = ex[r];
-                            usual = usual && usual_exponent<BF16>(e[k]);
+                            f[k] = row_scale(ex[r]);
                         }
-                        usual = usual && !(nan & 0x80808080u);
-                        usual = __all_sync(0xffffffffu, usual);
+                        __syncwarp();
                         if (lane == 0) mbar_arrive(&bar_re[st]);
-                        if (use > 0) ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
-                        if (!ok) break;
-                        auto line = [&](int k, int c, int i) {  // where 16-byte piece i of a unit goes
-                            const int row = row_in + 8 * C::kConverters * k;
-                            return tile + c * kChunkBytes + row * 128 + ((uint32_t)((2 * unit + i) ^ (row & 7)) << 4);
-                        };
-                        // (A branch per unit would keep the units from overlapping: 1010 -> 1629 us.)
-                        if (usual) {
+                        if (!live.every(key0, kTileRows)) {  // tokens that nobody sees: zeros
 #pragma unroll
                             for (int k = 0; k < kRows; ++k) {
-                                const uint32_t f = row_factor<BF16>(e[k]);
-#pragma unroll
-                                for (int c = 0; c < C::kChunks; ++c) {
-                                    uint32_t y[8];
-                                    scaled16<BF16>(x[k * C::kChunks + c], f, y);
-                                    sts_u32x4(line(k, c, 0), make_uint4(y[0], y[1], y[2], y[3]));
-                                    sts_u32x4(line(k, c, 1), make_uint4(y[4], y[5], y[6], y[7]));
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < kRows; ++k)
+                                if (live.token(key0 + row_of(k))) continue;
+                                f[k] = 0.0f;
 #pragma unroll
                                 for (int c = 0; c < C::kChunks; ++c)
-                                    convert_any<BF16>(x[k * C::kChunks + c], e[k],
-                                                      live.token(key0 + row_in + 8 * C::kConverters * k), line(k, c, 0),
-                                                      line(k, c, 1));
+                                    x[k * C::kChunks + c] = make_uint4(0u, 0u, 0u, 0u);
+                            }
+                        }
+                        if (use > 0) ok = wait_warp(&bar_e[slot], ((uint32_t)use & 1u) ^ 1u, abort_v, p.timeout_ns);
+                        if (!ok) break;
+#pragma unroll
+                        for (int k = 0; k < kRows; ++k) {
+                            const int row = row_of(k);
+#pragma unroll
+                            for (int c = 0; c < C::kChunks; ++c) {
+                                uint32_t y[8];
+                                scaled16<BF16>(x[k * C::kChunks + c], f2_make(f[k], f[k]), y);
+                                const uint32_t line = tile + c * kChunkBytes + row * 128;
+                                sts_u32x4(line + ((uint32_t)((2 * unit) ^ (row & 7)) << 4),
+                                          make_uint4(y[0], y[1], y[2], y[3]));
+                                sts_u32x4(line + ((uint32_t)((2 * unit + 1) ^ (row & 7)) << 4),
+                                          make_uint4(y[4], y[5], y[6], y[7]));
+                            }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
