@@ -62,12 +62,11 @@ struct ChunkCfg {
     // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 19: converters.
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
     static constexpr int kConverters = Q8 ? 8 : 0;
-    static constexpr int kThreads = (12 + kConverters) * 32;
-    // Registers per thread of the softmax warps and of the others.  At launch each thread has kRegs; the sums
-    // over the warpgroups are the same.
-    static constexpr int kRegs = Q8 ? 96 : 168;
-    static constexpr int kRegsSoftmax = Q8 ? 168 : 208, kRegsOther = Q8 ? 48 : 88;
-    static_assert(2 * kRegsSoftmax + (kThreads / 128 - 2) * kRegsOther == kThreads / 128 * kRegs,
+    static constexpr int kThreads = (Q8 ? 12 + kConverters : 11) * 32;
+    // e4m3: registers per thread of the softmax warps and of the others.  At launch each thread has kRegs; the
+    // sums over the warpgroups are the same.  (16-bit: 168 for everyone; 208 and 88 took 2% more.)
+    static constexpr int kRegs = 96, kRegsSoftmax = 168, kRegsOther = 48;
+    static_assert(!Q8 || 2 * kRegsSoftmax + (kThreads / 128 - 2) * kRegsOther == kThreads / 128 * kRegs,
                   "the launch's registers");
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kTmS = 0, kTmO = 256;
@@ -76,15 +75,6 @@ struct ChunkCfg {
     static constexpr uint32_t kIdescS = idesc_f16(BF16, 128, 128, false, false);
     static constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, false, true);
 };
-
-template <int N>
-__device__ __forceinline__ void regs_raise() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_lower() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 // Every lane of a warp holds a row's 128 bytes, 8 units of 16, bound for dst (null: not written).  The units
 // are transposed in groups of eight lanes (a butterfly of xor shuffles; see tmem_rows_to_global_xpose), so that
@@ -355,7 +345,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
 
     // (A warpgroup sets its registers with one instruction.)
     if (warp >= 8) {
-    regs_lower<C::kRegsOther>();
+    if constexpr (Q8) regs_lower<C::kRegsOther>();
     if (warp == C::kKWarp || warp == C::kVWarp) {
         // ------------------------------ TMA producers ------------------------------
         // The K warp brings each segment's query pair, and K's pages; the V warp V's.  Lane 8c + i issues page i
@@ -619,7 +609,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     }
     } else {
         // ------------------------------ softmax warps ------------------------------
-        regs_raise<C::kRegsSoftmax>();
+        if constexpr (Q8) regs_raise<C::kRegsSoftmax>();
         const int t = warp / 4, quad = warp % 4;
         const int row = quad * 32 + lane;  // row inside the tile == TMEM lane
         const int head = row / p.T, tok = row - head * p.T;
