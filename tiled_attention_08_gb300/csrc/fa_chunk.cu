@@ -20,7 +20,8 @@
 //  * split: lengths are known on the device only, and rows alone seldom fill 152 SMs.  Units (head, pair of
 //    query tiles, key tile) form one line, of which every CTA takes an equal stretch: each CTA first
 //    sums the pairs' key tiles.  A pair that lies whole in a stretch is written as O and LSE; of a cut
-//    one each CTA leaves an fp32 part (two at most), which fa_chunk_join_kernel joins.
+//    one each CTA leaves an fp32 part (two at most), and the one that finds the others' there joins them.  (A kernel
+//    of its own for that took 16 of 177 us for two prompts of 4096 tokens, 6 of 24 for one short turn.)
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
@@ -42,7 +43,7 @@ struct ChunkCfg {
     static constexpr int kTileBytes = kTileRows * D * 2;
     // Tile slots.  16-bit caches: a ring for K and one for V.  e4m3: one ring, K and V in turn, of three
     // slots at D = 128 (a step reads V_j and K_{j+1} while V_{j+1} is converted), which leaves room for
-    // twice as many bytes in flight (32 KB of them with two rings of two: 1139 us where 64 KB take XXX).
+    // twice as many bytes in flight (32 KB of them with two rings of two).
     static constexpr int kStages = (D == 128) ? 2 : 4;
     static constexpr int kSlots = Q8 ? ((D == 128) ? 3 : 6) : 2 * kStages;
     static constexpr int kOffQ = 0;
@@ -229,6 +230,89 @@ __device__ __forceinline__ int unit_cta(long long units, int grid, long long u) 
     return (int)(((u + 1) * grid - 1) / units);
 }
 
+// Joins the n_parts parts of a pair of query tiles, which CTAs owner, owner + 1, ... left: the tiles' rows are dealt
+// out to the warps, eight at a time.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).
+template <int D, bool BF16>
+__device__ __noinline__ void join_parts(const ChunkParams& p, int b, int hk, int t0, int fresh, int owner, int n_parts,
+                                        int warp, int lane) {
+    constexpr int kPer = D / 32, kRows = 8;
+    const int rows = t0 + p.T < fresh ? 2 * kTileRows : kTileRows, per_warp = rows / 8;
+#pragma unroll 1
+    for (int r0 = warp * per_warp; r0 < (warp + 1) * per_warp; r0 += kRows) {
+        // Lane 8 q + r: row r0 + r, of which it takes the log-sum-exp of parts q, q + 4, ...
+        const int my_r = r0 + (lane & (kRows - 1)), my_t = my_r >> 7, my_row = my_r & (kTileRows - 1);
+        const int my_head = my_row / p.T, my_i = t0 + my_t * p.T + my_row - my_head * p.T;
+        const bool mine = my_head < p.group && my_i < fresh;
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        auto part_at = [&](int r, int c) {  // row r of the two tiles
+            return (2 * (size_t)(owner + c) + (c == 0 ? 1 : 0)) * (2 * kTileRows) + r;
+        };
+        float top = -INFINITY, sum = 0.0f, x[kRows][kPer];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) x[r][e] = 0.0f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < n_parts; c0 += 2) {  // two parts: their loads are in flight together
+            const int q = lane >> 3;
+            const float y = mine && q < 2 && c0 + q < n_parts ? __ldcg(p.slot_lse + part_at(my_r, c0 + q)) : -INFINITY;
+            float v[2][kRows][kPer];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float* src = p.slot_o + part_at(r0, imin(c0 + c, n_parts - 1)) * D + lane * kPer;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    if constexpr (kPer == 4) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(src + (size_t)r * D));
+                        v[c][r][0] = u.x;
+                        v[c][r][1] = u.y;
+                        v[c][r][2] = u.z;
+                        v[c][r][3] = u.w;
+                    } else {
+                        const float2 u = __ldcg(reinterpret_cast<const float2*>(src + (size_t)r * D));
+                        v[c][r][0] = u.x;
+                        v[c][r][1] = u.y;
+                    }
+                }
+            }
+            const float other = __shfl_xor_sync(0xffffffffu, y, 8);  // (lanes 0 .. 15 hold the two parts)
+            const float next = fmaxf(top, fmaxf(y, other)), base = next == -INFINITY ? 0.0f : next;
+            const float f = ex2_approx(top - base);
+            const float w = y == -INFINITY ? 0.0f : ex2_approx(y - base);  // (a NaN stays)
+            sum = fmaf(sum, f, w + __shfl_xor_sync(0xffffffffu, w, 8));
+            top = next;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float fr = __shfl_sync(0xffffffffu, f, r);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) x[r][e] *= fr;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float wr = __shfl_sync(0xffffffffu, w, 8 * c + r);
+                    if (wr == 0.0f) continue;  // (of a part without a key nothing was written)
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) x[r][e] = fmaf(wr, v[c][r][e], x[r][e]);
+                }
+            }
+        }
+        const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;  // (in lanes 0 .. 15)
+        const size_t my_orow = (size_t)b * p.Hq + hk * p.group + my_head;
+        if (mine && lane < kRows)
+            p.lse[my_orow * p.L + my_i] = sum != 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        uint8_t* my_dst = mine ? reinterpret_cast<uint8_t*>(p.o) + row_offset(p.so, (int)my_orow, p.Hq, my_i) : nullptr;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float f = __shfl_sync(0xffffffffu, inv, r);
+            uint8_t* dst = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(my_dst), r));
+            if (!dst) continue;
+            uint32_t* d = reinterpret_cast<uint32_t*>(dst) + lane * (kPer / 2);
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2) d[e / 2] = pack2<BF16>(x[r][e] * f, x[r][e + 1] * f);
+        }
+    }
+}
+
 template <int D, bool BF16, bool Q8>
 __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     fa_chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -238,16 +322,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                                ~uintptr_t(1023));
     __shared__ uint64_t bar_qf, bar_qe, bar_f[C::kSlots], bar_e[C::kSlots];  // slots full / empty
     __shared__ uint64_t bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint64_t bar_part, bar_ticket;  // a part written by all softmax warps; counted
     __shared__ uint64_t bar_rf[Q8 ? 2 * C::kRaw : 1], bar_re[Q8 ? 2 * C::kRaw : 1];  // bytes landed / read
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     __shared__ int warp_sum[C::kThreads / 32];
     __shared__ Walk start_sh;
     __shared__ long long total_sh;
+    __shared__ int ticket_sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int* abort_v = &abort_flag;
 
-    pdl_launch_dependents();
     if (threadIdx.x == 0) {
         if (p.num_pages > 0) tma_prefetch_desc(&p.tm_q);
         if (p.num_pages > 0) {
@@ -271,6 +356,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             mbar_init(&bar_rf[s], 1);
             mbar_init(&bar_re[s], C::kConverters);
         }
+        mbar_init(&bar_part, 8);
+        mbar_init(&bar_ticket, 1);
         mbar_init(&bar_fin, 1);
         mbar_fence_init();
     }
@@ -610,6 +697,22 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     } else {
         // ------------------------------ softmax warps ------------------------------
         if constexpr (Q8) regs_raise<C::kRegsSoftmax>();
+        // While the first tiles are on their way: the rows without a token get zeros and -inf, 64 rows of a head
+        // at a time.
+        const int blocks_l = (p.L + 63) / 64;
+        const long long fills = (long long)p.B * p.Hq * blocks_l;
+        for (long long it = (long long)blockIdx.x * 8 + warp; it < fills; it += (long long)gridDim.x * 8) {
+            const int bh = (int)(it / blocks_l), i0 = (int)(it - (long long)bh * blocks_l) * 64;
+            int n, ahead;
+            sequence(p, bh / p.Hq, n, ahead);
+            const int from = imax(n, i0), to = imin(i0 + 64, p.L);
+            for (int e = from * (D / 8) + lane; e < to * (D / 8); e += 32) {
+                const int i = e / (D / 8), u = e % (D / 8);
+                reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.o) + row_offset(p.so, bh, p.Hq, i))[u] =
+                    make_uint4(0u, 0u, 0u, 0u);
+                if (u == 0) p.lse[(size_t)bh * p.L + i] = -INFINITY;
+            }
+        }
         const int t = warp / 4, quad = warp % 4;
         const int row = quad * 32 + lane;  // row inside the tile == TMEM lane
         const int head = row / p.T, tok = row - head * p.T;
@@ -617,8 +720,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         const uint32_t s_addr = tmem + lane_off + C::kTmS + 128 * t;
         const uint32_t o_addr = tmem + lane_off + C::kTmO + D * t;
         const uint64_t scale2 = f2_make(p.scale_log2, p.scale_log2);
-        bool ok = true, cut_behind = false;
-        int ps = 0, n_done = 0;
+        bool ok = true;
+        int ps = 0, n_done = 0, n_cut = 0;
         Segment sg;
         for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
             const int j1 = sg.j0 + sg.n, cnt = sg.count(t);
@@ -696,12 +799,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             if (!ok) break;
             const bool valid = head < p.group && sg.t0 + t * p.T + tok < sg.fresh;
             const bool whole = sg.whole(), behind = !whole && sg.j0 == 0;  // (behind: it goes on in the next CTA)
-            cut_behind |= behind;
-            if (behind && threadIdx.x == 0) {  // for the join: the pair and the CTAs that have its tiles
-                const long long x = (total_sh * blockIdx.x / workers) + (start_sh.left - walk.left);
-                const int n_parts = unit_cta(total_sh, workers, x + sg.n_all - 1) - (int)blockIdx.x + 1;
-                p.owners[blockIdx.x] = make_int4(sg.b, sg.hk, sg.t0, n_parts);
-            }
             const size_t slot = 2 * (size_t)blockIdx.x + (behind ? 1 : 0);
             const size_t part = (slot * 2 + t) * kTileRows + row;
             if (cnt > 0) {
@@ -750,10 +847,33 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                         rows_out(m, dst ? reinterpret_cast<uint8_t*>(dst + c * 32) : nullptr, lane);
                     }
                 }
+                // The CTA that ends the pair's last part joins them all.
+                const long long x0 = total_sh * blockIdx.x / workers + (start_sh.left - walk.left) - sg.j0;
+                const int owner = unit_cta(total_sh, workers, x0);
+                const int n_parts = unit_cta(total_sh, workers, x0 + sg.n_all - 1) - owner + 1;
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_part);
+                if (warp == 0) {
+                    ok = wait_warp(&bar_part, (uint32_t)n_cut & 1u, abort_v, p.timeout_ns);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        pdl_wait();  // the counters are zeroed
+                        *reinterpret_cast<volatile int*>(&ticket_sh) = atomicAdd(&p.counters[owner], 1);
+                        mbar_arrive(&bar_ticket);
+                    }
+                    __syncwarp();
+                }
+                ok = wait_warp(&bar_ticket, (uint32_t)n_cut & 1u, abort_v, p.timeout_ns);
+                if (!ok) break;
+                ++n_cut;
+                if (*reinterpret_cast<volatile int*>(&ticket_sh) == n_parts - 1) {
+                    __threadfence();
+                    join_parts<D, BF16>(p, sg.b, sg.hk, sg.t0, sg.fresh, owner, n_parts, warp, lane);
+                }
             }
         }
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
-        if (threadIdx.x == 0 && !(cut_behind && ok)) p.owners[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
 
     tc_fence_before_sync();
@@ -764,103 +884,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     }
 }
 
-// Joins the parts of the pairs that are cut: block (c, y) the rows 16 y .. of the pair that goes on behind
-// CTA c, two rows a warp.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).  And, before that, the rows
-// without a token: zeros and -inf, 64 rows of a head per warp.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) fa_chunk_join_kernel(const ChunkParams p) {
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int blocks_l = (p.L + 63) / 64;
-    const long long items = (long long)p.B * p.Hq * blocks_l;
-    for (long long it = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; it < items;
-         it += (long long)gridDim.x * gridDim.y * 8) {
-        const int bh = (int)(it / blocks_l), i0 = (int)(it - (long long)bh * blocks_l) * 64;
-        int n, ahead;
-        sequence(p, bh / p.Hq, n, ahead);
-        const int from = imax(n, i0), to = imin(i0 + 64, p.L);
-        for (int e = from * (D / 8) + lane; e < to * (D / 8); e += 32) {
-            const int i = e / (D / 8), u = e % (D / 8);
-            reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.o) + row_offset(p.so, bh, p.Hq, i))[u] =
-                make_uint4(0u, 0u, 0u, 0u);
-            if (u == 0) p.lse[(size_t)bh * p.L + i] = -INFINITY;
-        }
-    }
-    pdl_wait();
-    const int4 own = p.owners[blockIdx.x];
-    const int n_parts = own.w;
-    // (A kernel that gave up on a wait may have left an entry as it found it.)
-    if (n_parts < 2 || n_parts > (int)gridDim.x - (int)blockIdx.x || own.x < 0 || own.x >= p.B || own.y < 0 ||
-        own.y >= p.Hk || own.z < 0)
-        return;
-    int fresh, before;
-    sequence(p, own.x, fresh, before);
-    // Two rows a warp; lane c takes the log-sum-exp of parts c, c + 32, ...
-    int out_i[2];
-    size_t orow[2], part0[2] = {0, 0};
-    float top[2], sum[2], x[2][kPer];
-    auto part_at = [&](int r, int c) {  // of row r of the warp
-        return part0[r] + (c == 0 ? 0 : (2 * (size_t)c - 1) * 2 * kTileRows);
-    };
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int r2 = (int)blockIdx.y * 16 + warp * 2 + r;  // row of the two tiles
-        const int t = r2 >> 7, row = r2 & 127, head = row / p.T, tok = row - head * p.T;
-        const int i = own.z + t * p.T + tok;
-        out_i[r] = head < p.group && i < fresh ? i : -1;
-        orow[r] = (size_t)own.x * p.Hq + own.y * p.group + head;
-        part0[r] = ((2 * (size_t)blockIdx.x + 1) * 2 + t) * kTileRows + row;
-        top[r] = -INFINITY;
-        sum[r] = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) x[r][e] = 0.0f;
-    }
-    for (int c0 = 0; c0 < n_parts; c0 += 32) {
-        float y[2], w[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            y[r] = out_i[r] >= 0 && c0 + lane < n_parts ? p.slot_lse[part_at(r, c0 + lane)] : -INFINITY;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float m = y[r];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            const float next = fmaxf(top[r], m), base = next == -INFINITY ? 0.0f : next;
-            const float f = ex2_approx(top[r] - base);
-            w[r] = y[r] == -INFINITY ? 0.0f : ex2_approx(y[r] - base);  // (NaN stays)
-            float s = w[r];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-            sum[r] = fmaf(sum[r], f, s);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) x[r][e] *= f;
-            top[r] = next;
-        }
-        const int n = imin(n_parts - c0, 32);
-#pragma unroll 4
-        for (int c = 0; c < n; ++c) {
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float wc = __shfl_sync(0xffffffffu, w[r], c);
-                if (wc == 0.0f) continue;  // (of a part without a key nothing was written)
-                const float* src = p.slot_o + part_at(r, c0 + c) * D + lane * kPer;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) x[r][e] = fmaf(wc, src[e], x[r][e]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        if (out_i[r] < 0) continue;
-        const float inv = sum[r] != 0.0f ? 1.0f / sum[r] : 0.0f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.o) +
-                                                    row_offset(p.so, (int)orow[r], p.Hq, out_i[r])) +
-                        lane * (kPer / 2);
-#pragma unroll
-        for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack2<BF16>(x[r][e] * inv, x[r][e + 1] * inv);
-        if (lane == 0)
-            p.lse[orow[r] * p.L + out_i[r]] = sum[r] != 0.0f ? (top[r] + log2f(sum[r])) * kLn2 : -INFINITY;
-    }
+// The counters of the pairs that are cut.
+__global__ void __launch_bounds__(kChunkGrid) fa_chunk_zero_kernel(int* counters, int n) {
+    pdl_launch_dependents();
+    if ((int)threadIdx.x < n) counters[threadIdx.x] = 0;
 }
 
 template <int D, bool BF16, bool Q8>
@@ -870,7 +897,7 @@ cudaError_t launch_t(const ChunkParams& p, cudaStream_t s) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kern, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmemBytes, s, p);
+    return launch_kernel_early(kern, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmemBytes, s, p);
 }
 
 }  // namespace
@@ -891,13 +918,8 @@ cudaError_t launch_chunk(const ChunkParams& p, int D, bool bf16, bool q8, cudaSt
     return bf16 ? launch_t<128, true, false>(p, s) : launch_t<128, false, false>(p, s);
 }
 
-cudaError_t launch_chunk_join(const ChunkParams& p, int D, bool bf16, cudaStream_t s) {
-    const dim3 grid((unsigned)p.grid, 16), block(256);
-    if (D == 64)
-        return bf16 ? launch_kernel_early(fa_chunk_join_kernel<64, true>, grid, block, 0, s, p)
-                    : launch_kernel_early(fa_chunk_join_kernel<64, false>, grid, block, 0, s, p);
-    return bf16 ? launch_kernel_early(fa_chunk_join_kernel<128, true>, grid, block, 0, s, p)
-                : launch_kernel_early(fa_chunk_join_kernel<128, false>, grid, block, 0, s, p);
+cudaError_t launch_chunk_zero(const ChunkParams& p, cudaStream_t s) {
+    return launch_kernel(fa_chunk_zero_kernel, dim3(1), dim3(kChunkGrid), 0, s, p.counters, p.grid);
 }
 
 }  // namespace fa

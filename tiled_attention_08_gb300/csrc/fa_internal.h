@@ -303,8 +303,7 @@ struct ChunkParams {
     Strides so;
     float* lse;                  // [B, Hq, L]
     float *slot_o, *slot_lse;    // [2 * grid, 2 * 128, D], [2 * grid, 2 * 128]: parts of cut pairs (LSE in log2)
-    int4* owners;                // [grid]: sequence, cache head, first token and parts of the pair that goes
-                                 // on behind each CTA
+    int* counters;               // [grid]: parts that are there of the pair that goes on behind each CTA
     int B, Hq, Hk, L, group, num_pages, max_pages;
     int window, sinks;           // (no window: 2^30, 0)
     int T, max_pairs;            // tokens of a query tile, pairs of tiles of a sequence at most
@@ -410,7 +409,7 @@ cudaError_t launch_window_join(const WindowBwdParams& p, int D, bool bf16, cudaS
 // The work split of a chunk: fills T, max_pairs, grid.
 void chunk_plan(int B, int Hk, int group, int L, int max_pages, ChunkParams* p);
 cudaError_t launch_chunk(const ChunkParams& p, int D, bool bf16, bool q8, cudaStream_t s);
-cudaError_t launch_chunk_join(const ChunkParams& p, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_chunk_zero(const ChunkParams& p, cudaStream_t s);
 cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s);
 // Query rows of a block (8 or 16), the most warps that a step may launch (workspace), and those it
 // does (busy_sms: SMs that an earlier kernel still holds).

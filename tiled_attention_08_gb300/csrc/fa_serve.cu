@@ -273,7 +273,7 @@ fa_status check_chunk(int B, int Hq, int Hk, int L, int D, int num_pages, int ma
     return FA_OK;
 }
 
-// Workspace of a chunk's attention, in bytes from its start (the owners come first).
+// Workspace of a chunk's attention, in bytes from its start (the counters come first).
 struct ChunkWorkspace {
     size_t slot_lse, slot_o, bytes;
 };
@@ -607,7 +607,7 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
     p.lse = lse;
     p.slot_o = reinterpret_cast<float*>(ws + w.slot_o);
     p.slot_lse = reinterpret_cast<float*>(ws + w.slot_lse);
-    p.owners = reinterpret_cast<int4*>(ws);
+    p.counters = reinterpret_cast<int*>(ws);
     p.B = B;
     p.Hq = Hq;
     p.Hk = Hk;
@@ -625,9 +625,9 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
     p.timeout_ns = wait_timeout_ns();
     if (!p.status) return FA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (traced_launch(0, s, [&] { return launch_chunk(p, D, bf16, q8, s); }) != cudaSuccess) return FA_ERR_CUDA;
-    return traced_launch(1, s, [&] { return launch_chunk_join(p, D, bf16, s); }) == cudaSuccess ? FA_OK
-                                                                                               : FA_ERR_CUDA;
+    // (The second kernel starts beside the first, and waits for it before it counts.)
+    if (traced_launch(0, s, [&] { return launch_chunk_zero(p, s); }) != cudaSuccess) return FA_ERR_CUDA;
+    return traced_launch(1, s, [&] { return launch_chunk(p, D, bf16, q8, s); }) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 size_t fa_shared_prefix_workspace_bytes(int B, int Hq, int Hk, int D, int prefix_len,
