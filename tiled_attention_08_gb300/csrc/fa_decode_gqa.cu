@@ -85,7 +85,18 @@ constexpr int kGqaSms = 152;     // the grid is sized for this many SMs on any d
                                  // workspace does not depend on it
 constexpr int kGqaMinPages = 4;  // pages of a warp's stretch at least ...
 constexpr int kGqaFewPages = 1024;  // ... where there are more than this many
-constexpr int kClusterCtas = 8;  // of a unit in a short step
+constexpr int kClusterCtas = 8;  // of a unit in a short step (under a window 8, 4, 2 or 1)
+// Under a window sequences read up to the same number of pages, so that a unit per CTA (or two or four CTAs) balances
+// by itself, while the pages a CTA are few.  us with a cluster and with the line, group 4, sequences longer than the
+// window / of mixed length:
+//   e4m3, heads of 128, a CTA a unit, 512 units:  9 pages 11.4 and 14.4 / 11.4 and 15.6; 33 20.6 and 24.0 / 19.3 and
+//     21.4; 65 31.4 and 32.5 / 29.7 and 30.1; 129 52.2 and 51.6 / 50.0 and 39.6
+//   the same, four CTAs, 128 units:  33 pages a CTA 19.6 and 23.7 / 18.0 and 20.8; 65 29.6 and 32.9 / 28.7 and 29.2;
+//     129 50.2 and 51.7 / 49.4 and 44.4
+//   16-bit, a CTA a unit, 256 units:  65 pages 25.2 and 28.5 / 20.0 and 25.1; 129 44.8 and 48.2 / 34.8 and 37.6;
+//     513 160.5 and 165.8 / 123.8 and 124.3
+// (16-bit caches would gain from more, but one long sequence among short ones is then left to a few warps.)
+constexpr int kGqaWindowPagesQ8 = 72, kGqaWindowPages = 136;
 constexpr int kGqaManyUnits = 2048;  // from so many on the line is dealt out in three rounds
 
 // The split of the line of `total` pages.  One round: `workers` warps take equal stretches.  Not
@@ -292,8 +303,9 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
     const int per_seq = p.Hk * p.q_blocks;  // units of a sequence
-    const int unit_id = (int)blockIdx.x / kClusterCtas, short_b = unit_id / per_seq;  // (SHORT)
-    const int short_unit = unit_id - short_b * per_seq, rank = (int)blockIdx.x % kClusterCtas;
+    const int ctas_of = WIN ? p.short_step : kClusterCtas;  // (SHORT) CTAs of a unit
+    const int unit_id = (int)blockIdx.x / ctas_of, short_b = unit_id / per_seq;
+    const int short_unit = unit_id - short_b * per_seq, rank = (int)blockIdx.x % ctas_of;
     pdl_launch_dependents();
     // The queries into L2 (they are read when a warp begins a unit, behind the stream of pages).
     for (size_t at = ((size_t)blockIdx.x * (kWarps * 32) + threadIdx.x) * 128;
@@ -322,10 +334,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     int w = 0, mine = 0;  // this worker, and its pages x0 .. x0 + mine - 1 of the line (SHORT: of the unit)
     long long x0 = 0, total = 0;
     if constexpr (SHORT) {
-        const int n_pages = pages_of(short_b), i = warp * kClusterCtas + rank;  // neighbours on different SMs
-        constexpr int kWorkers = kClusterCtas * kWarps;
-        x0 = n_pages * (long long)i / kWorkers;
-        mine = (int)(n_pages * (long long)(i + 1) / kWorkers - x0);
+        const int n_pages = pages_of(short_b), i = warp * ctas_of + rank;  // neighbours on different SMs
+        const int workers = ctas_of * kWarps;
+        x0 = n_pages * (long long)i / workers;
+        mine = (int)(n_pages * (long long)(i + 1) / workers - x0);
         __syncthreads();  // (the barriers are initialised)
     } else {
         int sum = 0;
@@ -827,9 +839,11 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
         const size_t row = (size_t)short_b * p.Hq + (size_t)hk * p.group + q0;
         const uint32_t part0 = smem_u32(smem);
         constexpr uint32_t kPart = stages * 2 * C::kPageBytes;  // between two warps' parts
-        for (int qi = rank; qi < rows; qi += kClusterCtas) {
+        for (int qi = rank; qi < rows; qi += ctas_of) {
             // Lane i: part i, of warp i % 4 in CTA i / 4.
-            const float y = lds_cluster(part0 + lane % kWarps * kPart + (NT * 8 * D + qi) * 4, lane / kWarps);
+            const float y = lane < ctas_of * kWarps
+                                ? lds_cluster(part0 + lane % kWarps * kPart + (NT * 8 * D + qi) * 4, lane / kWarps)
+                                : -INFINITY;
             const uint32_t there = __ballot_sync(0xffffffffu, y != -INFINITY);  // (else nothing was written)
             float top = y;
 #pragma unroll
@@ -840,7 +854,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             float x = 0.0f;
 #pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < (WIN ? ctas_of * kWarps : 32); ++i) {
                 const float wv = __shfl_sync(0xffffffffu, wi, i);
                 if (threadIdx.x < D && (there >> i & 1u))
                     x = fmaf(wv,
@@ -978,8 +992,8 @@ cudaError_t launch_w(const GqaParams& p, cudaStream_t s) {
     const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT, WIN>>(kern, smem);
     if (e != cudaSuccess) return e;
     if constexpr (SHORT)
-        return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * kClusterCtas)),
-                                     dim3(kWarps * 32), (size_t)C::kRingBytes + 1024, kClusterCtas, s, p);
+        return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * p.short_step)),
+                                     dim3(kWarps * 32), (size_t)C::kRingBytes + 1024, p.short_step, s, p);
     const int here = C::kRingBytes + 1024 + (p.B + 1) * 4;
     const dim3 grid((unsigned)(p.warps / kWarps * p.rounds));
     return p.early ? launch_kernel_early(kern, grid, dim3(kWarps * 32), (size_t)here, s, p)
@@ -1024,10 +1038,15 @@ int gqa_warps(int B, int Hk, int group, int max_pages) {
     return kWarps * (int)(ctas < 1 ? 1 : ctas < 4 * kGqaSms ? ctas : 4 * kGqaSms);
 }
 
-bool gqa_short(int B, int Hk, int group, int max_pages, int D, bool q8) {
-    if (group > 8) return false;
-    const long long units = (long long)B * Hk;
-    return units <= (gqa_occupancy(D, q8, 1) == 4 ? 72 : 48) && max_pages <= (units < 32 ? 128 : 256);
+int gqa_short(int B, int Hk, int group, int span, int D, bool q8, bool window) {
+    if (group > 8) return 0;
+    const long long units = (long long)B * Hk, most = gqa_occupancy(D, q8, 1) == 4 ? 72 : 48;
+    if (units <= most && span <= (units < 32 ? 128 : 256)) return kClusterCtas;
+    if (!window) return 0;
+    for (int ctas = kClusterCtas / 2; ctas > 0; ctas /= 2)
+        if (units * ctas <= most * kClusterCtas)
+            return span <= (q8 ? kGqaWindowPagesQ8 : kGqaWindowPages) * ctas ? ctas : 0;
+    return 0;
 }
 
 int gqa_rounds(int B, int Hk, int group) {

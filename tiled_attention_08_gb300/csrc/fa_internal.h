@@ -201,7 +201,7 @@ struct GqaParams {
     int rounds;                // of the split, 1 or 3
     int slot_rows;             // rows of a slot: the group, at most 8 or (above 8) 16
     int parts_only;            // rows have other parts (a shared prefix): o, lse are the merge's
-    int short_step;            // a cluster per unit and no merge (gqa_short)
+    int short_step;            // CTAs of a cluster per unit, and no merge (gqa_short); 0: the line
     int early;                 // launched before the kernel in front of it has finished
     int window, sinks;         // window > 0: each sequence reads its last `window` tokens and its first
                                // `sinks` alone
@@ -416,8 +416,8 @@ cudaError_t launch_merge(const MergeParams& p, int D, bool bf16, cudaStream_t s)
 int gqa_q_rows(int group);
 int gqa_warps(int B, int Hk, int group, int max_pages);
 int gqa_rounds(int B, int Hk, int group);
-// Whether a step takes a cluster per unit (and no merge).
-bool gqa_short(int B, int Hk, int group, int max_pages, int D, bool q8);
+// CTAs of the cluster that takes a unit of the step (and no merge), or 0; span: pages of a sequence at most.
+int gqa_short(int B, int Hk, int group, int span, int D, bool q8, bool window);
 int gqa_launched_warps(int B, int Hk, int group, int max_pages, int D, bool q8, int busy_sms);
 // Splits of the page range per (sequence, head) for a decode step of this shape.
 int decode_splits(int B, int H, int max_pages);

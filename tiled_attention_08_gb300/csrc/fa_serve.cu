@@ -147,7 +147,7 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         c.full_o = reinterpret_cast<float*>(ws + w.full_o) + b0 * row_o;
         c.full_lse = reinterpret_cast<float*>(ws + w.full_lse) + (size_t)b0 * p.Hq;
         c.early = p.early && b0 == 0;
-        c.short_step = !p.parts_only && gqa_short(c.B, p.Hk, p.group, p.span, D, q8);
+        c.short_step = p.parts_only ? 0 : gqa_short(c.B, p.Hk, p.group, p.span, D, q8, p.window > 0);
         c.rounds = gqa_rounds(c.B, p.Hk, p.group);
         c.warps = gqa_launched_warps(c.B, p.Hk, p.group, p.span, D, q8, c.early ? busy_sms : 0);
         cudaError_t e = traced_launch(kernel++, s, [&] { return launch_decode_gqa(c, D, bf16, q8, s); });
@@ -241,8 +241,9 @@ fa_status decode_step(const void* q, const void* k_cache, const void* v_cache, c
     p.group = Hq / Hk;
     p.num_pages = num_pages;
     p.max_pages = max_pages;
-    p.window = window;
-    p.sinks = sinks;
+    const int room = imax(max_pages * kPageTokens, 1);  // (larger ones see no more, and sums with them pass 31 bits)
+    p.window = imin(window, room);
+    p.sinks = imin(sinks, room);
     p.span = span;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = status_ptr();
