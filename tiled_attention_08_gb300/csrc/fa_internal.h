@@ -257,6 +257,7 @@ struct WindowFwdParams {
     int Lq, Lk, Hq, Hk, B;
     int window, sinks;             // in [1, Lk], [0, Lk]
     int head_pairs;                // a work item is a query tile of two heads, not two tiles of one
+    int single;                    // ... or one tile (head_pairs = 0)
     int columns;                   // B * Hq, or half of it: heads (or pairs of them)
     int rows;                      // work items of one of them
     int sched_group;               // of the columns (tile_coords)

@@ -135,9 +135,10 @@ fa_status fa_window_fwd(const void* q, const void* k, const void* v, void* o, fl
     p.B = B;
     p.window = sh.window;
     p.sinks = sh.sinks;
-    p.head_pairs = (Hq / Hk) % 2 == 0;
+    p.single = (long long)B * Hq * sh.n_qtiles <= kWindowSms;
+    p.head_pairs = !p.single && (Hq / Hk) % 2 == 0;
     p.columns = p.head_pairs ? B * (Hq / 2) : B * Hq;
-    p.rows = p.head_pairs ? sh.n_qtiles : (sh.n_qtiles + 1) / 2;
+    p.rows = p.head_pairs || p.single ? sh.n_qtiles : (sh.n_qtiles + 1) / 2;
     const int per_key_head = p.columns / (B * Hk);
     const int span = imin(Lk, sh.window + sh.sinks + kTileRows);
     p.sched_group = per_key_head * sched_group(4 * D, span, Lk, per_key_head, B * Hk);
