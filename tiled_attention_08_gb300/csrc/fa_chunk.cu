@@ -230,17 +230,19 @@ __device__ __forceinline__ int unit_cta(long long units, int grid, long long u) 
     return (int)(((u + 1) * grid - 1) / units);
 }
 
-// Joins the n_parts parts of a pair of query tiles, which CTAs owner, owner + 1, ... left: the tiles' rows are dealt
-// out to the warps, eight at a time.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).
+// Joins the n_parts parts of a pair of query tiles, which CTAs owner, owner + 1, ... left: the tiles' T G rows are
+// dealt out to the warps, eight at a time.  O = sum w_i O_i / sum w_i, LSE = log sum exp(LSE_i).
 template <int D, bool BF16>
 __device__ __noinline__ void join_parts(const ChunkParams& p, int b, int hk, int t0, int fresh, int owner, int n_parts,
                                         int warp, int lane) {
     constexpr int kPer = D / 32, kRows = 8;
-    const int rows = t0 + p.T < fresh ? 2 * kTileRows : kTileRows, per_warp = rows / 8;
+    const int per_tile = (p.T * p.group + kRows - 1) / kRows * kRows;
+    const int rows = t0 + p.T < fresh ? 2 * per_tile : per_tile;
 #pragma unroll 1
-    for (int r0 = warp * per_warp; r0 < (warp + 1) * per_warp; r0 += kRows) {
-        // Lane 8 q + r: row r0 + r, of which it takes the log-sum-exp of parts q, q + 4, ...
-        const int my_r = r0 + (lane & (kRows - 1)), my_t = my_r >> 7, my_row = my_r & (kTileRows - 1);
+    for (int at = warp * kRows; at < rows; at += 8 * kRows) {
+        // Rows r0 .. of tile my_t; lane 8 q + r: row r0 + r, of which it takes the log-sum-exp of part q of two.
+        const int my_t = at >= per_tile, r0 = at + my_t * (kTileRows - per_tile);
+        const int my_r = r0 + (lane & (kRows - 1)), my_row = my_r & (kTileRows - 1);
         const int my_head = my_row / p.T, my_i = t0 + my_t * p.T + my_row - my_head * p.T;
         const bool mine = my_head < p.group && my_i < fresh;
         if (!__any_sync(0xffffffffu, mine)) continue;
