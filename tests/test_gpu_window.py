@@ -82,6 +82,11 @@ CASES = [
     (1, 3, 3, 900, 257, 64, BF16, "blhd", 7, 0),
     (1, 5, 5, 640, 640, 128, BF16, "bhld", 127, 128),
     (3, 16, 4, 1100, 1100, 64, FP16, "blhd", 250, 131),
+    # More query tiles than SMs: two heads, or two tiles, at a time.
+    (2, 9, 3, 1500, 1500, 64, BF16, "bhld", 200, 10),
+    (1, 24, 24, 1024, 1024, 128, FP16, "blhd", 256, 1),
+    (2, 16, 8, 700, 1900, 128, BF16, "bhld", 333, 0),
+    (3, 10, 2, 1900, 700, 64, FP16, "bhld", 333, 140),
 ]
 
 
@@ -302,6 +307,10 @@ def test_empty_and_query_free_calls():
     assert not leaves[1].grad.any() and not leaves[2].grad.any()
     with pytest.raises(fa.FaError):
         fa.window_forward(*operands(18, 1, 2, 1, 5, 0, 64, BF16)[:3], 4)
+    q, k, v, _ = operands(17, 1, 0, 1, 9, 9, 64, BF16)  # no query head
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    fa.attention_window(*leaves, 4).sum().backward()
+    assert not leaves[1].grad.any() and not leaves[2].grad.any()
 
 
 def test_a_saved_input_that_is_written_is_noticed():

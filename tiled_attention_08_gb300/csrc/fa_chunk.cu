@@ -895,9 +895,8 @@ __global__ void __launch_bounds__(kChunkGrid) fa_chunk_zero_kernel(int* counters
 template <int D, bool BF16, bool Q8>
 cudaError_t launch_t(const ChunkParams& p, cudaStream_t s) {
     using C = ChunkCfg<D, BF16, Q8>;
-    auto kern = fa_chunk_kernel<D, BF16, Q8>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    constexpr auto kern = fa_chunk_kernel<D, BF16, Q8>;
+    const cudaError_t e = allow_shared_once<kern>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
     return launch_kernel_early(kern, dim3((unsigned)p.grid), dim3(C::kThreads), C::kSmemBytes, s, p);
 }

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fa {
 
 // Status codes a kernel records in the device status word (first error wins).
@@ -340,7 +342,21 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
-// The same, allowed to start before the previous kernel of the stream has finished: `kern` calls
+// cudaFuncSetAttribute of a kernel's dynamic shared memory, once per kernel and device (small calls repeat
+// every few microseconds).
+template <auto Kern>
+cudaError_t allow_shared_once(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
+    const cudaError_t r = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (r == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
+    return r;
+}
+
+// launch_kernel, allowed to start before the previous kernel of the stream has finished: `kern` calls
 // griddepcontrol.wait before it touches anything that kernel writes.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,

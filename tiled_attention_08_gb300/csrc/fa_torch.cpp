@@ -576,6 +576,7 @@ WindowSizes window_sizes(const Tensor& q, const Tensor& k, const Tensor& v) {
 Tensor output_like(const char* name, const OptTensor& out, const Tensor& like) {
     if (!given(out)) return at::empty_like(like);
     TORCH_CHECK_TYPE(out->scalar_type() == like.scalar_type(), name, " must have the dtype of q");
+    TORCH_CHECK_VALUE(out->sizes() == like.sizes(), name, " has shape ", out->sizes(), ", expected ", like.sizes());
     same_device(name, *out, like.get_device());
     written(*out);
     return *out;
@@ -623,7 +624,7 @@ std::tuple<Tensor, Tensor, Tensor> window_bwd(const Tensor& q_, const Tensor& k_
     const fa_strides st[8] = {w.q, w.k, w.v, row_strides("o", o, q.sizes()), row_strides("dout", dout, q.sizes()),
                               row_strides("dq", dq, q.sizes()), row_strides("dk", dk, k.sizes()),
                               row_strides("dv", dv, k.sizes())};
-    if (w.Lq == 0 && w.Lk > 0) {  // no query: the keys have no gradient
+    if (q.numel() == 0) {  // no query: the keys have no gradient
         dk.zero_();
         dv.zero_();
         return {dq, dk, dv};

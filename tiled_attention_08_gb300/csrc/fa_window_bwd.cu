@@ -1063,8 +1063,8 @@ cudaError_t launch_dkdv_t(const WindowBwdParams& p, cudaStream_t s) {
     using C = DkdvCfg<D, BF16>;
     constexpr int kSmem = C::kOffBar + (int)sizeof(DkdvBarsT<D, BF16>);
     static_assert(kSmem <= 232448, "dynamic shared memory over the 227 KB per-block limit");
-    auto kern = fa_window_dkdv_kernel<D, BF16>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    constexpr auto kern = fa_window_dkdv_kernel<D, BF16>;
+    const cudaError_t e = allow_shared_once<kern>(kSmem);
     if (e != cudaSuccess) return e;
     const int sms = sm_count();
     const int grid = sms > 0 && sms < p.dkdv_items ? sms : p.dkdv_items;
@@ -1074,8 +1074,8 @@ cudaError_t launch_dkdv_t(const WindowBwdParams& p, cudaStream_t s) {
 template <int D, bool BF16>
 cudaError_t launch_dq_t(const WindowBwdParams& p, cudaStream_t s) {
     using C = DqCfg<D, BF16>;
-    auto kern = fa_window_dq_kernel<D, BF16>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    constexpr auto kern = fa_window_dq_kernel<D, BF16>;
+    const cudaError_t e = allow_shared_once<kern>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int total = (p.n_qtiles - p.q_first) * p.B * p.Hq, sms = sm_count();
     const int grid = sms > 0 && sms < total ? sms : total;

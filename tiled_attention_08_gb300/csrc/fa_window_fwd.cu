@@ -399,9 +399,8 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
 template <int D, bool BF16>
 cudaError_t launch_t(const WindowFwdParams& p, cudaStream_t s) {
     using C = WinCfg<D, BF16>;
-    auto kern = fa_window_fwd_kernel<D, BF16>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    constexpr auto kern = fa_window_fwd_kernel<D, BF16>;
+    const cudaError_t e = allow_shared_once<kern>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
     const int total = p.rows * p.columns, sms = sm_count();
     const int grid = sms > 0 && sms < total ? sms : total;
