@@ -452,7 +452,7 @@ size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hk, int Lq, int Lk, int 
  * summed over the heads of a group; zeros where no query sees a key).  strides[0..7] = q, k, v, o,
  * dout, dq, dk, dv; a gradient may be another part of one packed tensor with operands of its length.  Every
  * call gives the same bits.  Lq = Lk = 0 returns FA_OK; only one of them 0 returns FA_ERR_UNSUPPORTED.  Calls
- * that may overlap on the GPU need a workspace each.  Enqueues three or four kernels.
+ * that may overlap on the GPU need a workspace each.  Enqueues three to five kernels.
  */
 fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
                         const float* lse, void* dq, void* dk, void* dv, void* workspace,

@@ -276,7 +276,8 @@ struct WindowBwdParams {
     CUtensorMap tm_q, tm_k, tm_v, tm_do;
     const void* dout;
     Strides sdo;
-    const float *nlse2_pad, *delta_pad;  // [B*Hq, Lqpad]: -LSE * log2(e), rowsum(dO * O)
+    const float* nlse2_pad;              // [B*Hq, Lqpad]: -LSE * log2(e)
+    float* delta_pad;                    // [B*Hq, Lqpad]: Delta
     void *dq, *dk, *dv;
     Strides sdq, sdk, sdv;
     int Lq, Lk, Lqpad, Hq, Hk, B, n_qtiles, n_ktiles;
@@ -287,8 +288,9 @@ struct WindowBwdParams {
                                          // parts where there is more than one ...
     float* part;                         // ... [B*Hk, split_tiles, parts, 2 (dK, dV), D/4, 128, 4]
     int dkdv_items;
+    int delta_tiles;                     // query tiles from q_first on whose Delta is taken from P and dP
     float scale, scale_log2;
-    int* sched;                          // work counters: [0] dK/dV pass, [1] dQ pass
+    int* sched;                          // work counters: [0] dK/dV pass, [1] dQ pass, [2] Delta
     int* status;
     uint64_t timeout_ns;
 };
@@ -418,10 +420,11 @@ cudaError_t launch_prefix(const PrefixParams& p, int D, bool bf16, cudaStream_t 
 // The work split of a shared prefix: fills rows_b, n_tiles, n_pairs, key_tiles, grid, max_segments.
 void prefix_plan(int B, int Hk, int group, int prefix_len, PrefixParams* p);
 cudaError_t launch_window_fwd(const WindowFwdParams& p, int D, bool bf16, cudaStream_t s);
-// The split of the first tokens' key tiles: fills split_tiles, parts, dkdv_items from the sizes.
+// The split of the first tokens' key tiles: fills split_tiles, parts, dkdv_items, delta_tiles from the sizes.
 void window_bwd_plan(WindowBwdParams* p);
 cudaError_t launch_window_dkdv(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_window_dq(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
+cudaError_t launch_window_delta(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 cudaError_t launch_window_join(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s);
 // The work split of a chunk: fills T, max_pairs, grid.
 void chunk_plan(int B, int Hk, int group, int L, int max_pages, ChunkParams* p);

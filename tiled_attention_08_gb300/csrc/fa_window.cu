@@ -266,8 +266,11 @@ fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void*
     pp.bf16 = bf16 ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int n = 0;
-    if (traced_launch(n++, s, [&] { return launch_bwd_pre(pp, s); }) != cudaSuccess ||
-        traced_launch(n++, s, [&] { return launch_window_dkdv(p, D, bf16, s); }) != cudaSuccess)
+    if (traced_launch(n++, s, [&] { return launch_bwd_pre(pp, s); }) != cudaSuccess) return FA_ERR_CUDA;
+    if (p.delta_tiles > 0 &&
+        traced_launch(n++, s, [&] { return launch_window_delta(p, D, bf16, s); }) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (traced_launch(n++, s, [&] { return launch_window_dkdv(p, D, bf16, s); }) != cudaSuccess)
         return FA_ERR_CUDA;
     if (p.parts > 1 &&
         traced_launch(n++, s, [&] { return launch_window_join(p, D, bf16, s); }) != cudaSuccess)

@@ -5,7 +5,8 @@
 //     dS = P o (dP - Delta),  dQ_h = scale dS_h K,
 //     dK = scale sum_h dS_h^T Q_h,  dV = sum_h P_h^T dO_h   over the heads h of the key head's group.
 // Two passes on the plan of the dense backward's persistent kernels, deterministic: dK and dV per
-// (key tile, key head), dQ per (query tile, head); both recompute P from the saved LSE.  The pipelines,
+// (key tile, key head), dQ per (query tile, head); both recompute P from the saved LSE.  Before them Delta, from O
+// and dO (the dense backward's preprocess) and for rows of few keys from P and dP.  The pipelines,
 // barriers and TMEM layouts are those described there.  Bound by the tensor cores: 10 D FLOPs per
 // visible pair and head, 14 with the recomputed S and dP.  What differs:
 //  * a dK/dV item's units are the query tiles of all heads of the group that see its key tile, head
@@ -80,6 +81,10 @@ __device__ __forceinline__ void Unit::step(const DkdvItem& it) {
         ++h;
     }
 }
+
+// Rows that see fewer keys than this get their Delta from P and dP (fa_window_dq_kernel): the error that O's
+// rounding would leave there falls with the keys, and is 1% of dS's own from here on.
+constexpr int kDeltaKeys = 256;
 
 // Units u0 .. u1 - 1 of part i of n.
 __host__ __device__ __forceinline__ int part_start(int units, int i, int n) {
@@ -628,7 +633,12 @@ struct DqCfg {
 };
 
 // dQ.
-template <int D, bool BF16>
+//
+// DELTA: the same tiles' Delta = rowsum(P o dP) instead, summed in fp32, for the first p.delta_tiles query tiles that
+// see a key.  The preprocess takes Delta from the rounded O, off by O's rounding and that of P in it; a row of few
+// keys passes that on to all of its dS (error of dQ and dK relative to their rounding to 16 bits alone: 1.75 for a
+// window of 8, 1.5 for 1024, whose first rows are the largest; with Delta from P and dP 1.45, dS's own rounding).
+template <int D, bool BF16, bool DELTA>
 __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
     fa_window_dq_kernel(const __grid_constant__ WindowBwdParams p) {
     using C = DqCfg<D, BF16>;
@@ -656,7 +666,8 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
     const int lane = threadIdx.x & 31;
     volatile int* abort_v = &abort_flag;
     // Work ids: heads in L2-sized groups, the last query tiles first; the first q_first ones see no key.
-    const int rows = p.n_qtiles - p.q_first, total = rows * p.B * p.Hq;
+    const int rows = DELTA ? p.delta_tiles : p.n_qtiles - p.q_first, total = rows * p.B * p.Hq;
+    int* counter = p.sched + (DELTA ? 2 : 1);
     struct Tile {
         int bh, b, h, hk, qt, n_kv;
         KeyTiles keys;
@@ -667,7 +678,7 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
         t.b = t.bh / p.Hq;
         t.h = t.bh - t.b * p.Hq;
         t.hk = t.h / (p.Hq / p.Hk);
-        t.qt = p.n_qtiles - 1 - rank;
+        t.qt = DELTA ? p.q_first + rank : p.n_qtiles - 1 - rank;
         const int first = t.qt * kTileRows, off = p.Lk - p.Lq;
         t.keys = key_tiles(first + off, imin(first + kTileRows, p.Lq) - 1 + off, p.window, p.sinks);
         t.n_kv = t.keys.count();
@@ -714,12 +725,12 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
             int gk = 0;       // K/V fills handed to the TMA unit
             int q_loads = 0;  // Q fills handed to the TMA unit
             Tile t;
-            int next_id = queue_push(queue, 0, p.sched + 1, total, false, abort_v, p.timeout_ns);
+            int next_id = queue_push(queue, 0, counter, total, false, abort_v, p.timeout_ns);
             for (int round = 0; ok; ++round) {
                 const int id = next_id;
                 if (id == -2) ok = false;
                 if (id < 0) break;
-                next_id = queue_push(queue, round + 1, p.sched + 1, total, false, abort_v,
+                next_id = queue_push(queue, round + 1, counter, total, false, abort_v,
                                      p.timeout_ns);
                 tile_from(id, t);
                 if (q_loads > 0 &&
@@ -818,6 +829,7 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
             issue_s(g);
             if (n == 1) mma_commit_w(&bar_qe);  // the tile's only S: Q free once it completes
             issue_dp(g);
+            if constexpr (DELTA) mma_commit_w(&bar_kve[g % C::kStages]);  // K_0, V_0 read
             for (int j = 0; j < n; ++j) {
                 const int gg = g + j;
                 const uint32_t par = (uint32_t)gg & 1u;
@@ -836,7 +848,9 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
                     }
                     tc_fence_after_sync();
                     issue_dp(gg + 1);
+                    if constexpr (DELTA) mma_commit_w(&bar_kve[(gg + 1) % C::kStages]);
                 }
+                if constexpr (DELTA) continue;
                 if (!wait_warp(&bar_pd, par, abort_v, p.timeout_ns) ||
                     (j == 0 && tc > 0 &&
                      !wait_warp(&bar_dqr, (uint32_t)(tc - 1) & 1u, abort_v, p.timeout_ns))) {
@@ -854,7 +868,7 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
                 mma_commit_w(&bar_dqd);                   // dS_j consumed
             }
             if (!ok) break;
-            mma_commit_w(&bar_done);
+            if constexpr (!DELTA) mma_commit_w(&bar_done);
             g += n;
         }
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
@@ -898,6 +912,7 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
         float nlse2 = 0.0f, dlt = 0.0f;  // -LSE * log2(e) and Delta of this thread's row
         const int id0 = queue_pop_warp(queue, 0, abort_v, p.timeout_ns);
         bool ok = id0 != -2;
+        if constexpr (DELTA) ok = bar_and(1 + quad, 32 * C::kSplit, ok);
         const bool any = id0 >= 0;  // a CTA that starts late may find no tile left
         if (any) {
             tile_from(id0, cur);
@@ -908,7 +923,7 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
             const int idn = queue_pop_warp(queue, round + 1, abort_v, p.timeout_ns);
             if (idn == -2) {
                 ok = false;
-                break;
+                if constexpr (!DELTA) break;  // (DELTA: the quadrant's warps meet below on every path)
             }
             const bool has_next = idn >= 0;
             if (has_next) tile_from(idn, nxt);
@@ -917,7 +932,8 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
             const int pos = q_row + (p.Lk - p.Lq);
             const uint64_t dlt2 = f2_make(dlt, dlt);
             float nlse2_n = 0.0f, dlt_n = 0.0f;
-            for (int j = 0; j < n; ++j) {
+            uint64_t sum2 = 0ull;  // DELTA: (+0.0f, +0.0f)
+            for (int j = 0; ok && j < n; ++j) {
                 const int gg = g + j;
                 const int key0 = cur.keys.tile(j) * kTileRows + c0;
                 const bool masked = hides_later(key0, kC, pos - lane) ||
@@ -962,11 +978,9 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < kLd; i += 2) {  // P o (dP - Delta), two at a time
                             float* q = pv + h * kLd + i;
-                            f2_split(f2_mul(f2_make(q[0], q[1]),
-                                            f2_sub(f2_make(__uint_as_float(r[i]),
-                                                           __uint_as_float(r[i + 1])),
-                                                   dlt2)),
-                                     q[0], q[1]);
+                            const uint64_t dp = f2_make(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                            if constexpr (DELTA) sum2 = f2_fma(f2_make(q[0], q[1]), dp, sum2);
+                            else f2_split(f2_mul(f2_make(q[0], q[1]), f2_sub(dp, dlt2)), q[0], q[1]);
                         }
                     }
                     tc_fence_before_sync();
@@ -975,38 +989,62 @@ __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
                 if (!ok) break;
                 // dS has its own columns: wait until the previous dQ contraction (of this tile
                 // or the last one of the previous tile) has read them.
-                if (gg > 0) {
+                if (!DELTA && gg > 0) {
                     ok = wait_bounded(&bar_dqd, par ^ 1u, abort_v, p.timeout_ns);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after_sync();
                 }
-                {
+                if constexpr (!DELTA) {
                     uint32_t pk[kC / 2];
 #pragma unroll
                     for (int i = 0; i < kC / 2; ++i) pk[i] = pack2<BF16>(pv[2 * i], pv[2 * i + 1]);
                     tmem_st<kC / 2>(tmem + lane_off + C::kTmDS + part * (kC / 2), pk);
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    mbar_arrive(&bar_pd);
                 }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                mbar_arrive(&bar_pd);
                 // The tile's last dP has completed (it was read above), so the next tile's dO
                 // may take the dO columns now: the MMA warp can start that tile's dP while
                 // this tile's dQ is read out.
                 if (j == n - 1 && has_next) stage_do(nxt, nlse2_n, dlt_n);
             }
-            if (ok) {
-                ok = wait_bounded(&bar_done, (uint32_t)tc & 1u, abort_v, p.timeout_ns);
-                ok = __all_sync(0xffffffffu, ok);
+            if constexpr (DELTA) {
+                // The quadrant's warps add up by way of TMEM columns that are free here (of dS and of dQ, tile
+                // after tile: at this barrier the sums of two tiles ago have been read).
+                const uint32_t at = tmem + lane_off + ((tc & 1) ? C::kTmDQ : C::kTmDS);
+                float lo, hi;
+                f2_split(sum2, lo, hi);
+                uint32_t mine[8] = {__float_as_uint(lo + hi), 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+                tmem_st8(at + 8 * part, mine);
+                tmem_st_wait();
+                tc_fence_before_sync();
+                ok = bar_and(1 + quad, 32 * C::kSplit, ok);
+                if (!ok) break;
+                tc_fence_after_sync();
+                if (part == 0) {
+                    uint32_t all[8 * C::kSplit];
+                    tmem_ld<8 * C::kSplit>(at, all);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < C::kSplit; ++i) sum += __uint_as_float(all[8 * i]);
+                    p.delta_pad[(size_t)cur.bh * p.Lqpad + q_row] = sum;
+                    tc_fence_before_sync();
+                }
+            } else {
+                if (ok) {
+                    ok = wait_bounded(&bar_done, (uint32_t)tc & 1u, abort_v, p.timeout_ns);
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+                if (!ok) break;
+                tc_fence_after_sync();
+                uint8_t* dst_row = reinterpret_cast<uint8_t*>(p.dq) +
+                                   row_offset(p.sdq, cur.bh, p.Hq, q_row) + part * C::kOutCols * 2;
+                tmem_row_to_global<BF16, C::kOutCols>(tmem + lane_off + C::kTmDQ + part * C::kOutCols,
+                                                      dst_row, p.scale, q_row < p.Lq);
+                tc_fence_before_sync();
+                mbar_arrive(&bar_dqr);  // the accumulator is read: the next tile may overwrite it
             }
-            if (!ok) break;
-            tc_fence_after_sync();
-            uint8_t* dst_row = reinterpret_cast<uint8_t*>(p.dq) +
-                               row_offset(p.sdq, cur.bh, p.Hq, q_row) + part * C::kOutCols * 2;
-            tmem_row_to_global<BF16, C::kOutCols>(tmem + lane_off + C::kTmDQ + part * C::kOutCols,
-                                                  dst_row, p.scale, q_row < p.Lq);
-            tc_fence_before_sync();
-            mbar_arrive(&bar_dqr);  // the accumulator is read: the next tile may overwrite it
             g += n;
             if (!has_next) break;
             cur = nxt;
@@ -1071,13 +1109,13 @@ cudaError_t launch_dkdv_t(const WindowBwdParams& p, cudaStream_t s) {
     return launch_kernel(kern, (unsigned)grid, C::kThreads, kSmem, s, p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool DELTA>
 cudaError_t launch_dq_t(const WindowBwdParams& p, cudaStream_t s) {
     using C = DqCfg<D, BF16>;
-    constexpr auto kern = fa_window_dq_kernel<D, BF16>;
+    constexpr auto kern = fa_window_dq_kernel<D, BF16, DELTA>;
     const cudaError_t e = allow_shared_once<kern>(C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    const int total = (p.n_qtiles - p.q_first) * p.B * p.Hq, sms = sm_count();
+    const int total = (DELTA ? p.delta_tiles : p.n_qtiles - p.q_first) * p.B * p.Hq, sms = sm_count();
     const int grid = sms > 0 && sms < total ? sms : total;
     return launch_kernel(kern, (unsigned)grid, C::kThreads, C::kSmemBytes, s, p);
 }
@@ -1103,6 +1141,10 @@ void window_bwd_plan(WindowBwdParams* p) {
     const int most = (int)(share > usual ? share : usual);
     p->split_tiles = 2LL * heavy > 3LL * usual ? n_sink : 0;
     p->parts = p->split_tiles > 0 && 2LL * heavy > 3LL * most ? (heavy + most - 1) / most : 1;
+    // Query tiles in which some row sees fewer than kDeltaKeys keys: all of them under a short window, else the first.
+    const long long seen = (long long)p->window + imin(p->sinks, p->Lk - p->window);
+    const int short_rows = seen < kDeltaKeys ? p->Lq : kDeltaKeys - off;  // rows in front of this one
+    p->delta_tiles = imax(imin((short_rows + kTileRows - 1) / kTileRows, p->n_qtiles) - p->q_first, 0);
     p->dkdv_items = heads * (p->split_tiles * p->parts + p->n_ktiles - p->split_tiles);
 }
 
@@ -1111,8 +1153,12 @@ cudaError_t launch_window_dkdv(const WindowBwdParams& p, int D, bool bf16, cudaS
     return bf16 ? launch_dkdv_t<128, true>(p, s) : launch_dkdv_t<128, false>(p, s);
 }
 cudaError_t launch_window_dq(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s) {
-    if (D == 64) return bf16 ? launch_dq_t<64, true>(p, s) : launch_dq_t<64, false>(p, s);
-    return bf16 ? launch_dq_t<128, true>(p, s) : launch_dq_t<128, false>(p, s);
+    if (D == 64) return bf16 ? launch_dq_t<64, true, false>(p, s) : launch_dq_t<64, false, false>(p, s);
+    return bf16 ? launch_dq_t<128, true, false>(p, s) : launch_dq_t<128, false, false>(p, s);
+}
+cudaError_t launch_window_delta(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s) {
+    if (D == 64) return bf16 ? launch_dq_t<64, true, true>(p, s) : launch_dq_t<64, false, true>(p, s);
+    return bf16 ? launch_dq_t<128, true, true>(p, s) : launch_dq_t<128, false, true>(p, s);
 }
 cudaError_t launch_window_join(const WindowBwdParams& p, int D, bool bf16, cudaStream_t s) {
     if (D == 64) return bf16 ? launch_join_t<64, true>(p, s) : launch_join_t<64, false>(p, s);
