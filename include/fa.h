@@ -434,8 +434,8 @@ fa_status fa_decode_shared_prefix(const void* q, const void* k_cache, const void
  * views (strides[0..3] = q, k, v, o) with Hq a multiple of Hk, lse contiguous [B, Hq, Lq]; Lq, Lk <= 2^30 - 1024.
  * A row that sees no key (t < 0, only when Lq > Lk) gets O = 0 and LSE = -inf.  Lk = 0 with Lq > 0
  * is FA_ERR_UNSUPPORTED, as are more than 2^31 - 1 tiles.  o may be another part of one packed tensor
- * with an input of the same length (as in fa_rotary), else their extents must not overlap.  An infinity or NaN in V reaches every row of a tile
- * that some row of it sees.
+ * with an input of the same length (as in fa_rotary), else their extents must not overlap.  An infinity or
+ * NaN in V reaches every row of a tile that some row of it sees.
  * Enqueues one kernel (two when Lq > Lk).
  */
 fa_status fa_window_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -451,8 +451,9 @@ size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hk, int Lq, int Lk, int 
  * Its backward: given the forward's o and lse and the output gradient dout, writes dq, dk, dv (dk and dv
  * summed over the heads of a group; zeros where no query sees a key).  strides[0..7] = q, k, v, o,
  * dout, dq, dk, dv; a gradient may be another part of one packed tensor with operands of its length.  Every
- * call gives the same bits.  Lq = Lk = 0 returns FA_OK; only one of them 0 returns FA_ERR_UNSUPPORTED.  Calls
- * that may overlap on the GPU need a workspace each.  Enqueues three to five kernels.
+ * call gives the same bits.  Lq = Lk = 0 returns FA_OK, as does Hq = 0, which writes nothing (dk and dv neither);
+ * only one of Lq and Lk 0 returns FA_ERR_UNSUPPORTED.  Calls that may overlap on the GPU need a workspace each.
+ * Enqueues three to five kernels.
  */
 fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
                         const float* lse, void* dq, void* dk, void* dv, void* workspace,

@@ -177,6 +177,25 @@ def test_offsets_past_31_bits(q8):
         within(od[0, 2 * h:2 * h + 2, None], want["o"], "decode o")
 
 
+def test_rows_past_31_bits_without_a_token():
+    """More than 2^28 rows of which a few are new (q's rows overlap in memory, O's do not)."""
+    D, n, new, L = 64, 100, 40, (1 << 28) + 100
+    kc, vc = (randn(8, 1, PAGE, D, dtype=BF16, seed=s) for s in (1, 2))
+    bt = torch.arange(8, dtype=torch.int32, device="cuda")[None].contiguous()
+    sl, nl = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (n, new))
+    rows = randn(8 * L + D, dtype=BF16, seed=3)
+    q = rows.as_strided((1, 1, L, D), (8 * L, 8 * L, 8, 1))
+    o = torch.empty((1, 1, L, D), device="cuda", dtype=BF16)
+    o[:, :, :256] = o[:, :, -256:] = math.nan
+    lse = fa.attention_paged(q, kc, vc, bt, sl, nl, out=o)[1]
+    assert status() == fa.FA_OK
+    k, v = (x.reshape(1, 8 * PAGE, D)[:, :n] for x in (kc, vc))
+    check(o[:, :, :256], lse[:, :, :256], q[:, :, :256], [gh.f64(k)], [gh.f64(v)], [n], [new], 0, 0, 1 / math.sqrt(D))
+    assert not o[:, :, -256:].any() and (lse[:, :, new:] == -math.inf).all()
+    del o, lse, rows, q
+    torch.cuda.empty_cache()
+
+
 def test_captured_and_replayed_as_sequences_grow():
     rng = np.random.default_rng(10)
     lens, news = [900, 130], [64, 30]

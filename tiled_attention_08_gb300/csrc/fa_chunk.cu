@@ -15,7 +15,7 @@
 //  * keys: a 128-key tile is 8 pages.  Of a 16-bit cache each is its own TMA box, issued by one lane
 //    each; pages without a token that the pair sees are read at a row outside the map, as zeros, and
 //    slots of other pages that hold none are cleared in V by the MMA warp (0 * NaN).  Of an e4m3 cache
-//    four converter warps read the bytes, multiply by the row's power of two in fp32, round to q's type
+//    eight converter warps read the bytes, multiply by the row's power of two in fp32, round to q's type
 //    (exact in bf16) and write the tile in the swizzled layout that the contraction reads.
 //  * split: lengths are known on the device only, and rows alone seldom fill 152 SMs.  Units (head, pair of
 //    query tiles, key tile) form one line, of which every CTA takes an equal stretch: each CTA first
@@ -43,7 +43,7 @@ struct ChunkCfg {
     static constexpr int kTileBytes = kTileRows * D * 2;
     // Tile slots.  16-bit caches: a ring for K and one for V.  e4m3: one ring, K and V in turn, of three
     // slots at D = 128 (a step reads V_j and K_{j+1} while V_{j+1} is converted), which leaves room for
-    // twice as many bytes in flight (32 KB of them with two rings of two).
+    // 64 KB of bytes in flight, not 32.
     static constexpr int kStages = (D == 128) ? 2 : 4;
     static constexpr int kSlots = Q8 ? ((D == 128) ? 3 : 6) : 2 * kStages;
     static constexpr int kOffQ = 0;
@@ -708,8 +708,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             int n, ahead;
             sequence(p, bh / p.Hq, n, ahead);
             const int from = imax(n, i0), to = imin(i0 + 64, p.L);
-            for (int e = from * (D / 8) + lane; e < to * (D / 8); e += 32) {
-                const int i = e / (D / 8), u = e % (D / 8);
+            for (int e = lane; e < (to - from) * (D / 8); e += 32) {
+                const int i = from + e / (D / 8), u = e % (D / 8);
                 reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.o) + row_offset(p.so, bh, p.Hq, i))[u] =
                     make_uint4(0u, 0u, 0u, 0u);
                 if (u == 0) p.lse[(size_t)bh * p.L + i] = -INFINITY;
@@ -878,6 +878,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
     }
 
+    if (blockIdx.x == 0) pdl_wait();  // the kernel in front has ended before this one does
     tc_fence_before_sync();
     __syncthreads();
     if (warp == C::kMmaWarp) {

@@ -54,7 +54,7 @@ bool make_rows_map(CUtensorMap* m, const void* ptr, int B, int H, int L, int D, 
 // consecutive tiles of every head of a group; what they stream is `span` rows of a head and one more tile of
 // them for each further tile, `row_bytes` each.  As many heads as keep that within kStreamed of L2.
 constexpr long long kStreamed = 48LL << 20;
-int sched_group(int row_bytes, int span, int len, int items_per_tile, int heads) {
+int sched_group(long long row_bytes, int span, int len, int items_per_tile, int heads) {
     for (int g = heads; g > 1; g = g > 2 * kWindowSms ? g / 2 : g - 1) {
         const int at_once = imin(g, kWindowSms), tiles = kWindowSms / (g * items_per_tile);
         const long long rows = imin(len, span + kTileRows * (tiles < 1 ? 1 : tiles));
@@ -235,7 +235,7 @@ fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void*
     p.sdk = s8[6];
     p.sdv = s8[7];
     const int group = Hq / Hk, span = imin(Lk, sh.window + sh.sinks + kTileRows);
-    p.sched_group_k = sched_group(4 * D * group, sh.window + kTileRows, Lq, 1, B * Hk);
+    p.sched_group_k = sched_group(4LL * D * group, sh.window + kTileRows, Lq, 1, B * Hk);
     p.sched_group_q = group * sched_group(4 * D, span, Lk, group, B * Hk);
     p.part = reinterpret_cast<float*>(ws + part_at);
     p.scale = scale;
