@@ -366,8 +366,9 @@ fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cac
                            int Hk, int D, int num_pages, int max_pages, int window, int sinks,
                            float scale, int dtype, int cache_dtype, void* stream);
 
-/* Bytes of device workspace fa_attention_paged needs (fp32 parts of query tiles that several CTAs share; at most
- * 41 MB at D = 128, whatever the sizes).  0 for an empty problem or invalid sizes. */
+/* Bytes of device workspace fa_attention_paged needs (fp32 parts of query rows that several CTAs share; at most
+ * 41 MB at D = 128, with few rows per cache head 123 MB, whatever the sizes).  0 for an empty problem or invalid
+ * sizes. */
 size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, int max_pages);
 
 /*
@@ -381,13 +382,14 @@ size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, i
  *   new_lens:  [B] int32, device, 0 <= new_lens[b] <= min(L, seq_lens[b]); null: L for every sequence, 0 for
  *              one of length 0;
  *   caches, exponents, block_tables, seq_lens, scale: as for fa_decode_paged_ex.  An e4m3 row is its values times
- *              its power of two, rounded to dtype, as fa_cache_read gives it.
+ *              its power of two, rounded to dtype, as fa_cache_read gives it (not rounded where few rows are new).
  * Rows new_lens[b] .. L - 1 of o are written as zeros, of lse as -inf.  Pages without a token that some row of a
  * sequence sees, and their table entries, are not read; slots of other pages that hold no such token may
  * hold anything.  (An infinity or NaN in V of a token that counts may reach rows of the same chunk that do not see
  * it.)  Hq / Hk <= 128.  Bad lengths and page indexes (device data) are reported by fa_get_device_status() as
- * FA_ERR_INVALID_ARG: a sequence with a bad length counts as one without new tokens, a bad page as
- * zeros.  Calls that may overlap on the GPU need a workspace each.  Enqueues two kernels.
+ * FA_ERR_INVALID_ARG: a sequence with a bad length counts as one without new tokens, the tokens of a bad page as
+ * zeros or as others of the cache.  Calls that may overlap on the GPU need a workspace each.  Enqueues one or two
+ * kernels (for few rows of more than 1024 sequences, per 1024 of them).
  */
 fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
                              const void* v_exp, const int32_t* block_tables, const int32_t* seq_lens,

@@ -108,6 +108,78 @@ def test_splits(lens, news, Hq, Hk, window, sinks, q8):
     run(2, lens, news, Hq, Hk, 128, BF16, q8, window, sinks)
 
 
+# Few rows per cache head are queries of the decode kernel: a cluster per unit or the line, one or two blocks of
+# eight, two units of them over e4m3, and on either side of its limits of 16 and 32 rows.
+FEW = [(1, 1, 1), (3, 3, 5), (8, 2, 2), (8, 2, 4), (6, 2, 5), (5, 1, 3), (2, 2, 16), (2, 2, 17), (16, 2, 4), (11, 1, 3)]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (7, 40), (64, 3), (200, 0)])
+@pytest.mark.parametrize("D,dtype,q8", [(64, BF16, False), (128, FP16, False), (128, BF16, True), (64, FP16, True)])
+@pytest.mark.parametrize("Hq,Hk,L", FEW)
+def test_few_rows(Hq, Hk, L, D, dtype, q8, window, sinks):
+    lens = [0, 1, 17, 16, 300, 1000, 129, 640, L, 64 + L]
+    news = [0, 1, min(L, 17), 0, L, (L + 1) // 2, L, 1, L, L]
+    run(21, lens, news, Hq, Hk, D, dtype, q8, window, sinks, L=L)
+
+
+@pytest.mark.parametrize("lens,new,Hq,Hk,window,sinks,layout", [
+    ([9000], 4, 8, 2, 0, 0, "blhd"),              # every warp a stretch of one sequence
+    ([3000, 20, 4], 4, 4, 4, 0, 0, "blhd"),
+    ([700] * 40, 3, 8, 4, 500, 20, "blhd"),       # clusters of several sizes
+    ([700] * 200, 2, 4, 2, 100, 0, "bhld"),
+    ([4000, 50] * 60, 5, 12, 4, 0, 0, "blhd"),    # the line
+    ([40] * 1100, 2, 2, 1, 0, 0, "blhd"),         # two launches
+])
+@pytest.mark.parametrize("q8", [False, True])
+def test_few_rows_splits(lens, new, Hq, Hk, window, sinks, layout, q8):
+    run(22, lens, [new] * len(lens), Hq, Hk, 128, BF16, q8, window, sinks, layout=layout)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_few_rows_whose_padding_holds_nan(q8):
+    rng = np.random.default_rng(23)
+    lens, news = [300, 20, 5000], [3, 0, 1]
+    kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, lens, 2, 128, BF16, q8)
+    q = randn(3, 4, 4, 128, dtype=BF16)
+    for b, n in enumerate(news):
+        q[b, :, n:] = math.nan
+    nl = torch.tensor(news, dtype=torch.int32, device="cuda")
+    o, lse = fa.attention_paged(q, kc, vc, bt, sl, nl, k_exp=ke, v_exp=ve)
+    assert status() == fa.FA_OK
+    check(o, lse, q, ks, vs, lens, news, 0, 0, 1 / math.sqrt(128))
+
+
+def test_one_new_token_is_a_decode_step():
+    rng = np.random.default_rng(24)
+    kc, vc, ke, ve, bt, sl, _, _ = fill(rng, [300, 1, 5000, 77], 2, 128, BF16, True)
+    q = randn(4, 8, 1, 128, dtype=BF16)
+    kw = dict(window=200, sinks=9, k_exp=ke, v_exp=ve)
+    o, lse = fa.attention_paged(q, kc, vc, bt, sl, **kw)
+    od, lsed = fa.decode_paged(q[:, :, 0].contiguous(), kc, vc, bt, sl, **kw)
+    assert torch.equal(o[:, :, 0], od) and torch.equal(lse[:, :, 0], lsed)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_few_rows_with_bad_lengths(q8):
+    rng = np.random.default_rng(25)
+    kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, [100, 60], 1, 64, BF16, q8)
+    q = randn(2, 2, 4, 64, dtype=BF16)
+    kw = dict(k_exp=ke, v_exp=ve)
+    for n, new in ((16 * bt.shape[1] + 1, 4), (-1, 0), (3, 4), (100, 5), (100, -1)):
+        s2 = torch.tensor([n, 60], dtype=torch.int32, device="cuda")
+        nl = torch.tensor([new, 4], dtype=torch.int32, device="cuda")
+        o, lse = fa.attention_paged(q, kc, vc, bt, s2, nl, **kw)
+        assert status() == fa.FA_ERR_INVALID_ARG, (n, new)
+        check(o[1:], lse[1:], q[1:], ks[1:], vs[1:], [60], [4], 0, 0, 1 / 8)
+        assert not o[0].any() and (lse[0] == -math.inf).all()
+    for page in (kc.shape[0], -1):
+        b2 = bt.clone()
+        b2[0, 3] = page
+        o, lse = fa.attention_paged(q, kc, vc, b2, sl, **kw)
+        assert status() == fa.FA_ERR_INVALID_ARG, page
+        check(o[1:], lse[1:], q[1:], ks[1:], vs[1:], [60], [4], 0, 0, 1 / 8)
+
+
 @pytest.mark.parametrize("Hq,Hk", [(128, 1), (100, 1), (65, 1), (64, 2)])
 def test_large_groups(Hq, Hk):
     run(3, [70, 300], [20, 9], Hq, Hk, 64, FP16, False)

@@ -22,6 +22,7 @@
 //    sums the pairs' key tiles.  A pair that lies whole in a stretch is written as O and LSE; of a cut
 //    one each CTA leaves an fp32 part (two at most), and the one that finds the others' there joins them.  (A kernel
 //    of its own for that took 16 of 177 us for two prompts of 4096 tokens, 6 of 24 for one short turn.)
+// Chunks of very few rows per cache head are the decode kernel's (fa_decode_gqa.cu, kRows; few_rows in fa_serve.cu).
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
 #include "fa_ptx.cuh"

@@ -48,6 +48,13 @@
 // 512 23.7 and 21.4 (lengths spread from a quarter up: 20.6 and 20.6).  So 128 for fewer than 32 units, else
 // 256.  Both are careful: 16-bit caches still gain there (8 units of 256 pages, heads of 64: 10.4 and 9.9).
 //
+// Windows (kWindow).  A sequence's pages are those of its last `window` tokens and of the first `sinks`; the line
+// counts those alone, and slots of their pages that do not count are masked as those past the end are.
+//
+// Few new tokens (kRows).  The queries of a unit are then the new tokens of all heads of a group, so the cached rows
+// are read once for all of them, at HBM's rate where a 128-row tile of the chunk kernel (fa_chunk.cu) would be nearly
+// empty; pages that not every row sees whole are masked by row.  Its figures are at few_rows in fa_serve.cu.
+//
 // Softmax in the log2 domain.  The reference of a column is only raised when a score exceeds it
 // by more than 2^8 (a warp vote), so the maximum over the lanes is rarely taken.  An e4m3 cache
 // needs a second one: the sum of weights takes p_j = 2^(y_j - m); the products take
@@ -142,7 +149,7 @@ __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int ro
 }
 
 // cudaFuncSetAttribute once per kernel and device (the calls below repeat every few microseconds).
-template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, int MODE>
 struct kGqaKernelId {};
 template <typename Id, typename K>
 cudaError_t allow_shared(K kern, int bytes) {
@@ -241,9 +248,15 @@ struct Batch {
     int page_head;  // page * Hk + head in the cache
     int b, unit;    // sequence, and (cache head, query block) in it
     int flags;      // tokens that count (1..16) | first page of its unit << 8 | last << 9, and under a
-                    // window bit 16 + i: slot i counts
+                    // window bit 16 + i: slot i counts (for some row)
+    int token;      // (kRows) its first token
 };
 constexpr int kFirst = 1 << 8, kLast = 1 << 9;
+constexpr int kEdge = 1 << 10;  // (kRows) some row does not see all that others see of it
+
+// What a row sees: all tokens; those of a window and the first ones; or (few new tokens of every sequence, L rows
+// of a head, one per token) what the window, or none, leaves of those up to its own.
+constexpr int kAll = 0, kWindow = 1, kRows = 2;
 
 // The pages that a sequence of n tokens reads under a window: those of the first tokens, then those of
 // the last `window` (no page twice).
@@ -286,11 +299,14 @@ __device__ __forceinline__ void cluster_sync() {
 
 // BF16: the type of q and o (and of a 16-bit cache).  NT: blocks of 8 queries.  SHORT: a cluster per
 // unit, whose warps share the unit's pages and join their parts through distributed shared memory.
-// WIN: the pages of the window and of the first tokens alone; nothing else of a sequence's table is read.
-template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
+// MODE: kAll, kWindow, kRows.  Not kAll: the pages of the windows and of the first tokens alone; nothing else of a
+// sequence's table is read.  kRows: a unit's queries are the new tokens of all heads of the group, row L h + i being
+// token i of head h; the pages that some see in part (the last ones, and those where a window begins) are masked by row.
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     fa_decode_gqa_kernel(const __grid_constant__ GqaParams p) {
     using C = GqaCfg<D, Q8>;
+    constexpr bool WIN = MODE != kAll, ROWS = MODE == kRows;
     constexpr bool kMmaBf16 = BF16 && !Q8;  // e4m3 values are exact in fp16
     constexpr float kLiftM = Q8 || BF16 ? 0.0f : kLift;  // (over e4m3 m is the reference of the sum alone)
     constexpr int stages = C::kStages;
@@ -309,8 +325,22 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     pdl_launch_dependents();
     // The queries into L2 (they are read when a warp begins a unit, behind the stream of pages).
     for (size_t at = ((size_t)blockIdx.x * (kWarps * 32) + threadIdx.x) * 128;
-         !SHORT && at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
+         !SHORT && !ROWS && at < (size_t)p.B * p.Hq * D * 2; at += (size_t)gridDim.x * (kWarps * 32) * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(p.q) + at));
+    // (ROWS) Offset in bytes of query qi of cache head hk in q or o.
+    auto row_at = [&](const Strides& s, int b, int hk, int qi) {
+        const int heads = p.group / p.L, h = qi / p.L;
+        return row_offset(s, b * (p.Hk * heads) + hk * heads + h, p.Hk * heads, qi - h * p.L);
+    };
+    if constexpr (ROWS && !SHORT) {
+        const int per_b = p.Hk * p.group;
+        for (long long at = (long long)blockIdx.x * (kWarps * 32) + threadIdx.x; at < (long long)p.B * per_b;
+             at += (long long)gridDim.x * (kWarps * 32)) {
+            const int b = (int)(at / per_b), r = (int)(at - (long long)b * per_b), hk = r / p.group;
+            const uint8_t* src = static_cast<const uint8_t*>(p.q) + row_at(p.sq, b, hk, r - hk * p.group);
+            for (int i = 0; i < D * 2; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+        }
+    }
     if (threadIdx.x == 0 && p.num_pages > 0) {
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
@@ -321,13 +351,23 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     const int n_seqs = SHORT ? 0 : p.B;
     const int run = (p.B + kWarps * 32 - 1) / (kWarps * 32);
     const int s0 = min((int)threadIdx.x * run, n_seqs), s1 = min(s0 + run, n_seqs);
+    auto fresh_of = [&](int b, int n) { return p.new_lens ? p.new_lens[b] : n > 0 ? p.L : 0; };  // (ROWS) new tokens
+    auto seen_of = [&](int b, int n) {  // (WIN) pages that some row sees
+        return window_pages(n, ROWS ? p.window + fresh_of(b, n) - 1 : p.window, p.sinks);
+    };
     auto pages_of = [&](int b) {
         const int n = p.seq_lens[b];
-        if (n < 0 || n > (long long)p.max_pages * kPageTokens || (n > 0 && p.num_pages == 0)) {
+        bool bad = n < 0 || n > (long long)p.max_pages * kPageTokens || (n > 0 && p.num_pages == 0);
+        if constexpr (ROWS) {
+            const int fresh = fresh_of(b, n);
+            bad = bad || fresh < 0 || fresh > p.L || fresh > n;
+            if (!bad && fresh == 0) return 0;
+        }
+        if (bad) {
             if (SHORT || blockIdx.x == 0) atomicCAS(p.status, 0, (int)kDevBadArg);
             return 0;  // counts as empty
         }
-        if constexpr (WIN) return window_pages(n, p.window, p.sinks).count();
+        if constexpr (WIN) return seen_of(b, n).count();
         return (n + kPageTokens - 1) / kPageTokens;
     };
     GqaSplit split;
@@ -375,12 +415,22 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
 
     uint8_t* ring = smem + (size_t)warp * stages * (2 * C::kPageBytes);
     uint8_t* exps = smem + (size_t)kWarps * stages * (2 * C::kPageBytes) + warp * stages * 32;
+    // (WIN) What goes with page pg of a sequence of n tokens.
+    auto describe = [&](Batch& r, int b, int n, int pg) {
+        const WindowPages w = seen_of(b, n);
+        r.flags |= window_slots(w, pg, p.sinks) << 16;
+        if constexpr (ROWS) {
+            r.token = pg * kPageTokens;
+            const int last = r.token + kPageTokens - 1, fresh = fresh_of(b, n);
+            if (fresh < p.L || last > n - fresh || (r.token <= n - 1 - p.window && last >= p.sinks)) r.flags |= kEdge;
+        }
+    };
     auto lookup = [&](int first) {  // pages first .. first + 31 of this warp
-        Batch r = {0, 0, 0, 0};
+        Batch r = {0, 0, 0, 0, 0};
         if (SHORT && first + lane < mine) {
             int pg = (int)x0 + first + lane;
             const int n = p.seq_lens[short_b];
-            if constexpr (WIN) pg = window_pages(n, p.window, p.sinks).page(pg);
+            if constexpr (WIN) pg = seen_of(short_b, n).page(pg);
             int page = p.block_tables[(size_t)short_b * p.max_pages + pg];
             if (page < 0 || page >= p.num_pages) {  // as below
                 atomicCAS(p.status, 0, (int)kDevBadArg);
@@ -388,8 +438,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             }
             r.page_head = page * p.Hk + short_unit / p.q_blocks;
             r.flags = min(n - pg * kPageTokens, kPageTokens);
-            if constexpr (WIN)
-                r.flags |= window_slots(window_pages(n, p.window, p.sinks), pg, p.sinks) << 16;
+            if constexpr (WIN) describe(r, short_b, n, pg);
         } else if (!SHORT && first + lane < mine) {
             const long long x = x0 + first + lane;
             // (64-bit quotients cost ten times 32-bit ones)
@@ -408,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             const int at_page = (int)(rest - (long long)r.unit * n_pages);
             const int n = p.seq_lens[lo];
             int pg = at_page;
-            if constexpr (WIN) pg = window_pages(n, p.window, p.sinks).page(at_page);
+            if constexpr (WIN) pg = seen_of(lo, n).page(at_page);
             int page = p.block_tables[(size_t)lo * p.max_pages + pg];
             if (page < 0 || page >= p.num_pages) {
                 // Reported; page 0 is read instead: nothing outside the cache is touched.
@@ -418,8 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             r.page_head = page * p.Hk + r.unit / p.q_blocks;
             r.flags = min(n - pg * kPageTokens, kPageTokens) | (at_page == 0 ? kFirst : 0) |
                       (at_page == n_pages - 1 ? kLast : 0);
-            if constexpr (WIN)
-                r.flags |= window_slots(window_pages(n, p.window, p.sinks), pg, p.sinks) << 16;
+            if constexpr (WIN) describe(r, lo, n, pg);
         }
         return r;
     };
@@ -454,11 +502,12 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
     uint32_t qf[C::kSteps][NT][2];
     float q_factor[NT][2];  // factor of S^T's columns 2t, 2t+1: scale * log2(e), and for e4m3 the
                             // power of two that brought the query row into fp16's range
-    auto load_q = [&](size_t row0, int n_q) {
+    auto load_q = [&](size_t row0, int n_q, int b, int hk, int q0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int qi = nt * 8 + g;
-            const uint8_t* src = static_cast<const uint8_t*>(p.q) + (row0 + qi) * D * 2;
+            const uint8_t* src = static_cast<const uint8_t*>(p.q) +
+                                 (ROWS ? row_at(p.sq, b, hk, q0 + qi) : (row0 + qi) * D * 2);
             uint32_t w[C::kSteps][2];
 #pragma unroll
             for (int s = 0; s < C::kSteps; ++s) {
@@ -503,6 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
 
     float acc[C::kTiles][NT][4];
     float m[NT][2], eo[NT][2], l[NT][2];
+    int pos[NT][2];        // (ROWS) positions of queries 2t, 2t+1
     size_t row0 = 0;       // first query row of the unit
     int n_q = 0;           // queries of its block
     bool cut = false;      // the unit began in an earlier warp's stretch
@@ -519,7 +569,17 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
             n_q = min(NT * 8, p.group - q0);
             row0 = (size_t)b * p.Hq + (size_t)hk * p.group + q0;
             cut = !(flags & kFirst);
-            load_q(row0, n_q);
+            load_q(row0, n_q, b, hk, q0);
+            if constexpr (ROWS) {
+                const int n = p.seq_lens[b], fresh = fresh_of(b, n);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int i = (q0 + nt * 8 + 2 * t + j) % p.L;
+                        pos[nt][j] = i < fresh ? n - fresh + i : -1;  // (-1: no token, sees nothing)
+                    }
+            }
             if (!SHORT && !cut && lane == 0) {  // for the merge: the warps that have the unit's pages
                 const long long last = x0 + done + (cum[b + 1] - cum[b]) - 1;
                 const int n = done + (cum[b + 1] - cum[b]) <= mine ? 1 : split.worker_of(last) - w + 1;
@@ -665,6 +725,18 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 for (int nt = 0; nt < NT; ++nt) c[nt][2 * r] = c[nt][2 * r + 1] = -INFINITY;
             }
         }
+        if constexpr (ROWS) {
+            if (flags & kEdge) {
+                const int token = __shfl_sync(0xffffffffu, cons.token, done & 31) + g;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = token + (j >> 1) * 8, at = pos[nt][j & 1];
+                        if (key > at || (key <= at - p.window && key >= p.sinks)) c[nt][j] = -INFINITY;
+                    }
+            }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -780,6 +852,13 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                 part_lse = p.slot_lse + slot * p.slot_rows;
             }
         }
+        int unit_b = 0, unit_hk = 0, unit_q0 = 0;  // (ROWS)
+        if constexpr (ROWS) {
+            unit_b = SHORT ? short_b : __shfl_sync(0xffffffffu, cons.b, done & 31);
+            const int unit = SHORT ? short_unit : __shfl_sync(0xffffffffu, cons.unit, done & 31);
+            unit_hk = unit / p.q_blocks;
+            unit_q0 = (unit - unit_hk * p.q_blocks) * (NT * 8);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -806,8 +885,15 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                         v[2 * i] = acc[x * kRun + i][nt][j] * f * hop * hop;
                         v[2 * i + 1] = acc[x * kRun + i][nt][j + 2] * f * hop * hop;
                     }
+                    if (ROWS && L == 0.0f)  // (a row without a token: zeros whatever V holds)
+#pragma unroll
+                        for (int i = 0; i < 2 * kRun; ++i) v[i] = 0.0f;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (row0 + qi) * D + e);
+                        uint16_t* row = ROWS ? reinterpret_cast<uint16_t*>(
+                                                   static_cast<uint8_t*>(p.o) +
+                                                   row_at(p.so, unit_b, unit_hk, unit_q0 + qi))
+                                             : static_cast<uint16_t*>(p.o) + (row0 + qi) * D;
+                        uint4* dst = reinterpret_cast<uint4*>(row + e);
 #pragma unroll
                         for (int i = 0; i < kRun / 4; ++i)
                             dst[i] = make_uint4(pack2<BF16>(v[8 * i], v[8 * i + 1]),
@@ -862,9 +948,10 @@ __global__ void __launch_bounds__(kWarps * 32, gqa_occupancy(D, Q8, NT))
                              x);
             }
             const bool any = sum != 0.0f;  // (true of a NaN)
-            if (threadIdx.x < D)
-                static_cast<uint16_t*>(p.o)[(row + qi) * D + threadIdx.x] =
-                    any ? (uint16_t)pack2<BF16>(x / sum, 0.0f) : (uint16_t)0;
+            uint16_t* dst = ROWS ? reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.o) +
+                                                               row_at(p.so, short_b, hk, q0 + qi))
+                                 : static_cast<uint16_t*>(p.o) + (row + qi) * D;
+            if (threadIdx.x < D) dst[threadIdx.x] = any ? (uint16_t)pack2<BF16>(x / sum, 0.0f) : (uint16_t)0;
             if (threadIdx.x == 0) p.lse[row + qi] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
         }
         cluster_sync();  // the parts have been read
@@ -978,18 +1065,23 @@ __global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
     }
     const bool any = sum != 0.0f;  // (true of a NaN)
     const float f = any ? 1.0f / sum : 0.0f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + (size_t)row * D + lane * kPer);
+    size_t at = (size_t)row * D * 2;
+    if (p.L > 0) {  // rows of a strided output
+        const int heads = p.Hq / p.L, head = h / p.L;
+        at = row_offset(p.so, b * heads + head, heads, h - head * p.L);
+    }
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + at + lane * kPer * 2);
 #pragma unroll
     for (int e = 0; e < kPer; e += 2) dst[e / 2] = any ? pack2<BF16>(x[e] * f, x[e + 1] * f) : 0u;
     if (lane == 0) p.lse[row] = any ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool Q8, bool BF16, int NT, bool SHORT, bool WIN>
+template <int D, bool Q8, bool BF16, int NT, bool SHORT, int MODE>
 cudaError_t launch_w(const GqaParams& p, cudaStream_t s) {
     using C = GqaCfg<D, Q8>;
-    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT, WIN>;
+    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT, MODE>;
     const int smem = C::kRingBytes + 1024 + (kGqaMaxSequences + 1) * 4;
-    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT, WIN>>(kern, smem);
+    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT, MODE>>(kern, smem);
     if (e != cudaSuccess) return e;
     if constexpr (SHORT)
         return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * p.short_step)),
@@ -1002,8 +1094,9 @@ cudaError_t launch_w(const GqaParams& p, cudaStream_t s) {
 
 template <int D, bool Q8, bool BF16, int NT, bool SHORT>
 cudaError_t launch_t(const GqaParams& p, cudaStream_t s) {
-    return p.window > 0 ? launch_w<D, Q8, BF16, NT, SHORT, true>(p, s)
-                        : launch_w<D, Q8, BF16, NT, SHORT, false>(p, s);
+    if (p.L > 0) return launch_w<D, Q8, BF16, NT, SHORT, kRows>(p, s);
+    return p.window > 0 ? launch_w<D, Q8, BF16, NT, SHORT, kWindow>(p, s)
+                        : launch_w<D, Q8, BF16, NT, SHORT, kAll>(p, s);
 }
 
 template <int D, bool Q8, bool BF16>

@@ -208,6 +208,11 @@ struct GqaParams {
     int window, sinks;         // window > 0: each sequence reads its last `window` tokens and its first
                                // `sinks` alone
     int span;                  // pages that a sequence reads at most (max_pages without a window)
+    // L > 0: few new tokens of every sequence.  Hq and group count L rows for each head; q and o are views
+    // [B, heads, L, D]; lse is [B, Hq] all the same.  window > 0 (no window: the table's room).
+    int L;
+    Strides sq, so;
+    const int* new_lens;       // [B], or null: L each (0 for an empty sequence)
     int warps;                 // of a round, a multiple of 4
     int B, Hq, Hk, group, q_blocks, num_pages, max_pages;
     float scale_log2;          // scale * log2(e), either sign
@@ -224,6 +229,8 @@ struct MergeParams {
     void* o;     // [rows, D] 16-bit
     float* lse;  // [rows] natural log
     int rows, B, Hq, Hk, group, q_rows, q_blocks, slot_rows;
+    int L;       // > 0: o is a view [B, Hq / L, L, D], strides so
+    Strides so;
     int workers;  // warps that may have left parts, over all rounds
 };
 

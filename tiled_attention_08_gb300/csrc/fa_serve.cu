@@ -139,8 +139,9 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
     for (int b0 = 0; b0 < B; b0 += kGqaMaxSequences) {
         GqaParams c = p;
         c.B = B - b0 < kGqaMaxSequences ? B - b0 : kGqaMaxSequences;
-        c.q = static_cast<const uint16_t*>(p.q) + b0 * row_o;
-        c.o = static_cast<uint16_t*>(p.o) + b0 * row_o;
+        c.q = static_cast<const uint16_t*>(p.q) + (p.L > 0 ? (size_t)b0 * p.sq.b : b0 * row_o);
+        c.o = static_cast<uint16_t*>(p.o) + (p.L > 0 ? (size_t)b0 * p.so.b : b0 * row_o);
+        if (p.new_lens) c.new_lens = p.new_lens + b0;
         c.lse = p.lse + (size_t)b0 * p.Hq;
         c.block_tables = p.block_tables ? p.block_tables + (size_t)b0 * p.max_pages : nullptr;
         c.seq_lens = p.seq_lens + b0;
@@ -174,6 +175,8 @@ cudaError_t run_decode(GqaParams p, int B, int D, bool bf16, bool q8, uint8_t* w
         m.q_blocks = p.q_blocks;
         m.slot_rows = p.slot_rows;
         m.workers = c.warps * c.rounds;
+        m.L = p.L;
+        m.so = p.so;
         e = traced_launch(kernel++, s, [&] { return launch_merge(m, D, bf16, s); });
         if (e != cudaSuccess) return e;
     }
@@ -272,6 +275,18 @@ fa_status check_chunk(int B, int Hq, int Hk, int L, int D, int num_pages, int ma
     const long long line = (long long)B * p.max_pairs * (max_pages / 8 + 1);
     if (line > 0x7fffffffLL || line * Hk > 1LL << 37) return FA_ERR_UNSUPPORTED;
     return FA_OK;
+}
+
+// Whether the decode kernel takes a chunk, the new tokens of a group's heads as its queries: at most 16 rows per
+// cache head, over e4m3 rows of 64 at most 32, where reading the cache is all.  us of the decode kernel and the
+// chunk's, 64 sequences of 500 to 2000 tokens, 8 cache heads of 128 (of 64), a call with L2 flushed: 16-bit, 8 rows
+// 70 and 88 (48 and 72), 16 rows 87 and 89 (48 and 72), 32 133 and 89 (72 and 72); e4m3, 8 rows 54 and 113 (40 and 98),
+// 16 70 and 114 (50 and 97), 32 110 and 114 (80 and 97), 64 192 and 116 (137 and 99); four sequences of 300 to 30000
+// tokens, 128, e4m3, 32 rows: 89 and 81.
+bool few_rows(int B, int Hq, int Hk, int L, int D, int num_pages, int max_pages, bool q8) {
+    const long long rows = (long long)(Hq / Hk) * L;
+    return rows <= (q8 && D == 64 ? 32 : 16) && (long long)Hq * L <= 65535 &&
+           check_decode(B, Hq * L, Hk, D, num_pages, max_pages, 1.0f, FA_BF16, FA_CACHE_16BIT) == FA_OK;
 }
 
 // Workspace of a chunk's attention, in bytes from its start (the counters come first).
@@ -546,7 +561,10 @@ size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, i
         return 0;
     ChunkParams p;
     chunk_plan(B, Hk, Hq / Hk, L, max_pages, &p);
-    return chunk_workspace(p.grid, D).bytes;
+    const size_t chunk = chunk_workspace(p.grid, D).bytes;
+    if (!few_rows(B, Hq, Hk, L, D, 0, max_pages, true)) return chunk;
+    const size_t decode = decode_workspace(B, Hq * L, Hk, D, max_pages, false, 0).bytes;
+    return chunk > decode ? chunk : decode;
 }
 
 fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_cache, const void* k_exp,
@@ -570,7 +588,8 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
     std::memset(&p, 0, sizeof(p));
     chunk_plan(B, Hk, Hq / Hk, L, max_pages, &p);
     const ChunkWorkspace w = chunk_workspace(p.grid, D);
-    if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    const size_t ws_need = fa_attention_paged_workspace_bytes(B, Hq, Hk, L, D, max_pages);
+    if (!workspace || workspace_bytes < ws_need || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
     Strides sq;
     if (!take_strides(strides[0], B, Hq, &sq) || !take_strides(strides[1], B, Hq, &p.so))
         return FA_ERR_INVALID_ARG;
@@ -579,7 +598,7 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
     const Range ins[] = {extent(q, sq, B, Hq, L, D), range(k_cache, cb), range(v_cache, cb), range(k_exp, eb),
                          range(v_exp, eb), range(block_tables, (size_t)B * max_pages * 4u),
                          range(seq_lens, (size_t)B * 4u), range(new_lens, new_lens ? (size_t)B * 4u : 0)};
-    const Range outs[] = {extent(o, p.so, B, Hq, L, D), range(lse, rows * 4u), range(workspace, w.bytes)};
+    const Range outs[] = {extent(o, p.so, B, Hq, L, D), range(lse, rows * 4u), range(workspace, ws_need)};
     for (int a = 0; a < 3; ++a) {
         for (int i = 0; i < 8; ++i)
             // o may be another part of one packed tensor with q.
@@ -590,6 +609,42 @@ fa_status fa_attention_paged(const void* q, const void* k_cache, const void* v_c
             if (overlap(outs[a], outs[b])) return FA_ERR_INVALID_ARG;
     }
     if (!bind_context()) return FA_ERR_CUDA;
+    if (few_rows(B, Hq, Hk, L, D, num_pages, max_pages, q8)) {
+        GqaParams g;
+        std::memset(&g, 0, sizeof(g));
+        if (num_pages > 0 && (!make_cache_map(&g.tm_k, k_cache, num_pages, Hk, D, dtype, q8) ||
+                              !make_cache_map(&g.tm_v, v_cache, num_pages, Hk, D, dtype, q8)))
+            return FA_ERR_CUDA;
+        const int room = imax(max_pages * kPageTokens, 1);
+        g.q = q;
+        g.sq = sq;
+        g.so = p.so;
+        g.L = L;
+        g.new_lens = new_lens;
+        g.k_exp = static_cast<const uint8_t*>(k_exp);
+        g.v_exp = static_cast<const uint8_t*>(v_exp);
+        g.block_tables = block_tables;
+        g.seq_lens = seq_lens;
+        g.o = o;
+        g.lse = lse;
+        g.Hq = Hq * L;
+        g.Hk = Hk;
+        g.group = Hq / Hk * L;
+        g.num_pages = num_pages;
+        g.max_pages = max_pages;
+        g.window = window == 0 ? room : imin(window, room);
+        g.sinks = window == 0 ? 0 : imin(sinks, room);
+        g.span = window_span(max_pages, g.window + L - 1, g.sinks);
+        g.scale_log2 = scale * 1.4426950408889634f;
+        g.status = status_ptr();
+        g.timeout_ns = wait_timeout_ns();
+        if (!g.status) return FA_ERR_CUDA;
+        const DecodeWorkspace dw = decode_workspace(B, Hq * L, Hk, D, g.span, false, 0);
+        return run_decode(g, B, D, bf16, q8, static_cast<uint8_t*>(workspace), dw, 0, 0, 0,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? FA_OK
+                   : FA_ERR_CUDA;
+    }
     const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)L, (cuuint64_t)Hq, (cuuint64_t)B};
     const cuuint64_t qs[3] = {(cuuint64_t)sq.l * 2, (cuuint64_t)sq.h * 2, (cuuint64_t)sq.b * 2};
