@@ -17,9 +17,12 @@ TFLOPS to FlashAttention", sections 4.2-4.3).
 
 Around attention: ``rotary`` (differentiable), ``rotary_apply`` and ``rotary_freqs`` turn queries
 and keys by their positions; ``cache_append`` and ``cache_read`` write and read a paged cache of
-16-bit or e4m3 rows; ``decode_paged`` attends to such a cache with equal or grouped heads and
-``decode_shared_prefix`` does so for a batch whose sequences begin alike.  These go through
-``fa_torch.so``, a C++ binding over the same C ABI.
+16-bit or e4m3 rows; ``decode_paged`` attends to such a cache with equal or grouped heads, to all
+tokens or to a sliding window and the first ones, and ``decode_shared_prefix`` does so for a batch
+whose sequences begin alike; ``attention_paged`` attends a chunk of new tokens of every sequence to
+it.  ``attention_window`` (differentiable; ``window_forward``, ``window_backward``) is attention
+under such a window over dense tensors with grouped heads.  These go through ``fa_torch.so``, a C++
+binding over the same C ABI.
 """
 from __future__ import annotations
 

@@ -49,7 +49,8 @@
 // 256.  Both are careful: 16-bit caches still gain there (8 units of 256 pages, heads of 64: 10.4 and 9.9).
 //
 // Windows (kWindow).  A sequence's pages are those of its last `window` tokens and of the first `sinks`; the line
-// counts those alone, and slots of their pages that do not count are masked as those past the end are.
+// counts those alone, and slots of their pages that do not count are masked as those past the end are.  256 sequences,
+// window 4096, 524 us (7.2 TB/s, 107% of the measured copy); 48 of window 1024, 64 heads on 8 of 128, e4m3, 33 us.
 //
 // Few new tokens (kRows).  The queries of a unit are then the new tokens of all heads of a group, so the cached rows
 // are read once for all of them, at HBM's rate where a 128-row tile of the chunk kernel (fa_chunk.cu) would be nearly

@@ -17,6 +17,14 @@
 //    then sits out the last key tiles and B the window's first ones.  A short call, whose single tiles find
 //    an SM each, takes them one by one (the last 200 of 1500 tokens, 32 heads on 8: 20.5 -> 17.7 us).
 //  * a row may see nothing in a tile that its item visits, so that its reference is still -inf there.
+//
+// Measured: 16384 tokens, 32 heads on 8 of 128, window 4096, 4 first tokens 640 us (1500 TFLOP/s of visible pairs);
+// 8 x 4096, 32 heads of 128, window 1024 450 us (1070); 3 x 5001, 16 heads on 4 of 64, window 777, 131 first 106 us
+// (480).  A step of both tiles takes 3400 cycles where its contractions take 2050: the chain from S to softmax to PV
+// counts, as in the dense forward.  Short windows lose the hidden halves of their first and last tiles and 4000 to 5000
+// cycles an item (first step, read-out).  Tried and dropped: S of the next item in front of this one's last PV (642 ->
+// 646, 451 -> 455 us); a tile of few first tokens as its first 32 keys alone (483 -> 480 us with them, 447 -> 462
+// without: code of two widths).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_sched.h"
