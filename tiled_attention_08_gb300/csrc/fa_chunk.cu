@@ -64,6 +64,11 @@ struct ChunkCfg {
     static constexpr int kOffRaw = kOffKV + kSlots * kTileBytes;
     static constexpr int kOffExp = kOffRaw + 2 * kRaw * kRawBytes;
     static constexpr int kSmemBytes = kOffExp + 2 * kRaw * kTileRows + 1024;
+    // 16-bit: the K warp works the segments out and leaves them in a ring of this many.  Done by every warp for itself
+    // that took 3000 of the 10000 cycles of an item of one tile (its code is cold whenever it is reached): 309 -> 295 us
+    // for chunks of 2048, 167.5 -> 163.4 for prompts of 4096.  (e4m3: 92 -> 86 us for 64 chunks of 20,
+    // but 788 -> 817 for eight of 512, whose loops fill the instruction cache; every warp for itself.)
+    static constexpr int kSegs = Q8 ? 1 : 4;
     // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 19: converters.
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
     static constexpr int kConverters = Q8 ? 8 : 0;
@@ -165,6 +170,7 @@ struct Segment {
     KeyTiles all;
     int n_all, j0, n;
     int a_end, b_0, b_1;   // A sees tiles j < a_end of `all`, B those of j < b_0 and j >= b_1
+    int done;              // units of the CTA in front of it
     bool has_b;
     __device__ __forceinline__ bool active(int t, int j) const { return t ? has_b && (j < b_0 || j >= b_1) : j < a_end; }
     __device__ __forceinline__ int count(int t) const {  // of the segment's
@@ -328,6 +334,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                                                ~uintptr_t(1023));
     __shared__ uint64_t bar_qf, bar_qe, bar_f[C::kSlots], bar_e[C::kSlots];  // slots full / empty
     __shared__ uint64_t bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint64_t bar_segf[C::kSegs], bar_sege[C::kSegs];  // segments there / taken
+    __shared__ Segment seg_sh[C::kSegs];
     __shared__ uint64_t bar_part, bar_ticket;  // a part written by all softmax warps; counted
     __shared__ uint64_t bar_rf[Q8 ? 2 * C::kRaw : 1], bar_re[Q8 ? 2 * C::kRaw : 1];  // bytes landed / read
     __shared__ uint32_t tmem_base_sh;
@@ -361,6 +369,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         for (int s = 0; s < 2 * C::kRaw; ++s) {
             mbar_init(&bar_rf[s], 1);
             mbar_init(&bar_re[s], C::kConverters);
+        }
+        for (int s = 0; s < C::kSegs; ++s) {
+            mbar_init(&bar_segf[s], 1);
+            mbar_init(&bar_sege[s], 10);  // V, MMA and softmax warps
         }
         mbar_init(&bar_part, 8);
         mbar_init(&bar_ticket, 1);
@@ -435,6 +447,17 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base_sh;
     Walk walk = start_sh;
+    // (16-bit) The i-th segment of this CTA, for all warps but K's; false behind the last one, and (ok = false)
+    // without it.
+    auto take = [&](int i, Segment& s, bool& ok) -> bool {
+        const int at = i % C::kSegs;
+        ok = wait_warp(&bar_segf[at], (uint32_t)(i / C::kSegs) & 1u, abort_v, p.timeout_ns);
+        if (!ok) return false;
+        s = seg_sh[at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_sege[at]);
+        return s.n > 0;
+    };
 
     // (A warpgroup sets its registers with one instruction.)
     if (warp >= 8) {
@@ -455,7 +478,23 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         bool ok = true;
         int issued = 0, n_seg = 0;
         Segment sg;
-        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+        // The next segment, K: worked out and left for the others.
+        auto leave = [&](int i) -> bool {
+            if (!segment_at(p, walk, sg)) sg.n = 0;
+            sg.done = start_sh.left - walk.left;
+            const int at = i % C::kSegs;
+            if (i >= C::kSegs) ok = wait_warp(&bar_sege[at], (uint32_t)(i / C::kSegs - 1) & 1u, abort_v, p.timeout_ns);
+            if (!ok) return false;
+            if (lane == 0) {
+                seg_sh[at] = sg;
+                mbar_arrive(&bar_segf[at]);
+            }
+            __syncwarp();
+            return sg.n > 0;
+        };
+        int i = 0;
+        for (; ok && (Q8 ? segment_at(p, walk, sg) : is_k ? leave(i) : take(i, sg, ok));
+             Q8 || is_k ? step(p, sg, walk) : void(), ++i) {
             if (is_k) {
                 if (n_seg > 0) ok = wait_warp(&bar_qe, (uint32_t)(n_seg - 1) & 1u, abort_v, p.timeout_ns);
                 if (!ok) break;
@@ -535,7 +574,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             return r;
         };
         Segment sg;
-        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+        int i = 0;
+        for (; ok && (Q8 ? segment_at(p, walk, sg) : take(i, sg, ok)); Q8 ? step(p, sg, walk) : void(++i)) {
             const Live live = live_of(p, sg);
             const int j1 = sg.j0 + sg.n;
             const int n_of[2] = {sg.count(0), sg.count(1)};
@@ -729,7 +769,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
         bool ok = true;
         int ps = 0, n_done = 0, n_cut = 0;
         Segment sg;
-        for (; ok && segment_at(p, walk, sg); step(p, sg, walk)) {
+        int i = 0;
+        for (; ok && (Q8 ? segment_at(p, walk, sg) : take(i, sg, ok)); Q8 ? step(p, sg, walk) : void(++i)) {
             const int j1 = sg.j0 + sg.n, cnt = sg.count(t);
             const int first = sg.before + sg.t0 + t * p.T, pos = first + tok;
             const int last = imin(first + p.T, sg.before + sg.fresh) - 1;
@@ -818,10 +859,10 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
             if (whole) {
                 const int h = sg.hk * p.group + head;
                 const size_t orow = (size_t)sg.b * p.Hq + h;
-                const int i = sg.t0 + t * p.T + tok;
-                if (valid) p.lse[orow * p.L + i] = lse2 * kLn2;
+                const int new_i = sg.t0 + t * p.T + tok;
+                if (valid) p.lse[orow * p.L + new_i] = lse2 * kLn2;
                 uint8_t* dst = valid ? reinterpret_cast<uint8_t*>(p.o) +
-                                           row_offset(p.so, (int)orow, p.Hq, i)
+                                           row_offset(p.so, (int)orow, p.Hq, new_i)
                                      : nullptr;
                 if (cnt > 0) {
 #pragma unroll 1
@@ -854,7 +895,7 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                     }
                 }
                 // The CTA that ends the pair's last part joins them all.
-                const long long x0 = total_sh * blockIdx.x / workers + (start_sh.left - walk.left) - sg.j0;
+                const long long x0 = total_sh * blockIdx.x / workers + (Q8 ? start_sh.left - walk.left : sg.done) - sg.j0;
                 const int owner = unit_cta(total_sh, workers, x0);
                 const int n_parts = unit_cta(total_sh, workers, x0 + sg.n_all - 1) - owner + 1;
                 __threadfence();
