@@ -19,9 +19,9 @@
 //  * a row may see nothing in a tile that its item visits, so that its reference is still -inf there.
 //
 // Measured: 16384 tokens, 32 heads on 8 of 128, window 4096, 4 first tokens 640 us (1500 TFLOP/s of visible pairs);
-// 8 x 4096, 32 heads of 128, window 1024 450 us (1070); 3 x 5001, 16 heads on 4 of 64, window 777, 131 first 106 us
-// (480).  A step of both tiles takes 3400 cycles where its contractions take 2050: the chain from S to softmax to PV
-// counts, as in the dense forward.  Short windows lose the hidden halves of their first and last tiles and 4000 to 5000
+// 8 x 4096, 32 heads of 128, window 1024 441 us (1090); 3 x 5001, 16 heads on 4 of 64, window 777, 131 first 102 us
+// (497).  A step of both tiles takes 3400 cycles where its contractions take 2050: the chain from S to softmax to PV
+// counts, as in the dense forward.  Short windows lose the hidden halves of their first and last tiles and about 4000
 // cycles an item (first step, read-out).  Tried and dropped: S of the next item in front of this one's last PV (642 ->
 // 646, 451 -> 455 us); a tile of few first tokens as its first 32 keys alone (483 -> 480 us with them, 447 -> 462
 // without: code of two widths).
@@ -53,6 +53,10 @@ struct WinCfg {
     static constexpr int kSmemBytes = kOffStage + 8 * kStageBytes + 1024;
     static constexpr int kProducerWarp = 8, kMmaWarp = 9, kVProducerWarp = 10;
     static constexpr int kThreads = (kMergedKV ? 10 : 11) * 32;
+    // The producer works the items out and leaves them in a ring of this many.  (Every warp for itself, in code that is
+    // cold whenever it is reached: heads of 64, window 256 192 us against 176, window 1024 380 and 361; heads of 128,
+    // window 1024 447 and 441, window 256 286 and 293.)
+    static constexpr int kItems = 4;
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kTmS = 0, kTmO = 256;
     static_assert(kTmO + 2 * D <= kTmemCols, "TMEM budget");
@@ -110,6 +114,8 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
     __shared__ uint64_t bar_qf[C::kQSlots], bar_qe[C::kQSlots];  // Q pair landed / read by S
     __shared__ uint64_t bar_kf[C::kStages], bar_ke[C::kStages], bar_vf[C::kStages], bar_ve[C::kStages];
     __shared__ uint64_t bar_sf[2], bar_pf[2], bar_oready[2], bar_fin;
+    __shared__ uint64_t bar_itf[C::kItems], bar_ite[C::kItems];  // items there / taken
+    __shared__ Item item_sh[C::kItems];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,6 +138,10 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
             mbar_init(&bar_pf[t], 128);
             mbar_init(&bar_oready[t], 1);
         }
+        for (int s = 0; s < C::kItems; ++s) {
+            mbar_init(&bar_itf[s], 1);
+            mbar_init(&bar_ite[s], C::kMergedKV ? 9 : 10);  // MMA, softmax and V warps
+        }
         mbar_init(&bar_fin, 1);
         mbar_fence_init();
     }
@@ -140,6 +150,19 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base_sh;
+    // The i-th item with a key to see, for all warps but the producer; false behind the last one, and (ok = false)
+    // without it.  One of a warp's lanes may call it alone.
+    auto take = [&](int i, Item& it, bool whole_warp, bool& ok) -> bool {
+        const int at = i % C::kItems;
+        const uint32_t ph = (uint32_t)(i / C::kItems) & 1u;
+        ok = whole_warp ? wait_warp(&bar_itf[at], ph, abort_v, p.timeout_ns)
+                        : wait_bounded(&bar_itf[at], ph, abort_v, p.timeout_ns);
+        if (!ok) return false;
+        it = item_sh[at];
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(&bar_ite[at]);
+        return it.n > 0;
+    };
     auto q_tile = [&](int slot, int t) { return smem + C::kOffQ + (slot * 2 + t) * C::kTileBytes; };
 
     if (warp == C::kProducerWarp || warp == C::kVProducerWarp) {
@@ -157,8 +180,21 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
             bool ok = true;
             int issued = 0, n_q = 0;  // ring fills and Q pairs handed to the TMA unit
             Item it;
-            for (int round = 0; ok && item_at(p, round, it); ++round) {
-                if (it.n == 0) continue;  // no row sees a key
+            int round = 0;
+            // The next item, the producer: worked out and left for the others.
+            auto leave = [&](int i) -> bool {
+                bool more;
+                while ((more = item_at(p, round++, it)) && it.n == 0) {}  // (no row sees a key)
+                if (!more) it.n = 0;
+                const int at = i % C::kItems;
+                if (i >= C::kItems)
+                    ok = wait_bounded(&bar_ite[at], (uint32_t)(i / C::kItems - 1) & 1u, abort_v, p.timeout_ns);
+                if (!ok) return false;
+                item_sh[at] = it;
+                mbar_arrive(&bar_itf[at]);
+                return more;
+            };
+            for (int i = 0; ok && (is_k ? leave(i) : take(i, it, false, ok)); ++i) {
                 if (is_k) {
                     const int qs = n_q % C::kQSlots, use = n_q / C::kQSlots;
                     if (use > 0 && !wait_bounded(&bar_qe[qs], (uint32_t)(use - 1) & 1u, abort_v, p.timeout_ns)) {
@@ -214,8 +250,7 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
             return true;
         };
         Item it;
-        for (int round = 0; ok && item_at(p, round, it); ++round) {
-            if (it.n == 0) continue;
+        for (int i = 0; ok && take(i, it, true, ok); ++i) {
             const int qs = n_item % C::kQSlots;
             int done[2] = {0, 0};  // PV of tile t in this item
             auto issue_s = [&](int t, int gk) {  // S_t = Q_t K^T for ring fill gk
@@ -300,7 +335,7 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
         bool ok = true;
         int ps = 0, n_done = 0;
         Item it;
-        for (int round = 0; ok && item_at(p, round, it); ++round) {
+        for (int i = 0; ok && take(i, it, true, ok); ++i) {
             const KeyTiles mine = t ? it.of[1] : it.of[0];
             const int n = mine.count();
             if (n == 0) continue;
