@@ -22,9 +22,10 @@
 //    sums the pairs' key tiles.  A pair that lies whole in a stretch is written as O and LSE; of a cut
 //    one each CTA leaves an fp32 part (two at most), and the one that finds the others' there joins them.  (A kernel
 //    of its own for that took 16 of 177 us for two prompts of 4096 tokens, 6 of 24 for one short turn.)
-// Measured: two prompts of 4096 tokens, 32 heads of 128, 170 us (980 TFLOP/s); four chunks of 2048 of a window
-// of 4096 310 us (1220); eight of 512 behind up to 16384 tokens, 64 heads on 8, e4m3, 850 us (1150); 17 of up to 127
-// tokens, 16 heads on 4 of 64, 48 us.  A CTA's start (lengths, line, first tiles) is 4 us, a cut pair 6 to 13 us.
+// Measured, this kernel alone: two prompts of 4096 tokens, 32 heads of 128, 163 us (1060 TFLOP/s); four chunks of 2048
+// under a window of 4096, 32 heads on 8, 295 us (1320); eight of 512 behind up to 16384 tokens, 64 heads on 8, e4m3,
+// 790 us (1240); 17 of up to 127 tokens, 16 heads on 4 of 64, 47 us.  A CTA's start (lengths, line, first tiles) is
+// 4 us, a cut pair 6 to 13 us.
 // Chunks of very few rows per cache head are the decode kernel's (fa_decode_gqa.cu, kRows; few_rows in fa_serve.cu).
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
