@@ -180,6 +180,37 @@ def test_few_rows_with_bad_lengths(q8):
         check(o[1:], lse[1:], q[1:], ks[1:], vs[1:], [60], [4], 0, 0, 1 / 8)
 
 
+@pytest.mark.parametrize("pages", [64, 2000])
+def test_few_rows_captured_and_replayed_on_a_side_stream(pages):
+    """Lengths and counts change between replays; a cluster per unit (a short table) and the line."""
+    rng = np.random.default_rng(26)
+    lens, news = [900, 130, 3], [4, 1, 3]
+    kc, vc, ke, ve, bt, sl, ks, vs = fill(rng, lens, 2, 64, FP16, True)
+    bt = torch.nn.functional.pad(bt, (0, pages - bt.shape[1])).contiguous()
+    q = randn(3, 4, 4, 64, dtype=FP16)
+    nl, o, lse = torch.ones(3, dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty(3, 4, 4, device="cuda")
+    ws = torch.empty(fa.fa_attention_paged_workspace_bytes(3, 4, 2, 4, 64, pages), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+
+    def step():
+        fa.attention_paged(q, kc, vc, bt, sl, nl, out=o, lse=lse, workspace=ws, k_exp=ke, v_exp=ve)
+
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for n, m in (([400, 0, 1], [4, 0, 1]), (lens, news)):
+        sl.copy_(torch.tensor(n))
+        nl.copy_(torch.tensor(m))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(o, lse, q, [x[:, :a] for x, a in zip(ks, n)], [x[:, :a] for x, a in zip(vs, n)], n, m, 0, 0, 1 / 8)
+    assert status() == fa.FA_OK
+
+
 @pytest.mark.parametrize("Hq,Hk", [(128, 1), (100, 1), (65, 1), (64, 2)])
 def test_large_groups(Hq, Hk):
     run(3, [70, 300], [20, 9], Hq, Hk, 64, FP16, False)

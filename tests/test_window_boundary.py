@@ -213,5 +213,8 @@ def test_chunk_workspace():
     need = fa.fa_attention_paged_workspace_bytes
     assert need(64, 64, 8, 4096, 128, 4096) <= 41_000_000
     assert 0 < need(1, 8, 8, 16, 128, 4) < need(64, 64, 8, 4096, 128, 4096)
+    # Few rows per cache head, whatever the sizes.
+    assert max(need(B, G * Hk, Hk, L, 128, pages) for B in (1, 64, 1024, 4096) for Hk in (1, 8, 128)
+               for G in (1, 8, 16) for L in (1, 4, 16) for pages in (1, 64, 4096)) <= 123_000_000
     for bad in ((0, 4, 2, 32, 64, 4), (2, 4, 3, 32, 64, 4), (2, 4, 2, 0, 64, 4), (2, 4, 2, 32, 96, 4)):
         assert need(*bad) == 0
