@@ -899,7 +899,6 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                 const long long x0 = total_sh * blockIdx.x / workers + (Q8 ? start_sh.left - walk.left : sg.done) - sg.j0;
                 const int owner = unit_cta(total_sh, workers, x0);
                 const int n_parts = unit_cta(total_sh, workers, x0 + sg.n_all - 1) - owner + 1;
-                __threadfence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_part);
                 if (warp == 0) {
@@ -907,7 +906,11 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                     if (!ok) break;
                     if (lane == 0) {
                         pdl_wait();  // the counters are zeroed
+                        // The thread that counts fences on both sides: its atomic alone orders nothing, and the
+                        // barriers carry the other warps' stores to it, and what it has seen to their loads.
+                        __threadfence();
                         *reinterpret_cast<volatile int*>(&ticket_sh) = atomicAdd(&p.counters[owner], 1);
+                        __threadfence();
                         mbar_arrive(&bar_ticket);
                     }
                     __syncwarp();
@@ -915,10 +918,8 @@ __global__ void __launch_bounds__(ChunkCfg<D, BF16, Q8>::kThreads, 1)
                 ok = wait_warp(&bar_ticket, (uint32_t)n_cut & 1u, abort_v, p.timeout_ns);
                 if (!ok) break;
                 ++n_cut;
-                if (*reinterpret_cast<volatile int*>(&ticket_sh) == n_parts - 1) {
-                    __threadfence();
+                if (*reinterpret_cast<volatile int*>(&ticket_sh) == n_parts - 1)
                     join_parts<D, BF16>(p, sg.b, sg.hk, sg.t0, sg.fresh, owner, n_parts, warp, lane);
-                }
             }
         }
         if (!ok && lane == 0) record_timeout(p.status, abort_v);
