@@ -35,6 +35,10 @@ namespace {
 
 constexpr float kRescaleThreshold = 8.0f;
 constexpr float kLn2 = 0.6931471805599453f;
+// fp16 weights are taken relative to a reference 2^7 below the largest, so that small ones behind a large one (a first
+// token that stays visible) keep their bits: 2^-20.5 of the largest is off by eps/2, not by 2.8%.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
 
 template <int D, bool BF16>
 struct WinCfg {
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
                 }
                 const float m_cand = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * p.scale_log2;
                 float m_new = m_ref;
-                if (m_cand > m_ref + kRescaleThreshold) m_new = m_cand;
+                if (m_cand > m_ref + (kRescaleThreshold + kLift<BF16>)) m_new = m_cand - kLift<BF16>;
                 const bool rescale = (j > 0) && (m_new != m_ref);
                 const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
                 const float alpha = rescale ? ex2_approx(m_ref - m_new) : 1.0f;
