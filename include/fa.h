@@ -376,7 +376,7 @@ size_t fa_attention_paged_workspace_bytes(int B, int Hq, int Hk, int L, int D, i
  * values have been written (fa_cache_append).  Sequence b has seq_lens[b] tokens in the cache, the last
  * new_lens[b] of them new; row i < new_lens[b] of q[b, h] is token t = seq_lens[b] - new_lens[b] + i and
  * attends to tokens j <= t of cache head h / (Hq / Hk), with window > 0 to those with j > t - window or
- * j < sinks alone (window = 0: to all; sinks is ignored).
+ * j < sinks alone (window = 0: to all, whatever sinks >= 0 is).
  *   q, o:      [B, Hq, L, D] views of dtype (strides[0..1]); o may be another part of one packed tensor with q;
  *   lse:       [B, Hq, L] fp32, contiguous;
  *   new_lens:  [B] int32, device, 0 <= new_lens[b] <= min(L, seq_lens[b]); null: L for every sequence, 0 for

@@ -31,8 +31,8 @@ import math
 import os
 import threading
 
-__all__ = ["FaError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa_bwd", "fa_bwd_ex",
-           "fa_bwd_workspace_bytes", "fa_bwd_workspace_bytes_ex", "fa_set_forward_pair",
+__all__ = ["FaError", "FaArgumentError", "load_library", "library_path", "fa_fwd", "fa_fwd_ex", "fa_bwd",
+           "fa_bwd_ex", "fa_bwd_workspace_bytes", "fa_bwd_workspace_bytes_ex", "fa_set_forward_pair",
            "fa_get_device_status",
            "fa_set_wait_timeout_ns",
            "fa_selftest_wait_timeout", "fa_trace_next_call", "fa_launch_count", "fa_status_string",
@@ -78,9 +78,18 @@ class FaStrides(ctypes.Structure):
 
 
 class FaError(RuntimeError):
+    """A call's status other than FA_OK; for FA_ERR_INVALID_ARG it is a FaArgumentError."""
+
+    def __new__(cls, call: str, status: int):
+        return super().__new__(FaArgumentError if status == FA_ERR_INVALID_ARG else cls, call, status)
+
     def __init__(self, call: str, status: int):
         super().__init__(f"{call} failed: {fa_status_string(status)} ({status})")
         self.status = status
+
+
+class FaArgumentError(FaError, ValueError):
+    """FaError of a call that was refused for its arguments: a ValueError, too."""
 
 
 def library_path() -> str:
@@ -559,7 +568,8 @@ def decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale: float | Non
     and may be float8_e4m3fn with the exponents ``k_exp``, ``v_exp`` that ``cache_append`` wrote.
 
     With ``window`` a sequence attends to its last ``window`` and its first ``sinks`` tokens alone; pages of
-    other tokens are not looked up (fa_decode_window in fa.h).  ``sinks`` counts with a window only."""
+    other tokens are not looked up (fa_decode_window in fa.h).  ``sinks`` (0 or more) counts with a window
+    only."""
     return (_binding or _ops()).decode_paged(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse,
                                              workspace, k_exp, v_exp, window, sinks)
 

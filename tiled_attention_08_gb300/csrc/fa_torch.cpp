@@ -73,6 +73,11 @@ int as_int(const char* name, int64_t v) {
 // Windows and counts of first tokens are ints in the C interface; beyond its lengths they mean the same.
 int as_span(int64_t v) { return (int)std::clamp<int64_t>(v, INT32_MIN, INT32_MAX); }
 
+// A window (none: all tokens) and a count of first tokens, refused alike by every call that takes them.
+void check_span(const char* call, std::optional<int64_t> window, int64_t sinks) {
+    if ((window && *window < 1) || sinks < 0) throw StatusError(call, FA_ERR_INVALID_ARG);
+}
+
 // Whether the kernels can step by a view's stride of dimension i.
 bool usable_stride(const Tensor& t, int i) { return t.stride(i) > 0 && (t.stride(i) & 7) == 0; }
 
@@ -485,6 +490,7 @@ std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, 
                                         const OptTensor& lse, const OptTensor& workspace,
                                         const OptTensor& k_exp, const OptTensor& v_exp,
                                         std::optional<int64_t> window, int64_t sinks) {
+    check_span("decode_paged", window, sinks);
     if (window || given(k_exp) || given(v_exp) || q.dim() != 3 || k_cache.dim() != 4 ||
         k_cache.size(1) != q.size(1))
         return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
@@ -592,6 +598,7 @@ void check_lse(const Tensor& lse, const WindowSizes& w) {
 
 std::tuple<Tensor, Tensor> window_fwd(const Tensor& q_, const Tensor& k_, const Tensor& v_, const Window& win,
                                       const OptTensor& out, const OptTensor& lse) {
+    check_span("attention_window", win.window, win.sinks);
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
     const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_);
     const WindowSizes w = window_sizes(q, k, v);
@@ -611,6 +618,7 @@ std::tuple<Tensor, Tensor, Tensor> window_bwd(const Tensor& q_, const Tensor& k_
                                               const Tensor& o_, const Tensor& lse, const Tensor& dout_,
                                               const Window& win, const OptTensor& workspace,
                                               const OptTensor& dq_, const OptTensor& dk_, const OptTensor& dv_) {
+    check_span("window_backward", win.window, win.sinks);
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
     const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_), o = kernel_view(o_),
                  dout = kernel_view(dout_);
@@ -695,6 +703,7 @@ std::tuple<Tensor, Tensor> attention_paged(const Tensor& q_, const Tensor& k_cac
                                            std::optional<double> scale, const OptTensor& out, const OptTensor& lse,
                                            const OptTensor& workspace, const OptTensor& k_exp,
                                            const OptTensor& v_exp) {
+    check_span("attention_paged", window, sinks);
     const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
     const int index = cuda_index("q", q_);
     TORCH_CHECK_VALUE(q_.dim() == 4, "q must be a [B, H, L, D] view");
@@ -706,7 +715,6 @@ std::tuple<Tensor, Tensor> attention_paged(const Tensor& q_, const Tensor& k_cac
     TORCH_CHECK_VALUE(c.D == D, "the cache has heads of ", c.D, ", q of ", D);
     const int max_pages = check_tables(block_tables, seq_lens, B, index);
     if (given(new_lens)) int32_vector("new_lens", *new_lens, B, index);
-    TORCH_CHECK_VALUE(!window || *window >= 1, "window must be at least 1 (or None)");
     const Tensor o = output_like("out", out, q);
     const Tensor l = given(lse) ? *lse : at::empty({B, Hq, L}, q.options().dtype(at::kFloat));
     const int64_t shape[3] = {B, Hq, L};
