@@ -46,6 +46,14 @@ def test_refused_alike(name, window, sinks):
     assert e.value.status == fa.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_others_go_on(name):
+    """To the next check: these tensors are not on a GPU."""
+    for window, sinks in ((1, 0), (1 << 40, 1 << 40), *(((None, 0), (None, 5)) if name in PAGED else ())):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            calls()[name](window, sinks)
+
+
 def test_errors_by_status():
     bad, other = fa.FaError("fa_call", fa.FA_ERR_INVALID_ARG), fa.FaError("fa_call", fa.FA_ERR_UNSUPPORTED)
     assert type(bad) is fa.FaArgumentError and type(other) is fa.FaError

@@ -448,7 +448,7 @@ std::tuple<Tensor, Tensor> decode_paged_ex(const Tensor& q, const Tensor& k_cach
                                            const OptTensor& lse, const OptTensor& workspace,
                                            const OptTensor& k_exp, const OptTensor& v_exp,
                                            std::optional<int64_t> window = {}, int64_t sinks = 0) {
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)cuda_index("q", q));
     const Step s = decode_outputs(q, out, lse);
     const Cache c = check_cache(k_cache, v_cache, k_exp, v_exp, q.scalar_type(), s.index);
     TORCH_CHECK_VALUE(c.D == s.D, "the cache has heads of ", c.D, ", q of ", s.D);
@@ -495,8 +495,8 @@ std::tuple<Tensor, Tensor> decode_paged(const Tensor& q, const Tensor& k_cache, 
         k_cache.size(1) != q.size(1))
         return decode_paged_ex(q, k_cache, v_cache, block_tables, seq_lens, scale, out, lse, workspace,
                                k_exp, v_exp, window, sinks);
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
     const int index = cuda_index("q", q);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
     TORCH_CHECK_VALUE(q.is_contiguous(), "q must be contiguous");
     const int dt = dtype_code(q);
     const Cache c = check_cache(k_cache, v_cache, {}, {}, q.scalar_type(), index);
@@ -529,7 +529,7 @@ std::tuple<Tensor, Tensor> decode_shared_prefix(const Tensor& q, const Tensor& k
                                                 const Tensor& seq_lens, std::optional<double> scale,
                                                 const OptTensor& out, const OptTensor& lse,
                                                 const OptTensor& workspace) {
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q));
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)cuda_index("q", q));
     const Step s = decode_outputs(q, out, lse);
     const Cache c = check_cache(k_cache, v_cache, {}, {}, q.scalar_type(), s.index);
     TORCH_CHECK_VALUE(c.D == s.D, "the cache has heads of ", c.D, ", q of ", s.D);
@@ -599,7 +599,7 @@ void check_lse(const Tensor& lse, const WindowSizes& w) {
 std::tuple<Tensor, Tensor> window_fwd(const Tensor& q_, const Tensor& k_, const Tensor& v_, const Window& win,
                                       const OptTensor& out, const OptTensor& lse) {
     check_span("attention_window", win.window, win.sinks);
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)cuda_index("q", q_));
     const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_);
     const WindowSizes w = window_sizes(q, k, v);
     const Tensor o = output_like("out", out, q);
@@ -619,7 +619,7 @@ std::tuple<Tensor, Tensor, Tensor> window_bwd(const Tensor& q_, const Tensor& k_
                                               const Window& win, const OptTensor& workspace,
                                               const OptTensor& dq_, const OptTensor& dk_, const OptTensor& dv_) {
     check_span("window_backward", win.window, win.sinks);
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)cuda_index("q", q_));
     const Tensor q = kernel_view(q_), k = kernel_view(k_), v = kernel_view(v_), o = kernel_view(o_),
                  dout = kernel_view(dout_);
     const WindowSizes w = window_sizes(q, k, v);
@@ -704,8 +704,8 @@ std::tuple<Tensor, Tensor> attention_paged(const Tensor& q_, const Tensor& k_cac
                                            const OptTensor& workspace, const OptTensor& k_exp,
                                            const OptTensor& v_exp) {
     check_span("attention_paged", window, sinks);
-    const c10::cuda::OptionalCUDAGuard guard(at::device_of(q_));
     const int index = cuda_index("q", q_);
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
     TORCH_CHECK_VALUE(q_.dim() == 4, "q must be a [B, H, L, D] view");
     const int dt = dtype_code(q_);
     const Tensor q = kernel_view(q_);
