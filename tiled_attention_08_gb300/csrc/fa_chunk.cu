@@ -21,11 +21,11 @@
 //    query tiles, key tile) form one line, of which every CTA takes an equal stretch: each CTA first
 //    sums the pairs' key tiles.  A pair that lies whole in a stretch is written as O and LSE; of a cut
 //    one each CTA leaves an fp32 part (two at most), and the one that finds the others' there joins them.  (A kernel
-//    of its own for that took 16 of 177 us for two prompts of 4096 tokens, 6 of 24 for one short turn.)
-// Measured, this kernel alone: two prompts of 4096 tokens, 32 heads of 128, 163 us (1060 TFLOP/s); four chunks of 2048
-// under a window of 4096, 32 heads on 8, 295 us (1320); eight of 512 behind up to 16384 tokens, 64 heads on 8, e4m3,
-// 790 us (1240); 17 of up to 127 tokens, 16 heads on 4 of 64, 47 us.  A CTA's start (lengths, line, first tiles) is
-// 4 us, a cut pair 6 to 13 us.
+//    of its own for that took 16 of 177 us for the two prompts below, 6 of 24 for one short turn.)
+// Measured, this kernel alone: prompts of 2048 and 4096 tokens, 32 heads of 128, 163 us (1060 TFLOP/s); four chunks of
+// 1024 to 2048 under a window of 4096, 32 heads on 8, 295 us (1320); eight of 256 to 512 behind 512 to 16384 tokens, 64
+// heads on 8, e4m3, 790 us (1240); 17 of 63 to 127 tokens, 16 heads on 4 of 64, 47 us.  A CTA's start (lengths, line,
+// first tiles) is 4 us, a cut pair 6 to 13 us.
 // Chunks of very few rows per cache head are the decode kernel's (fa_decode_gqa.cu, kRows; few_rows in fa_serve.cu).
 #include "fa_e4m3.cuh"
 #include "fa_internal.h"
@@ -67,15 +67,17 @@ struct ChunkCfg {
     static constexpr int kSmemBytes = kOffExp + 2 * kRaw * kTileRows + 1024;
     // 16-bit: the K warp works the segments out and leaves them in a ring of this many.  Done by every warp for itself
     // that took 3000 of the 10000 cycles of an item of one tile (its code is cold whenever it is reached): 309 -> 295 us
-    // for chunks of 2048, 167.5 -> 163.4 for prompts of 4096.  (e4m3: 92 -> 86 us for 64 chunks of 20,
-    // but 788 -> 817 for eight of 512, whose loops fill the instruction cache; every warp for itself.)
+    // for the chunks of up to 2048 above, 167.5 -> 163.4 for the prompts.  (e4m3: 92 -> 86 us for 64 chunks of 10 to
+    // 20, but 788 -> 817 for the eight of up to 512, whose loops fill the instruction cache; every warp for itself.)
     static constexpr int kSegs = Q8 ? 1 : 4;
     // Warp 8: queries and K; 9: V; 10: MMA; 12 .. 19: converters.
     static constexpr int kKWarp = 8, kVWarp = 9, kMmaWarp = 10, kConvWarp = 12;
     static constexpr int kConverters = Q8 ? 8 : 0;
     static constexpr int kThreads = (Q8 ? 12 + kConverters : 11) * 32;
     // e4m3: registers per thread of the softmax warps and of the others.  At launch each thread has kRegs; the
-    // sums over the warpgroups are the same.  (16-bit: 168 for everyone; 208 and 88 took 2% more.)
+    // sums over the warpgroups are the same.  (16-bit: 168 for everyone; 208 and 88 took 2% more.)  The
+    // e4m3 instances store 596 to 624 bytes of spills a thread, most of them in the softmax warps' loop (248 and 160
+    // are left without it, 484 and 520 without the converters'); 16-bit ones 48.
     static constexpr int kRegs = 96, kRegsSoftmax = 168, kRegsOther = 48;
     static_assert(!Q8 || 2 * kRegsSoftmax + (kThreads / 128 - 2) * kRegsOther == kThreads / 128 * kRegs,
                   "the launch's registers");
@@ -118,8 +120,8 @@ __device__ __forceinline__ void rows_out(uint32_t (&m)[8][4], uint8_t* dst, int 
 // Sixteen e4m3 bytes times an fp32 power of two, rounded once to 16 bits.  By way of fp16 and fp32: five
 // instructions per two values, over the conversion, fp and integer pipes.  (Moving sign, exponent and mantissa to
 // their places in bf16 and one 16-bit product are as many, most of them on the integer pipe, and lose a NaN byte and
-// rows of extreme size, which then have to be looked for: 792 and 829 us against 774 for chunks of 512 behind
-// up to 16384 tokens, 64 heads on 8 of 128.)
+// rows of extreme size, which then have to be looked for: 792 and 829 us against 774 for the eight chunks of up to 512
+// above.)
 template <bool BF16>
 __device__ __forceinline__ void scaled16(const uint4& x, uint64_t f2, uint32_t (&y)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};

@@ -103,7 +103,15 @@ constexpr int kClusterCtas = 8;  // of a unit in a short step (under a window 8,
 //     129 50.2 and 51.7 / 49.4 and 44.4
 //   16-bit, a CTA a unit, 256 units:  65 pages 25.2 and 28.5 / 20.0 and 25.1; 129 44.8 and 48.2 / 34.8 and 37.6;
 //     513 160.5 and 165.8 / 123.8 and 124.3
-// (16-bit caches would gain from more, but one long sequence among short ones is then left to a few warps.)
+// (16-bit caches would gain from more, but one long sequence among short ones is then left to a few warps.)  With
+// groups of 8 the line gains a little: 384 units of 69 pages over e4m3, 38.0 and 35.9 / 34.0 and 31.8.
+// Few new tokens without a window take the same rule, although their sequences may differ in length.  256 sequences
+// with 4 new tokens each, one cache head of 128, the longest of 2000 tokens (125 pages, two CTAs a unit), with clusters
+// and with the line: all of 2000 40.1 and 44.2 us over e4m3, 56.4 and 59.6 over 16-bit; evenly from 16 up 31.9 and
+// 36.0, 40.1 and 40.1; one of 2000 among 255 of 16 25.7 and 31.9, 32.9 and 31.9; one in sixteen of 2000, others of 64
+// 27.7 and 27.8, 36.0 and 25.7.  Over 60 batches of each kind (both types of cache and widths of heads, 64 to 500
+// sequences, 128 to 512 units, 19 to 250 pages) clusters take 0.90, 0.88, 0.86 and 0.98 of the line's time in the
+// geometric mean, 0.76 to 1.03, 0.72 to 1.06, 0.43 to 1.17 and 0.60 to 1.47: they lose where a few are long.
 constexpr int kGqaWindowPagesQ8 = 72, kGqaWindowPages = 136;
 constexpr int kGqaManyUnits = 2048;  // from so many on the line is dealt out in three rounds
 

@@ -279,10 +279,10 @@ fa_status check_chunk(int B, int Hq, int Hk, int L, int D, int num_pages, int ma
 
 // Whether the decode kernel takes a chunk, the new tokens of a group's heads as its queries: at most 16 rows per
 // cache head, over e4m3 rows of 64 at most 32, where reading the cache is all.  us of the decode kernel and the
-// chunk's, 64 sequences of 500 to 2000 tokens, 8 cache heads of 128 (of 64), a call with L2 flushed: 16-bit, 8 rows
-// 70 and 88 (48 and 72), 16 rows 87 and 89 (48 and 72), 32 133 and 89 (72 and 72); e4m3, 8 rows 54 and 113 (40 and 98),
-// 16 70 and 114 (50 and 97), 32 110 and 114 (80 and 97), 64 192 and 116 (137 and 99); four sequences of 300 to 30000
-// tokens, 128, e4m3, 32 rows: 89 and 81.
+// chunk's, 64 sequences of 500 to 2000 tokens and half to all of the rows' tokens new, 8 cache heads of 128 (of 64), a
+// call with L2 flushed: 16-bit, 8 rows 70 and 88 (48 and 72), 16 rows 87 and 89 (48 and 72), 32 133 and 89 (72 and 72);
+// e4m3, 8 rows 54 and 113 (40 and 98), 16 70 and 114 (50 and 97), 32 110 and 114 (80 and 97), 64 192 and 116 (137 and
+// 99); four sequences of 300 to 30000 tokens, 128, e4m3, 32 rows: 89 and 81.
 bool few_rows(int B, int Hq, int Hk, int L, int D, int num_pages, int max_pages, bool q8) {
     const long long rows = (long long)(Hq / Hk) * L;
     return rows <= (q8 && D == 64 ? 32 : 16) && (long long)Hq * L <= 65535 &&

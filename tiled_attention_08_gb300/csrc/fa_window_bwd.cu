@@ -643,6 +643,10 @@ struct DqCfg {
 // see a key.  The preprocess takes Delta from the rounded O, off by O's rounding and that of P in it; a row of few
 // keys passes that on to all of its dS (error of dQ and dK relative to their rounding to 16 bits alone: 1.75 for a
 // window of 8, 1.5 for 1024, whose first rows are the largest; with Delta from P and dP 1.45, dS's own rounding).
+// Its price: 8 to 26 us where only the first 256 rows of a head see so few keys (8 x 4096, 32 heads of 128, window 1024:
+// 26 of 1580 us); with window and first tokens below kDeltaKeys every query tile takes it, a quarter of the backward:
+// windows of 16, 64, 128, 255 295, 294, 276, 292 of 1120, 1114, 1072, 1192 us (heads of 64: 200, 192, 184, 219 of 834,
+// 818, 804, 947), where 256 takes 26 of 920 (20 of 742).
 template <int D, bool BF16, bool DELTA>
 __global__ void __launch_bounds__(DqCfg<D, BF16>::kThreads, 1)
     fa_window_dq_kernel(const __grid_constant__ WindowBwdParams p) {

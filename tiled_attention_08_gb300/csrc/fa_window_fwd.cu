@@ -21,10 +21,12 @@
 // Measured: 16384 tokens, 32 heads on 8 of 128, window 4096, 4 first tokens 640 us (1500 TFLOP/s of visible pairs);
 // 8 x 4096, 32 heads of 128, window 1024 441 us (1090); 3 x 5001, 16 heads on 4 of 64, window 777, 131 first 102 us
 // (497).  A step of both tiles takes 3400 cycles where its contractions take 2050: the chain from S to softmax to PV
-// counts, as in the dense forward.  Short windows lose the hidden halves of their first and last tiles and about 4000
-// cycles an item (first step, read-out).  Tried and dropped: S of the next item in front of this one's last PV (642 ->
-// 646, 451 -> 455 us); a tile of few first tokens as its first 32 keys alone (483 -> 480 us with them, 447 -> 462
-// without: code of two widths).
+// counts, as in the dense forward (heads of 64: tensor cores 30%, issue slots 47%, ALU 44%, XU 33%: no pipe is full
+// there either).  Short windows lose the hidden halves of their first and last tiles and about 4000 cycles an item
+// (first step, read-out).  Tried and dropped: S of the next item in front of this one's last PV (window 1024: 441 ->
+// 435 us, others 1 to 6% slower; before the producer worked the items out 451 -> 455, and 642 -> 646 for window 4096);
+// a tile of few first tokens as its first 32 keys alone (483 -> 480 us with them, 447 -> 462 without: code of two
+// widths).
 #include "fa_internal.h"
 #include "fa_ptx.cuh"
 #include "fa_sched.h"
@@ -331,7 +333,6 @@ __global__ void __launch_bounds__(WinCfg<D, BF16>::kThreads, 1)
     } else {
         // ------------------------------ softmax warps ------------------------------
         const int t = warp / 4, quad = warp % 4;
-        const int row = quad * 32 + lane;  // row inside the tile == TMEM lane
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const uint32_t s_addr = tmem + lane_off + C::kTmS + 128 * t;
         const uint32_t o_addr = tmem + lane_off + C::kTmO + D * t;
