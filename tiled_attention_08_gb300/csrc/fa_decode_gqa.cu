@@ -75,7 +75,6 @@
 // 32 sequences of 8192, 4 cache heads, groups of 8, 16, 32, 64: heads of 128 e4m3 62, 74, 128, 234 us,
 // 16-bit 97, 105, 181, 343; heads of 64 e4m3 43, 53, 88, 159, 16-bit 59, 59, 97, 178.  Two query blocks at
 // heads of 128 spill 36 words of 168 registers.
-#include <atomic>
 #include <type_traits>
 
 #include "fa_e4m3.cuh"
@@ -155,21 +154,6 @@ __device__ __forceinline__ GqaSplit gqa_split(long long total, int warps, int ro
     s.third = s.rounds > 1 ? total / 64 * 60 : total;
     s.total = total;
     return s;
-}
-
-// cudaFuncSetAttribute once per kernel and device (the calls below repeat every few microseconds).
-template <int D, bool Q8, bool BF16, int NT, bool SHORT, int MODE>
-struct kGqaKernelId {};
-template <typename Id, typename K>
-cudaError_t allow_shared(K kern, int bytes) {
-    static std::atomic<uint64_t> done{0};
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && (done.load() >> dev & 1)) return cudaSuccess;
-    const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (r == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev);
-    return r;
 }
 
 // Q8: an e4m3 cache.
@@ -1088,9 +1072,9 @@ __global__ void __launch_bounds__(256) fa_merge_kernel(const MergeParams p) {
 template <int D, bool Q8, bool BF16, int NT, bool SHORT, int MODE>
 cudaError_t launch_w(const GqaParams& p, cudaStream_t s) {
     using C = GqaCfg<D, Q8>;
-    auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT, MODE>;
+    constexpr auto kern = fa_decode_gqa_kernel<D, Q8, BF16, NT, SHORT, MODE>;
     const int smem = C::kRingBytes + 1024 + (kGqaMaxSequences + 1) * 4;
-    const cudaError_t e = allow_shared<kGqaKernelId<D, Q8, BF16, NT, SHORT, MODE>>(kern, smem);
+    const cudaError_t e = allow_shared_once<kern>(smem);
     if (e != cudaSuccess) return e;
     if constexpr (SHORT)
         return launch_kernel_cluster(kern, dim3((unsigned)(p.B * p.Hk * p.q_blocks * p.short_step)),
