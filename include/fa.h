@@ -454,8 +454,8 @@ size_t fa_window_bwd_workspace_bytes(int B, int Hq, int Hk, int Lq, int Lk, int 
  * summed over the heads of a group; zeros where no query sees a key).  strides[0..7] = q, k, v, o,
  * dout, dq, dk, dv; a gradient may be another part of one packed tensor with operands of its length.  Every
  * call gives the same bits.  An infinity or NaN in a row of an operand may reach the gradients of all rows and keys of
- * the tiles that meet there, also of those that do not see it.  Lq = Lk = 0 returns FA_OK, as does Hq = 0, which writes nothing (dk and dv neither);
- * only one of Lq and Lk 0 returns FA_ERR_UNSUPPORTED.  Calls that may overlap on the GPU need a workspace each.
+ * the tiles that meet there, also of those that do not see it.  Lq = Lk = 0 returns FA_OK, as does Hq = 0, which writes
+ * nothing (dk and dv neither); only one of Lq and Lk 0 returns FA_ERR_UNSUPPORTED.  Calls that may overlap on the GPU need a workspace each.
  * Enqueues three to five kernels.
  */
 fa_status fa_window_bwd(const void* q, const void* k, const void* v, const void* o, const void* dout,
