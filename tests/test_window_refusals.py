@@ -59,3 +59,10 @@ def test_errors_by_status():
     assert type(bad) is fa.FaArgumentError and type(other) is fa.FaError
     assert not isinstance(other, ValueError) and isinstance(bad, RuntimeError)
     assert str(bad).startswith("fa_call failed: ") and bad.status == fa.FA_ERR_INVALID_ARG
+
+
+def test_a_class_derived_from_the_error_stays_itself():
+    class Mine(fa.FaError):
+        pass
+
+    assert type(Mine("fa_call", fa.FA_ERR_INVALID_ARG)) is Mine

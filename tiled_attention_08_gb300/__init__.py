@@ -81,7 +81,9 @@ class FaError(RuntimeError):
     """A call's status other than FA_OK; for FA_ERR_INVALID_ARG it is a FaArgumentError."""
 
     def __new__(cls, call: str, status: int):
-        return super().__new__(FaArgumentError if status == FA_ERR_INVALID_ARG else cls, call, status)
+        if cls is FaError and status == FA_ERR_INVALID_ARG:
+            cls = FaArgumentError
+        return super().__new__(cls, call, status)
 
     def __init__(self, call: str, status: int):
         super().__init__(f"{call} failed: {fa_status_string(status)} ({status})")
